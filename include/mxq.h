@@ -1,6 +1,6 @@
 /*
- * mxq.h — C ABI of libmxq: weight-quantized scaled GEMM and routed fused MoE
- * on one NVIDIA GB300 (sm_103a).
+ * mxq.h — C ABI of libmxq: weight-quantized scaled GEMM, routed fused MoE and
+ * attention with a paged key/value cache on one NVIDIA GB300 (sm_103a).
  *
  * Conventions (all entry points):
  *   - The caller owns all memory.  Tensor arguments are DEVICE pointers on the
@@ -12,8 +12,8 @@
  *   - Arguments are validated on the host before anything is launched; on an
  *     error nothing is launched, outputs are untouched, and
  *     mxq_last_error() (thread-local) describes the problem.
- *   - Problems detected on the device (an expert id outside [0, E), a bounded
- *     wait that expired) set a device status word that mxq_sync_status reads.
+ *   - Problems detected on the device (an expert id outside [0, E), a cache slot
+ *     or page outside its range, a bounded wait that expired) set a device status word that mxq_sync_status reads.
  *   - The device must be compute capability 10.3 (GB300, sm_103a); any other
  *     device gives MXQ_ERR_UNSUPPORTED.
  *   - Row strides (ld*) are in elements.  Operands read by the tensor-memory
@@ -411,6 +411,112 @@ mxq_status mxq_fused_experts_ex(const void* hidden, int64_t T, int64_t K, int64_
 mxq_status mxq_fused_experts_workspace_size(int64_t T, int64_t K, int32_t E, int64_t N,
                                             int32_t topk, int32_t block_m, int32_t wtype,
                                             size_t* bytes);
+
+/*
+ * Rotate and append: the new tokens' keys and values go into a paged cache,
+ * the position rotation applied to q and k on the way.  No page describes it;
+ * it is the step between a QKV linear and the attention below.
+ *   q (or NULL with Hq = 0), k, v   bf16 [T, heads, D], token and head strides
+ *          s*_t, s*_h (e.g. slices of one QKV row)
+ *   q_out  bf16 [T, Hq, D] (written); may be q itself, with its strides
+ *   D      a multiple of 16 up to 512;  rot: 0, or a multiple of 16 up to D
+ *   cos_sin   fp32 [max_pos, rot] contiguous: rot/2 cosines, then rot/2 sines
+ *   positions int32 [T], in [0, max_pos)
+ *   With c, s of the token's position, each pair of the first rot elements
+ *   becomes (x1 c - x2 s, x2 c + x1 s) in fp32, every product and sum rounded
+ *   on its own; the pairs are (i, i + rot/2), or (2i, 2i + 1) if interleaved.
+ *   slots  int64 [T]: page * page_size + offset of each token, distinct;
+ *          a negative slot: the token's q is rotated, nothing is stored
+ *   k_cache, v_cache  [pages, page_size, Hkv, D] of cache_dtype MXQ_BF16 (y
+ *          rounded once) or MXQ_E4M3 (e4m3_rne(clamp(y / scale, +-448)), IEEE
+ *          division), any strides sc*_p, sc*_t, sc*_h of at least D
+ *   k_scale, v_scale  fp32 [Hkv], or NULL (1); MXQ_E4M3 only
+ * bf16 tensors (q, k, v, q_out, bf16 caches) need bases and strides of 16-byte
+ * multiples, e4m3 caches of 8.  A position or slot past its range skips
+ * the token (its slot: the store) and sets MXQ_ERR_DEVICE for mxq_sync_status.
+ * T == 0 is a no-op.
+ */
+mxq_status mxq_rope_append_kv(const void* q, int64_t sq_t, int64_t sq_h, int32_t Hq, void* q_out,
+                              int64_t so_t, int64_t so_h, const void* k, int64_t sk_t,
+                              int64_t sk_h, const void* v, int64_t sv_t, int64_t sv_h, int64_t T,
+                              int32_t Hkv, int32_t D, const float* cos_sin, int64_t max_pos,
+                              int32_t rot, const int32_t* positions, int32_t interleaved,
+                              const int64_t* slots, void* k_cache, void* v_cache,
+                              int32_t cache_dtype, int64_t pages, int32_t page_size,
+                              int64_t sck_p, int64_t sck_t, int64_t sck_h, int64_t scv_p,
+                              int64_t scv_t, int64_t scv_h, const float* k_scale,
+                              const float* v_scale, mxq_stream_t stream);
+
+/*
+ * Attention of one new token per sequence over the paged cache.  Sequence b's
+ * key j is row j % page_size of page page_table[b, j / page_size]; its length
+ * seq_lens[b] counts the new token, whose key is already in the cache.  For
+ * query head h on key/value head h / (Hq / Hkv), over the visible j:
+ *   s_j = scale * k_scale * (q . k_j),  lse = ln sum_j e^(s_j) (+ e^(sinks[h])),
+ *   out = v_scale * sum_j e^(s_j - lse) v_j
+ *   visible: all j < seq_lens[b], with window > 0 the last `window` of them;
+ *          none: out = 0 and lse = -inf (or the sink)
+ *   q, out bf16 [B, Hq, D] (strides s*_b, s*_h), D 64 or 128, Hq a multiple of
+ *          Hkv, at most 128 query heads per key/value head; sums, maxima and
+ *          the normalisation are fp32, the weights e^(s - m) enter the value
+ *          product as bf16 (bf16 cache) or f16 (e4m3 cache)
+ *   k_cache, v_cache as in mxq_rope_append_kv, 16-byte bases and strides for
+ *          either type; only the rows of visible keys are read
+ *   page_table int32 [B, max_pages], row stride ld_table; entries past a
+ *          sequence's pages are not read.  seq_lens int32 [B]
+ *   sinks  fp32 [Hq] or NULL: a logit per head without a value
+ *   lse    fp32 [B, Hq] or NULL
+ *   workspace mxq_paged_attention_decode_workspace_size bytes (NULL if 0),
+ *          256-byte aligned, not read before it is written
+ * A length outside [0, max_pages * page_size] is clamped, a page outside
+ * [0, pages) skipped; either sets MXQ_ERR_DEVICE for mxq_sync_status.
+ * B == 0 is a no-op.
+ */
+mxq_status mxq_paged_attention_decode(const void* q, int64_t sq_b, int64_t sq_h, int64_t B,
+                                      int32_t Hq, int32_t Hkv, int32_t D, const void* k_cache,
+                                      const void* v_cache, int32_t cache_dtype, int64_t pages,
+                                      int32_t page_size, int64_t sck_p, int64_t sck_t,
+                                      int64_t sck_h, int64_t scv_p, int64_t scv_t, int64_t scv_h,
+                                      const int32_t* page_table, int64_t ld_table,
+                                      int64_t max_pages, const int32_t* seq_lens, float scale,
+                                      int32_t window, const float* sinks, const float* k_scale,
+                                      const float* v_scale, void* out, int64_t so_b, int64_t so_h,
+                                      float* lse, void* workspace, size_t ws_bytes,
+                                      mxq_stream_t stream);
+mxq_status mxq_paged_attention_decode_workspace_size(int64_t B, int32_t Hq, int32_t Hkv, int32_t D,
+                                                     size_t* bytes);
+
+/*
+ * Attention of whole prompts, B sequences packed along the tokens.  Sequence b
+ * holds query rows [cu_seqlens_q[b], cu_seqlens_q[b+1]) and keys
+ * [cu_seqlens_k[b], cu_seqlens_k[b+1]); query i of nq stands at key position
+ * i + nk - nq (its chunk ends the keys).
+ *   visible keys j: j <= that position if causal, all otherwise; with
+ *          window > 0 (causal only) also j > position - window; none: out = 0
+ *          and lse = -inf (or the sink)
+ *   q, out bf16 [Tq, Hq, D], k, v bf16 [Tk, Hkv, D] (strides s*_t, s*_h);
+ *          heads, D, scale, sinks, lse (fp32 [Tq, Hq]) and precisions as in
+ *          mxq_paged_attention_decode
+ *   cu_seqlens_q, cu_seqlens_k int32 [B + 1], on the device
+ *   workspace mxq_attention_varlen_workspace_size bytes (NULL if 0), 256-byte
+ *          aligned, not read before it is written
+ * Rows outside every sequence are not written.  Keys and values of one
+ * sequence never reach another's output, whatever they hold; within a
+ * sequence a value that is not finite may reach any of its rows, as
+ * 0 * inf is not 0.  Offsets that decrease or leave [0, Tq] or [0, Tk] make
+ * their sequence empty and set MXQ_ERR_DEVICE for mxq_sync_status.
+ * B == 0 or Tq == 0 is a no-op.
+ */
+mxq_status mxq_attention_varlen(const void* q, int64_t sq_t, int64_t sq_h, const void* k,
+                                int64_t sk_t, int64_t sk_h, const void* v, int64_t sv_t,
+                                int64_t sv_h, const int32_t* cu_seqlens_q,
+                                const int32_t* cu_seqlens_k, int64_t B, int64_t Tq, int64_t Tk,
+                                int32_t Hq, int32_t Hkv, int32_t D, float scale, int32_t causal,
+                                int32_t window, const float* sinks, void* out, int64_t so_t,
+                                int64_t so_h, float* lse, void* workspace, size_t ws_bytes,
+                                mxq_stream_t stream);
+mxq_status mxq_attention_varlen_workspace_size(int64_t Tq, int64_t B, int32_t Hq, int32_t Hkv,
+                                               int32_t D, size_t* bytes);
 
 #ifdef __cplusplus
 }

@@ -1,4 +1,5 @@
-"""GB300-native weight-quantized scaled GEMM and routed fused MoE.
+"""GB300-native weight-quantized scaled GEMM, routed fused MoE and attention
+with a paged key/value cache.
 
 A thin PyTorch binding over libmxq (the C ABI in ``include/mxq.h``).  Torch
 provides device memory and the current stream; every step of the hot path
@@ -11,6 +12,9 @@ arguments: shapes, strides, output/workspace allocation and the stream.
     moe_align_block(topk_ids, num_experts, block_m) -> (sorted_ids, expert_ids,
                                                         offsets, num_blocks)
     fused_experts(hidden, w1, w1_scale, w2, w2_scale, topk_weights, topk_ids, ...)
+    rope_append_kv(k, v, k_cache, v_cache, slots, cos_sin, positions, q=None, ...)
+    paged_attention_decode(q, k_cache, v_cache, page_table, seq_lens, ...)
+    attention_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k=None, ...)
 """
 from __future__ import annotations
 
@@ -25,6 +29,8 @@ __all__ = [
     "MxqError", "per_token_group_quant_fp8", "fp8_scaled_mm", "w8a8_block_fp8_linear",
     "PackedWeight", "prepack_weight", "fp8_scaled_bmm", "quantize_mxfp4",
     "fp8_per_tensor_linear", "moe_align_block", "fused_experts", "align_capacity",
+    "rope_append_kv", "paged_attention_decode", "paged_attention_decode_workspace_size",
+    "attention_varlen", "attention_varlen_workspace_size",
     "set_option", "get_option", "sync_status", "W_FP8_BLOCK128", "W_MXFP4",
 ]
 
@@ -434,3 +440,231 @@ def fused_experts(hidden, w1, w1_scale, w2, w2_scale, topk_weights, topk_ids,
         return out, act, y, h
     check(lib.mxq_fused_experts(*args, _stream(hidden.device)))
     return out
+
+
+# ------------------------------------------------- paged cache and attention
+
+def _heads3(name, t, piece=8):
+    """t [n, heads, D] as the kernels read it: unit inner stride, outer strides
+    of `piece` elements' multiples and at least D (copies only if needed)."""
+    if t.dim() != 3:
+        raise ValueError("%s must be [tokens, heads, head_dim], got %d dimensions"
+                         % (name, t.dim()))
+    if t.dtype != torch.bfloat16:
+        raise TypeError("%s must be bf16" % name)
+    s0, s1, s2 = t.stride()
+    n0, n1, D = t.shape
+    if s2 != 1 or (n0 > 1 and (s0 < D or s0 % piece)) or (n1 > 1 and (s1 < D or s1 % piece)) \
+            or t.data_ptr() % 16:
+        t = t.clone(memory_format=torch.contiguous_format)
+    return t
+
+
+def _cache(name, t, kv_heads, D):
+    if t.dim() != 4 or t.shape[2] != kv_heads or t.shape[3] != D:
+        raise ValueError("%s must be [pages, page_size, %d, %d], got %s"
+                         % (name, kv_heads, D, list(t.shape)))
+    if t.stride(3) != 1:
+        raise ValueError("%s needs a unit stride along the head dimension" % name)
+    if t.dtype == torch.bfloat16:
+        return _lib.BF16
+    if t.dtype == torch.float8_e4m3fn:
+        return _lib.E4M3
+    raise TypeError("%s must be bf16 or float8_e4m3fn" % name)
+
+
+def _vec(name, t, dtype, n):
+    """A contiguous vector of n elements; its address (None for None)."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.numel() != n or not t.is_contiguous():
+        raise ValueError("%s must be contiguous %s of %d elements" % (name, dtype, n))
+    return t.data_ptr()
+
+
+def _same_device(dev, *ts):
+    for t in ts:
+        if t is not None and t.device != dev:
+            raise ValueError("mxq operates on CUDA tensors of one device (got %s and %s)"
+                             % (dev, t.device))
+
+
+def _check_out(name, t, shape):
+    if t.dtype != torch.bfloat16 or t.shape != shape or t.stride(2) != 1:
+        raise ValueError("%s must be bf16 %s with a unit inner stride" % (name, list(shape)))
+
+
+def _workspace(workspace, need, dev):
+    """(address, bytes) of a caller's workspace or of a new one."""
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    if workspace is None:
+        return None, 0, None
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+
+
+def rope_append_kv(k, v, k_cache, v_cache, slots, cos_sin=None, positions=None, q=None,
+                   q_out=None, k_scale=None, v_scale=None, interleaved: bool = False):
+    """Rotate q and k by position and write k and v into a paged cache.
+
+    k, v: bf16 [T, Hkv, D] (any token and head strides, e.g. slices of one QKV
+    row); q: None or bf16 [T, Hq, D]; k_cache, v_cache: [pages, page_size,
+    Hkv, D] bf16 or float8_e4m3fn, any outer strides (a head-major cache is
+    passed transposed); slots: int64 [T], page * page_size + offset, negative
+    = not stored; cos_sin: fp32 [max_pos, R], R/2 cosines then R/2 sines (None:
+    no rotation); positions: int32 [T]; k_scale, v_scale: fp32 [Hkv] of an
+    e4m3 cache (None: 1).  interleaved: the pairs are adjacent elements
+    instead of (i, i + R/2).  Returns the rotated q (q_out if given; it may be
+    q itself), or None without q."""
+    dev = k.device
+    _need_cuda(k)
+    _same_device(dev, v, k_cache, v_cache, slots, cos_sin, positions, q, q_out, k_scale, v_scale)
+    k, v = _heads3("k", k), _heads3("v", v)
+    T, Hkv, D = k.shape
+    if v.shape != k.shape:
+        raise ValueError("k and v must have the same shape")
+    dtype = _cache("k_cache", k_cache, Hkv, D)
+    if _cache("v_cache", v_cache, Hkv, D) != dtype or v_cache.shape != k_cache.shape:
+        raise ValueError("k_cache and v_cache must have the same shape and dtype")
+    rot = max_pos = 0
+    if cos_sin is not None:
+        if cos_sin.dim() != 2 or cos_sin.dtype != torch.float32 or not cos_sin.is_contiguous():
+            raise ValueError("cos_sin must be contiguous fp32 [max_pos, R]")
+        max_pos, rot = cos_sin.shape
+        if positions is None:
+            raise ValueError("a rotation needs positions")
+    pos = _vec("positions", positions, torch.int32, T)
+    Hq, q_args = 0, (None, 0, 0, 0, None, 0, 0)
+    if q is not None:
+        given = q
+        q = _heads3("q", q)
+        Hq = q.shape[1]
+        if q.shape[0] != T or q.shape[2] != D:
+            raise ValueError("q must be [%d, heads, %d]" % (T, D))
+        if q_out is None:
+            q_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev)
+        else:
+            _check_out("q_out", q_out, given.shape)
+        q_args = (q.data_ptr(), q.stride(0), q.stride(1), Hq, q_out.data_ptr(), q_out.stride(0),
+                  q_out.stride(1))
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    check(_lib_handle().mxq_rope_append_kv(
+        *q_args, k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(), v.stride(0), v.stride(1),
+        T, Hkv, D, None if cos_sin is None else cos_sin.data_ptr(), max_pos, rot, pos,
+        1 if interleaved else 0, _vec("slots", slots, torch.int64, T), k_cache.data_ptr(),
+        v_cache.data_ptr(), dtype, k_cache.shape[0], k_cache.shape[1], *k_cache.stride()[:3],
+        *v_cache.stride()[:3], _vec("k_scale", k_scale, torch.float32, Hkv),
+        _vec("v_scale", v_scale, torch.float32, Hkv),
+        torch.cuda.current_stream(dev).cuda_stream))
+    return q_out
+
+
+def paged_attention_decode_workspace_size(batch: int, heads: int, kv_heads: int,
+                                          head_dim: int) -> int:
+    n = ctypes.c_size_t(0)
+    check(_lib_handle().mxq_paged_attention_decode_workspace_size(
+        batch, heads, kv_heads, head_dim, ctypes.byref(n)))
+    return n.value
+
+
+def paged_attention_decode(q, k_cache, v_cache, page_table, seq_lens, scale=None, window: int = 0,
+                           sinks=None, k_scale=None, v_scale=None, return_lse: bool = False,
+                           out=None, workspace=None):
+    """Attention of one new token per sequence over a paged cache.
+
+    q: bf16 [B, Hq, D], D 64 or 128; k_cache, v_cache as in rope_append_kv,
+    the new token's key included; page_table: int32 [B, max_pages]; seq_lens:
+    int32 [B] (0: the row is 0); scale: default D**-0.5; window: only the last
+    `window` keys (0: all); sinks: fp32 [Hq], a logit per head without a
+    value; k_scale, v_scale: fp32 [Hkv] of an e4m3 cache.  Returns out bf16
+    [B, Hq, D], with return_lse also the fp32 [B, Hq] log-sum-exp.  workspace:
+    a caller's buffer of paged_attention_decode_workspace_size bytes (None:
+    allocated here)."""
+    dev = q.device
+    _need_cuda(q)
+    _same_device(dev, k_cache, v_cache, page_table, seq_lens, sinks, k_scale, v_scale, out,
+                 workspace)
+    q = _heads3("q", q)
+    B, Hq, D = q.shape
+    Hkv = k_cache.shape[2] if k_cache.dim() == 4 else 0
+    dtype = _cache("k_cache", k_cache, Hkv, D)
+    if _cache("v_cache", v_cache, Hkv, D) != dtype or v_cache.shape != k_cache.shape:
+        raise ValueError("k_cache and v_cache must have the same shape and dtype")
+    if page_table.dim() != 2 or page_table.shape[0] != B or page_table.dtype != torch.int32 \
+            or (page_table.shape[1] > 1 and page_table.stride(1) != 1):
+        raise ValueError("page_table must be int32 [%d, max_pages] with a unit inner stride" % B)
+    lib = _lib_handle()
+    if out is None:
+        out = torch.empty((B, Hq, D), dtype=torch.bfloat16, device=dev)
+    else:
+        _check_out("out", out, q.shape)
+    lse = torch.empty((B, Hq), dtype=torch.float32, device=dev) if return_lse else None
+    n = ctypes.c_size_t(0)
+    if workspace is None:
+        check(lib.mxq_paged_attention_decode_workspace_size(B, Hq, Hkv, D, ctypes.byref(n)))
+    ws, ws_bytes, workspace = _workspace(workspace, n.value, dev)
+    check(lib.mxq_paged_attention_decode(
+        q.data_ptr(), q.stride(0), q.stride(1), B, Hq, Hkv, D, k_cache.data_ptr(),
+        v_cache.data_ptr(), dtype, k_cache.shape[0], k_cache.shape[1], *k_cache.stride()[:3],
+        *v_cache.stride()[:3], page_table.data_ptr(), max(page_table.stride(0), page_table.shape[1]),
+        page_table.shape[1], _vec("seq_lens", seq_lens, torch.int32, B),
+        D ** -0.5 if scale is None else scale, window, _vec("sinks", sinks, torch.float32, Hq),
+        _vec("k_scale", k_scale, torch.float32, Hkv), _vec("v_scale", v_scale, torch.float32, Hkv),
+        out.data_ptr(), out.stride(0), out.stride(1), None if lse is None else lse.data_ptr(), ws,
+        ws_bytes, torch.cuda.current_stream(dev).cuda_stream))
+    return (out, lse) if return_lse else out
+
+
+def attention_varlen_workspace_size(tokens: int, batch: int, heads: int, kv_heads: int,
+                                    head_dim: int) -> int:
+    n = ctypes.c_size_t(0)
+    check(_lib_handle().mxq_attention_varlen_workspace_size(
+        tokens, batch, heads, kv_heads, head_dim, ctypes.byref(n)))
+    return n.value
+
+
+def attention_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k=None, scale=None, causal: bool = True,
+                     window: int = 0, sinks=None, return_lse: bool = False, out=None,
+                     workspace=None):
+    """Attention of whole prompts, sequences of different lengths packed.
+
+    q: bf16 [Tq, Hq, D], k, v: bf16 [Tk, Hkv, D] (any token and head strides),
+    D 64 or 128, Hq a multiple of Hkv; cu_seqlens_q, cu_seqlens_k: int32
+    [B + 1] offsets (None: the keys' are the queries'); causal: query i of nq
+    stands at key i + nk - nq and sees the keys up to it; window: only the
+    last `window` of these (0: all); sinks: fp32 [Hq].  A row that sees no key
+    is 0.  Returns out bf16 [Tq, Hq, D], with return_lse also the fp32
+    [Tq, Hq] log-sum-exp.  workspace: a caller's buffer of
+    attention_varlen_workspace_size bytes (None: allocated here)."""
+    dev = q.device
+    _need_cuda(q)
+    _same_device(dev, k, v, cu_seqlens_q, cu_seqlens_k, sinks, out, workspace)
+    q, k, v = _heads3("q", q), _heads3("k", k), _heads3("v", v)
+    Tq, Hq, D = q.shape
+    Tk, Hkv, Dk = k.shape
+    if Dk != D or v.shape != k.shape:
+        raise ValueError("k and v must be [tokens, kv_heads, %d] alike" % D)
+    if cu_seqlens_k is None:
+        cu_seqlens_k = cu_seqlens_q
+    B = cu_seqlens_q.numel() - 1
+    lib = _lib_handle()
+    if out is None:
+        out = torch.empty((Tq, Hq, D), dtype=torch.bfloat16, device=dev)
+    else:
+        _check_out("out", out, q.shape)
+    lse = torch.empty((Tq, Hq), dtype=torch.float32, device=dev) if return_lse else None
+    n = ctypes.c_size_t(0)
+    if workspace is None:
+        check(lib.mxq_attention_varlen_workspace_size(Tq, B, Hq, Hkv, D, ctypes.byref(n)))
+    ws, ws_bytes, workspace = _workspace(workspace, n.value, dev)
+    check(lib.mxq_attention_varlen(
+        q.data_ptr(), q.stride(0), q.stride(1), k.data_ptr(), k.stride(0), k.stride(1),
+        v.data_ptr(), v.stride(0), v.stride(1),
+        _vec("cu_seqlens_q", cu_seqlens_q, torch.int32, B + 1),
+        _vec("cu_seqlens_k", cu_seqlens_k, torch.int32, B + 1), B, Tq, Tk, Hq, Hkv, D,
+        D ** -0.5 if scale is None else scale, 1 if causal else 0, window,
+        _vec("sinks", sinks, torch.float32, Hq), out.data_ptr(), out.stride(0), out.stride(1),
+        None if lse is None else lse.data_ptr(), ws, ws_bytes,
+        torch.cuda.current_stream(dev).cuda_stream))
+    return (out, lse) if return_lse else out

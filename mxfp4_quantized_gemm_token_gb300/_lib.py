@@ -32,6 +32,8 @@ EXPORTED = [
     "mxq_prepacked_weight_size", "mxq_prepack_weight", "mxq_fp8_scaled_mm_prepacked",
     "mxq_fp8_scaled_bmm", "mxq_quantize_mxfp4", "mxq_fused_experts_ex",
     "mxq_w8a8_block_fp8_linear", "mxq_w8a8_block_fp8_linear_workspace_size",
+    "mxq_rope_append_kv", "mxq_paged_attention_decode", "mxq_paged_attention_decode_workspace_size",
+    "mxq_attention_varlen", "mxq_attention_varlen_workspace_size",
 ]
 
 NOALLOC_SCRATCH_BYTES = 16 * 1024 * 1024
@@ -82,6 +84,18 @@ def _declare(lib):
                                       I32, I32, I32, F, F, P, I64, P, SZ, P, P, P, P]),
         "mxq_fused_experts_workspace_size": (st, [I64, I64, I32, I64, I32, I32, I32,
                                                   ctypes.POINTER(SZ)]),
+        "mxq_rope_append_kv": (st, [P, I64, I64, I32, P, I64, I64, P, I64, I64, P, I64, I64, I64,
+                                    I32, I32, P, I64, I32, P, I32, P, P, P, I32, I64, I32, I64,
+                                    I64, I64, I64, I64, I64, P, P, P]),
+        "mxq_paged_attention_decode": (st, [P, I64, I64, I64, I32, I32, I32, P, P, I32, I64, I32,
+                                            I64, I64, I64, I64, I64, I64, P, I64, I64, P, F, I32,
+                                            P, P, P, P, I64, I64, P, P, SZ, P]),
+        "mxq_paged_attention_decode_workspace_size": (st, [I64, I32, I32, I32,
+                                                           ctypes.POINTER(SZ)]),
+        "mxq_attention_varlen": (st, [P, I64, I64, P, I64, I64, P, I64, I64, P, P, I64, I64, I64,
+                                      I32, I32, I32, F, I32, I32, P, P, I64, I64, P, P, SZ, P]),
+        "mxq_attention_varlen_workspace_size": (st, [I64, I64, I32, I32, I32,
+                                                     ctypes.POINTER(SZ)]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)

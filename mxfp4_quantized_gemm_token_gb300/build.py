@@ -20,7 +20,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmxq.so")
 
 SOURCES = ["api.cu", "quant.cu", "moe_aux.cu", "gemm_dense.cu", "gemm_moe.cu", "noalloc.cu",
-           "prepack.cu"]
+           "prepack.cu", "attn_api.cu", "rope_append.cu", "attn_decode.cu", "attn_prompt.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -178,7 +178,10 @@ extern "C" mxq_status mxq_sync_status(mxq_stream_t stream) {
   }
   if (word & kStatusTimeout)
     return fail(MXQ_ERR_TIMEOUT, "a bounded device wait expired; the kernel stopped early");
-  if (word & kStatusBadIndex) return fail(MXQ_ERR_DEVICE, "an expert id outside [0, E) was skipped");
+  if (word & kStatusBadIndex)
+    return fail(MXQ_ERR_DEVICE,
+                "an expert id outside [0, E), or a position, cache slot, page or sequence length "
+                "outside its range, was skipped");
   return MXQ_OK;
 }
 

@@ -12,7 +12,7 @@ namespace mxq {
 // Device status word bits (read back by mxq_sync_status).
 enum : int {
   kStatusTimeout = 1,     // a bounded wait gave up
-  kStatusBadIndex = 2,    // an expert id outside [0, E) was skipped
+  kStatusBadIndex = 2,    // an expert id, slot, page, position or length out of range
 };
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
