@@ -94,9 +94,11 @@ bool device_info(DeviceInfo* info, std::string* err) {
   return true;
 }
 
-bool make_map_2d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base, uint64_t inner,
-                 uint64_t outer, uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer,
-                 CUtensorMapSwizzle swizzle, std::string* err) {
+namespace {
+
+bool encode_map(CUtensorMap* map, CUtensorMapDataType dtype, uint32_t rank, const void* base,
+                const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box,
+                CUtensorMapSwizzle swizzle, std::string* err) {
   std::call_once(g_encode_once, [] {
     void* fn = nullptr;
     cudaDriverEntryPointQueryResult q;
@@ -110,11 +112,8 @@ bool make_map_2d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base, 
     return false;
   }
   std::memset(map, 0, sizeof(*map));
-  const cuuint64_t dims[2] = {inner, outer};
-  const cuuint64_t strides[1] = {row_bytes};
-  const cuuint32_t box[2] = {box_inner, box_outer};
-  const cuuint32_t estr[2] = {1, 1};
-  CUresult r = g_encode(map, dtype, 2, const_cast<void*>(base), dims, strides, box, estr,
+  const cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = g_encode(map, dtype, rank, const_cast<void*>(base), dims, strides, box, estr,
                         CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) {
@@ -122,6 +121,25 @@ bool make_map_2d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base, 
     return false;
   }
   return true;
+}
+
+}  // namespace
+
+bool make_map_2d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base, uint64_t inner,
+                 uint64_t outer, uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer,
+                 CUtensorMapSwizzle swizzle, std::string* err) {
+  const cuuint64_t dims[2] = {inner, outer};
+  const cuuint64_t strides[1] = {row_bytes};
+  const cuuint32_t box[2] = {box_inner, box_outer};
+  return encode_map(map, dtype, 2, base, dims, strides, box, swizzle, err);
+}
+
+bool make_map_bf16_3d(CUtensorMap* map, const void* base, const uint64_t dims[3],
+                      const uint64_t strides[2], const uint32_t box[3], std::string* err) {
+  const cuuint64_t d[3] = {dims[0], dims[1], dims[2]};
+  const cuuint64_t s[2] = {strides[0], strides[1]};
+  return encode_map(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, d, s, box,
+                    CU_TENSOR_MAP_SWIZZLE_128B, err);
 }
 
 }  // namespace mxq

@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <string>
+
 namespace mxq {
 
 // Strides are in elements; the innermost (head dimension) stride is 1.
@@ -73,6 +75,8 @@ cudaError_t launch_rope_append(const RopeAppendParams& p, int num_sms, cudaStrea
 size_t decode_workspace_bytes(int64_t B, int Hq, int Hkv, int D, int num_sms);
 cudaError_t launch_decode(const DecodeParams& p, int num_sms, cudaStream_t stream);
 size_t prompt_workspace_bytes(int64_t Tq, int64_t B, int Hq, int Hkv, int D, int num_sms);
-cudaError_t launch_prompt(const PromptParams& p, int num_sms, cudaStream_t stream);
+// err: set where the tensor maps cannot be made
+cudaError_t launch_prompt(const PromptParams& p, int num_sms, cudaStream_t stream,
+                          std::string* err);
 
 }  // namespace mxq

@@ -1,5 +1,6 @@
 // attn_api.cu — the extern "C" entry points of the paged cache and attention
 // operators (declared in mxq.h): host-side checks, then one launch function.
+#include <algorithm>
 #include <string>
 
 #include "attn.h"
@@ -210,7 +211,7 @@ extern "C" mxq_status mxq_paged_attention_decode(
   p.pages = pages, p.page_size = page_size;
   p.ck_p = sck_p, p.ck_t = sck_t, p.ck_h = sck_h, p.cv_p = scv_p, p.cv_t = scv_t, p.cv_h = scv_h;
   p.page_table = page_table, p.ld_table = ld_table, p.max_pages = max_pages, p.seq_lens = seq_lens;
-  p.scale = scale, p.window = window, p.sinks = sinks, p.k_scale = k_scale, p.v_scale = v_scale;
+  p.scale = scale, p.window = std::min(window, 1 << 30), p.sinks = sinks, p.k_scale = k_scale, p.v_scale = v_scale;
   p.out = out, p.o_b = so_b, p.o_h = so_h, p.lse = lse, p.workspace = workspace;
   p.status = d.status;
   const cudaError_t e = launch_decode(p, d.num_sms, reinterpret_cast<cudaStream_t>(stream));
@@ -268,9 +269,10 @@ extern "C" mxq_status mxq_attention_varlen(
   p.k = k, p.k_t = sk_t, p.k_h = sk_h, p.v = v, p.v_t = sv_t, p.v_h = sv_h;
   p.cu_q = cu_seqlens_q, p.cu_k = cu_seqlens_k;
   p.B = static_cast<int>(B), p.Tq = Tq, p.Tk = Tk, p.Hq = Hq, p.Hkv = Hkv, p.D = D;
-  p.scale = scale, p.causal = causal != 0, p.window = window, p.sinks = sinks;
+  p.scale = scale, p.causal = causal != 0, p.window = std::min(window, 1 << 30), p.sinks = sinks;
   p.out = out, p.o_t = so_t, p.o_h = so_h, p.lse = lse, p.workspace = workspace;
   p.status = d.status;
-  const cudaError_t e = launch_prompt(p, d.num_sms, reinterpret_cast<cudaStream_t>(stream));
+  const cudaError_t e = launch_prompt(p, d.num_sms, reinterpret_cast<cudaStream_t>(stream), &err);
+  if (!err.empty()) return fail(MXQ_ERR_CUDA, err);
   return e == cudaSuccess ? MXQ_OK : cuda_fail(e, "prompt attention launch");
 }

@@ -1,72 +1,599 @@
 // attn_prompt.cu — attention of whole prompts: packed sequences of different
 // lengths, grouped heads, causal and windowed masks.
+//
+//   S = Q K^T,  P = 2^(c S - c m),  l = rowsum P,  O = P V / l   (c = scale log2 e)
+//
+// one pass over the keys with the running maximum m and sum l of each row.
+//
+// Rows.  The G query heads of a key/value head read the same keys, so a tile's
+// 128 rows are (token, head of the group) pairs, token-major: TB = 128 / G tokens.  A
+// tile then spans few positions, which keeps both the masked part of the
+// diagonal tiles and the waste of short sequences small, and one 3-D TMA box
+// [64, G, TB] brings it in that order.  A CTA takes two tiles (2 TB
+// consecutive tokens) against 128-key blocks.
+//
+// Both products run on the tensor cores with their accumulators in tensor
+// memory: S0, S1 (128 columns each, later overwritten by P as bf16) and O0, O1 (D
+// columns each).  Q and K are K-major operands; V keeps its [key, d] rows and
+// enters as an MN-major operand; P is read from tensor memory.  While the
+// softmax of one tile runs on its warpgroup (one thread per row), the tensor
+// core works on the other tile.
+//   warps 0-3, 4-7   softmax of tile 0 and 1, and their output
+//   warp 8           issues the MMAs
+//   warp 9           loads Q, K and V with TMA (one ring; K and V alternate)
+// The maximum a row subtracts is only raised when it grows by more than 2^8 in the
+// exponent: O is rescaled (by the row's own thread) in few blocks,
+// and l and O stay far from the range's ends.  l and O use the same reference, so
+// the result does not depend on it.
+//
+// Work.  A kernel of one block first lists the work items (sequence, pair of
+// tiles, its blocks of keys) with the costliest first; the persistent CTAs
+// take them in turn, in alternating direction, which balances lengths.
+#include <cuda_bf16.h>
+#include <math.h>
+
+#include <string>
+
 #include "attn.h"
-#include "attn_simple.cuh"
 #include "internal.h"
 
 namespace mxq {
 
 namespace {
 
-// [start, start + len) of sequence b in cu, held inside [0, total]
-__device__ __forceinline__ bool seq_range(const int32_t* cu, int b, int64_t total, int64_t* start,
-                                          int64_t* len) {
+constexpr int kBM = 128;             // rows of a tile, keys of a block
+constexpr int kPromptThreads = 320;
+
+struct PromptMaps {
+  CUtensorMap q, k, v;
+};
+
+// One pair of tiles: tokens [q_row, q_row + ntok) of the packed queries, the
+// first of which stands at key position at0 of its sequence's nk keys, and the
+// key blocks [kb0, kb1) that any of them sees.
+struct __align__(16) PromptItem {
+  int q_row, ntok, at0, k_row;
+  int nk, kb0, kb1, pad;
+};
+
+struct PromptArgs {
+  PromptParams p;
+  const int* n_items;                // header of the workspace
+  const PromptItem* items;
+  int G, TB;
+  unsigned long long budget_ns;
+  int inject_stall;
+};
+
+constexpr int kBuckets = 512;
+
+// [start, start + len) of sequence b in cu, or nothing if it leaves [0, total]
+__device__ __forceinline__ bool seq_range(const int32_t* cu, int b, int64_t total, int* start,
+                                          int* len) {
   const int64_t a = cu[b], e = cu[b + 1];
   const bool ok = a >= 0 && e >= a && e <= total;
-  *start = ok ? a : 0;
-  *len = ok ? e - a : 0;
+  *start = ok ? static_cast<int>(a) : 0;
+  *len = ok ? static_cast<int>(e - a) : 0;
   return ok;
 }
 
-template <int D>
-__global__ void prompt_kernel(const PromptParams p) {
-  constexpr int N = D / 32;
+// Lists the items, ordered by falling number of key blocks (a counting sort; more than
+// 511 blocks count as 511).
+__global__ void __launch_bounds__(1024) prompt_plan_kernel(const PromptParams p, int tokens_per_item,
+                                                           int* n_items, PromptItem* items,
+                                                           int cap) {
+  __shared__ int count[kBuckets];
   pdl_wait();
   pdl_launch_dependents();
-  const int lane = threadIdx.x & 31;
-  const int h = blockIdx.y;
-  const int hk = h / (p.Hq / p.Hkv);
-  const int b = blockIdx.z;
-  int64_t q0, nq, k0, nk;
-  const bool okq = seq_range(p.cu_q, b, p.Tq, &q0, &nq);
-  const bool okk = seq_range(p.cu_k, b, p.Tk, &k0, &nk);
-  if (!(okq && okk) && threadIdx.x == 0) atomicOr(p.status, kStatusBadIndex);
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5);
-       i < nq; i += static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5)) {
-    float q[N];
-    load_row<N, false>(static_cast<const __nv_bfloat16*>(p.q) + (q0 + i) * p.q_t + h * p.q_h, lane,
-                       q);
-#pragma unroll
-    for (int e = 0; e < N; ++e) q[e] *= p.scale;
-    const int64_t at = i + nk - nq;
-    const int64_t hi = p.causal ? (at + 1 < nk ? at + 1 : nk) : nk;
-    const int64_t lo = p.window > 0 && at - p.window + 1 > 0 ? at - p.window + 1 : 0;
-    SoftmaxRow<N> row;
-    for (int64_t j = lo; j < hi; ++j) {
-      float k[N], v[N];
-      load_row<N, false>(static_cast<const __nv_bfloat16*>(p.k) + (k0 + j) * p.k_t + hk * p.k_h,
-                         lane, k);
-      load_row<N, false>(static_cast<const __nv_bfloat16*>(p.v) + (k0 + j) * p.v_t + hk * p.v_h,
-                         lane, v);
-      row.add(q, k, v);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int i = threadIdx.x; i < kBuckets; i += blockDim.x) count[i] = 0;
+  __syncthreads();
+  for (int pass = 0; pass < 2; ++pass) {
+    for (int b = warp; b < p.B; b += 32) {
+      int q0, nq, k0, nk;
+      const bool okq = seq_range(p.cu_q, b, p.Tq, &q0, &nq);
+      const bool okk = seq_range(p.cu_k, b, p.Tk, &k0, &nk);
+      if (!(okq && okk)) {
+        if (lane == 0) atomicOr(p.status, kStatusBadIndex);
+        continue;
+      }
+      const int pairs = (nq + tokens_per_item - 1) / tokens_per_item;
+      for (int i = lane; i < pairs; i += 32) {
+        PromptItem it;
+        const int first = i * tokens_per_item;
+        it.q_row = q0 + first;
+        it.ntok = min(tokens_per_item, nq - first);
+        it.at0 = first + nk - nq;
+        it.k_row = k0;
+        it.nk = nk;
+        const int hi = p.causal ? min(nk, it.at0 + it.ntok) : nk;
+        it.kb1 = hi > 0 ? (hi + kBM - 1) / kBM : 0;
+        it.kb0 = p.window > 0 ? max(0, it.at0 - p.window + 1) / kBM : 0;
+        it.pad = 0;
+        const int bucket = kBuckets - 1 - min(kBuckets - 1, max(0, it.kb1 - it.kb0));
+        if (pass == 0) {
+          atomicAdd(&count[bucket], 1);
+        } else {
+          const int at = atomicAdd(&count[bucket], 1);
+          if (at < cap) items[at] = it;
+        }
+      }
     }
-    if (p.sinks) row.sink(p.sinks[h]);
-    row.store(static_cast<__nv_bfloat16*>(p.out) + (q0 + i) * p.o_t + h * p.o_h, lane,
-              p.lse ? p.lse + (q0 + i) * p.Hq + h : nullptr, 1.f);
+    __syncthreads();
+    if (pass == 0) {
+      // exclusive prefix sum over the buckets, by one warp
+      if (warp == 0) {
+        int run = 0;
+        for (int i = 0; i < kBuckets; i += 32) {
+          const int c = count[i + lane];
+          int x = c;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+          }
+          count[i + lane] = run + x - c;
+          run += __shfl_sync(0xffffffffu, x, 31);
+        }
+        // only offsets that run backwards give more items than there is room for
+        if (lane == 0) {
+          if (run > cap) atomicOr(p.status, kStatusBadIndex);
+          *n_items = min(run, cap);
+        }
+      }
+      __syncthreads();
+    }
   }
+}
+
+template <int D>
+struct PromptLayout {
+  static constexpr int kChunks = D / 64;
+  static constexpr int kChunkBytes = kBM * 128;          // 128 rows of 64 elements
+  static constexpr int kTileBytes = kChunks * kChunkBytes;
+  static constexpr int kStages = D == 128 ? 5 : 9;
+  static constexpr int kBars = 2 * 4 + 2 * kStages + 1;
+  static constexpr int kSmem = (2 + kStages) * kTileBytes + 8 * kBars + 16;
+  static_assert(kSmem + 1024 <= 227 * 1024, "shared memory over budget");
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t r, float* a, float* b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(*a), "=f"(*b) : "l"(r));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// position r of the sequence of items that this CTA takes, in alternating direction
+__device__ __forceinline__ int item_index(int r) {
+  return r * gridDim.x + ((r & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kPromptThreads, 1)
+    prompt_kernel(const __grid_constant__ PromptMaps maps, const PromptArgs a) {
+  using L = PromptLayout<D>;
+  constexpr int ST = L::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint8_t* sQ = smem;
+  uint8_t* ring = smem + 2 * L::kTileBytes;
+  uint64_t* q_full = reinterpret_cast<uint64_t*>(ring + ST * L::kTileBytes);
+  uint64_t* q_empty = q_full + 2;
+  uint64_t* s_full = q_empty + 2;
+  uint64_t* p_full = s_full + 2;
+  uint64_t* kv_full = p_full + 2;
+  uint64_t* kv_empty = kv_full + ST;
+  uint64_t* drain = kv_empty + ST;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const PromptParams& p = a.p;
+  WaitCtx wc{p.status, abort_flag, a.budget_ns};
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&q_full[i], 1);
+      mbar_init(&q_empty[i], 1);
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 4);       // the warps of the tile's warpgroup
+    }
+    for (int i = 0; i < ST; ++i) {
+      mbar_init(&kv_full[i], 1);
+      mbar_init(&kv_empty[i], 1);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 9 && lane == 0) {
+    tma_prefetch_desc(&maps.q);
+    tma_prefetch_desc(&maps.k);
+    tma_prefetch_desc(&maps.v);
+  }
+  if (warp == 8) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_wait();
+  pdl_launch_dependents();
+  const int total = *a.n_items * p.Hkv;
+
+  if (warp == 9) {
+    // ------------------------------------------------------------ loads
+    if (lane == 0 && !a.inject_stall) {
+      uint32_t fill = 0, nq = 0;
+      const uint32_t q_bytes = static_cast<uint32_t>(a.G * a.TB) * 128 * L::kChunks;
+      bool ok = true;
+      for (int r = 0; ok && item_index(r) < total; ++r) {
+        const int idx = item_index(r);
+        const PromptItem it = a.items[idx / p.Hkv];
+        const int hk = idx % p.Hkv;
+        if (it.kb1 <= it.kb0) continue;
+        auto load_q = [&](int s) {
+          if (!mbar_wait(&q_empty[s], (nq & 1) ^ 1, wc)) return false;
+          mbar_expect_tx(&q_full[s], q_bytes);
+          for (int c = 0; c < L::kChunks; ++c)
+            tma_load_3d(sQ + s * L::kTileBytes + c * L::kChunkBytes, &maps.q, &q_full[s], c * 64,
+                        hk * a.G, it.q_row + s * a.TB);
+          return true;
+        };
+        auto load_kv = [&](const CUtensorMap* map, int kb) {
+          const int st = fill % ST;
+          if (!mbar_wait(&kv_empty[st], ((fill / ST) & 1) ^ 1, wc)) return false;
+          mbar_expect_tx(&kv_full[st], L::kTileBytes);
+          for (int c = 0; c < L::kChunks; ++c)
+            tma_load_3d(ring + st * L::kTileBytes + c * L::kChunkBytes, map, &kv_full[st], c * 64,
+                        hk, it.k_row + kb * kBM);
+          ++fill;
+          return true;
+        };
+        ok = load_q(0) && load_kv(&maps.k, it.kb1 - 1) && load_q(1) &&
+             load_kv(&maps.v, it.kb1 - 1);
+        ++nq;
+        for (int kb = it.kb1 - 2; ok && kb >= it.kb0; --kb)
+          ok = load_kv(&maps.k, kb) && load_kv(&maps.v, kb);
+      }
+      if (*abort_flag) {
+        // let every copy already issued land before the CTA goes away
+        volatile int zero = 0;
+        WaitCtx dw{p.status, &zero, 1000000000ull};
+        for (uint32_t i = fill > ST ? fill - ST : 0; i < fill; ++i)
+          mbar_wait(&kv_full[i % ST], (i / ST) & 1, dw);
+        for (int s = 0; s < 2; ++s)
+          if (nq > 0) mbar_wait(&q_full[s], (nq - 1) & 1, dw);
+      }
+    }
+  } else if (warp == 8) {
+    // -------------------------------------------------------------- MMAs
+    constexpr uint32_t kDescS = idesc_bf16(kBM, kBM);
+    constexpr uint32_t kDescO = idesc_bf16_bmn(kBM, D);
+    const bool leader = elect_one();
+    const uint32_t q_addr = smem_u32(sQ), ring_addr = smem_u32(ring);
+    uint32_t base = 0, nq = 0, np = 0;     // ring position of K_0, items, blocks so far
+    auto issue_s = [&](int s, uint32_t fill) {
+      const uint32_t qa = q_addr + s * L::kTileBytes;
+      const uint32_t ka = ring_addr + (fill % ST) * L::kTileBytes;
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        const uint32_t off = (k / 4) * L::kChunkBytes + (k % 4) * 32;
+        mma_f16(tmem + s * 128, sw128_desc(qa + off), sw128_desc(ka + off), kDescS, k > 0);
+      }
+    };
+    auto issue_o = [&](int s, uint32_t fill, bool accumulate) {
+      const uint32_t va = ring_addr + (fill % ST) * L::kTileBytes;
+#pragma unroll
+      for (int k = 0; k < kBM / 16; ++k)
+        mma_f16_ts(tmem + 256 + s * 128, tmem + s * 128 + k * 8,
+                   sw128_desc_mn(va + k * 2048, L::kChunkBytes), kDescO, accumulate || k > 0);
+    };
+    auto wait_kv = [&](uint32_t fill) {
+      return mbar_wait_warp(&kv_full[fill % ST], (fill / ST) & 1, wc);
+    };
+    for (int r = 0; item_index(r) < total; ++r) {
+      const PromptItem it = a.items[item_index(r) / p.Hkv];
+      const int n = it.kb1 - it.kb0;
+      if (n <= 0) continue;
+      if (!wait_kv(base)) goto mma_done;
+      for (int s = 0; s < 2; ++s) {
+        if (!mbar_wait_warp(&q_full[s], nq & 1, wc)) goto mma_done;
+        if (leader) {
+          tc_fence_after();
+          issue_s(s, base);
+          mma_commit(&s_full[s]);
+          if (n == 1) mma_commit(&q_empty[s]);
+          if (s == 1) mma_commit(&kv_empty[base % ST]);
+        }
+        __syncwarp();
+      }
+      for (int j = 0; j < n; ++j, ++np) {
+        const uint32_t vf = base + 2 * j + 1, kf = vf + 1;
+        if (!wait_kv(vf)) goto mma_done;
+        for (int s = 0; s < 2; ++s) {
+          if (!mbar_wait_warp(&p_full[s], np & 1, wc)) goto mma_done;
+          if (leader) {
+            tc_fence_after();
+            issue_o(s, vf, j > 0);
+            if (s == 1) mma_commit(&kv_empty[vf % ST]);
+          }
+          __syncwarp();
+          if (j + 1 < n) {
+            if (s == 0 && !wait_kv(kf)) goto mma_done;
+            if (leader) {
+              tc_fence_after();
+              issue_s(s, kf);
+              mma_commit(&s_full[s]);
+              if (j + 2 == n) mma_commit(&q_empty[s]);
+              if (s == 1) mma_commit(&kv_empty[kf % ST]);
+            }
+          } else if (leader) {
+            mma_commit(&s_full[s]);        // the item's O is complete
+          }
+          __syncwarp();
+        }
+      }
+      base += 2 * n;
+      ++nq;
+    }
+  mma_done:
+    if (*abort_flag) {
+      // wait for the MMAs in flight before the tensor memory is freed
+      if (leader) mma_commit(drain);
+      volatile int zero = 0;
+      WaitCtx dw{p.status, &zero, 1000000000ull};
+      mbar_wait(drain, 0, dw);
+    }
+  } else {
+    // ----------------------------------------------------------- softmax
+    const int s = warp >> 2;                            // tile
+    const int row = threadIdx.x & 127;
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + s * 128 + lanes, tO = tmem + 256 + s * 128 + lanes;
+    const int tok = row / a.G, g = row - tok * a.G;
+    const float c = p.scale * 1.44269504088896340736f;  // log2 e
+    uint32_t ns = 0, base = 0;
+    for (int r = 0; item_index(r) < total; ++r) {
+      const int idx = item_index(r);
+      const PromptItem it = a.items[idx / p.Hkv];
+      const int n = it.kb1 - it.kb0;
+      const int h = (idx % p.Hkv) * a.G + g;
+      const int i = s * a.TB + tok;
+      const bool valid = tok < a.TB && i < it.ntok;
+      // visible keys [lo, hi) of this row
+      const int at = it.at0 + i;
+      const int hi = !valid ? 0 : (p.causal ? min(it.nk, at + 1) : it.nk);
+      const int lo = p.window > 0 ? max(0, at - p.window + 1) : 0;
+      float m = -INFINITY, l = 0.f;
+      for (int j = 0; j < n; ++j) {
+        const int kb = it.kb1 - 1 - j;
+        if (!mbar_wait_warp(&s_full[s], ns & 1, wc)) goto softmax_done;
+        ++ns;
+        tc_fence_after();
+        float x[128];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) tmem_ld32_async(tS + 32 * q, x + 32 * q);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) tmem_wait32(x + 32 * q);
+        const int c_hi = hi - kb * kBM, c_lo = lo - kb * kBM;
+        if (__any_sync(0xffffffffu, c_hi < kBM || c_lo > 0)) {
+#pragma unroll
+          for (int e = 0; e < 128; ++e) x[e] = e < c_hi && e >= c_lo ? x[e] : -INFINITY;
+        }
+        float mx = x[0];
+#pragma unroll
+        for (int e = 1; e < 127; e += 2) mx = fmaxf(mx, fmaxf(x[e], x[e + 1]));
+        mx = fmaxf(mx, x[127]);
+        // raise the reference if it grows by more than 2^8 (at first: from -inf)
+        const bool raise = (mx - m) * c > 8.f || (m == -INFINITY && mx > -INFINITY);
+        if (__any_sync(0xffffffffu, raise)) {
+          const float f = raise ? (m == -INFINITY ? 0.f : ex2((m - mx) * c)) : 1.f;
+          if (__any_sync(0xffffffffu, raise && m > -INFINITY)) {
+            // the products of the blocks before are complete: their commit came
+            // before this block's scores
+#pragma unroll 1
+            for (int q = 0; q < D; q += 32) {
+              float o[32];
+              tmem_ld32(tO + q, o);
+              uint32_t w[32];
+#pragma unroll
+              for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(o[e] * f);
+              tmem_st32(tO + q, w);
+            }
+          }
+          l *= f;
+          if (raise) m = mx;
+        }
+        const float mc = m == -INFINITY ? 0.f : m * c;
+        const uint64_t c2 = pack2(c, c), n2 = pack2(-mc, -mc);
+        uint64_t sum0 = pack2(0.f, 0.f), sum1 = sum0;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          uint32_t w[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            float u, v;
+            unpack2(fma2(pack2(x[64 * q + 2 * e], x[64 * q + 2 * e + 1]), c2, n2), &u, &v);
+            u = ex2(u), v = ex2(v);
+            w[e] = bf16x2(u, v);
+            if (e & 1)
+              sum1 = add2(sum1, pack2(u, v));
+            else
+              sum0 = add2(sum0, pack2(u, v));
+          }
+          tmem_st32(tS + 32 * q, w);
+        }
+        float s0, s1;
+        unpack2(add2(sum0, sum1), &s0, &s1);
+        l += s0 + s1;
+        if (j == 0 && s == 0 && it.nk < it.kb1 * kBM) {
+          // the last block's rows past the sequence are other keys' (or none): their
+          // weights are 0, and the values become 0 too, as 0 * inf is not 0
+          const uint32_t vf = base + 1;
+          if (!mbar_wait_warp(&kv_full[vf % ST], (vf / ST) & 1, wc)) goto softmax_done;
+          if (kb * kBM + row >= it.nk) {
+            uint8_t* vr = ring + (vf % ST) * L::kTileBytes + row * 128;
+            for (int ch = 0; ch < L::kChunks; ++ch)
+#pragma unroll
+              for (int q = 0; q < 8; ++q)
+                *reinterpret_cast<uint4*>(vr + ch * L::kChunkBytes + 16 * q) =
+                    make_uint4(0u, 0u, 0u, 0u);
+          }
+          fence_proxy_async_smem();
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[s]);
+      }
+      base += n > 0 ? 2 * n : 0;
+      if (n > 0) {
+        if (!mbar_wait_warp(&s_full[s], ns & 1, wc)) goto softmax_done;
+        ++ns;
+        tc_fence_after();
+      }
+      // out = O / l, with the sink's logit in the sum; both taken relative to
+      // the larger of the row's reference and the sink
+      const float ms = m * p.scale;
+      float f = 1.f, top = ms;
+      if (p.sinks != nullptr && valid) {
+        const float sink = __ldg(p.sinks + h);
+        top = fmaxf(ms, sink);
+        f = ms == -INFINITY ? 0.f : expf(ms - top);
+        l = l * f + (sink == -INFINITY ? 0.f : expf(sink - top));
+      }
+      const bool none = l == 0.f;           // the row saw nothing
+      const float inv = none ? 0.f : f / l;
+      const int64_t tokr = it.q_row + i;
+      __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + tokr * p.o_t + h * p.o_h;
+#pragma unroll
+      for (int q = 0; q < D; q += 32) {
+        float o[32];
+        if (n > 0) {
+          tmem_ld32(tO + q, o);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = 0.f;
+        }
+        if (valid) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 8) {
+            uint4 w;
+            w.x = bf16x2(none ? 0.f : o[e] * inv, none ? 0.f : o[e + 1] * inv);
+            w.y = bf16x2(none ? 0.f : o[e + 2] * inv, none ? 0.f : o[e + 3] * inv);
+            w.z = bf16x2(none ? 0.f : o[e + 4] * inv, none ? 0.f : o[e + 5] * inv);
+            w.w = bf16x2(none ? 0.f : o[e + 6] * inv, none ? 0.f : o[e + 7] * inv);
+            *reinterpret_cast<uint4*>(dst + q + e) = w;
+          }
+        }
+      }
+      if (p.lse != nullptr && valid)
+        p.lse[tokr * p.Hq + h] = none ? -INFINITY : top + logf(l);
+      tc_fence_before();
+    }
+  softmax_done:;
+  }
+
+  __syncthreads();
+  if (warp == 8) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+int tokens_per_tile(int Hq, int Hkv) { return kBM / (Hq / Hkv); }
+
+int64_t max_items(int64_t Tq, int64_t B, int Hq, int Hkv) {
+  const int64_t per = 2 * tokens_per_tile(Hq, Hkv);
+  // each sequence's last item may be ragged
+  return Tq / per + (B < Tq ? B : Tq) + 1;
+}
+
+template <int D>
+cudaError_t launch(const PromptMaps& maps, const PromptArgs& a, int grid, cudaStream_t stream) {
+  const int smem = PromptLayout<D>::kSmem + 1024;
+  static bool configured[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (!configured[dev]) {
+    e = cudaFuncSetAttribute(prompt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    configured[dev] = true;
+  }
+  return launch_k(prompt_kernel<D>, dim3(grid), dim3(kPromptThreads), static_cast<size_t>(smem),
+                  stream, maps, a);
 }
 
 }  // namespace
 
-size_t prompt_workspace_bytes(int64_t, int64_t, int, int, int, int) { return 0; }
+size_t prompt_workspace_bytes(int64_t Tq, int64_t B, int Hq, int Hkv, int, int) {
+  return 256 + static_cast<size_t>(max_items(Tq, B, Hq, Hkv)) * sizeof(PromptItem);
+}
 
-cudaError_t launch_prompt(const PromptParams& p, int, cudaStream_t stream) {
-  int64_t gx = (p.Tq + 3) / 4;
-  if (gx > 2048) gx = 2048;
-  const dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(p.Hq),
-                  static_cast<unsigned>(p.B));
-  if (p.D == 128) return launch_k(prompt_kernel<128>, grid, dim3(128), 0, stream, p);
-  return launch_k(prompt_kernel<64>, grid, dim3(128), 0, stream, p);
+cudaError_t launch_prompt(const PromptParams& p, int num_sms, cudaStream_t stream,
+                          std::string* err) {
+  PromptArgs a = {};
+  a.p = p;
+  a.G = p.Hq / p.Hkv;
+  a.TB = tokens_per_tile(p.Hq, p.Hkv);
+  a.n_items = static_cast<const int*>(p.workspace);
+  a.items = reinterpret_cast<const PromptItem*>(static_cast<const char*>(p.workspace) + 256);
+  a.budget_ns = static_cast<unsigned long long>(option(MXQ_OPT_WAIT_BUDGET_NS));
+  a.inject_stall = static_cast<int>(option(MXQ_OPT_INJECT_STALL));
+  // [n, heads, D] as (D, heads, n); a dimension of one takes any legal stride
+  auto map3 = [&](CUtensorMap* m, const void* base, int heads, int64_t n, int64_t st, int64_t sh,
+                  int box_h, int box_n) {
+    const int64_t row = static_cast<int64_t>(p.D) * 2;
+    const uint64_t dims[3] = {static_cast<uint64_t>(p.D), static_cast<uint64_t>(heads),
+                              static_cast<uint64_t>(n)};
+    const uint64_t strides[2] = {static_cast<uint64_t>(heads > 1 ? sh * 2 : row),
+                                 static_cast<uint64_t>(n > 1 ? st * 2 : row)};
+    const uint32_t box[3] = {64, static_cast<uint32_t>(box_h), static_cast<uint32_t>(box_n)};
+    return make_map_bf16_3d(m, base, dims, strides, box, err);
+  };
+  PromptMaps maps;
+  // without keys no block is loaded: any tensor serves as the maps' base
+  const bool keys = p.Tk > 0;
+  if (!map3(&maps.q, p.q, p.Hq, p.Tq, p.q_t, p.q_h, a.G, a.TB) ||
+      !map3(&maps.k, keys ? p.k : p.q, p.Hkv, keys ? p.Tk : 1, p.k_t, keys ? p.k_h : p.D, 1, kBM) ||
+      !map3(&maps.v, keys ? p.v : p.q, p.Hkv, keys ? p.Tk : 1, p.v_t, keys ? p.v_h : p.D, 1, kBM))
+    return cudaErrorInvalidValue;
+  const cudaError_t e =
+      launch_k(prompt_plan_kernel, dim3(1), dim3(1024), 0, stream, p, 2 * a.TB,
+               static_cast<int*>(p.workspace), const_cast<PromptItem*>(a.items),
+               static_cast<int>(max_items(p.Tq, p.B, p.Hq, p.Hkv)));
+  if (e != cudaSuccess) return e;
+  const int64_t most = max_items(p.Tq, p.B, p.Hq, p.Hkv) * p.Hkv;
+  const int grid = static_cast<int>(most < num_sms ? most : num_sms);
+  return p.D == 128 ? launch<128>(maps, a, grid, stream) : launch<64>(maps, a, grid, stream);
 }
 
 }  // namespace mxq

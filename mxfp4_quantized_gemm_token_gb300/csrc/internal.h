@@ -47,6 +47,11 @@ bool make_map_2d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base, 
                  uint64_t outer, uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer,
                  CUtensorMapSwizzle swizzle, std::string* err);
 
+// bf16 tensor of three dimensions (innermost first, contiguous), byte strides
+// of the outer two, 128-byte swizzle
+bool make_map_bf16_3d(CUtensorMap* map, const void* base, const uint64_t dims[3],
+                      const uint64_t strides[2], const uint32_t box[3], std::string* err);
+
 // Launch kernel<<<grid, block, smem, stream>>>(args...), with programmatic
 // stream serialization (the kernel may launch while the previous one on
 // the stream finishes; it waits for it in pdl_wait()) unless MXQ_OPT_PDL

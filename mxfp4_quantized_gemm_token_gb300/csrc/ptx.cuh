@@ -130,6 +130,15 @@ __device__ __forceinline__ void tma_load_2d_hint(void* dst, const void* map, uin
       : "memory");
 }
 
+__device__ __forceinline__ void tma_load_3d(void* dst, const void* map, uint64_t* bar, int32_t c0,
+                                            int32_t c1, int32_t c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(map), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
+
 // One contiguous block of `bytes` (a multiple of 16, both addresses 16-byte
 // aligned) from global to shared memory, completing on `bar`.
 __device__ __forceinline__ void bulk_load_hint(void* dst, const void* src, uint32_t bytes,
@@ -353,6 +362,20 @@ __device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr) {
   return d;
 }
 
+// The same for an MN-major operand stored as rows of 64 16-bit elements along
+// M/N, one row per K index (a row-major [K, N] matrix loaded in 64-column
+// boxes): 8 K rows to the next 8 are 1024 bytes apart, 64 columns to the next
+// 64 `chunk_bytes`.
+__device__ __forceinline__ uint64_t sw128_desc_mn(uint32_t saddr, uint32_t chunk_bytes) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(chunk_bytes >> 4) << 16;     // leading byte offset: along M/N
+  d |= static_cast<uint64_t>(1024 >> 4) << 32;            // stride byte offset: along K
+  d |= static_cast<uint64_t>(1) << 46;
+  d |= static_cast<uint64_t>(2) << 61;
+  return d;
+}
+
 // Instruction descriptors (dense, fp32 accumulator, both operands K-major).
 __host__ __device__ constexpr uint32_t idesc_e4m3(int m, int n) {
   return (1u << 4) | (0u << 7) | (0u << 10) | (static_cast<uint32_t>(n >> 3) << 17) |
@@ -361,6 +384,10 @@ __host__ __device__ constexpr uint32_t idesc_e4m3(int m, int n) {
 __host__ __device__ constexpr uint32_t idesc_bf16(int m, int n) {
   return (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) |
          (static_cast<uint32_t>(m >> 4) << 24);
+}
+// bf16 with an MN-major B operand
+__host__ __device__ constexpr uint32_t idesc_bf16_bmn(int m, int n) {
+  return idesc_bf16(m, n) | (1u << 16);
 }
 __host__ __device__ constexpr uint32_t idesc_f16(int m, int n) {
   return (1u << 4) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);

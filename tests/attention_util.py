@@ -2,12 +2,15 @@
 error bounds their tests use.
 
 Attention output, per element, with w the exact softmax weights and
-A = sum_j w_j |v_j|: the weights enter the value product rounded to bf16
-(relative 2^-9 each; f16 for an e4m3 cache, less), the result rounds to bf16
-(2^-9 of it); score, exponential and sum errors in fp32 are below 2^-11 of A
-for the scores drawn here (score error <= D 2^-24 sum |q k| scale, under 2^-12).
-    |got - ref| <= 2^-9 |ref| + (2^-9 + 2^-11) A + 2^-134
-(2^-134 is half of bf16's smallest step: no bf16 result is nearer than that.)
+A = sum_j w_j |v_j|.  bf16 keeps 8 significant bits, so rounding to it moves a
+value by up to 2^-8 of it (half of 2^-7, the step above 1); f16 keeps 11, so
+2^-11.  The weights enter the value product rounded to u = 2^-8 (bf16 cache)
+or u = 2^-11 (e4m3 cache, f16 weights, whose smallest step below 2^-14 adds 2^-25
+of the largest weight for every key), the result rounds to bf16 (2^-8 of it, or half
+of the smallest step, 2^-134); score, exponential and sum errors in fp32 are
+below 2^-11 of A for the scores drawn here (score error <= D 2^-24 sum |q k|
+scale, under 2^-12).
+    |got - ref| <= 2^-8 |ref| + (u + 2^-11) A + 2^-134 (+ 2^-25 max w sum |v|)
 Log-sum-exp: the largest score error, plus 2^-18 for exponential, sum and
 logarithm, plus 2^-22 relative for its own rounding and that of the maximum.
 """
@@ -16,7 +19,7 @@ import math
 import torch
 
 
-def attend(q, k, v, visible, scale, sink=None):
+def attend(q, k, v, visible, scale, sink=None, f16=False):
     """q [n, D], k, v [m, D], visible [n, m], all on one device: (out, lse,
     bound of out, bound of lse) in float64."""
     q, k, v = q.double(), k.double(), v.double()
@@ -35,7 +38,10 @@ def attend(q, k, v, visible, scale, sink=None):
                                                             device=q.device).double()
     w = torch.exp(x[:, :k.shape[0]] - torch.where(lse == -math.inf, 0.0, lse)[:, None])
     out = w @ v
-    bound = 2.0 ** -9 * out.abs() + (2.0 ** -9 + 2.0 ** -11) * (w @ v.abs()) + 2.0 ** -134
+    u = 2.0 ** -11 if f16 else 2.0 ** -8
+    bound = 2.0 ** -8 * out.abs() + (u + 2.0 ** -11) * (w @ v.abs()) + 2.0 ** -134
+    if f16 and k.shape[0]:
+        bound = bound + 2.0 ** -25 * w.amax(1)[:, None] * (visible.double() @ v.abs())
     lse_bound = D * 2.0 ** -24 * size + 2.0 ** -18 + 2.0 ** -22 * torch.where(
         lse == -math.inf, 0.0, lse.abs())
     return out, lse, bound, lse_bound
@@ -68,7 +74,8 @@ def decode_ref(q, k_cache, v_cache, page_table, lens, scale, window=0, sinks=Non
                 v = v * v_scale[g].double()
             vis = (j >= (n - window if window else 0))[None]
             rows.append(attend(q[b, h:h + 1], k, v, vis, scale,
-                               None if sinks is None else sinks[h]))
+                               None if sinks is None else sinks[h],
+                               k_cache.dtype == torch.float8_e4m3fn))
         res.append([torch.cat([r[i] for r in rows]) for i in range(4)])
     return [torch.stack([r[i] for r in res]) for i in range(4)]
 
