@@ -1,69 +1,654 @@
 // attn_decode.cu — attention of one new token per sequence over a paged
 // key/value cache.
+//
+// Every visible key and value is read once (2 D elements a key and key/value
+// head) for 4 D multiply-adds per query head: HBM-bound, so the kernel is built
+// around keeping loads in flight.
+//
+// Work.  A sequence's visible keys are cut into steps of KS keys; the steps of
+// all (sequence, key/value head) units form one line, cut into equal parts, one
+// per warp of the grid, whatever the lengths.  A warp is on its own: its
+// ring of shared-memory stages filled with 16-byte asynchronous copies, its own
+// running maximum, sum and accumulators, no block-wide barrier.  A
+// unit that lies inside one part is written out by its warp; the others
+// leave at most two partial results per warp in the workspace, which
+// a second kernel joins in a fixed order.
+//
+// Arithmetic.  The G query heads of a key/value head are the rows of 16-row
+// tensor-core products (mma.sync m16n8k16: with at most 16 rows per 64 KB of
+// keys the products take a fraction of the load time, and their operands come from
+// registers and ldmatrix without a pass through tensor memory); G above 16 makes
+// further units.  Scores and outputs accumulate in fp32.  The reference a
+// row's weights are relative to is raised only when a score exceeds it by 2^8
+// in the exponent, so most steps need no exchange between lanes.
+//   bf16 cache: bf16 products, weights rounded to bf16.
+//   e4m3 cache: keys and values converted to f16 (exact), q scaled per row by
+//   a power of two to use f16's range (exact for elements within 2^31 of the
+//   row's largest), weights rounded to f16.
+// The order of the elements of D inside a product is free as long as both
+// operands agree: the e4m3 path takes the order that ldmatrix delivers.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <math.h>
+
+#include <algorithm>
+
 #include "attn.h"
-#include "attn_simple.cuh"
+#include "attn_math.cuh"
 #include "internal.h"
 
 namespace mxq {
 
 namespace {
 
+constexpr int kWarps = 8;
+constexpr int kEntries = 2048;      // entries of the shared prefix table
+constexpr int kRows = 16;           // rows of a product
+
+struct DecodeArgs {
+  DecodeParams p;
+  int G, tiles, rows;               // query heads per kv head, units per kv head, rows stored
+  int chunk, entries;               // sequences per entry of the prefix table, its entries
+  int min_steps;
+  int64_t* cum;                     // workspace: steps before each sequence [B + 1], then `per`
+  float2* part_ml;                  // [warps][2][rows]
+  float* part_o;                    // [warps][2][rows][D]
+};
+
 template <int D, bool FP8>
-__global__ void decode_kernel(const DecodeParams p) {
-  constexpr int N = D / 32;
+struct DecodeShape {
+  static constexpr int kRowBytes = FP8 ? D : 2 * D;
+  static constexpr int KS = kRowBytes == 256 ? 16 : 32;        // keys per step
+  static constexpr int kTile = KS * kRowBytes;                 // K (or V) of a step
+  static constexpr int kStages = kTile == 4096 ? 3 : 6;
+  static constexpr int kLPR = kRowBytes / 16;                  // lanes per row
+  static constexpr int kSmem = kWarps * kStages * 2 * kTile + 8 * kEntries + 4 * kWarps * kStages;
+};
+
+struct SeqRange {
+  int lo, len, first, steps;        // visible keys [lo, len); the first step's key; its steps
+};
+
+// The visible keys of sequence b, in steps from a multiple of 16; at least one
+// step (without keys), so that every output is written.
+template <int KS>
+__device__ __forceinline__ SeqRange seq_steps(const DecodeParams& p, int b, bool* bad) {
+  SeqRange r;
+  const int cap = static_cast<int>(p.max_pages * p.page_size);
+  const int len = p.seq_lens[b];
+  *bad = len < 0 || len > cap;
+  r.len = min(max(len, 0), cap);
+  r.lo = p.window > 0 ? max(0, r.len - p.window) : 0;
+  r.first = r.lo & ~15;
+  r.steps = max(1, (r.len - r.first + KS - 1) / KS);
+  return r;
+}
+
+// byte offset of 16-byte chunk c of row r in a tile, conflict-free for ldmatrix
+template <int ROWB>
+__device__ __forceinline__ uint32_t tile_off(int r, int c) {
+  if constexpr (ROWB == 64)
+    return r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+  else
+    return r * ROWB + ((c ^ (r & 7)) << 4);
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t* r) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t* r) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+
+template <bool F16>
+__device__ __forceinline__ void mma16816(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  if constexpr (F16)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// two e4m3 (low 16 bits) -> f16x2
+__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t x) {
+  uint32_t r;
+  asm("{ .reg .b16 t; cvt.u16.u32 t, %1; cvt.rn.f16x2.e4m3x2 %0, t; }" : "=r"(r) : "r"(x));
+  return r;
+}
+
+// 16 bytes to shared memory, zeros if !valid (the source is not read then)
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool valid) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(valid ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// A place on the line of steps.
+struct Cursor {
+  int b, head, step;                // head: key/value head * tiles + tile
+  SeqRange s;
+};
+
+template <int KS>
+__device__ __forceinline__ void advance(Cursor& c, const DecodeArgs& a) {
+  if (++c.step < c.s.steps) return;
+  c.step = 0;
+  if (++c.head < a.p.Hkv * a.tiles) return;
+  c.head = 0;
+  if (++c.b < a.p.B) {
+    bool bad;
+    c.s = seq_steps<KS>(a.p, c.b, &bad);
+  }
+}
+
+template <int D, bool FP8>
+__global__ void __launch_bounds__(32 * kWarps, 1) decode_kernel(const DecodeArgs a) {
+  using S = DecodeShape<D, FP8>;
+  constexpr int KS = S::KS, ROWB = S::kRowBytes, ST = S::kStages;
+  constexpr int NT = KS / 8;                           // score tiles of 8 keys
+  constexpr int DT = D / 8;                            // output tiles of 8 elements
+  extern __shared__ __align__(128) uint8_t smem[];
+  const DecodeParams& p = a.p;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int quad = lane & 3, r0 = lane >> 2;
+  int64_t* table = reinterpret_cast<int64_t*>(smem + kWarps * ST * 2 * S::kTile);
+  uint32_t* masks = reinterpret_cast<uint32_t*>(table + kEntries) + warp * ST;
+  __shared__ int64_t warp_sum[kWarps];
   pdl_wait();
   pdl_launch_dependents();
-  const int lane = threadIdx.x & 31;
-  const int64_t w = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
-  if (w >= static_cast<int64_t>(p.B) * p.Hq) return;
-  const int64_t b = w / p.Hq;
-  const int h = static_cast<int>(w - b * p.Hq);
-  const int hk = h / (p.Hq / p.Hkv);
-  int64_t len = p.seq_lens[b];
-  const int64_t cap = p.max_pages * p.page_size;
-  if (len < 0 || len > cap) {
-    if (lane == 0) atomicOr(p.status, kStatusBadIndex);
-    len = len < 0 ? 0 : cap;
-  }
-  float q[N];
-  load_row<N, false>(static_cast<const __nv_bfloat16*>(p.q) + b * p.q_b + h * p.q_h, lane, q);
-  const float ks = p.scale * (p.k_scale ? p.k_scale[hk] : 1.f);
+
+  // ---- steps before each entry (a.chunk sequences) of the prefix table
+  const int per_thread = (a.entries + 32 * kWarps - 1) / (32 * kWarps);
+  const int e0 = threadIdx.x * per_thread;
+  int64_t mine = 0;
+  for (int e = e0; e < min(a.entries, e0 + per_thread); ++e)
+    for (int b = e * a.chunk; b < min(p.B, (e + 1) * a.chunk); ++b) {
+      bool bad;
+      mine += seq_steps<KS>(p, b, &bad).steps;
+      if (bad && blockIdx.x == 0) atomicOr(p.status, kStatusBadIndex);
+    }
+  int64_t incl = mine;
 #pragma unroll
-  for (int i = 0; i < N; ++i) q[i] *= ks;
-  SoftmaxRow<N> row;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) warp_sum[warp] = incl;
+  __syncthreads();
+  int64_t before = incl - mine, total = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) before += warp_sum[w];
+    total += warp_sum[w];
+  }
+  const int heads = p.Hkv * a.tiles;
+  const int64_t workers = static_cast<int64_t>(gridDim.x) * kWarps;
+  int64_t per = (total * heads + workers - 1) / workers;
+  if (per < a.min_steps) per = a.min_steps;
+  for (int e = e0; e < min(a.entries, e0 + per_thread); ++e) {
+    table[e] = before;
+    for (int b = e * a.chunk; b < min(p.B, (e + 1) * a.chunk); ++b) {
+      if (blockIdx.x == 0) a.cum[b] = before;
+      if (blockIdx.x == 0 || a.chunk * per_thread > 1) {
+        bool bad;
+        before += seq_steps<KS>(p, b, &bad).steps;
+      }
+    }
+  }
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    a.cum[p.B] = total;
+    a.cum[p.B + 1] = per;
+  }
+  __syncthreads();
+
+  // ---- this warp's part; few parts are spread over the SMs
+  const int64_t worker = static_cast<int64_t>(warp) * gridDim.x + blockIdx.x;
+  const int64_t s0 = worker * per;
+  const int64_t s1 = min(s0 + per, total * heads);
+  if (s0 >= s1) return;
+  Cursor in;                                           // of the copies
+  {
+    int lo = 0, hi = a.entries - 1;                    // the last entry at or before s0
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (table[mid] * heads <= s0) lo = mid;
+      else hi = mid - 1;
+    }
+    bool bad;
+    int64_t at = table[lo] * heads;
+    in.b = lo * a.chunk;
+    in.s = seq_steps<KS>(p, in.b, &bad);
+    while (at + static_cast<int64_t>(in.s.steps) * heads <= s0) {
+      at += static_cast<int64_t>(in.s.steps) * heads;
+      in.s = seq_steps<KS>(p, ++in.b, &bad);
+    }
+    in.head = static_cast<int>((s0 - at) / in.s.steps);
+    in.step = static_cast<int>((s0 - at) - static_cast<int64_t>(in.head) * in.s.steps);
+  }
+  Cursor at = in;                                      // of the arithmetic
+
+  const uint32_t ring = smem_u32(smem) + warp * ST * 2 * S::kTile;
   constexpr int es = FP8 ? 1 : 2;
-  int64_t j = p.window > 0 && len > p.window ? len - p.window : 0;
-  for (; j < len; ++j) {
-    const int64_t page = p.page_table[b * p.ld_table + j / p.page_size];
-    const int64_t off = j % p.page_size;
-    if (page < 0 || page >= p.pages) {
-      if (lane == 0) atomicOr(p.status, kStatusBadIndex);
+  const int row_in = lane / S::kLPR, ch_in = lane % S::kLPR;
+  constexpr int kRPI = 32 / S::kLPR;                   // rows per copy instruction
+
+  // the page of this lane's key of the step at `in`: read one step ahead
+  int page = 0, off = 0;
+  bool seen = false;
+  auto look_up = [&]() {
+    const int key = in.s.first + in.step * KS + lane;
+    seen = lane < KS && key >= in.s.lo && key < in.s.len;
+    page = off = 0;
+    if (seen) {
+      const uint32_t n = static_cast<uint32_t>(key) / static_cast<uint32_t>(p.page_size);
+      off = key - static_cast<int>(n) * p.page_size;
+      page = __ldg(p.page_table + in.b * p.ld_table + n);
+    }
+  };
+  int64_t left = s1 - s0;                              // steps still to be copied
+  uint32_t fill = 0;
+  auto copy_step = [&]() {
+    if (left > 0) {
+      const bool ok = seen && static_cast<uint32_t>(page) < static_cast<uint32_t>(p.pages);
+      if (seen && !ok) {
+        atomicOr(p.status, kStatusBadIndex);
+        page = off = 0;
+      }
+      const uint32_t mask = __ballot_sync(0xffffffffu, ok);
+      const int st = fill % ST;
+      if (lane == 0) masks[st] = mask;
+      const int hk = in.head / a.tiles;
+      const char* kb = static_cast<const char*>(p.k_cache) + (hk * p.ck_h) * es + ch_in * 16;
+      const char* vb = static_cast<const char*>(p.v_cache) + (hk * p.cv_h) * es + ch_in * 16;
+      const uint32_t dst = ring + st * 2 * S::kTile;
+#pragma unroll
+      for (int i = 0; i < KS / kRPI; ++i) {
+        const int r = i * kRPI + row_in;
+        const int64_t pg = __shfl_sync(0xffffffffu, page, r);
+        const int64_t of = __shfl_sync(0xffffffffu, off, r);
+        const bool v = (mask >> r) & 1;
+        const uint32_t d = dst + tile_off<ROWB>(r, ch_in);
+        cp16(d, kb + (pg * p.ck_p + of * p.ck_t) * es, v);
+        cp16(d + S::kTile, vb + (pg * p.cv_p + of * p.cv_t) * es, v);
+      }
+      ++fill;
+      if (--left > 0) {
+        advance<KS>(in, a);
+        look_up();
+      }
+    }
+    cp_commit();
+  };
+  look_up();
+#pragma unroll 1
+  for (int i = 0; i < ST - 1; ++i) copy_step();
+
+  uint32_t qf[D / 16][4];                              // rows r0, r0 + 8 of q
+  float o[DT][4];
+  float m[2], l[2], cs[2];
+  uint32_t use = 0;
+  bool fresh = true, opened = false;                   // opened: the unit began in this part
+  for (int64_t s = s0; s < s1; ++s, ++use) {
+    const int hk = at.head / a.tiles, tile = at.head - hk * a.tiles;
+    if (fresh) {
+      // a new unit: its q, and nothing summed yet
+      fresh = false;
+      opened = at.step == 0;
+      const float ks = p.k_scale != nullptr ? __ldg(p.k_scale + hk) : 1.f;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const int gr = tile * kRows + r0 + 8 * half;
+        const bool in_group = gr < a.G;
+        const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + at.b * p.q_b +
+                                 static_cast<int64_t>(hk * a.G + gr) * p.q_h;
+        float unscale = 1.f;
+        if constexpr (FP8) {
+          float big = 0.f;
+          uint2 raw[D / 16];
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            raw[k] = in_group ? __ldg(reinterpret_cast<const uint2*>(q + 16 * k + 4 * quad))
+                              : make_uint2(0u, 0u);
+            const uint32_t w[2] = {raw[k].x, raw[k].y};
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              big = fmaxf(big, fabsf(__uint_as_float(w[i] << 16)));
+              big = fmaxf(big, fabsf(__uint_as_float(w[i] & 0xFFFF0000u)));
+            }
+          }
+          big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+          big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+          // the power of two that brings the largest to [2^14, 2^15)
+          const int e = big > 0.f && big < INFINITY ? min(max(14 - ilogbf(big), -100), 100) : 0;
+          const float up = ldexpf(1.f, e);
+          unscale = ldexpf(1.f, -e);
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t w[2] = {raw[k].x, raw[k].y};
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              qf[k][half + 2 * i] = f16x2(__uint_as_float(w[i] << 16) * up,
+                                          __uint_as_float(w[i] & 0xFFFF0000u) * up);
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              qf[k][half + 2 * i] =
+                  in_group ? __ldg(reinterpret_cast<const uint32_t*>(q + 16 * k + 8 * i + 2 * quad))
+                           : 0u;
+        }
+        cs[half] = p.scale * ks * kLog2e * unscale;
+        m[half] = -INFINITY;
+        l[half] = 0.f;
+      }
+#pragma unroll
+      for (int t = 0; t < DT; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[t][i] = 0.f;
+    }
+    cp_wait<ST - 2>();
+    __syncwarp();
+    copy_step();                                       // into the stage used one step ago
+    const int st = use % ST;
+    const uint32_t mask = masks[st];
+    const uint32_t kt = ring + st * 2 * S::kTile, vt = kt + S::kTile;
+
+    // ---- scores: rows x keys
+    float x[NT][4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[n][i] = 0.f;
+#pragma unroll
+    for (int n = 0; n < NT; n += 2) {
+      if constexpr (FP8) {
+        // matrices: keys 8n.. and 8(n+1).. of chunk k (16 elements), then of k + 1
+        const int r = 8 * n + (lane & 15);
+#pragma unroll
+        for (int k = 0; k < D / 16; k += 2) {
+          uint32_t f[4];
+          ldsm4(kt + tile_off<ROWB>(r, k + (lane >> 4)), f);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            mma16816<true>(x[n + (i & 1)], qf[k + (i >> 1)], e4m3x2_f16x2(f[i]),
+                           e4m3x2_f16x2(f[i] >> 16));
+        }
+      } else {
+        // matrices: (keys 8n.., chunks 2k and 2k + 1), (keys 8(n+1).., the same)
+        const int r = 8 * n + ((lane >> 4) << 3) + (lane & 7);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          uint32_t f[4];
+          ldsm4(kt + tile_off<ROWB>(r, 2 * k + ((lane >> 3) & 1)), f);
+          mma16816<false>(x[n], qf[k], f[0], f[1]);
+          mma16816<false>(x[n + 1], qf[k], f[2], f[3]);
+        }
+      }
+    }
+
+    // ---- weights
+    float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const bool vis = (mask >> (8 * n + 2 * quad + (i & 1))) & 1;
+        x[n][i] = vis ? x[n][i] * cs[i >> 1] : -INFINITY;
+        mx[i >> 1] = fmaxf(mx[i >> 1], x[n][i]);
+      }
+    if (__any_sync(0xffffffffu, mx[0] > m[0] + 8.f || mx[1] > m[1] + 8.f)) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
+        mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
+        const float n = fmaxf(m[h], mx[h]);
+        const float f = m[h] == -INFINITY ? 0.f : ex2(m[h] - n);
+        m[h] = n;
+        l[h] *= f;
+#pragma unroll
+        for (int t = 0; t < DT; ++t) {
+          o[t][2 * h] *= f;
+          o[t][2 * h + 1] *= f;
+        }
+      }
+    }
+    const float ref[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
+    uint32_t pf[KS / 16][4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        x[n][i] = ex2(x[n][i] - ref[i >> 1]);
+        l[i >> 1] += x[n][i];
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        pf[n / 2][h + 2 * (n & 1)] = FP8 ? f16x2(x[n][2 * h], x[n][2 * h + 1])
+                                         : bf16x2(x[n][2 * h], x[n][2 * h + 1]);
+    }
+
+    // ---- values
+#pragma unroll
+    for (int kk = 0; kk < KS / 16; ++kk) {
+      // matrices: keys 16kk.. and 16kk + 8.. of chunk c, then of c + 1
+      const int r = 16 * kk + (lane & 15);
+      constexpr int kChunks = ROWB / 16;
+#pragma unroll
+      for (int c = 0; c < kChunks; c += 2) {
+        uint32_t f[4];
+        ldsm4_t(vt + tile_off<ROWB>(r, c + (lane >> 4)), f);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if constexpr (FP8) {
+            // a register holds keys 2q, 2q + 1 of two elements: even elements
+            // make one output tile, odd ones the next
+            const uint32_t b0 = __byte_perm(f[2 * i], 0, 0x3120);
+            const uint32_t b1 = __byte_perm(f[2 * i + 1], 0, 0x3120);
+            mma16816<true>(o[2 * (c + i)], pf[kk], e4m3x2_f16x2(b0), e4m3x2_f16x2(b1));
+            mma16816<true>(o[2 * (c + i) + 1], pf[kk], e4m3x2_f16x2(b0 >> 16),
+                           e4m3x2_f16x2(b1 >> 16));
+          } else {
+            mma16816<false>(o[c + i], pf[kk], f[2 * i], f[2 * i + 1]);
+          }
+        }
+      }
+    }
+
+    // ---- the unit's or the part's end
+    const bool closed = at.step + 1 == at.s.steps;
+    if (!closed && s + 1 < s1) {
+      ++at.step;
       continue;
     }
-    float k[N], v[N];
-    load_row<N, FP8>(static_cast<const char*>(p.k_cache) +
-                         (page * p.ck_p + off * p.ck_t + hk * p.ck_h) * es, lane, k);
-    load_row<N, FP8>(static_cast<const char*>(p.v_cache) +
-                         (page * p.cv_p + off * p.cv_t + hk * p.cv_h) * es, lane, v);
-    row.add(q, k, v);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+      const int gl = r0 + 8 * h, gr = tile * kRows + gl;
+      if (gr >= a.G) continue;
+      if (opened && closed) {
+        const int hq = hk * a.G + gr;
+        const RowEnd end = finish_row(m[h] * kLn2, l[h], p.sinks ? p.sinks + hq : nullptr);
+        const float f = end.factor * (p.v_scale != nullptr ? __ldg(p.v_scale + hk) : 1.f);
+        __nv_bfloat16* dst =
+            static_cast<__nv_bfloat16*>(p.out) + at.b * p.o_b + static_cast<int64_t>(hq) * p.o_h;
+#pragma unroll
+        for (int t = 0; t < DT; t += 2) {
+          if constexpr (FP8) {
+            *reinterpret_cast<uint2*>(dst + 8 * t + 4 * quad) =
+                make_uint2(bf16x2(o[t][2 * h] * f, o[t + 1][2 * h] * f),
+                           bf16x2(o[t][2 * h + 1] * f, o[t + 1][2 * h + 1] * f));
+          } else {
+            *reinterpret_cast<uint32_t*>(dst + 8 * t + 2 * quad) =
+                bf16x2(o[t][2 * h] * f, o[t][2 * h + 1] * f);
+            *reinterpret_cast<uint32_t*>(dst + 8 * t + 8 + 2 * quad) =
+                bf16x2(o[t + 1][2 * h] * f, o[t + 1][2 * h + 1] * f);
+          }
+        }
+        if (p.lse != nullptr && quad == 0)
+          p.lse[static_cast<int64_t>(at.b) * p.Hq + hq] = end.lse;
+      } else {
+        // the first unit of a part goes to its slot 0, the last to slot 1
+        const int64_t slot = (worker * 2 + (opened && s0 != s - at.step ? 1 : 0)) * a.rows + gl;
+        if (quad == 0) a.part_ml[slot] = make_float2(m[h], l[h]);
+        float* dst = a.part_o + slot * D;
+#pragma unroll
+        for (int t = 0; t < DT; t += 2) {
+          if constexpr (FP8) {
+            *reinterpret_cast<float4*>(dst + 8 * t + 4 * quad) = make_float4(
+                o[t][2 * h], o[t + 1][2 * h], o[t][2 * h + 1], o[t + 1][2 * h + 1]);
+          } else {
+            *reinterpret_cast<float2*>(dst + 8 * t + 2 * quad) =
+                make_float2(o[t][2 * h], o[t][2 * h + 1]);
+            *reinterpret_cast<float2*>(dst + 8 * t + 8 + 2 * quad) =
+                make_float2(o[t + 1][2 * h], o[t + 1][2 * h + 1]);
+          }
+        }
+      }
+    }
+    fresh = true;
+    advance<KS>(at, a);
   }
-  if (p.sinks) row.sink(p.sinks[h]);
-  row.store(static_cast<__nv_bfloat16*>(p.out) + b * p.o_b + h * p.o_h, lane,
-            p.lse ? p.lse + b * p.Hq + h : nullptr, p.v_scale ? p.v_scale[hk] : 1.f);
+  cp_wait<0>();
+}
+
+// Joins the partial results of one row of a unit that several parts share, in the parts'
+// order: out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i.
+template <int D>
+__global__ void __launch_bounds__(32 * kWarps) decode_join_kernel(const DecodeArgs a) {
+  constexpr int N = D / 32;
+  const DecodeParams& p = a.p;
+  __shared__ float so[kWarps][D];
+  __shared__ float sm[kWarps], sl[kWarps];
+  pdl_wait();
+  pdl_launch_dependents();
+  const int b = blockIdx.y, head = blockIdx.x / a.rows, row = blockIdx.x - head * a.rows;
+  const int hk = head / a.tiles, gr = (head - hk * a.tiles) * kRows + row;
+  if (gr >= a.G) return;
+  const int64_t per = a.cum[p.B + 1];
+  const int64_t steps = a.cum[b + 1] - a.cum[b];
+  const int64_t u0 = a.cum[b] * (p.Hkv * a.tiles) + head * steps, u1 = u0 + steps;
+  const int64_t w0 = u0 / per, w1 = (u1 - 1) / per;
+  if (w0 == w1) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  float m = -INFINITY, l = 0.f, o[N] = {};
+  for (int64_t w = w0 + warp; w <= w1; w += kWarps) {
+    const int64_t slot = (w * 2 + (w * per < u0 ? 1 : 0)) * a.rows + row;
+    const float2 ml = a.part_ml[slot];
+    float v[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = a.part_o[slot * D + lane + 32 * i];
+    const float n = fmaxf(m, ml.x);
+    if (n == -INFINITY) continue;
+    const float f = ex2(m - n), g = ex2(ml.x - n);
+    l = l * f + ml.y * g;
+#pragma unroll
+    for (int i = 0; i < N; ++i) o[i] = o[i] * f + v[i] * g;
+    m = n;
+  }
+  if (lane == 0) sm[warp] = m, sl[warp] = l;
+#pragma unroll
+  for (int i = 0; i < N; ++i) so[warp][lane + 32 * i] = o[i];
+  __syncthreads();
+  const int d = threadIdx.x;
+  if (d >= D) return;
+  float top = -INFINITY, sum = 0.f, acc = 0.f;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sm[w]);
+  if (top > -INFINITY) {
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float g = ex2(sm[w] - top);
+      sum += sl[w] * g;
+      acc += so[w][d] * g;
+    }
+  }
+  const int hq = hk * a.G + gr;
+  const RowEnd end = finish_row(top * kLn2, sum, p.sinks ? p.sinks + hq : nullptr);
+  const float f = end.factor * (p.v_scale != nullptr ? __ldg(p.v_scale + hk) : 1.f);
+  static_cast<__nv_bfloat16*>(p.out)[b * p.o_b + static_cast<int64_t>(hq) * p.o_h + d] =
+      __float2bfloat16_rn(acc * f);
+  if (p.lse != nullptr && d == 0) p.lse[static_cast<int64_t>(b) * p.Hq + hq] = end.lse;
+}
+
+int stored_rows(int Hq, int Hkv) { return std::min(kRows, Hq / Hkv); }
+
+size_t round256(size_t n) { return (n + 255) / 256 * 256; }
+
+// bytes of the workspace before the partial maxima, and before the partial outputs
+size_t cum_bytes(int64_t B) { return round256(static_cast<size_t>(B + 2) * 8); }
+size_t ml_bytes(int rows, int num_sms) {
+  return round256(static_cast<size_t>(num_sms) * kWarps * 2 * rows * sizeof(float2));
+}
+
+template <int D, bool FP8>
+cudaError_t launch(const DecodeArgs& a, int grid, cudaStream_t stream) {
+  using S = DecodeShape<D, FP8>;
+  static_assert(S::kSmem <= 226 * 1024, "shared memory over budget");
+  static bool configured[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (!configured[dev]) {
+    e = cudaFuncSetAttribute(decode_kernel<D, FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             S::kSmem);
+    if (e != cudaSuccess) return e;
+    configured[dev] = true;
+  }
+  DecodeArgs b = a;
+  b.min_steps = 64 / S::KS;
+  e = launch_k(decode_kernel<D, FP8>, dim3(grid), dim3(32 * kWarps),
+               static_cast<size_t>(S::kSmem), stream, b);
+  if (e != cudaSuccess) return e;
+  return launch_k(decode_join_kernel<D>,
+                  dim3(static_cast<unsigned>(a.p.Hkv * a.tiles * a.rows),
+                       static_cast<unsigned>(a.p.B)),
+                  dim3(32 * kWarps), 0, stream, b);
 }
 
 }  // namespace
 
-size_t decode_workspace_bytes(int64_t, int, int, int, int) { return 0; }
+size_t decode_workspace_bytes(int64_t B, int Hq, int Hkv, int D, int num_sms) {
+  const int rows = stored_rows(Hq, Hkv);
+  return cum_bytes(B) + ml_bytes(rows, num_sms) +
+         static_cast<size_t>(num_sms) * kWarps * 2 * rows * D * sizeof(float);
+}
 
-cudaError_t launch_decode(const DecodeParams& p, int, cudaStream_t stream) {
-  const int64_t warps = static_cast<int64_t>(p.B) * p.Hq;
-  const dim3 grid(static_cast<unsigned>((warps + 3) / 4)), block(128);
+cudaError_t launch_decode(const DecodeParams& p, int num_sms, cudaStream_t stream) {
+  DecodeArgs a = {};
+  a.p = p;
+  a.G = p.Hq / p.Hkv;
+  a.tiles = (a.G + kRows - 1) / kRows;
+  a.rows = stored_rows(p.Hq, p.Hkv);
+  a.chunk = (p.B + kEntries - 1) / kEntries;
+  a.entries = (p.B + a.chunk - 1) / a.chunk;
+  char* ws = static_cast<char*>(p.workspace);
+  a.cum = reinterpret_cast<int64_t*>(ws);
+  a.part_ml = reinterpret_cast<float2*>(ws + cum_bytes(p.B));
+  a.part_o = reinterpret_cast<float*>(ws + cum_bytes(p.B) + ml_bytes(a.rows, num_sms));
   if (p.D == 128)
-    return p.fp8 ? launch_k(decode_kernel<128, true>, grid, block, 0, stream, p)
-                 : launch_k(decode_kernel<128, false>, grid, block, 0, stream, p);
-  return p.fp8 ? launch_k(decode_kernel<64, true>, grid, block, 0, stream, p)
-               : launch_k(decode_kernel<64, false>, grid, block, 0, stream, p);
+    return p.fp8 ? launch<128, true>(a, num_sms, stream) : launch<128, false>(a, num_sms, stream);
+  return p.fp8 ? launch<64, true>(a, num_sms, stream) : launch<64, false>(a, num_sms, stream);
 }
 
 }  // namespace mxq

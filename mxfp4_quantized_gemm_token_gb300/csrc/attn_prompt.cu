@@ -35,6 +35,7 @@
 #include <string>
 
 #include "attn.h"
+#include "attn_math.cuh"
 #include "internal.h"
 
 namespace mxq {
@@ -152,16 +153,10 @@ struct PromptLayout {
   static constexpr int kChunkBytes = kBM * 128;          // 128 rows of 64 elements
   static constexpr int kTileBytes = kChunks * kChunkBytes;
   static constexpr int kStages = D == 128 ? 5 : 9;
-  static constexpr int kBars = 2 * 4 + 2 * kStages + 1;
+  static constexpr int kBars = 2 * 5 + 2 * kStages + 1;
   static constexpr int kSmem = (2 + kStages) * kTileBytes + 8 * kBars + 16;
   static_assert(kSmem + 1024 <= 227 * 1024, "shared memory over budget");
 };
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 
 __device__ __forceinline__ uint64_t pack2(float a, float b) {
   uint64_t r;
@@ -181,12 +176,6 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
-__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
 // position r of the sequence of items that this CTA takes, in alternating direction
 __device__ __forceinline__ int item_index(int r) {
   return r * gridDim.x + ((r & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
@@ -206,7 +195,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   uint64_t* q_empty = q_full + 2;
   uint64_t* s_full = q_empty + 2;
   uint64_t* p_full = s_full + 2;
-  uint64_t* kv_full = p_full + 2;
+  // an item's O has a barrier of its own: its commit is followed by the next
+  // item's S without a word from the softmax, which would let one barrier run
+  // two phases ahead of its waiter
+  uint64_t* o_full = p_full + 2;
+  uint64_t* kv_full = o_full + 2;
   uint64_t* kv_empty = kv_full + ST;
   uint64_t* drain = kv_empty + ST;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
@@ -220,6 +213,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       mbar_init(&q_full[i], 1);
       mbar_init(&q_empty[i], 1);
       mbar_init(&s_full[i], 1);
+      mbar_init(&o_full[i], 1);
       mbar_init(&p_full[i], 4);       // the warps of the tile's warpgroup
     }
     for (int i = 0; i < ST; ++i) {
@@ -355,7 +349,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
               if (s == 1) mma_commit(&kv_empty[kf % ST]);
             }
           } else if (leader) {
-            mma_commit(&s_full[s]);        // the item's O is complete
+            mma_commit(&o_full[s]);        // the item's O is complete
           }
           __syncwarp();
         }
@@ -378,8 +372,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + s * 128 + lanes, tO = tmem + 256 + s * 128 + lanes;
     const int tok = row / a.G, g = row - tok * a.G;
-    const float c = p.scale * 1.44269504088896340736f;  // log2 e
-    uint32_t ns = 0, base = 0;
+    const float c = p.scale * kLog2e;
+    uint32_t ns = 0, no = 0, base = 0;
     for (int r = 0; item_index(r) < total; ++r) {
       const int idx = item_index(r);
       const PromptItem it = a.items[idx / p.Hkv];
@@ -475,22 +469,14 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       }
       base += n > 0 ? 2 * n : 0;
       if (n > 0) {
-        if (!mbar_wait_warp(&s_full[s], ns & 1, wc)) goto softmax_done;
-        ++ns;
+        if (!mbar_wait_warp(&o_full[s], no & 1, wc)) goto softmax_done;
+        ++no;
         tc_fence_after();
       }
-      // out = O / l, with the sink's logit in the sum; both taken relative to
-      // the larger of the row's reference and the sink
-      const float ms = m * p.scale;
-      float f = 1.f, top = ms;
-      if (p.sinks != nullptr && valid) {
-        const float sink = __ldg(p.sinks + h);
-        top = fmaxf(ms, sink);
-        f = ms == -INFINITY ? 0.f : expf(ms - top);
-        l = l * f + (sink == -INFINITY ? 0.f : expf(sink - top));
-      }
-      const bool none = l == 0.f;           // the row saw nothing
-      const float inv = none ? 0.f : f / l;
+      const RowEnd end =
+          finish_row(m * p.scale, l, p.sinks != nullptr && valid ? p.sinks + h : nullptr);
+      const float inv = end.factor;
+      const bool none = end.none;
       const int64_t tokr = it.q_row + i;
       __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + tokr * p.o_t + h * p.o_h;
 #pragma unroll
@@ -515,7 +501,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         }
       }
       if (p.lse != nullptr && valid)
-        p.lse[tokr * p.Hq + h] = none ? -INFINITY : top + logf(l);
+        p.lse[tokr * p.Hq + h] = end.lse;
       tc_fence_before();
     }
   softmax_done:;
