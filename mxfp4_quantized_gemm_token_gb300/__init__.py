@@ -443,38 +443,63 @@ def fused_experts(hidden, w1, w1_scale, w2, w2_scale, topk_weights, topk_ids,
 
 
 # ------------------------------------------------- paged cache and attention
+# A decode step makes these calls for every layer, with kernels of a few
+# microseconds: the helpers below read each property of a tensor once.
 
-def _heads3(name, t, piece=8):
-    """t [n, heads, D] as the kernels read it: unit inner stride, outer strides
-    of `piece` elements' multiples and at least D (copies only if needed)."""
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_bf16, _fp8, _f32, _i32 = torch.bfloat16, torch.float8_e4m3fn, torch.float32, torch.int32
+
+
+def _one_device(*ts):
+    """The index of the one CUDA device of all tensors (None: not given)."""
+    dev = ts[0].get_device()
+    for t in ts:
+        if t is not None and (t.get_device() != dev or dev < 0):
+            raise ValueError("mxq operates on CUDA tensors of one device (got %s and %s)"
+                             % (ts[0].device, t.device))
+    return dev
+
+
+def _heads3(name, t):
+    """t [n, heads, D] as the kernels read it, with unit inner stride, outer
+    strides of 16-byte multiples and at least D (copied only if needed):
+    (tensor, address, stride 0, stride 1)."""
     if t.dim() != 3:
         raise ValueError("%s must be [tokens, heads, head_dim], got %d dimensions"
                          % (name, t.dim()))
-    if t.dtype != torch.bfloat16:
+    if t.dtype != _bf16:
         raise TypeError("%s must be bf16" % name)
     s0, s1, s2 = t.stride()
     n0, n1, D = t.shape
-    if s2 != 1 or (n0 > 1 and (s0 < D or s0 % piece)) or (n1 > 1 and (s1 < D or s1 % piece)) \
-            or t.data_ptr() % 16:
+    p = t.data_ptr()
+    if s2 != 1 or (n0 > 1 and (s0 < D or s0 & 7)) or (n1 > 1 and (s1 < D or s1 & 7)) or p & 15:
         t = t.clone(memory_format=torch.contiguous_format)
-    return t
+        s0, s1, _ = t.stride()
+        p = t.data_ptr()
+    return t, p, s0, s1
 
 
-def _cache(name, t, kv_heads, D):
-    if t.dim() != 4 or t.shape[2] != kv_heads or t.shape[3] != D:
-        raise ValueError("%s must be [pages, page_size, %d, %d], got %s"
-                         % (name, kv_heads, D, list(t.shape)))
-    if t.stride(3) != 1:
-        raise ValueError("%s needs a unit stride along the head dimension" % name)
-    if t.dtype == torch.bfloat16:
-        return _lib.BF16
-    if t.dtype == torch.float8_e4m3fn:
-        return _lib.E4M3
-    raise TypeError("%s must be bf16 or float8_e4m3fn" % name)
+def _caches(k, v, kv_heads, D):
+    """Tag, pages, page size, and the strides of k and v of a cache."""
+    shape = k.shape
+    if len(shape) != 4 or shape[3] != D or (kv_heads is not None and shape[2] != kv_heads):
+        raise ValueError("k_cache must be [pages, page_size, %s, %d], got %s"
+                         % ("kv_heads" if kv_heads is None else kv_heads, D, list(shape)))
+    dtype = k.dtype
+    if v.shape != shape or v.dtype != dtype:
+        raise ValueError("k_cache and v_cache must have the same shape and dtype")
+    if dtype != _bf16 and dtype != _fp8:
+        raise TypeError("k_cache and v_cache must be bf16 or float8_e4m3fn")
+    k0, k1, k2, k3 = k.stride()
+    v0, v1, v2, v3 = v.stride()
+    if k3 != 1 or v3 != 1:
+        raise ValueError("k_cache and v_cache need a unit stride along the head dimension")
+    return (_lib.BF16 if dtype == _bf16 else _lib.E4M3, shape[0], shape[1], k0, k1, k2, v0, v1,
+            v2, shape[2])
 
 
 def _vec(name, t, dtype, n):
-    """A contiguous vector of n elements; its address (None for None)."""
+    """The address of a contiguous vector of n elements (None for None)."""
     if t is None:
         return None
     if t.dtype != dtype or t.numel() != n or not t.is_contiguous():
@@ -482,25 +507,14 @@ def _vec(name, t, dtype, n):
     return t.data_ptr()
 
 
-def _same_device(dev, *ts):
-    for t in ts:
-        if t is not None and t.device != dev:
-            raise ValueError("mxq operates on CUDA tensors of one device (got %s and %s)"
-                             % (dev, t.device))
-
-
-def _check_out(name, t, shape):
-    if t.dtype != torch.bfloat16 or t.shape != shape or t.stride(2) != 1:
+def _output(name, t, shape, dev):
+    """(tensor, address, stride 0, stride 1) of a given output or a new one."""
+    if t is None:
+        t = torch.empty(shape, dtype=_bf16, device=dev)
+    elif t.dtype != _bf16 or t.shape != shape or t.stride(2) != 1:
         raise ValueError("%s must be bf16 %s with a unit inner stride" % (name, list(shape)))
-
-
-def _workspace(workspace, need, dev):
-    """(address, bytes) of a caller's workspace or of a new one."""
-    if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-    if workspace is None:
-        return None, 0, None
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+    s0, s1, _ = t.stride()
+    return t, t.data_ptr(), s0, s1
 
 
 def rope_append_kv(k, v, k_cache, v_cache, slots, cos_sin=None, positions=None, q=None,
@@ -516,54 +530,45 @@ def rope_append_kv(k, v, k_cache, v_cache, slots, cos_sin=None, positions=None, 
     e4m3 cache (None: 1).  interleaved: the pairs are adjacent elements
     instead of (i, i + R/2).  Returns the rotated q (q_out if given; it may be
     q itself), or None without q."""
-    dev = k.device
-    _need_cuda(k)
-    _same_device(dev, v, k_cache, v_cache, slots, cos_sin, positions, q, q_out, k_scale, v_scale)
-    k, v = _heads3("k", k), _heads3("v", v)
-    T, Hkv, D = k.shape
-    if v.shape != k.shape:
+    dev = _one_device(k, v, k_cache, v_cache, slots, cos_sin, positions, q, q_out, k_scale,
+                      v_scale)
+    T, Hkv, D = shape = k.shape
+    if v.shape != shape:
         raise ValueError("k and v must have the same shape")
-    dtype = _cache("k_cache", k_cache, Hkv, D)
-    if _cache("v_cache", v_cache, Hkv, D) != dtype or v_cache.shape != k_cache.shape:
-        raise ValueError("k_cache and v_cache must have the same shape and dtype")
-    rot = max_pos = 0
+    k, kp, k0, k1 = _heads3("k", k)
+    v, vp, v0, v1 = _heads3("v", v)
+    cache = _caches(k_cache, v_cache, Hkv, D)
+    cp, rot, max_pos, pos = None, 0, 0, None
     if cos_sin is not None:
-        if cos_sin.dim() != 2 or cos_sin.dtype != torch.float32 or not cos_sin.is_contiguous():
+        if cos_sin.dim() != 2 or cos_sin.dtype != _f32 or not cos_sin.is_contiguous():
             raise ValueError("cos_sin must be contiguous fp32 [max_pos, R]")
-        max_pos, rot = cos_sin.shape
         if positions is None:
             raise ValueError("a rotation needs positions")
-    pos = _vec("positions", positions, torch.int32, T)
-    Hq, q_args = 0, (None, 0, 0, 0, None, 0, 0)
+        max_pos, rot = cos_sin.shape
+        cp, pos = cos_sin.data_ptr(), _vec("positions", positions, _i32, T)
+    qp = op = None
+    Hq = q0 = q1 = o0 = o1 = 0
     if q is not None:
-        given = q
-        q = _heads3("q", q)
-        Hq = q.shape[1]
-        if q.shape[0] != T or q.shape[2] != D:
+        given = q.shape
+        if len(given) != 3 or given[0] != T or given[2] != D:
             raise ValueError("q must be [%d, heads, %d]" % (T, D))
-        if q_out is None:
-            q_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev)
-        else:
-            _check_out("q_out", q_out, given.shape)
-        q_args = (q.data_ptr(), q.stride(0), q.stride(1), Hq, q_out.data_ptr(), q_out.stride(0),
-                  q_out.stride(1))
+        Hq = given[1]
+        q_in, qp, q0, q1 = _heads3("q", q)
+        q_out, op, o0, o1 = _output("q_out", q_out, given, k.device)
     elif q_out is not None:
         raise ValueError("q_out without q")
-    check(_lib_handle().mxq_rope_append_kv(
-        *q_args, k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(), v.stride(0), v.stride(1),
-        T, Hkv, D, None if cos_sin is None else cos_sin.data_ptr(), max_pos, rot, pos,
+    check(_lib.load().mxq_rope_append_kv(
+        qp, q0, q1, Hq, op, o0, o1, kp, k0, k1, vp, v0, v1, T, Hkv, D, cp, max_pos, rot, pos,
         1 if interleaved else 0, _vec("slots", slots, torch.int64, T), k_cache.data_ptr(),
-        v_cache.data_ptr(), dtype, k_cache.shape[0], k_cache.shape[1], *k_cache.stride()[:3],
-        *v_cache.stride()[:3], _vec("k_scale", k_scale, torch.float32, Hkv),
-        _vec("v_scale", v_scale, torch.float32, Hkv),
-        torch.cuda.current_stream(dev).cuda_stream))
+        v_cache.data_ptr(), *cache[:9], _vec("k_scale", k_scale, _f32, Hkv),
+        _vec("v_scale", v_scale, _f32, Hkv), _raw_stream(dev)))
     return q_out
 
 
 def paged_attention_decode_workspace_size(batch: int, heads: int, kv_heads: int,
                                           head_dim: int) -> int:
     n = ctypes.c_size_t(0)
-    check(_lib_handle().mxq_paged_attention_decode_workspace_size(
+    check(_lib.load().mxq_paged_attention_decode_workspace_size(
         batch, heads, kv_heads, head_dim, ctypes.byref(n)))
     return n.value
 
@@ -581,45 +586,39 @@ def paged_attention_decode(q, k_cache, v_cache, page_table, seq_lens, scale=None
     [B, Hq, D], with return_lse also the fp32 [B, Hq] log-sum-exp.  workspace:
     a caller's buffer of paged_attention_decode_workspace_size bytes (None:
     allocated here)."""
-    dev = q.device
-    _need_cuda(q)
-    _same_device(dev, k_cache, v_cache, page_table, seq_lens, sinks, k_scale, v_scale, out,
-                 workspace)
-    q = _heads3("q", q)
-    B, Hq, D = q.shape
-    Hkv = k_cache.shape[2] if k_cache.dim() == 4 else 0
-    dtype = _cache("k_cache", k_cache, Hkv, D)
-    if _cache("v_cache", v_cache, Hkv, D) != dtype or v_cache.shape != k_cache.shape:
-        raise ValueError("k_cache and v_cache must have the same shape and dtype")
-    if page_table.dim() != 2 or page_table.shape[0] != B or page_table.dtype != torch.int32 \
-            or (page_table.shape[1] > 1 and page_table.stride(1) != 1):
+    dev = _one_device(q, k_cache, v_cache, page_table, seq_lens, sinks, k_scale, v_scale, out,
+                      workspace)
+    shape = q.shape
+    q, qp, q0, q1 = _heads3("q", q)
+    B, Hq, D = shape
+    cache = _caches(k_cache, v_cache, None, D)
+    Hkv = cache[9]
+    if page_table.dim() != 2 or page_table.dtype != _i32:
+        raise ValueError("page_table must be int32 [%d, max_pages]" % B)
+    rows, width = page_table.shape
+    t0, t1 = page_table.stride()
+    if rows != B or (width > 1 and t1 != 1) or (rows > 1 and t0 < width):
         raise ValueError("page_table must be int32 [%d, max_pages] with a unit inner stride" % B)
-    lib = _lib_handle()
-    if out is None:
-        out = torch.empty((B, Hq, D), dtype=torch.bfloat16, device=dev)
-    else:
-        _check_out("out", out, q.shape)
-    lse = torch.empty((B, Hq), dtype=torch.float32, device=dev) if return_lse else None
-    n = ctypes.c_size_t(0)
+    out, op, o0, o1 = _output("out", out, shape, q.device)
+    lse = torch.empty((B, Hq), dtype=_f32, device=q.device) if return_lse else None
     if workspace is None:
-        check(lib.mxq_paged_attention_decode_workspace_size(B, Hq, Hkv, D, ctypes.byref(n)))
-    ws, ws_bytes, workspace = _workspace(workspace, n.value, dev)
-    check(lib.mxq_paged_attention_decode(
-        q.data_ptr(), q.stride(0), q.stride(1), B, Hq, Hkv, D, k_cache.data_ptr(),
-        v_cache.data_ptr(), dtype, k_cache.shape[0], k_cache.shape[1], *k_cache.stride()[:3],
-        *v_cache.stride()[:3], page_table.data_ptr(), max(page_table.stride(0), page_table.shape[1]),
-        page_table.shape[1], _vec("seq_lens", seq_lens, torch.int32, B),
-        D ** -0.5 if scale is None else scale, window, _vec("sinks", sinks, torch.float32, Hq),
-        _vec("k_scale", k_scale, torch.float32, Hkv), _vec("v_scale", v_scale, torch.float32, Hkv),
-        out.data_ptr(), out.stride(0), out.stride(1), None if lse is None else lse.data_ptr(), ws,
-        ws_bytes, torch.cuda.current_stream(dev).cuda_stream))
+        workspace = torch.empty(paged_attention_decode_workspace_size(B, Hq, Hkv, D),
+                                dtype=torch.uint8, device=q.device)
+    check(_lib.load().mxq_paged_attention_decode(
+        qp, q0, q1, B, Hq, Hkv, D, k_cache.data_ptr(), v_cache.data_ptr(), *cache[:9],
+        page_table.data_ptr(), t0 if rows > 1 else width, width,
+        _vec("seq_lens", seq_lens, _i32, B), D ** -0.5 if scale is None else scale, window,
+        _vec("sinks", sinks, _f32, Hq), _vec("k_scale", k_scale, _f32, Hkv),
+        _vec("v_scale", v_scale, _f32, Hkv), op, o0, o1,
+        None if lse is None else lse.data_ptr(), workspace.data_ptr(), workspace.nbytes,
+        _raw_stream(dev)))
     return (out, lse) if return_lse else out
 
 
 def attention_varlen_workspace_size(tokens: int, batch: int, heads: int, kv_heads: int,
                                     head_dim: int) -> int:
     n = ctypes.c_size_t(0)
-    check(_lib_handle().mxq_attention_varlen_workspace_size(
+    check(_lib.load().mxq_attention_varlen_workspace_size(
         tokens, batch, heads, kv_heads, head_dim, ctypes.byref(n)))
     return n.value
 
@@ -634,37 +633,30 @@ def attention_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k=None, scale=None, causa
     [B + 1] offsets (None: the keys' are the queries'); causal: query i of nq
     stands at key i + nk - nq and sees the keys up to it; window: only the
     last `window` of these (0: all); sinks: fp32 [Hq].  A row that sees no key
-    is 0.  Returns out bf16 [Tq, Hq, D], with return_lse also the fp32
-    [Tq, Hq] log-sum-exp.  workspace: a caller's buffer of
-    attention_varlen_workspace_size bytes (None: allocated here)."""
-    dev = q.device
-    _need_cuda(q)
-    _same_device(dev, k, v, cu_seqlens_q, cu_seqlens_k, sinks, out, workspace)
-    q, k, v = _heads3("q", q), _heads3("k", k), _heads3("v", v)
-    Tq, Hq, D = q.shape
-    Tk, Hkv, Dk = k.shape
-    if Dk != D or v.shape != k.shape:
+    is 0; rows outside every sequence are not written.  Returns out bf16
+    [Tq, Hq, D], with return_lse also the fp32 [Tq, Hq] log-sum-exp.
+    workspace: a caller's buffer of attention_varlen_workspace_size bytes
+    (None: allocated here)."""
+    dev = _one_device(q, k, v, cu_seqlens_q, cu_seqlens_k, sinks, out, workspace)
+    shape, kshape = q.shape, k.shape
+    q, qp, q0, q1 = _heads3("q", q)
+    k, kp, k0, k1 = _heads3("k", k)
+    v, vp, v0, v1 = _heads3("v", v)
+    Tq, Hq, D = shape
+    Tk, Hkv, Dk = kshape
+    if Dk != D or v.shape != kshape:
         raise ValueError("k and v must be [tokens, kv_heads, %d] alike" % D)
-    if cu_seqlens_k is None:
-        cu_seqlens_k = cu_seqlens_q
     B = cu_seqlens_q.numel() - 1
-    lib = _lib_handle()
-    if out is None:
-        out = torch.empty((Tq, Hq, D), dtype=torch.bfloat16, device=dev)
-    else:
-        _check_out("out", out, q.shape)
-    lse = torch.empty((Tq, Hq), dtype=torch.float32, device=dev) if return_lse else None
-    n = ctypes.c_size_t(0)
+    cq = _vec("cu_seqlens_q", cu_seqlens_q, _i32, B + 1)
+    ck = cq if cu_seqlens_k is None else _vec("cu_seqlens_k", cu_seqlens_k, _i32, B + 1)
+    out, op, o0, o1 = _output("out", out, shape, q.device)
+    lse = torch.empty((Tq, Hq), dtype=_f32, device=q.device) if return_lse else None
     if workspace is None:
-        check(lib.mxq_attention_varlen_workspace_size(Tq, B, Hq, Hkv, D, ctypes.byref(n)))
-    ws, ws_bytes, workspace = _workspace(workspace, n.value, dev)
-    check(lib.mxq_attention_varlen(
-        q.data_ptr(), q.stride(0), q.stride(1), k.data_ptr(), k.stride(0), k.stride(1),
-        v.data_ptr(), v.stride(0), v.stride(1),
-        _vec("cu_seqlens_q", cu_seqlens_q, torch.int32, B + 1),
-        _vec("cu_seqlens_k", cu_seqlens_k, torch.int32, B + 1), B, Tq, Tk, Hq, Hkv, D,
+        workspace = torch.empty(attention_varlen_workspace_size(Tq, B, Hq, Hkv, D),
+                                dtype=torch.uint8, device=q.device)
+    check(_lib.load().mxq_attention_varlen(
+        qp, q0, q1, kp, k0, k1, vp, v0, v1, cq, ck, B, Tq, Tk, Hq, Hkv, D,
         D ** -0.5 if scale is None else scale, 1 if causal else 0, window,
-        _vec("sinks", sinks, torch.float32, Hq), out.data_ptr(), out.stride(0), out.stride(1),
-        None if lse is None else lse.data_ptr(), ws, ws_bytes,
-        torch.cuda.current_stream(dev).cuda_stream))
+        _vec("sinks", sinks, _f32, Hq), op, o0, o1, None if lse is None else lse.data_ptr(),
+        workspace.data_ptr(), workspace.nbytes, _raw_stream(dev)))
     return (out, lse) if return_lse else out

@@ -110,6 +110,8 @@ def lib_path() -> str:
 def load(build_if_missing: bool = True):
     """Load libmxq.so (building it first if it does not exist)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib

@@ -43,7 +43,11 @@ namespace mxq {
 namespace {
 
 constexpr int kBM = 128;             // rows of a tile, keys of a block
-constexpr int kPromptThreads = 320;
+constexpr int kPromptThreads = 384;
+// registers a thread: the launch gives 168 to each of the 384; the softmax
+// warpgroups keep a row of 128 scores and take what the third one gives up
+constexpr int kSoftmaxRegs = 208, kOtherRegs = 80;
+static_assert(2 * kSoftmaxRegs + kOtherRegs <= 3 * 168, "register split above the launch's");
 
 struct PromptMaps {
   CUtensorMap q, k, v;
@@ -153,7 +157,7 @@ struct PromptLayout {
   static constexpr int kChunkBytes = kBM * 128;          // 128 rows of 64 elements
   static constexpr int kTileBytes = kChunks * kChunkBytes;
   static constexpr int kStages = D == 128 ? 5 : 9;
-  static constexpr int kBars = 2 * 5 + 2 * kStages + 1;
+  static constexpr int kBars = 2 * 6 + 2 * kStages + 1;
   static constexpr int kSmem = (2 + kStages) * kTileBytes + 8 * kBars + 16;
   static_assert(kSmem + 1024 <= 227 * 1024, "shared memory over budget");
 };
@@ -181,6 +185,31 @@ __device__ __forceinline__ int item_index(int r) {
   return r * gridDim.x + ((r & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
 }
 
+// The items this CTA takes, each read one ahead of its use.
+struct Items {
+  const PromptArgs& a;
+  int total, r = 0, head = 0, next_head = 0;
+  bool more;
+  PromptItem it, ahead;
+  __device__ __forceinline__ Items(const PromptArgs& args, int n) : a(args), total(n) { fetch(); }
+  __device__ __forceinline__ void fetch() {
+    const int idx = item_index(r++);
+    more = idx < total;
+    if (more) {
+      const int i = idx / a.p.Hkv;
+      next_head = idx - i * a.p.Hkv;
+      ahead = a.items[i];
+    }
+  }
+  __device__ __forceinline__ bool next() {
+    if (!more) return false;
+    it = ahead;
+    head = next_head;
+    fetch();
+    return true;
+  }
+};
+
 template <int D>
 __global__ void __launch_bounds__(kPromptThreads, 1)
     prompt_kernel(const __grid_constant__ PromptMaps maps, const PromptArgs a) {
@@ -198,7 +227,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   // an item's O has a barrier of its own: its commit is followed by the next
   // item's S without a word from the softmax, which would let one barrier run
   // two phases ahead of its waiter
-  uint64_t* o_full = p_full + 2;
+  uint64_t* o_full = p_full + 4;
   uint64_t* kv_full = o_full + 2;
   uint64_t* kv_empty = kv_full + ST;
   uint64_t* drain = kv_empty + ST;
@@ -214,7 +243,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       mbar_init(&q_empty[i], 1);
       mbar_init(&s_full[i], 1);
       mbar_init(&o_full[i], 1);
-      mbar_init(&p_full[i], 4);       // the warps of the tile's warpgroup
+      mbar_init(&p_full[2 * i], 4);       // the warps of the tile's warpgroup; P
+      mbar_init(&p_full[2 * i + 1], 4);   // of keys 0-63 and of 64-127
     }
     for (int i = 0; i < ST; ++i) {
       mbar_init(&kv_full[i], 1);
@@ -241,132 +271,143 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   pdl_launch_dependents();
   const int total = *a.n_items * p.Hkv;
 
-  if (warp == 9) {
-    // ------------------------------------------------------------ loads
-    if (lane == 0 && !a.inject_stall) {
-      uint32_t fill = 0, nq = 0;
-      const uint32_t q_bytes = static_cast<uint32_t>(a.G * a.TB) * 128 * L::kChunks;
-      bool ok = true;
-      for (int r = 0; ok && item_index(r) < total; ++r) {
-        const int idx = item_index(r);
-        const PromptItem it = a.items[idx / p.Hkv];
-        const int hk = idx % p.Hkv;
-        if (it.kb1 <= it.kb0) continue;
-        auto load_q = [&](int s) {
-          if (!mbar_wait(&q_empty[s], (nq & 1) ^ 1, wc)) return false;
-          mbar_expect_tx(&q_full[s], q_bytes);
-          for (int c = 0; c < L::kChunks; ++c)
-            tma_load_3d(sQ + s * L::kTileBytes + c * L::kChunkBytes, &maps.q, &q_full[s], c * 64,
-                        hk * a.G, it.q_row + s * a.TB);
-          return true;
-        };
-        auto load_kv = [&](const CUtensorMap* map, int kb) {
-          const int st = fill % ST;
-          if (!mbar_wait(&kv_empty[st], ((fill / ST) & 1) ^ 1, wc)) return false;
-          mbar_expect_tx(&kv_full[st], L::kTileBytes);
-          for (int c = 0; c < L::kChunks; ++c)
-            tma_load_3d(ring + st * L::kTileBytes + c * L::kChunkBytes, map, &kv_full[st], c * 64,
-                        hk, it.k_row + kb * kBM);
-          ++fill;
-          return true;
-        };
-        ok = load_q(0) && load_kv(&maps.k, it.kb1 - 1) && load_q(1) &&
-             load_kv(&maps.v, it.kb1 - 1);
-        ++nq;
-        for (int kb = it.kb1 - 2; ok && kb >= it.kb0; --kb)
-          ok = load_kv(&maps.k, kb) && load_kv(&maps.v, kb);
-      }
-      if (*abort_flag) {
-        // let every copy already issued land before the CTA goes away
-        volatile int zero = 0;
-        WaitCtx dw{p.status, &zero, 1000000000ull};
-        for (uint32_t i = fill > ST ? fill - ST : 0; i < fill; ++i)
-          mbar_wait(&kv_full[i % ST], (i / ST) & 1, dw);
-        for (int s = 0; s < 2; ++s)
-          if (nq > 0) mbar_wait(&q_full[s], (nq - 1) & 1, dw);
-      }
-    }
-  } else if (warp == 8) {
-    // -------------------------------------------------------------- MMAs
-    constexpr uint32_t kDescS = idesc_bf16(kBM, kBM);
-    constexpr uint32_t kDescO = idesc_bf16_bmn(kBM, D);
-    const bool leader = elect_one();
-    const uint32_t q_addr = smem_u32(sQ), ring_addr = smem_u32(ring);
-    uint32_t base = 0, nq = 0, np = 0;     // ring position of K_0, items, blocks so far
-    auto issue_s = [&](int s, uint32_t fill) {
-      const uint32_t qa = q_addr + s * L::kTileBytes;
-      const uint32_t ka = ring_addr + (fill % ST) * L::kTileBytes;
-#pragma unroll
-      for (int k = 0; k < D / 16; ++k) {
-        const uint32_t off = (k / 4) * L::kChunkBytes + (k % 4) * 32;
-        mma_f16(tmem + s * 128, sw128_desc(qa + off), sw128_desc(ka + off), kDescS, k > 0);
-      }
-    };
-    auto issue_o = [&](int s, uint32_t fill, bool accumulate) {
-      const uint32_t va = ring_addr + (fill % ST) * L::kTileBytes;
-#pragma unroll
-      for (int k = 0; k < kBM / 16; ++k)
-        mma_f16_ts(tmem + 256 + s * 128, tmem + s * 128 + k * 8,
-                   sw128_desc_mn(va + k * 2048, L::kChunkBytes), kDescO, accumulate || k > 0);
-    };
-    auto wait_kv = [&](uint32_t fill) {
-      return mbar_wait_warp(&kv_full[fill % ST], (fill / ST) & 1, wc);
-    };
-    for (int r = 0; item_index(r) < total; ++r) {
-      const PromptItem it = a.items[item_index(r) / p.Hkv];
-      const int n = it.kb1 - it.kb0;
-      if (n <= 0) continue;
-      if (!wait_kv(base)) goto mma_done;
-      for (int s = 0; s < 2; ++s) {
-        if (!mbar_wait_warp(&q_full[s], nq & 1, wc)) goto mma_done;
-        if (leader) {
-          tc_fence_after();
-          issue_s(s, base);
-          mma_commit(&s_full[s]);
-          if (n == 1) mma_commit(&q_empty[s]);
-          if (s == 1) mma_commit(&kv_empty[base % ST]);
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp == 9) {
+      // ------------------------------------------------------------ loads
+      if (lane == 0 && !a.inject_stall) {
+        uint32_t fill = 0, nq = 0;
+        const uint32_t q_bytes = static_cast<uint32_t>(a.G * a.TB) * 128 * L::kChunks;
+        bool ok = true;
+        Items items(a, total);
+        while (ok && items.next()) {
+          const PromptItem& it = items.it;
+          const int hk = items.head;
+          if (it.kb1 <= it.kb0) continue;
+          auto load_q = [&](int s) {
+            if (!mbar_wait(&q_empty[s], (nq & 1) ^ 1, wc)) return false;
+            mbar_expect_tx(&q_full[s], q_bytes);
+            for (int c = 0; c < L::kChunks; ++c)
+              tma_load_3d(sQ + s * L::kTileBytes + c * L::kChunkBytes, &maps.q, &q_full[s], c * 64,
+                          hk * a.G, it.q_row + s * a.TB);
+            return true;
+          };
+          auto load_kv = [&](const CUtensorMap* map, int kb) {
+            const int st = fill % ST;
+            if (!mbar_wait(&kv_empty[st], ((fill / ST) & 1) ^ 1, wc)) return false;
+            mbar_expect_tx(&kv_full[st], L::kTileBytes);
+            for (int c = 0; c < L::kChunks; ++c)
+              tma_load_3d(ring + st * L::kTileBytes + c * L::kChunkBytes, map, &kv_full[st], c * 64,
+                          hk, it.k_row + kb * kBM);
+            ++fill;
+            return true;
+          };
+          ok = load_q(0) && load_kv(&maps.k, it.kb1 - 1) && load_q(1) &&
+               load_kv(&maps.v, it.kb1 - 1);
+          ++nq;
+          for (int kb = it.kb1 - 2; ok && kb >= it.kb0; --kb)
+            ok = load_kv(&maps.k, kb) && load_kv(&maps.v, kb);
         }
-        __syncwarp();
+        if (*abort_flag) {
+          // let every copy already issued land before the CTA goes away
+          volatile int zero = 0;
+          WaitCtx dw{p.status, &zero, 1000000000ull};
+          for (uint32_t i = fill > ST ? fill - ST : 0; i < fill; ++i)
+            mbar_wait(&kv_full[i % ST], (i / ST) & 1, dw);
+          for (int s = 0; s < 2; ++s)
+            if (nq > 0) mbar_wait(&q_full[s], (nq - 1) & 1, dw);
+        }
       }
-      for (int j = 0; j < n; ++j, ++np) {
-        const uint32_t vf = base + 2 * j + 1, kf = vf + 1;
-        if (!wait_kv(vf)) goto mma_done;
+    } else if (warp == 8) {
+      // -------------------------------------------------------------- MMAs
+      constexpr uint32_t kDescS = idesc_bf16(kBM, kBM);
+      constexpr uint32_t kDescO = idesc_bf16_bmn(kBM, D);
+      const bool leader = elect_one();
+      // descriptors of the first tiles; offsets are added in 16-byte units
+      const uint64_t q_desc = sw128_desc(smem_u32(sQ)), k_desc = sw128_desc(smem_u32(ring));
+      const uint64_t v_desc = sw128_desc_mn(smem_u32(ring), L::kChunkBytes);
+      uint32_t base = 0, nq = 0, np = 0;     // ring position of K_0, items, blocks so far
+      auto issue_s = [&](int s, uint32_t fill) {
+        const uint64_t qd = q_desc + s * (L::kTileBytes / 16);
+        const uint64_t kd = k_desc + (fill % ST) * (L::kTileBytes / 16);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const int off = (k / 4) * (L::kChunkBytes / 16) + (k % 4) * 2;
+          mma_f16(tmem + s * 128, qd + off, kd + off, kDescS, k > 0);
+        }
+      };
+      // the keys of half `part` of a block
+      auto issue_o = [&](int s, uint32_t fill, int part, bool accumulate) {
+        const uint64_t vd = v_desc + (fill % ST) * (L::kTileBytes / 16) + part * (4 * 2048 / 16);
+        const uint32_t pa = tmem + s * 128 + part * 32;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          mma_f16_ts(tmem + 256 + s * 128, pa + k * 8, vd + k * (2048 / 16), kDescO,
+                     accumulate || k > 0);
+      };
+      auto wait_kv = [&](uint32_t fill) {
+        return mbar_wait_warp(&kv_full[fill % ST], (fill / ST) & 1, wc);
+      };
+      Items items(a, total);
+      while (items.next()) {
+        const int n = items.it.kb1 - items.it.kb0;
+        if (n <= 0) continue;
+        if (!wait_kv(base)) goto mma_done;
         for (int s = 0; s < 2; ++s) {
-          if (!mbar_wait_warp(&p_full[s], np & 1, wc)) goto mma_done;
+          if (!mbar_wait_warp(&q_full[s], nq & 1, wc)) goto mma_done;
           if (leader) {
             tc_fence_after();
-            issue_o(s, vf, j > 0);
-            if (s == 1) mma_commit(&kv_empty[vf % ST]);
-          }
-          __syncwarp();
-          if (j + 1 < n) {
-            if (s == 0 && !wait_kv(kf)) goto mma_done;
-            if (leader) {
-              tc_fence_after();
-              issue_s(s, kf);
-              mma_commit(&s_full[s]);
-              if (j + 2 == n) mma_commit(&q_empty[s]);
-              if (s == 1) mma_commit(&kv_empty[kf % ST]);
-            }
-          } else if (leader) {
-            mma_commit(&o_full[s]);        // the item's O is complete
+            issue_s(s, base);
+            mma_commit(&s_full[s]);
+            if (n == 1) mma_commit(&q_empty[s]);
+            if (s == 1) mma_commit(&kv_empty[base % ST]);
           }
           __syncwarp();
         }
+        for (int j = 0; j < n; ++j, ++np) {
+          const uint32_t vf = base + 2 * j + 1, kf = vf + 1;
+          if (!wait_kv(vf)) goto mma_done;
+          for (int s = 0; s < 2; ++s) {
+#pragma unroll
+            for (int part = 0; part < 2; ++part) {
+              if (!mbar_wait_warp(&p_full[2 * s + part], np & 1, wc)) goto mma_done;
+              if (leader) {
+                tc_fence_after();
+                issue_o(s, vf, part, j > 0 || part > 0);
+              }
+              __syncwarp();
+            }
+            if (leader && s == 1) mma_commit(&kv_empty[vf % ST]);
+            if (j + 1 < n) {
+              if (s == 0 && !wait_kv(kf)) goto mma_done;
+              if (leader) {
+                tc_fence_after();
+                issue_s(s, kf);
+                mma_commit(&s_full[s]);
+                if (j + 2 == n) mma_commit(&q_empty[s]);
+                if (s == 1) mma_commit(&kv_empty[kf % ST]);
+              }
+            } else if (leader) {
+              mma_commit(&o_full[s]);        // the item's O is complete
+            }
+            __syncwarp();
+          }
+        }
+        base += 2 * n;
+        ++nq;
       }
-      base += 2 * n;
-      ++nq;
-    }
-  mma_done:
-    if (*abort_flag) {
-      // wait for the MMAs in flight before the tensor memory is freed
-      if (leader) mma_commit(drain);
-      volatile int zero = 0;
-      WaitCtx dw{p.status, &zero, 1000000000ull};
-      mbar_wait(drain, 0, dw);
+    mma_done:
+      if (*abort_flag) {
+        // wait for the MMAs in flight before the tensor memory is freed
+        if (leader) mma_commit(drain);
+        volatile int zero = 0;
+        WaitCtx dw{p.status, &zero, 1000000000ull};
+        mbar_wait(drain, 0, dw);
+      }
     }
   } else {
     // ----------------------------------------------------------- softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     const int s = warp >> 2;                            // tile
     const int row = threadIdx.x & 127;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
@@ -374,41 +415,51 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     const int tok = row / a.G, g = row - tok * a.G;
     const float c = p.scale * kLog2e;
     uint32_t ns = 0, no = 0, base = 0;
-    for (int r = 0; item_index(r) < total; ++r) {
-      const int idx = item_index(r);
-      const PromptItem it = a.items[idx / p.Hkv];
+    Items items(a, total);
+    while (items.next()) {
+      const PromptItem& it = items.it;
       const int n = it.kb1 - it.kb0;
-      const int h = (idx % p.Hkv) * a.G + g;
+      const int h = items.head * a.G + g;
       const int i = s * a.TB + tok;
       const bool valid = tok < a.TB && i < it.ntok;
-      // visible keys [lo, hi) of this row
+      // visible keys [lo, hi) of this row, and those every row of the warp sees
       const int at = it.at0 + i;
       const int hi = !valid ? 0 : (p.causal ? min(it.nk, at + 1) : it.nk);
       const int lo = p.window > 0 ? max(0, at - p.window + 1) : 0;
+      const int all_lo = __reduce_max_sync(0xffffffffu, lo);
+      const int all_hi = __reduce_min_sync(0xffffffffu, hi);
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < n; ++j) {
-        const int kb = it.kb1 - 1 - j;
+        const int k0 = (it.kb1 - 1 - j) * kBM;
         if (!mbar_wait_warp(&s_full[s], ns & 1, wc)) goto softmax_done;
         ++ns;
         tc_fence_after();
+        // the row's scores, its maximum following the loads
         float x[128];
+        float mx = -INFINITY;
+        tmem_ld32_async(tS, x);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) tmem_ld32_async(tS + 32 * q, x + 32 * q);
+        for (int q = 0; q < 4; ++q) {
+          float* v = x + 32 * q;
+          tmem_wait32(v);
+          if (q < 3) tmem_ld32_async(tS + 32 * (q + 1), v + 32);
+          if (k0 + kBM > all_hi || k0 < all_lo) {
+            const int c_hi = hi - k0 - 32 * q, c_lo = lo - k0 - 32 * q;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) tmem_wait32(x + 32 * q);
-        const int c_hi = hi - kb * kBM, c_lo = lo - kb * kBM;
-        if (__any_sync(0xffffffffu, c_hi < kBM || c_lo > 0)) {
+            for (int e = 0; e < 32; ++e) v[e] = e < c_hi && e >= c_lo ? v[e] : -INFINITY;
+          }
+          float m0 = fmaxf(v[0], v[1]), m1 = fmaxf(v[2], v[3]);
 #pragma unroll
-          for (int e = 0; e < 128; ++e) x[e] = e < c_hi && e >= c_lo ? x[e] : -INFINITY;
+          for (int e = 4; e < 32; e += 4) {
+            m0 = fmaxf(m0, fmaxf(v[e], v[e + 1]));
+            m1 = fmaxf(m1, fmaxf(v[e + 2], v[e + 3]));
+          }
+          mx = fmaxf(mx, fmaxf(m0, m1));
         }
-        float mx = x[0];
-#pragma unroll
-        for (int e = 1; e < 127; e += 2) mx = fmaxf(mx, fmaxf(x[e], x[e + 1]));
-        mx = fmaxf(mx, x[127]);
         // raise the reference if it grows by more than 2^8 (at first: from -inf)
-        const bool raise = (mx - m) * c > 8.f || (m == -INFINITY && mx > -INFINITY);
+        const bool raise = (mx - m) * c > 8.f;
         if (__any_sync(0xffffffffu, raise)) {
-          const float f = raise ? (m == -INFINITY ? 0.f : ex2((m - mx) * c)) : 1.f;
+          const float f = raise ? ex2((m - mx) * c) : 1.f;
           if (__any_sync(0xffffffffu, raise && m > -INFINITY)) {
             // the products of the blocks before are complete: their commit came
             // before this block's scores
@@ -427,32 +478,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         }
         const float mc = m == -INFINITY ? 0.f : m * c;
         const uint64_t c2 = pack2(c, c), n2 = pack2(-mc, -mc);
-        uint64_t sum0 = pack2(0.f, 0.f), sum1 = sum0;
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          uint32_t w[32];
-#pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            float u, v;
-            unpack2(fma2(pack2(x[64 * q + 2 * e], x[64 * q + 2 * e + 1]), c2, n2), &u, &v);
-            u = ex2(u), v = ex2(v);
-            w[e] = bf16x2(u, v);
-            if (e & 1)
-              sum1 = add2(sum1, pack2(u, v));
-            else
-              sum0 = add2(sum0, pack2(u, v));
-          }
-          tmem_st32(tS + 32 * q, w);
-        }
-        float s0, s1;
-        unpack2(add2(sum0, sum1), &s0, &s1);
-        l += s0 + s1;
-        if (j == 0 && s == 0 && it.nk < it.kb1 * kBM) {
+        if (j == 0 && s == 0 && it.nk < k0 + kBM) {
           // the last block's rows past the sequence are other keys' (or none): their
           // weights are 0, and the values become 0 too, as 0 * inf is not 0
           const uint32_t vf = base + 1;
           if (!mbar_wait_warp(&kv_full[vf % ST], (vf / ST) & 1, wc)) goto softmax_done;
-          if (kb * kBM + row >= it.nk) {
+          if (k0 + row >= it.nk) {
             uint8_t* vr = ring + (vf % ST) * L::kTileBytes + row * 128;
             for (int ch = 0; ch < L::kChunks; ++ch)
 #pragma unroll
@@ -462,10 +493,27 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           }
           fence_proxy_async_smem();
         }
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[s]);
+        uint64_t sum[4];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          uint32_t w[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            float u, v;
+            unpack2(fma2(pack2(x[64 * q + 2 * e], x[64 * q + 2 * e + 1]), c2, n2), &u, &v);
+            u = ex2(u), v = ex2(v);
+            w[e] = bf16x2(u, v);
+            sum[e & 3] = q == 0 && e < 4 ? pack2(u, v) : add2(sum[e & 3], pack2(u, v));
+          }
+          tmem_st32(tS + 32 * q, w);
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[2 * s + q]);
+        }
+        float s0, s1;
+        unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), &s0, &s1);
+        l += s0 + s1;
       }
       base += n > 0 ? 2 * n : 0;
       if (n > 0) {
