@@ -156,9 +156,11 @@ struct PromptLayout {
   static constexpr int kChunks = D / 64;
   static constexpr int kChunkBytes = kBM * 128;          // 128 rows of 64 elements
   static constexpr int kTileBytes = kChunks * kChunkBytes;
-  static constexpr int kStages = D == 128 ? 5 : 9;
+  static constexpr int kStages = D == 128 ? 4 : 8;       // five measured no faster than four
+  static constexpr int kOutBytes = 8 * 32 * 128;         // output staging: 32 rows x 128 B a warp
   static constexpr int kBars = 2 * 6 + 2 * kStages + 1;
-  static constexpr int kSmem = (2 + kStages) * kTileBytes + 8 * kBars + 16;
+  static constexpr int kSmem =
+      (2 + kStages) * kTileBytes + kOutBytes + 8 * kBars + 16;
   static_assert(kSmem + 1024 <= 227 * 1024, "shared memory over budget");
 };
 
@@ -180,6 +182,11 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
+// bits 0 .. n-1
+__device__ __forceinline__ uint32_t low_bits(int n) {
+  return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
+}
+
 // position r of the sequence of items that this CTA takes, in alternating direction
 __device__ __forceinline__ int item_index(int r) {
   return r * gridDim.x + ((r & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
@@ -220,7 +227,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t* sQ = smem;
   uint8_t* ring = smem + 2 * L::kTileBytes;
-  uint64_t* q_full = reinterpret_cast<uint64_t*>(ring + ST * L::kTileBytes);
+  uint8_t* sOut = ring + ST * L::kTileBytes;
+  uint64_t* q_full = reinterpret_cast<uint64_t*>(sOut + L::kOutBytes);
   uint64_t* q_empty = q_full + 2;
   uint64_t* s_full = q_empty + 2;
   uint64_t* p_full = s_full + 2;
@@ -422,10 +430,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       const int h = items.head * a.G + g;
       const int i = s * a.TB + tok;
       const bool valid = tok < a.TB && i < it.ntok;
-      // visible keys [lo, hi) of this row, and those every row of the warp sees
+      // visible keys [lo, hi) of this row, and those every row of the warp sees;
+      // a row that is not stored may see anything
       const int at = it.at0 + i;
-      const int hi = !valid ? 0 : (p.causal ? min(it.nk, at + 1) : it.nk);
-      const int lo = p.window > 0 ? max(0, at - p.window + 1) : 0;
+      const int hi = !valid ? 1 << 30 : (p.causal ? min(it.nk, at + 1) : it.nk);
+      const int lo = valid && p.window > 0 ? max(0, at - p.window + 1) : 0;
       const int all_lo = __reduce_max_sync(0xffffffffu, lo);
       const int all_hi = __reduce_min_sync(0xffffffffu, hi);
       float m = -INFINITY, l = 0.f;
@@ -434,28 +443,26 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         if (!mbar_wait_warp(&s_full[s], ns & 1, wc)) goto softmax_done;
         ++ns;
         tc_fence_after();
-        // the row's scores, its maximum following the loads
-        float x[128];
-        float mx = -INFINITY;
-        tmem_ld32_async(tS, x);
+        // the row's scores and their maximum
+        float x[128], mq[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) tmem_ld32_async(tS + 32 * q, x + 32 * q);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           float* v = x + 32 * q;
           tmem_wait32(v);
-          if (q < 3) tmem_ld32_async(tS + 32 * (q + 1), v + 32);
-          if (k0 + kBM > all_hi || k0 < all_lo) {
-            const int c_hi = hi - k0 - 32 * q, c_lo = lo - k0 - 32 * q;
+          const int kq = k0 + 32 * q;
+          if (kq + 32 > all_hi || kq < all_lo) {
+            // a warp's rows span few positions: most chunks need no mask
+            const uint32_t vis = low_bits(hi - kq) & ~low_bits(lo - kq);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) v[e] = e < c_hi && e >= c_lo ? v[e] : -INFINITY;
+            for (int e = 0; e < 32; ++e) v[e] = (vis >> e) & 1 ? v[e] : -INFINITY;
           }
-          float m0 = fmaxf(v[0], v[1]), m1 = fmaxf(v[2], v[3]);
+          mq[q] = fmaxf(v[0], v[1]);
 #pragma unroll
-          for (int e = 4; e < 32; e += 4) {
-            m0 = fmaxf(m0, fmaxf(v[e], v[e + 1]));
-            m1 = fmaxf(m1, fmaxf(v[e + 2], v[e + 3]));
-          }
-          mx = fmaxf(mx, fmaxf(m0, m1));
+          for (int e = 2; e < 32; e += 2) mq[q] = fmaxf(mq[q], fmaxf(v[e], v[e + 1]));
         }
+        const float mx = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3]));
         // raise the reference if it grows by more than 2^8 (at first: from -inf)
         const bool raise = (mx - m) * c > 8.f;
         if (__any_sync(0xffffffffu, raise)) {
@@ -493,24 +500,33 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           }
           fence_proxy_async_smem();
         }
-        uint64_t sum[4];
+        // weights, in two halves of 64 keys; the first is handed over a little
+        // into the second, when its store is surely complete
+        uint64_t sum[4] = {};
+        auto weights = [&](uint32_t* w, int first, int last) {
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          uint32_t w[32];
-#pragma unroll
-          for (int e = 0; e < 32; ++e) {
+          for (int e = first; e < last; e += 2) {
             float u, v;
-            unpack2(fma2(pack2(x[64 * q + 2 * e], x[64 * q + 2 * e + 1]), c2, n2), &u, &v);
+            unpack2(fma2(pack2(x[e], x[e + 1]), c2, n2), &u, &v);
             u = ex2(u), v = ex2(v);
-            w[e] = bf16x2(u, v);
-            sum[e & 3] = q == 0 && e < 4 ? pack2(u, v) : add2(sum[e & 3], pack2(u, v));
+            w[(e & 63) / 2] = bf16x2(u, v);
+            sum[(e / 2) & 3] = add2(sum[(e / 2) & 3], pack2(u, v));
           }
-          tmem_st32(tS + 32 * q, w);
+        };
+        auto hand_over = [&](int part) {
           tmem_st_wait();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&p_full[2 * s + q]);
-        }
+          if (lane == 0) mbar_arrive(&p_full[2 * s + part]);
+        };
+        uint32_t w0[32], w1[32];
+        weights(w0, 0, 64);
+        tmem_st32(tS, w0);
+        weights(w1, 64, 80);
+        hand_over(0);
+        weights(w1, 80, 128);
+        tmem_st32(tS + 32, w1);
+        hand_over(1);
         float s0, s1;
         unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), &s0, &s1);
         l += s0 + s1;
@@ -525,28 +541,38 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           finish_row(m * p.scale, l, p.sinks != nullptr && valid ? p.sinks + h : nullptr);
       const float inv = end.factor;
       const bool none = end.none;
+      // through shared memory, so that 8 lanes write 128 adjacent bytes of a row
       const int64_t tokr = it.q_row + i;
-      __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + tokr * p.o_t + h * p.o_h;
-#pragma unroll
-      for (int q = 0; q < D; q += 32) {
-        float o[32];
+      const int64_t dst = tokr * p.o_t + static_cast<int64_t>(h) * p.o_h;
+      const uint32_t stored = __ballot_sync(0xffffffffu, valid);
+      uint8_t* stage = sOut + warp * (32 * 128);
+      for (int d0 = 0; d0 < D; d0 += 64) {
+        float o[64];
         if (n > 0) {
-          tmem_ld32(tO + q, o);
+          tmem_ld64(tO + d0, o);
         } else {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = 0.f;
+          for (int e = 0; e < 64; ++e) o[e] = 0.f;
         }
-        if (valid) {
 #pragma unroll
-          for (int e = 0; e < 32; e += 8) {
-            uint4 w;
-            w.x = bf16x2(none ? 0.f : o[e] * inv, none ? 0.f : o[e + 1] * inv);
-            w.y = bf16x2(none ? 0.f : o[e + 2] * inv, none ? 0.f : o[e + 3] * inv);
-            w.z = bf16x2(none ? 0.f : o[e + 4] * inv, none ? 0.f : o[e + 5] * inv);
-            w.w = bf16x2(none ? 0.f : o[e + 6] * inv, none ? 0.f : o[e + 7] * inv);
-            *reinterpret_cast<uint4*>(dst + q + e) = w;
-          }
+        for (int e = 0; e < 8; ++e) {
+          uint32_t w[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            w[k] = none ? 0u : bf16x2(o[8 * e + 2 * k] * inv, o[8 * e + 2 * k + 1] * inv);
+          *reinterpret_cast<uint4*>(stage + lane * 128 + ((e ^ (lane & 7)) << 4)) =
+              make_uint4(w[0], w[1], w[2], w[3]);
         }
+        __syncwarp();
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int rw = 4 * e + (lane >> 3), ch = lane & 7;
+          const uint4 w = *reinterpret_cast<const uint4*>(stage + rw * 128 + ((ch ^ (rw & 7)) << 4));
+          const int64_t to = __shfl_sync(0xffffffffu, dst, rw);
+          if ((stored >> rw) & 1)
+            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + to + d0 + 8 * ch) = w;
+        }
+        __syncwarp();
       }
       if (p.lse != nullptr && valid)
         p.lse[tokr * p.Hq + h] = end.lse;
