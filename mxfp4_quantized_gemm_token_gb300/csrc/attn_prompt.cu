@@ -28,7 +28,13 @@
 //
 // Work.  A kernel of one block first lists the work items (sequence, pair of
 // tiles, its blocks of keys) with the costliest first; the persistent CTAs
-// take them in turn, in alternating direction, which balances lengths.
+// take them in turn, in alternating direction, which balances lengths.  Where
+// the longest item is longer than a CTA's share of all blocks (few rows, many keys), the
+// blocks of all items form one line instead, cut into equal parts, one per CTA; items
+// that parts share leave partial results in the workspace, at most two per
+// CTA, and whichever warp is the last to finish its 32 rows of an item joins them,
+// in the parts' order, so the result does not depend on who was last.  One
+// sequence with enough rows needs no list: its items are in order as they stand.
 #include <cuda_bf16.h>
 #include <math.h>
 
@@ -53,24 +59,54 @@ struct PromptMaps {
   CUtensorMap q, k, v;
 };
 
-// One pair of tiles: tokens [q_row, q_row + ntok) of the packed queries, the
-// first of which stands at key position at0 of its sequence's nk keys, and the
-// key blocks [kb0, kb1) that any of them sees.
+// One pair of tiles of a key/value head: tokens [q_row, q_row + ntok) of the packed
+// queries, the first of which stands at key position at0 of its sequence's nk
+// keys, against the key blocks [kb0, kb1).
 struct __align__(16) PromptItem {
   int q_row, ntok, at0, k_row;
-  int nk, kb0, kb1, pad;
+  int nk, kb0, kb1;
+  int head;                          // + kPiece: only some of the item's blocks
 };
+constexpr int kPiece = 1 << 30;
+
+// Where a piece's result goes, and who has the item's others: part w0 in its slot
+// `first`, parts w0 + 1 .. w1 in their slot 0.
+struct __align__(16) PromptPiece {
+  int slot;                          // part * 2 + 0 or 1
+  int w0, w1;
+  int key;                           // 2 * (counter of the item's finished pieces) + first
+};
+
+// What the plan leaves at the head of the workspace.
+struct PromptHeader {
+  int n;                             // entries of the list
+  int per;                           // blocks of a part; 0: whole items
+};
+
+constexpr int kRowsPerItem = 2 * kBM;
+constexpr int kMinSplit = 8;         // items of at most this many blocks stay whole
+constexpr int kMaxSplitItems = 16;   // items per SM above which all do
 
 struct PromptArgs {
   PromptParams p;
-  const int* n_items;                // header of the workspace
-  const PromptItem* items;
+  PromptHeader* header;              // in the workspace; null: one sequence, no list
+  PromptItem* list;                  // what the CTAs work on
+  PromptItem* items;                 // the plan's own; null: items stay whole
+  PromptPiece* pieces;               // for the list's entries
+  int* start;                        // each part's first entry
+  int* done;                         // [item][8 warps]: finished pieces
+  float2* part_ml;                   // [slot][256]: reference and sum
+  float* part_o;                     // [slot][256][D]
+  int cap;                           // room for items, before their heads
+  int grid;                          // CTAs
   int G, TB;
   unsigned long long budget_ns;
   int inject_stall;
 };
 
 constexpr int kBuckets = 512;
+
+__device__ __forceinline__ int item_blocks(const PromptItem& it) { return max(1, it.kb1 - it.kb0); }
 
 // [start, start + len) of sequence b in cu, or nothing if it leaves [0, total]
 __device__ __forceinline__ bool seq_range(const int32_t* cu, int b, int64_t total, int* start,
@@ -82,17 +118,59 @@ __device__ __forceinline__ bool seq_range(const int32_t* cu, int b, int64_t tota
   return ok;
 }
 
+// Item i of a sequence.
+__device__ __forceinline__ PromptItem make_item(const PromptParams& p, int tokens_per_item, int q0,
+                                                int nq, int k0, int nk, int i) {
+  PromptItem it;
+  const int first = i * tokens_per_item;
+  it.q_row = q0 + first;
+  it.ntok = min(tokens_per_item, nq - first);
+  it.at0 = first + nk - nq;
+  it.k_row = k0;
+  it.nk = nk;
+  const int hi = p.causal ? min(nk, it.at0 + it.ntok) : nk;
+  it.kb1 = hi > 0 ? (hi + kBM - 1) / kBM : 0;
+  it.kb0 = p.window > 0 ? max(0, it.at0 - p.window + 1) / kBM : 0;
+  it.head = 0;
+  return it;
+}
+
+// Exclusive prefix sum over the block's 1024 threads, and the sum of all.
+__device__ __forceinline__ int block_scan(int v, int* sums, int* all) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) sums[warp] = x;
+  __syncthreads();
+  int before = 0, total = 0;
+#pragma unroll
+  for (int w = 0; w < 32; ++w) {
+    if (w < warp) before += sums[w];
+    total += sums[w];
+  }
+  __syncthreads();
+  *all = total;
+  return before + x - v;
+}
+
 // Lists the items, ordered by falling number of key blocks (a counting sort; more than
-// 511 blocks count as 511).
-__global__ void __launch_bounds__(1024) prompt_plan_kernel(const PromptParams p, int tokens_per_item,
-                                                           int* n_items, PromptItem* items,
-                                                           int cap) {
+// 511 blocks count as 511), and cuts them into pieces where one is too long.
+__global__ void __launch_bounds__(1024) prompt_plan_kernel(const PromptArgs a) {
+  const PromptParams& p = a.p;
+  const int tokens_per_item = 2 * a.TB;
   __shared__ int count[kBuckets];
+  __shared__ int n_items, sums[32], longest, all_blocks;
   pdl_wait();
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   for (int i = threadIdx.x; i < kBuckets; i += blockDim.x) count[i] = 0;
+  if (threadIdx.x == 0) longest = all_blocks = 0;
   __syncthreads();
+  bool split = false;
   for (int pass = 0; pass < 2; ++pass) {
     for (int b = warp; b < p.B; b += 32) {
       int q0, nq, k0, nk;
@@ -104,23 +182,23 @@ __global__ void __launch_bounds__(1024) prompt_plan_kernel(const PromptParams p,
       }
       const int pairs = (nq + tokens_per_item - 1) / tokens_per_item;
       for (int i = lane; i < pairs; i += 32) {
-        PromptItem it;
-        const int first = i * tokens_per_item;
-        it.q_row = q0 + first;
-        it.ntok = min(tokens_per_item, nq - first);
-        it.at0 = first + nk - nq;
-        it.k_row = k0;
-        it.nk = nk;
-        const int hi = p.causal ? min(nk, it.at0 + it.ntok) : nk;
-        it.kb1 = hi > 0 ? (hi + kBM - 1) / kBM : 0;
-        it.kb0 = p.window > 0 ? max(0, it.at0 - p.window + 1) / kBM : 0;
-        it.pad = 0;
+        PromptItem it = make_item(p, tokens_per_item, q0, nq, k0, nk, i);
         const int bucket = kBuckets - 1 - min(kBuckets - 1, max(0, it.kb1 - it.kb0));
         if (pass == 0) {
           atomicAdd(&count[bucket], 1);
+          if (a.items != nullptr) {
+            atomicMax(&longest, item_blocks(it));
+            atomicAdd(&all_blocks, item_blocks(it));
+          }
+          continue;
+        }
+        const int at = atomicAdd(&count[bucket], 1);
+        if (at >= a.cap) continue;
+        if (split) {
+          a.items[at] = it;
         } else {
-          const int at = atomicAdd(&count[bucket], 1);
-          if (at < cap) items[at] = it;
+          for (; it.head < p.Hkv; ++it.head)
+            a.list[static_cast<int64_t>(at) * p.Hkv + it.head] = it;
         }
       }
     }
@@ -142,12 +220,56 @@ __global__ void __launch_bounds__(1024) prompt_plan_kernel(const PromptParams p,
         }
         // only offsets that run backwards give more items than there is room for
         if (lane == 0) {
-          if (run > cap) atomicOr(p.status, kStatusBadIndex);
-          *n_items = min(run, cap);
+          if (run > a.cap) atomicOr(p.status, kStatusBadIndex);
+          n_items = min(run, a.cap);
+          a.header->n = n_items * p.Hkv;
+          a.header->per = 0;
         }
       }
       __syncthreads();
+      split = a.items != nullptr && longest > kMinSplit &&
+              longest > (all_blocks * p.Hkv + a.grid - 1) / a.grid;
     }
+  }
+  if (!split) return;
+  // the line of all items' blocks, heads inside items; an item without keys
+  // counts as one block
+  const int per = max(kMinSplit / 2, (all_blocks * p.Hkv + a.grid - 1) / a.grid);
+  int line = 0, entries = 0;
+  for (int i0 = 0; i0 < n_items * p.Hkv; i0 += 1024) {
+    const int idx = i0 + threadIdx.x, i = idx / p.Hkv;
+    const bool in = i < n_items;
+    PromptItem it = {};
+    if (in) it = a.items[i];
+    const int n = in ? item_blocks(it) : 0;
+    int sum;
+    const int p0 = line + block_scan(n, sums, &sum), p1 = p0 + n;
+    line += sum;
+    const int w0 = p0 / per, w1 = in ? (p1 - 1) / per : w0 - 1;
+    int e = entries + block_scan(w1 - w0 + 1, sums, &sum);
+    entries += sum;
+    if (!in) continue;
+    for (int k = 0; k < 8; ++k) a.done[idx * 8 + k] = 0;
+    const int kb1 = it.kb1;
+    const bool whole = w0 == w1, keys = it.kb1 > it.kb0;
+    it.head = idx - i * p.Hkv + (whole ? 0 : kPiece);
+    for (int w = w0; w <= w1; ++w, ++e) {
+      const int from = max(p0, w * per), to = min(p1, (w + 1) * per);
+      if (keys) {
+        it.kb1 = kb1 - (from - p0);
+        it.kb0 = it.kb1 - (to - from);
+      }
+      a.list[e] = it;
+      if (!whole) a.pieces[e] = {2 * w + (from == w * per ? 0 : 1), w0, w1,
+                                 2 * idx + (w0 * per < p0 ? 1 : 0)};
+      if (from == w * per) a.start[w] = e;
+    }
+  }
+  // parts past the line's end are empty
+  for (int w = (line + per - 1) / per + threadIdx.x; w <= a.grid; w += 1024) a.start[w] = entries;
+  if (threadIdx.x == 0) {
+    a.header->n = entries;
+    a.header->per = per;
   }
 }
 
@@ -192,30 +314,113 @@ __device__ __forceinline__ int item_index(int r) {
   return r * gridDim.x + ((r & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
 }
 
-// The items this CTA takes, each read one ahead of its use.
+// The entries this CTA takes, each read one ahead of its use: in turn, or
+// those of its part of the line.
 struct Items {
   const PromptArgs& a;
-  int total, r = 0, head = 0, next_head = 0;
-  bool more;
   PromptItem it, ahead;
-  __device__ __forceinline__ Items(const PromptArgs& args, int n) : a(args), total(n) { fetch(); }
+  int entry = 0, next_entry = 0;     // of the list
+  int r = 0, first = 0, limit = 0;
+  bool more = false, parts = false;
+  int q0 = 0, nq = 0, k0 = 0, nk = 0;     // without a list: the sequence
+  __device__ __forceinline__ explicit Items(const PromptArgs& args) : a(args) {
+    if (a.header == nullptr) {
+      const bool okq = seq_range(a.p.cu_q, 0, a.p.Tq, &q0, &nq);
+      const bool okk = seq_range(a.p.cu_k, 0, a.p.Tk, &k0, &nk);
+      if (okq && okk)
+        limit = (nq + 2 * a.TB - 1) / (2 * a.TB) * a.p.Hkv;
+      else if (threadIdx.x == 0)
+        atomicOr(a.p.status, kStatusBadIndex);
+    } else {
+      parts = a.header->per > 0;
+      limit = parts ? a.start[blockIdx.x + 1] : a.header->n;
+      if (parts) first = a.start[blockIdx.x];
+    }
+    fetch();
+  }
   __device__ __forceinline__ void fetch() {
-    const int idx = item_index(r++);
-    more = idx < total;
-    if (more) {
-      const int i = idx / a.p.Hkv;
-      next_head = idx - i * a.p.Hkv;
-      ahead = a.items[i];
+    next_entry = parts ? first + r : item_index(r);
+    ++r;
+    more = next_entry < limit;
+    if (!more) return;
+    if (a.header != nullptr) {
+      ahead = a.list[next_entry];
+    } else {
+      // the last rows see most keys
+      const int k = next_entry / a.p.Hkv;
+      ahead = make_item(a.p, 2 * a.TB, q0, nq, k0, nk, limit / a.p.Hkv - 1 - k);
+      ahead.head = next_entry - k * a.p.Hkv;
     }
   }
   __device__ __forceinline__ bool next() {
     if (!more) return false;
     it = ahead;
-    head = next_head;
+    entry = next_entry;
     fetch();
     return true;
   }
 };
+
+// Joins a warp's 32 rows of an item from the parts that hold its blocks:
+// out = sum_i 2^(c (m_i - M)) O_i / sum_i 2^(c (m_i - M)) l_i.  A lane weighs
+// one row and sums four columns of each; 16 loads are in flight.
+template <int D>
+__device__ __forceinline__ void join_rows(const PromptArgs& a, const PromptPiece& piece, int row0,
+                                          float c, int h, int64_t dst, int64_t lse_at, bool valid) {
+  constexpr int kLPR = D / 4, kRPI = 32 / kLPR, kBatch = 16;
+  const PromptParams& p = a.p;
+  const int lane = threadIdx.x & 31;
+  const int w0 = piece.w0, w1 = piece.w1;
+  auto first_row = [&](int w) {
+    return static_cast<int64_t>(2 * w + (w == w0 ? piece.key & 1 : 0)) * kRowsPerItem + row0;
+  };
+  float m = -INFINITY, l = 0.f;
+  for (int w = w0; w <= w1; ++w) m = fmaxf(m, __ldcg(a.part_ml + first_row(w) + lane).x);
+  const float top = m == -INFINITY ? 0.f : m;
+  for (int w = w0; w <= w1; ++w) {
+    const float2 ml = __ldcg(a.part_ml + first_row(w) + lane);
+    l += ml.y * ex2((ml.x - top) * c);
+  }
+  const RowEnd end =
+      finish_row(m * p.scale, l, p.sinks != nullptr && valid ? p.sinks + h : nullptr);
+  if (p.lse != nullptr && valid) p.lse[lse_at] = end.lse;
+  const uint32_t stored = __ballot_sync(0xffffffffu, valid);
+  const int sub = lane / kLPR, col = 4 * (lane % kLPR);
+#pragma unroll 1
+  for (int r0 = 0; r0 < 32; r0 += kBatch * kRPI) {
+    float4 acc[kBatch];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+    for (int w = w0; w <= w1; ++w) {
+      const float g = ex2((__ldcg(a.part_ml + first_row(w) + lane).x - top) * c);
+      const float* src = a.part_o + (first_row(w) + r0 + sub) * D + col;
+      float4 v[kBatch];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k)
+        v[k] = __ldcg(reinterpret_cast<const float4*>(src + k * kRPI * D));
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const float f = __shfl_sync(0xffffffffu, g, r0 + k * kRPI + sub);
+        acc[k].x += v[k].x * f;
+        acc[k].y += v[k].y * f;
+        acc[k].z += v[k].z * f;
+        acc[k].w += v[k].w * f;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int rw = r0 + k * kRPI + sub;
+      const float f = __shfl_sync(0xffffffffu, end.factor, rw);
+      const bool none = __shfl_sync(0xffffffffu, end.none ? 1 : 0, rw) != 0;
+      const int64_t to = __shfl_sync(0xffffffffu, dst, rw);
+      if ((stored >> rw) & 1)
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + to + col) =
+            none ? make_uint2(0u, 0u)
+                 : make_uint2(bf16x2(acc[k].x * f, acc[k].y * f), bf16x2(acc[k].z * f, acc[k].w * f));
+    }
+  }
+}
 
 template <int D>
 __global__ void __launch_bounds__(kPromptThreads, 1)
@@ -277,7 +482,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   const uint32_t tmem = *tmem_slot;
   pdl_wait();
   pdl_launch_dependents();
-  const int total = *a.n_items * p.Hkv;
 
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
@@ -287,10 +491,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         uint32_t fill = 0, nq = 0;
         const uint32_t q_bytes = static_cast<uint32_t>(a.G * a.TB) * 128 * L::kChunks;
         bool ok = true;
-        Items items(a, total);
+        Items items(a);
         while (ok && items.next()) {
           const PromptItem& it = items.it;
-          const int hk = items.head;
+          const int hk = it.head & ~kPiece;
           if (it.kb1 <= it.kb0) continue;
           auto load_q = [&](int s) {
             if (!mbar_wait(&q_empty[s], (nq & 1) ^ 1, wc)) return false;
@@ -356,7 +560,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       auto wait_kv = [&](uint32_t fill) {
         return mbar_wait_warp(&kv_full[fill % ST], (fill / ST) & 1, wc);
       };
-      Items items(a, total);
+      Items items(a);
       while (items.next()) {
         const int n = items.it.kb1 - items.it.kb0;
         if (n <= 0) continue;
@@ -423,11 +627,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     const int tok = row / a.G, g = row - tok * a.G;
     const float c = p.scale * kLog2e;
     uint32_t ns = 0, no = 0, base = 0;
-    Items items(a, total);
+    Items items(a);
     while (items.next()) {
       const PromptItem& it = items.it;
       const int n = it.kb1 - it.kb0;
-      const int h = items.head * a.G + g;
+      const int h = (it.head & ~kPiece) * a.G + g;
       const int i = s * a.TB + tok;
       const bool valid = tok < a.TB && i < it.ntok;
       // visible keys [lo, hi) of this row, and those every row of the warp sees;
@@ -532,20 +736,61 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         l += s0 + s1;
       }
       base += n > 0 ? 2 * n : 0;
+      const int64_t tokr = it.q_row + i;
+      const int64_t dst = tokr * p.o_t + static_cast<int64_t>(h) * p.o_h;
+      uint8_t* stage = sOut + warp * (32 * 128);
+      const RowEnd row_end =
+          finish_row(m * p.scale, l, p.sinks != nullptr && valid ? p.sinks + h : nullptr);
       if (n > 0) {
         if (!mbar_wait_warp(&o_full[s], no & 1, wc)) goto softmax_done;
         ++no;
         tc_fence_after();
       }
-      const RowEnd end =
-          finish_row(m * p.scale, l, p.sinks != nullptr && valid ? p.sinks + h : nullptr);
-      const float inv = end.factor;
-      const bool none = end.none;
+      if (it.head & kPiece) {
+        const PromptPiece piece = a.pieces[items.entry];
+        // a piece: its reference, sum and unscaled output, 32 columns at a time
+        const int64_t first = static_cast<int64_t>(piece.slot) * kRowsPerItem + warp * 32;
+        a.part_ml[first + lane] = make_float2(m, l);
+        for (int d0 = 0; d0 < D; d0 += 32) {
+          float o[32];
+          tmem_ld32(tO + d0, o);
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            *reinterpret_cast<float4*>(stage + lane * 128 + ((e ^ (lane & 7)) << 4)) =
+                make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+          __syncwarp();
+          const int sub = lane >> 3, ch = lane & 7;
+          float4 w[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            w[e] = *reinterpret_cast<const float4*>(stage + (4 * e + sub) * 128 +
+                                                    ((ch ^ ((4 * e + sub) & 7)) << 4));
+          __syncwarp();
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            *reinterpret_cast<float4*>(a.part_o + (first + 4 * e + sub) * D + d0 + 4 * ch) = w[e];
+        }
+        tc_fence_before();
+        // the last of the item's pieces joins them
+        __threadfence();
+        __syncwarp();
+        int last = 0;
+        if (lane == 0)
+          last = atomicAdd(a.done + (piece.key >> 1) * 8 + warp, 1) == piece.w1 - piece.w0;
+        if (__shfl_sync(0xffffffffu, last, 0)) {
+          __threadfence();
+          join_rows<D>(a, piece, warp * 32, c, h, dst, tokr * p.Hq + h, valid);
+        }
+        continue;
+      }
       // through shared memory, so that 8 lanes write 128 adjacent bytes of a row
-      const int64_t tokr = it.q_row + i;
-      const int64_t dst = tokr * p.o_t + static_cast<int64_t>(h) * p.o_h;
       const uint32_t stored = __ballot_sync(0xffffffffu, valid);
-      uint8_t* stage = sOut + warp * (32 * 128);
+      const int sub = lane >> 3, ch = lane & 7;
+      int64_t to[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        to[e] = __shfl_sync(0xffffffffu, dst, 4 * e + sub) + 8 * ch;
+#pragma unroll
       for (int d0 = 0; d0 < D; d0 += 64) {
         float o[64];
         if (n > 0) {
@@ -554,28 +799,30 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
 #pragma unroll
           for (int e = 0; e < 64; ++e) o[e] = 0.f;
         }
+        const float f = row_end.factor;
+        uint4 w[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          uint32_t w[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            w[k] = none ? 0u : bf16x2(o[8 * e + 2 * k] * inv, o[8 * e + 2 * k + 1] * inv);
-          *reinterpret_cast<uint4*>(stage + lane * 128 + ((e ^ (lane & 7)) << 4)) =
-              make_uint4(w[0], w[1], w[2], w[3]);
+          const float* v = o + 8 * e;
+          w[e] = row_end.none ? make_uint4(0u, 0u, 0u, 0u)
+                              : make_uint4(bf16x2(v[0] * f, v[1] * f), bf16x2(v[2] * f, v[3] * f),
+                                           bf16x2(v[4] * f, v[5] * f), bf16x2(v[6] * f, v[7] * f));
         }
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          *reinterpret_cast<uint4*>(stage + lane * 128 + ((e ^ (lane & 7)) << 4)) = w[e];
         __syncwarp();
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int rw = 4 * e + (lane >> 3), ch = lane & 7;
-          const uint4 w = *reinterpret_cast<const uint4*>(stage + rw * 128 + ((ch ^ (rw & 7)) << 4));
-          const int64_t to = __shfl_sync(0xffffffffu, dst, rw);
-          if ((stored >> rw) & 1)
-            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + to + d0 + 8 * ch) = w;
-        }
+        for (int e = 0; e < 8; ++e)
+          w[e] = *reinterpret_cast<const uint4*>(stage + (4 * e + sub) * 128 +
+                                                 ((ch ^ ((4 * e + sub) & 7)) << 4));
         __syncwarp();
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if ((stored >> (4 * e + sub)) & 1)
+            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + to[e] + d0) = w[e];
       }
-      if (p.lse != nullptr && valid)
-        p.lse[tokr * p.Hq + h] = end.lse;
+      if (p.lse != nullptr && valid) p.lse[tokr * p.Hq + h] = row_end.lse;
       tc_fence_before();
     }
   softmax_done:;
@@ -596,8 +843,40 @@ int64_t max_items(int64_t Tq, int64_t B, int Hq, int Hkv) {
   return Tq / per + (B < Tq ? B : Tq) + 1;
 }
 
+size_t round256(size_t n) { return (n + 255) / 256 * 256; }
+
+struct PromptSpace {
+  size_t list, items, pieces, start, done, ml, o, total;   // offsets
+  bool split;
+};
+PromptSpace prompt_space(int64_t Tq, int64_t B, int Hq, int Hkv, int D, int num_sms) {
+  const size_t items = static_cast<size_t>(max_items(Tq, B, Hq, Hkv)), n = items * Hkv;
+  PromptSpace s;
+  s.split = n <= static_cast<size_t>(kMaxSplitItems) * num_sms;
+  size_t at = 256;
+  auto take = [&](size_t bytes) {
+    const size_t here = at;
+    at += round256(bytes);
+    return here;
+  };
+  // every part's end may cut an item
+  s.list = take((n + (s.split ? num_sms : 0)) * sizeof(PromptItem));
+  s.items = s.pieces = s.start = s.done = s.ml = s.o = at;
+  if (s.split) {
+    s.items = take(items * sizeof(PromptItem));
+    s.pieces = take((n + num_sms) * sizeof(PromptPiece));
+    s.start = take((num_sms + 1) * sizeof(int));
+    s.done = take(n * 8 * sizeof(int));
+    const size_t rows = static_cast<size_t>(num_sms) * 2 * kRowsPerItem;
+    s.ml = take(rows * sizeof(float2));
+    s.o = take(rows * D * sizeof(float));
+  }
+  s.total = at;
+  return s;
+}
+
 template <int D>
-cudaError_t launch(const PromptMaps& maps, const PromptArgs& a, int grid, cudaStream_t stream) {
+cudaError_t launch(const PromptMaps& maps, const PromptArgs& a, cudaStream_t stream) {
   const int smem = PromptLayout<D>::kSmem + 1024;
   static bool configured[64] = {};
   int dev = 0;
@@ -608,24 +887,46 @@ cudaError_t launch(const PromptMaps& maps, const PromptArgs& a, int grid, cudaSt
     if (e != cudaSuccess) return e;
     configured[dev] = true;
   }
-  return launch_k(prompt_kernel<D>, dim3(grid), dim3(kPromptThreads), static_cast<size_t>(smem),
+  return launch_k(prompt_kernel<D>, dim3(a.grid), dim3(kPromptThreads), static_cast<size_t>(smem),
                   stream, maps, a);
 }
 
 }  // namespace
 
-size_t prompt_workspace_bytes(int64_t Tq, int64_t B, int Hq, int Hkv, int, int) {
-  return 256 + static_cast<size_t>(max_items(Tq, B, Hq, Hkv)) * sizeof(PromptItem);
+size_t prompt_workspace_bytes(int64_t Tq, int64_t B, int Hq, int Hkv, int D, int num_sms) {
+  return prompt_space(Tq, B, Hq, Hkv, D, num_sms).total;
 }
 
 cudaError_t launch_prompt(const PromptParams& p, int num_sms, cudaStream_t stream,
                           std::string* err) {
+  const PromptSpace space = prompt_space(p.Tq, p.B, p.Hq, p.Hkv, p.D, num_sms);
+  char* ws = static_cast<char*>(p.workspace);
   PromptArgs a = {};
   a.p = p;
   a.G = p.Hq / p.Hkv;
   a.TB = tokens_per_tile(p.Hq, p.Hkv);
-  a.n_items = static_cast<const int*>(p.workspace);
-  a.items = reinterpret_cast<const PromptItem*>(static_cast<const char*>(p.workspace) + 256);
+  const int64_t most = max_items(p.Tq, p.B, p.Hq, p.Hkv);
+  a.cap = static_cast<int>(most);
+  // Splitting: no sequence has more keys than there are, so there is nothing to
+  // split below kMinSplit blocks; the line's length stays below 2^31 (at most kMaxSplitItems
+  // pairs per SM).  One causal sequence with two items per SM or more has none longer
+  // than a CTA's share.
+  const bool keys_long = p.Tk > kMinSplit * kBM && p.Tk <= (1 << 26);
+  const bool alone = p.B == 1 && (!keys_long || most * p.Hkv >= 2 * num_sms);
+  const bool split = space.split && keys_long && !alone;
+  if (!alone) {
+    a.header = reinterpret_cast<PromptHeader*>(ws);
+    a.list = reinterpret_cast<PromptItem*>(ws + space.list);
+  }
+  if (split) {
+    a.items = reinterpret_cast<PromptItem*>(ws + space.items);
+    a.pieces = reinterpret_cast<PromptPiece*>(ws + space.pieces);
+    a.start = reinterpret_cast<int*>(ws + space.start);
+    a.done = reinterpret_cast<int*>(ws + space.done);
+    a.part_ml = reinterpret_cast<float2*>(ws + space.ml);
+    a.part_o = reinterpret_cast<float*>(ws + space.o);
+  }
+  a.grid = split || most * p.Hkv > num_sms ? num_sms : static_cast<int>(most * p.Hkv);
   a.budget_ns = static_cast<unsigned long long>(option(MXQ_OPT_WAIT_BUDGET_NS));
   a.inject_stall = static_cast<int>(option(MXQ_OPT_INJECT_STALL));
   // [n, heads, D] as (D, heads, n); a dimension of one takes any legal stride
@@ -646,14 +947,11 @@ cudaError_t launch_prompt(const PromptParams& p, int num_sms, cudaStream_t strea
       !map3(&maps.k, keys ? p.k : p.q, p.Hkv, keys ? p.Tk : 1, p.k_t, keys ? p.k_h : p.D, 1, kBM) ||
       !map3(&maps.v, keys ? p.v : p.q, p.Hkv, keys ? p.Tk : 1, p.v_t, keys ? p.v_h : p.D, 1, kBM))
     return cudaErrorInvalidValue;
-  const cudaError_t e =
-      launch_k(prompt_plan_kernel, dim3(1), dim3(1024), 0, stream, p, 2 * a.TB,
-               static_cast<int*>(p.workspace), const_cast<PromptItem*>(a.items),
-               static_cast<int>(max_items(p.Tq, p.B, p.Hq, p.Hkv)));
-  if (e != cudaSuccess) return e;
-  const int64_t most = max_items(p.Tq, p.B, p.Hq, p.Hkv) * p.Hkv;
-  const int grid = static_cast<int>(most < num_sms ? most : num_sms);
-  return p.D == 128 ? launch<128>(maps, a, grid, stream) : launch<64>(maps, a, grid, stream);
+  if (!alone) {
+    const cudaError_t e = launch_k(prompt_plan_kernel, dim3(1), dim3(1024), 0, stream, a);
+    if (e != cudaSuccess) return e;
+  }
+  return p.D == 128 ? launch<128>(maps, a, stream) : launch<64>(maps, a, stream);
 }
 
 }  // namespace mxq

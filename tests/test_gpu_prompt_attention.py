@@ -98,6 +98,17 @@ def test_long():
     check([40], [20000], 8, 2, 128, seed=11)
 
 
+@pytest.mark.parametrize("nq,nk,H,KV,D,window", [
+    ([5], [1025], 2, 1, 128, 0), ([64], [1153], 8, 8, 64, 0), ([300, 9], [5000, 2111], 8, 2, 128, 0),
+    ([1, 1, 0, 7], [3000, 129, 50, 4001], 6, 2, 64, 0), ([30], [6000], 4, 1, 64, 3000),
+    ([700], [3500], 3, 1, 128, 0), ([16, 16], [0, 9000], 128, 1, 64, 0)])
+@pytest.mark.parametrize("sinks", [False, True])
+def test_few_rows_many_keys(nq, nk, H, KV, D, window, sinks):
+    """The keys of one item go to several CTAs and are joined."""
+    check(nq, nk, H, KV, D, window=window, sinks=sinks, seed=20)
+    check(nq, nk, H, KV, D, causal=False, sinks=sinks, seed=21)
+
+
 def test_many_sequences():
     lens = [(i * 37) % 90 for i in range(150)]
     check(lens, lens, 4, 2, 64, seed=12)
