@@ -78,7 +78,7 @@ struct __align__(16) PromptPiece {
 };
 
 // What the plan leaves at the head of the workspace.
-struct PromptHeader {
+struct __align__(8) PromptHeader {
   int n;                             // entries of the list
   int per;                           // blocks of a part; 0: whole items
 };
@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(1024) prompt_plan_kernel(const PromptArgs a) {
   const PromptParams& p = a.p;
   const int tokens_per_item = 2 * a.TB;
   __shared__ int count[kBuckets];
-  __shared__ int n_items, sums[32], longest, all_blocks;
+  __shared__ int sums[32], longest, all_blocks;
   pdl_wait();
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -171,6 +171,7 @@ __global__ void __launch_bounds__(1024) prompt_plan_kernel(const PromptArgs a) {
   if (threadIdx.x == 0) longest = all_blocks = 0;
   __syncthreads();
   bool split = false;
+  int n_items = 0;
   for (int pass = 0; pass < 2; ++pass) {
     for (int b = warp; b < p.B; b += 32) {
       int q0, nq, k0, nk;
@@ -204,30 +205,18 @@ __global__ void __launch_bounds__(1024) prompt_plan_kernel(const PromptArgs a) {
     }
     __syncthreads();
     if (pass == 0) {
-      // exclusive prefix sum over the buckets, by one warp
-      if (warp == 0) {
-        int run = 0;
-        for (int i = 0; i < kBuckets; i += 32) {
-          const int c = count[i + lane];
-          int x = c;
-#pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, x, o);
-            if (lane >= o) x += y;
-          }
-          count[i + lane] = run + x - c;
-          run += __shfl_sync(0xffffffffu, x, 31);
-        }
+      int run;
+      const int c = threadIdx.x < kBuckets ? count[threadIdx.x] : 0;
+      const int at = block_scan(c, sums, &run);
+      if (threadIdx.x < kBuckets) count[threadIdx.x] = at;
+      n_items = min(run, a.cap);
+      if (threadIdx.x == 0) {
         // only offsets that run backwards give more items than there is room for
-        if (lane == 0) {
-          if (run > a.cap) atomicOr(p.status, kStatusBadIndex);
-          n_items = min(run, a.cap);
-          a.header->n = n_items * p.Hkv;
-          a.header->per = 0;
-        }
+        if (run > a.cap) atomicOr(p.status, kStatusBadIndex);
+        *a.header = {n_items * p.Hkv, 0};
       }
       __syncthreads();
-      split = a.items != nullptr && longest > kMinSplit &&
+      split = a.items != nullptr && run <= a.cap && longest > kMinSplit &&
               longest > (all_blocks * p.Hkv + a.grid - 1) / a.grid;
     }
   }
@@ -267,10 +256,7 @@ __global__ void __launch_bounds__(1024) prompt_plan_kernel(const PromptArgs a) {
   }
   // parts past the line's end are empty
   for (int w = (line + per - 1) / per + threadIdx.x; w <= a.grid; w += 1024) a.start[w] = entries;
-  if (threadIdx.x == 0) {
-    a.header->n = entries;
-    a.header->per = per;
-  }
+  if (threadIdx.x == 0) *a.header = {entries, per};
 }
 
 template <int D>
@@ -332,9 +318,20 @@ struct Items {
       else if (threadIdx.x == 0)
         atomicOr(a.p.status, kStatusBadIndex);
     } else {
-      parts = a.header->per > 0;
-      limit = parts ? a.start[blockIdx.x + 1] : a.header->n;
-      if (parts) first = a.start[blockIdx.x];
+      // the first whole item's entry is read along with the header
+      const PromptItem guess = a.list[blockIdx.x];
+      const PromptHeader head = *a.header;
+      limit = head.n;
+      parts = head.per > 0;
+      if (!parts) {
+        r = 1;
+        next_entry = blockIdx.x;
+        more = next_entry < limit;
+        ahead = guess;
+        return;
+      }
+      first = a.start[blockIdx.x];
+      limit = a.start[blockIdx.x + 1];
     }
     fetch();
   }
