@@ -12,7 +12,8 @@
 // running maximum, sum and accumulators, no block-wide barrier.  A
 // unit that lies inside one part is written out by its warp; the others
 // leave at most two partial results per warp in the workspace, which
-// a second kernel joins in a fixed order.
+// a second kernel joins in a fixed order.  A part's end that falls into a short
+// unit moves to the nearer end of it: splitting a few steps costs more than it balances.
 //
 // Arithmetic.  The G query heads of a key/value head are the rows of 16-row
 // tensor-core products (mma.sync m16n8k16: with at most 16 rows per 64 KB of
@@ -44,12 +45,14 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kEntries = 2048;      // entries of the shared prefix table
 constexpr int kRows = 16;           // rows of a product
+constexpr int kWhole = 8;           // units of at most this many steps stay whole
 
 struct DecodeArgs {
   DecodeParams p;
   int G, tiles, rows;               // query heads per kv head, units per kv head, rows stored
   int chunk, entries;               // sequences per entry of the prefix table, its entries
   int min_steps;
+  bool alike;                       // both caches have the same page and token strides
   int64_t* cum;                     // workspace: steps before each sequence [B + 1], then `per`
   float2* part_ml;                  // [warps][2][rows]
   float* part_o;                    // [warps][2][rows][D]
@@ -122,11 +125,11 @@ __device__ __forceinline__ void mma16816(float* d, const uint32_t* a, uint32_t b
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// two e4m3 (low 16 bits) -> f16x2
-__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t x) {
-  uint32_t r;
-  asm("{ .reg .b16 t; cvt.u16.u32 t, %1; cvt.rn.f16x2.e4m3x2 %0, t; }" : "=r"(r) : "r"(x));
-  return r;
+// four e4m3 -> two f16x2
+__device__ __forceinline__ void e4m3x4_f16(uint32_t x, uint32_t* lo, uint32_t* hi) {
+  asm("{ .reg .b16 a, b; mov.b32 {a, b}, %2; cvt.rn.f16x2.e4m3x2 %0, a; cvt.rn.f16x2.e4m3x2 %1, b; }"
+      : "=r"(*lo), "=r"(*hi)
+      : "r"(x));
 }
 
 // 16 bytes to shared memory, zeros if !valid (the source is not read then)
@@ -146,6 +149,12 @@ struct Cursor {
   int b, head, step;                // head: key/value head * tiles + tile
   SeqRange s;
 };
+
+// a / b for a >= 0, b > 0: 64-bit division only where it is needed
+__device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
 
 template <int KS>
 __device__ __forceinline__ void advance(Cursor& c, const DecodeArgs& a) {
@@ -201,7 +210,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) decode_kernel(const DecodeArgs
   }
   const int heads = p.Hkv * a.tiles;
   const int64_t workers = static_cast<int64_t>(gridDim.x) * kWarps;
-  int64_t per = (total * heads + workers - 1) / workers;
+  int64_t per = divide(total * heads + workers - 1, workers);
   if (per < a.min_steps) per = a.min_steps;
   for (int e = e0; e < min(a.entries, e0 + per_thread); ++e) {
     table[e] = before;
@@ -221,28 +230,42 @@ __global__ void __launch_bounds__(32 * kWarps, 1) decode_kernel(const DecodeArgs
 
   // ---- this warp's part; few parts are spread over the SMs
   const int64_t worker = static_cast<int64_t>(warp) * gridDim.x + blockIdx.x;
-  const int64_t s0 = worker * per;
-  const int64_t s1 = min(s0 + per, total * heads);
-  if (s0 >= s1) return;
-  Cursor in;                                           // of the copies
-  {
-    int lo = 0, hi = a.entries - 1;                    // the last entry at or before s0
+  const int64_t raw0 = worker * per;
+  if (raw0 >= total * heads) return;
+  // the part's end `pos` on the line, moved out of a short unit, and where that is
+  auto locate = [&](int64_t pos, Cursor* c) {
+    if (pos >= total * heads) return total * heads;
+    int lo = 0, hi = a.entries - 1;                    // the last entry at or before pos
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (table[mid] * heads <= s0) lo = mid;
+      if (table[mid] * heads <= pos) lo = mid;
       else hi = mid - 1;
     }
     bool bad;
     int64_t at = table[lo] * heads;
-    in.b = lo * a.chunk;
-    in.s = seq_steps<KS>(p, in.b, &bad);
-    while (at + static_cast<int64_t>(in.s.steps) * heads <= s0) {
-      at += static_cast<int64_t>(in.s.steps) * heads;
-      in.s = seq_steps<KS>(p, ++in.b, &bad);
+    c->b = lo * a.chunk;
+    c->s = seq_steps<KS>(p, c->b, &bad);
+    while (at + static_cast<int64_t>(c->s.steps) * heads <= pos) {
+      at += static_cast<int64_t>(c->s.steps) * heads;
+      c->s = seq_steps<KS>(p, ++c->b, &bad);
     }
-    in.head = static_cast<int>((s0 - at) / in.s.steps);
-    in.step = static_cast<int>((s0 - at) - static_cast<int64_t>(in.head) * in.s.steps);
-  }
+    const int n = c->s.steps;
+    c->head = static_cast<int>(divide(pos - at, n));
+    c->step = static_cast<int>((pos - at) - static_cast<int64_t>(c->head) * n);
+    if (n <= kWhole && c->step > 0) {
+      pos -= c->step;
+      const bool up = 2 * c->step >= n;
+      c->step = up ? n - 1 : 0;
+      if (up) {
+        pos += n;
+        advance<KS>(*c, a);
+      }
+    }
+    return pos;
+  };
+  Cursor in, end;                                      // of the copies
+  const int64_t s0 = locate(raw0, &in), s1 = locate(raw0 + per, &end);
+  if (s0 >= s1) return;
   Cursor at = in;                                      // of the arithmetic
 
   const uint32_t ring = smem_u32(smem) + warp * ST * 2 * S::kTile;
@@ -279,15 +302,26 @@ __global__ void __launch_bounds__(32 * kWarps, 1) decode_kernel(const DecodeArgs
       const char* kb = static_cast<const char*>(p.k_cache) + (hk * p.ck_h) * es + ch_in * 16;
       const char* vb = static_cast<const char*>(p.v_cache) + (hk * p.cv_h) * es + ch_in * 16;
       const uint32_t dst = ring + st * 2 * S::kTile;
+      // the lane's key's row, in both caches if they are laid out alike
+      const int64_t ko = (page * p.ck_p + off * p.ck_t) * es;
+      if (a.alike) {
 #pragma unroll
-      for (int i = 0; i < KS / kRPI; ++i) {
-        const int r = i * kRPI + row_in;
-        const int64_t pg = __shfl_sync(0xffffffffu, page, r);
-        const int64_t of = __shfl_sync(0xffffffffu, off, r);
-        const bool v = (mask >> r) & 1;
-        const uint32_t d = dst + tile_off<ROWB>(r, ch_in);
-        cp16(d, kb + (pg * p.ck_p + of * p.ck_t) * es, v);
-        cp16(d + S::kTile, vb + (pg * p.cv_p + of * p.cv_t) * es, v);
+        for (int i = 0; i < KS / kRPI; ++i) {
+          const int r = i * kRPI + row_in;
+          const int64_t from = __shfl_sync(0xffffffffu, ko, r);
+          const uint32_t d = dst + tile_off<ROWB>(r, ch_in);
+          cp16(d, kb + from, (mask >> r) & 1);
+          cp16(d + S::kTile, vb + from, (mask >> r) & 1);
+        }
+      } else {
+        const int64_t vo = (page * p.cv_p + off * p.cv_t) * es;
+#pragma unroll
+        for (int i = 0; i < KS / kRPI; ++i) {
+          const int r = i * kRPI + row_in;
+          const uint32_t d = dst + tile_off<ROWB>(r, ch_in);
+          cp16(d, kb + __shfl_sync(0xffffffffu, ko, r), (mask >> r) & 1);
+          cp16(d + S::kTile, vb + __shfl_sync(0xffffffffu, vo, r), (mask >> r) & 1);
+        }
       }
       ++fill;
       if (--left > 0) {
@@ -338,7 +372,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) decode_kernel(const DecodeArgs
           big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
           // the power of two that brings the largest to [2^14, 2^15)
           const int e = big > 0.f && big < INFINITY ? min(max(14 - ilogbf(big), -100), 100) : 0;
-          const float up = ldexpf(1.f, e);
+          const float up = copysignf(ldexpf(1.f, e), ks);
           unscale = ldexpf(1.f, -e);
 #pragma unroll
           for (int k = 0; k < D / 16; ++k) {
@@ -357,7 +391,9 @@ __global__ void __launch_bounds__(32 * kWarps, 1) decode_kernel(const DecodeArgs
                   in_group ? __ldg(reinterpret_cast<const uint32_t*>(q + 16 * k + 8 * i + 2 * quad))
                            : 0u;
         }
-        cs[half] = p.scale * ks * kLog2e * unscale;
+        // > 0: the sign of a key scale goes into q, and a scale of 0 counts as next to
+        // nothing, so that it keeps a masked key's -inf
+        cs[half] = fmaxf(p.scale * fabsf(ks) * kLog2e * unscale, 1e-30f);
         m[half] = -INFINITY;
         l[half] = 0.f;
       }
@@ -379,50 +415,54 @@ __global__ void __launch_bounds__(32 * kWarps, 1) decode_kernel(const DecodeArgs
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int i = 0; i < 4; ++i) x[n][i] = 0.f;
+    // (elements outside, keys inside: the products that follow one another are independent)
 #pragma unroll
-    for (int n = 0; n < NT; n += 2) {
-      if constexpr (FP8) {
-        // matrices: keys 8n.. and 8(n+1).. of chunk k (16 elements), then of k + 1
-        const int r = 8 * n + (lane & 15);
+    for (int k = 0; k < D / 16; k += FP8 ? 2 : 1) {
 #pragma unroll
-        for (int k = 0; k < D / 16; k += 2) {
-          uint32_t f[4];
-          ldsm4(kt + tile_off<ROWB>(r, k + (lane >> 4)), f);
+      for (int n = 0; n < NT; n += 2) {
+        uint32_t f[4];
+        if constexpr (FP8) {
+          // matrices: keys 8n.. and 8(n+1).. of chunk k (16 elements), then of k + 1
+          ldsm4(kt + tile_off<ROWB>(8 * n + (lane & 15), k + (lane >> 4)), f);
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            mma16816<true>(x[n + (i & 1)], qf[k + (i >> 1)], e4m3x2_f16x2(f[i]),
-                           e4m3x2_f16x2(f[i] >> 16));
-        }
-      } else {
-        // matrices: (keys 8n.., chunks 2k and 2k + 1), (keys 8(n+1).., the same)
-        const int r = 8 * n + ((lane >> 4) << 3) + (lane & 7);
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          uint32_t f[4];
-          ldsm4(kt + tile_off<ROWB>(r, 2 * k + ((lane >> 3) & 1)), f);
+          for (int i = 0; i < 4; ++i) {
+            uint32_t b0, b1;
+            e4m3x4_f16(f[i], &b0, &b1);
+            mma16816<true>(x[n + (i & 1)], qf[k + (i >> 1)], b0, b1);
+          }
+        } else {
+          // matrices: (keys 8n.., chunks 2k and 2k + 1), (keys 8(n+1).., the same)
+          ldsm4(kt + tile_off<ROWB>(8 * n + ((lane >> 4) << 3) + (lane & 7),
+                                    2 * k + ((lane >> 3) & 1)), f);
           mma16816<false>(x[n], qf[k], f[0], f[1]);
           mma16816<false>(x[n + 1], qf[k], f[2], f[3]);
         }
       }
     }
 
-    // ---- weights
+    // ---- weights, relative to the reference m (of the unscaled scores)
+    constexpr uint32_t kAll = KS == 32 ? 0xffffffffu : (1u << KS) - 1;
+    if (mask != kAll) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (!((mask >> (8 * n + 2 * quad + (i & 1))) & 1)) x[n][i] = -INFINITY;
+    }
     float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const bool vis = (mask >> (8 * n + 2 * quad + (i & 1))) & 1;
-        x[n][i] = vis ? x[n][i] * cs[i >> 1] : -INFINITY;
-        mx[i >> 1] = fmaxf(mx[i >> 1], x[n][i]);
-      }
-    if (__any_sync(0xffffffffu, mx[0] > m[0] + 8.f || mx[1] > m[1] + 8.f)) {
+      for (int h = 0; h < 2; ++h) mx[h] = fmaxf(mx[h], fmaxf(x[n][2 * h], x[n][2 * h + 1]));
+    if (__any_sync(0xffffffffu, (mx[0] - m[0]) * cs[0] > 8.f || (mx[1] - m[1]) * cs[1] > 8.f ||
+                                    (m[0] == -INFINITY && mx[0] > m[0]) ||
+                                    (m[1] == -INFINITY && mx[1] > m[1]))) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
         mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
         const float n = fmaxf(m[h], mx[h]);
-        const float f = m[h] == -INFINITY ? 0.f : ex2(m[h] - n);
+        const float f = m[h] == -INFINITY ? 0.f : ex2((m[h] - n) * cs[h]);
         m[h] = n;
         l[h] *= f;
 #pragma unroll
@@ -432,13 +472,14 @@ __global__ void __launch_bounds__(32 * kWarps, 1) decode_kernel(const DecodeArgs
         }
       }
     }
-    const float ref[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
+    const float ref[2] = {m[0] == -INFINITY ? 0.f : m[0] * cs[0],
+                          m[1] == -INFINITY ? 0.f : m[1] * cs[1]};
     uint32_t pf[KS / 16][4];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        x[n][i] = ex2(x[n][i] - ref[i >> 1]);
+        x[n][i] = ex2(fmaf(x[n][i], cs[i >> 1], -ref[i >> 1]));
         l[i >> 1] += x[n][i];
       }
 #pragma unroll
@@ -462,11 +503,11 @@ __global__ void __launch_bounds__(32 * kWarps, 1) decode_kernel(const DecodeArgs
           if constexpr (FP8) {
             // a register holds keys 2q, 2q + 1 of two elements: even elements
             // make one output tile, odd ones the next
-            const uint32_t b0 = __byte_perm(f[2 * i], 0, 0x3120);
-            const uint32_t b1 = __byte_perm(f[2 * i + 1], 0, 0x3120);
-            mma16816<true>(o[2 * (c + i)], pf[kk], e4m3x2_f16x2(b0), e4m3x2_f16x2(b1));
-            mma16816<true>(o[2 * (c + i) + 1], pf[kk], e4m3x2_f16x2(b0 >> 16),
-                           e4m3x2_f16x2(b1 >> 16));
+            uint32_t e0, o0, e1, o1;
+            e4m3x4_f16(__byte_perm(f[2 * i], 0, 0x3120), &e0, &o0);
+            e4m3x4_f16(__byte_perm(f[2 * i + 1], 0, 0x3120), &e1, &o1);
+            mma16816<true>(o[2 * (c + i)], pf[kk], e0, e1);
+            mma16816<true>(o[2 * (c + i) + 1], pf[kk], o0, o1);
           } else {
             mma16816<false>(o[c + i], pf[kk], f[2 * i], f[2 * i + 1]);
           }
@@ -486,9 +527,10 @@ __global__ void __launch_bounds__(32 * kWarps, 1) decode_kernel(const DecodeArgs
       l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
       const int gl = r0 + 8 * h, gr = tile * kRows + gl;
       if (gr >= a.G) continue;
+      const float top = m[h] == -INFINITY ? m[h] : m[h] * cs[h];
       if (opened && closed) {
         const int hq = hk * a.G + gr;
-        const RowEnd end = finish_row(m[h] * kLn2, l[h], p.sinks ? p.sinks + hq : nullptr);
+        const RowEnd end = finish_row(top * kLn2, l[h], p.sinks ? p.sinks + hq : nullptr);
         const float f = end.factor * (p.v_scale != nullptr ? __ldg(p.v_scale + hk) : 1.f);
         __nv_bfloat16* dst =
             static_cast<__nv_bfloat16*>(p.out) + at.b * p.o_b + static_cast<int64_t>(hq) * p.o_h;
@@ -508,9 +550,9 @@ __global__ void __launch_bounds__(32 * kWarps, 1) decode_kernel(const DecodeArgs
         if (p.lse != nullptr && quad == 0)
           p.lse[static_cast<int64_t>(at.b) * p.Hq + hq] = end.lse;
       } else {
-        // the first unit of a part goes to its slot 0, the last to slot 1
-        const int64_t slot = (worker * 2 + (opened && s0 != s - at.step ? 1 : 0)) * a.rows + gl;
-        if (quad == 0) a.part_ml[slot] = make_float2(m[h], l[h]);
+        // a unit that begins after the part's (unmoved) begin goes to slot 1
+        const int64_t slot = (worker * 2 + (opened && raw0 < s - at.step ? 1 : 0)) * a.rows + gl;
+        if (quad == 0) a.part_ml[slot] = make_float2(top, l[h]);
         float* dst = a.part_o + slot * D;
 #pragma unroll
         for (int t = 0; t < DT; t += 2) {
@@ -532,63 +574,128 @@ __global__ void __launch_bounds__(32 * kWarps, 1) decode_kernel(const DecodeArgs
   cp_wait<0>();
 }
 
-// Joins the partial results of one row of a unit that several parts share, in the parts'
-// order: out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i.
+// Joins the partial results of the rows of units that several parts share, in the parts'
+// order: out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i.  A warp takes a row,
+// reading eight parts at a time; a row of more than 32 parts is shared by the
+// block's eight warps.
 template <int D>
-__global__ void __launch_bounds__(32 * kWarps) decode_join_kernel(const DecodeArgs a) {
-  constexpr int N = D / 32;
-  const DecodeParams& p = a.p;
-  __shared__ float so[kWarps][D];
-  __shared__ float sm[kWarps], sl[kWarps];
-  pdl_wait();
-  pdl_launch_dependents();
-  const int b = blockIdx.y, head = blockIdx.x / a.rows, row = blockIdx.x - head * a.rows;
-  const int hk = head / a.tiles, gr = (head - hk * a.tiles) * kRows + row;
-  if (gr >= a.G) return;
-  const int64_t per = a.cum[p.B + 1];
-  const int64_t steps = a.cum[b + 1] - a.cum[b];
-  const int64_t u0 = a.cum[b] * (p.Hkv * a.tiles) + head * steps, u1 = u0 + steps;
-  const int64_t w0 = u0 / per, w1 = (u1 - 1) / per;
-  if (w0 == w1) return;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+struct JoinRow {
+  static constexpr int N = D / 32;
   float m = -INFINITY, l = 0.f, o[N] = {};
-  for (int64_t w = w0 + warp; w <= w1; w += kWarps) {
-    const int64_t slot = (w * 2 + (w * per < u0 ? 1 : 0)) * a.rows + row;
-    const float2 ml = a.part_ml[slot];
-    float v[N];
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = a.part_o[slot * D + lane + 32 * i];
-    const float n = fmaxf(m, ml.x);
-    if (n == -INFINITY) continue;
-    const float f = ex2(m - n), g = ex2(ml.x - n);
-    l = l * f + ml.y * g;
+  __device__ __forceinline__ void add(float pm, float pl, const float* v) {
+    const float n = fmaxf(m, pm);
+    if (n == -INFINITY) return;
+    const float f = ex2(m - n), g = ex2(pm - n);
+    l = l * f + pl * g;
 #pragma unroll
     for (int i = 0; i < N; ++i) o[i] = o[i] * f + v[i] * g;
     m = n;
   }
-  if (lane == 0) sm[warp] = m, sl[warp] = l;
+  // parts w, w + stride, ... up to w1 of the unit that begins at u0
+  __device__ __forceinline__ void read(const DecodeArgs& a, int64_t w, int64_t w1, int stride,
+                                       int64_t per, int64_t u0, int row, int lane) {
+    constexpr int U = 8;
+    for (; w <= w1; w += U * stride) {
+      float2 ml[U];
+      float v[U][N];
 #pragma unroll
-  for (int i = 0; i < N; ++i) so[warp][lane + 32 * i] = o[i];
-  __syncthreads();
-  const int d = threadIdx.x;
-  if (d >= D) return;
-  float top = -INFINITY, sum = 0.f, acc = 0.f;
+      for (int u = 0; u < U; ++u) {
+        const int64_t k = w + u * stride;
+        ml[u] = make_float2(-INFINITY, 0.f);
+        if (k > w1) continue;
+        const int64_t slot = (k * 2 + (k * per < u0 ? 1 : 0)) * a.rows + row;
+        ml[u] = a.part_ml[slot];
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sm[w]);
-  if (top > -INFINITY) {
+        for (int i = 0; i < N; ++i) v[u][i] = a.part_o[slot * D + lane + 32 * i];
+      }
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const float g = ex2(sm[w] - top);
-      sum += sl[w] * g;
-      acc += so[w][d] * g;
+      for (int u = 0; u < U; ++u)
+        if (w + u * stride <= w1) add(ml[u].x, ml[u].y, v[u]);
     }
   }
-  const int hq = hk * a.G + gr;
-  const RowEnd end = finish_row(top * kLn2, sum, p.sinks ? p.sinks + hq : nullptr);
-  const float f = end.factor * (p.v_scale != nullptr ? __ldg(p.v_scale + hk) : 1.f);
-  static_cast<__nv_bfloat16*>(p.out)[b * p.o_b + static_cast<int64_t>(hq) * p.o_h + d] =
-      __float2bfloat16_rn(acc * f);
-  if (p.lse != nullptr && d == 0) p.lse[static_cast<int64_t>(b) * p.Hq + hq] = end.lse;
+  __device__ __forceinline__ void write(const DecodeArgs& a, int b, int hk, int gr, int lane) {
+    const DecodeParams& p = a.p;
+    const int hq = hk * a.G + gr;
+    const RowEnd end = finish_row(m * kLn2, l, p.sinks ? p.sinks + hq : nullptr);
+    const float f = end.factor * (p.v_scale != nullptr ? __ldg(p.v_scale + hk) : 1.f);
+    __nv_bfloat16* dst =
+        static_cast<__nv_bfloat16*>(p.out) + b * p.o_b + static_cast<int64_t>(hq) * p.o_h;
+#pragma unroll
+    for (int i = 0; i < N; ++i) dst[lane + 32 * i] = __float2bfloat16_rn(o[i] * f);
+    if (p.lse != nullptr && lane == 0) p.lse[static_cast<int64_t>(b) * p.Hq + hq] = end.lse;
+  }
+};
+
+template <int D>
+__global__ void __launch_bounds__(32 * kWarps) decode_join_kernel(const DecodeArgs a) {
+  constexpr int N = D / 32;
+  constexpr int kAlone = 32;                           // parts that one warp reads
+  const DecodeParams& p = a.p;
+  __shared__ float so[kWarps][D];
+  __shared__ float2 sml[kWarps];
+  __shared__ int shared_rows;                          // bit k: row k needs the block
+  if (threadIdx.x == 0) shared_rows = 0;
+  pdl_wait();
+  pdl_launch_dependents();
+  __syncthreads();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int heads = p.Hkv * a.tiles;
+  const int64_t per = a.cum[p.B + 1];
+  struct Where {
+    int b, hk, gr, row;
+    int64_t u0, w0, w1;
+    bool split;
+  };
+  auto where = [&](int64_t item) {
+    Where r = {};
+    if (item >= static_cast<int64_t>(p.B) * heads * a.rows) return r;
+    const int64_t unit = divide(item, a.rows);
+    r.row = static_cast<int>(item - unit * a.rows);
+    r.b = static_cast<int>(divide(unit, heads));
+    const int head = static_cast<int>(unit - static_cast<int64_t>(r.b) * heads);
+    r.hk = head / a.tiles;
+    r.gr = (head - r.hk * a.tiles) * kRows + r.row;
+    const int64_t before = a.cum[r.b], steps = a.cum[r.b + 1] - before;
+    r.u0 = before * heads + head * steps;
+    r.w0 = divide(r.u0, per);
+    r.w1 = divide(r.u0 + steps - 1, per);
+    r.split = steps > kWhole && r.w0 < r.w1 && r.gr < a.G;
+    return r;
+  };
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * kWarps;
+  const Where mine = where(first + warp);
+  if (mine.split) {
+    if (mine.w1 - mine.w0 < kAlone) {
+      JoinRow<D> r;
+      r.read(a, mine.w0, mine.w1, 1, per, mine.u0, mine.row, lane);
+      r.write(a, mine.b, mine.hk, mine.gr, lane);
+    } else if (lane == 0) {
+      atomicOr(&shared_rows, 1 << warp);
+    }
+  }
+  __syncthreads();
+  for (int k = 0; k < kWarps; ++k) {
+    if (!((shared_rows >> k) & 1)) continue;
+    const Where at = where(first + k);
+    JoinRow<D> r;
+    r.read(a, at.w0 + warp, at.w1, kWarps, per, at.u0, at.row, lane);
+    if (lane == 0) sml[warp] = make_float2(r.m, r.l);
+#pragma unroll
+    for (int i = 0; i < N; ++i) so[warp][lane + 32 * i] = r.o[i];
+    __syncthreads();
+    if (warp == 0) {
+      JoinRow<D> all;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        float v[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = so[w][lane + 32 * i];
+        all.add(sml[w].x, sml[w].y, v);
+      }
+      all.write(a, at.b, at.hk, at.gr, lane);
+    }
+    __syncthreads();
+  }
 }
 
 int stored_rows(int Hq, int Hkv) { return std::min(kRows, Hq / Hkv); }
@@ -620,9 +727,8 @@ cudaError_t launch(const DecodeArgs& a, int grid, cudaStream_t stream) {
   e = launch_k(decode_kernel<D, FP8>, dim3(grid), dim3(32 * kWarps),
                static_cast<size_t>(S::kSmem), stream, b);
   if (e != cudaSuccess) return e;
-  return launch_k(decode_join_kernel<D>,
-                  dim3(static_cast<unsigned>(a.p.Hkv * a.tiles * a.rows),
-                       static_cast<unsigned>(a.p.B)),
+  const int64_t rows = static_cast<int64_t>(a.p.B) * a.p.Hkv * a.tiles * a.rows;
+  return launch_k(decode_join_kernel<D>, dim3(static_cast<unsigned>((rows + kWarps - 1) / kWarps)),
                   dim3(32 * kWarps), 0, stream, b);
 }
 
@@ -640,6 +746,7 @@ cudaError_t launch_decode(const DecodeParams& p, int num_sms, cudaStream_t strea
   a.G = p.Hq / p.Hkv;
   a.tiles = (a.G + kRows - 1) / kRows;
   a.rows = stored_rows(p.Hq, p.Hkv);
+  a.alike = p.ck_p == p.cv_p && p.ck_t == p.cv_t;
   a.chunk = (p.B + kEntries - 1) / kEntries;
   a.entries = (p.B + a.chunk - 1) / a.chunk;
   char* ws = static_cast<char*>(p.workspace);
