@@ -14,8 +14,10 @@
 // members of its pairs and two 16-byte loads are its own: elements [8c, 8c + 8) of
 // both halves of the rotated part, or 16 adjacent ones (adjacent pairs, the
 // part past R, v).  Its position in the head is the same for every head it
-// takes, so its cosines and sines are loaded once, and its heads' elements are
-// on their way before the slot and the position are known.  The quotient is x r + (x - x r s) r with r = 1/s rounded (P. Markstein,
+// takes, so its cosines and sines are loaded once a token.  The blocks are
+// persistent: while a token is worked on, the elements of the next two are on their way
+// to shared memory (asynchronous copies that only the issuing thread reads, so
+// nothing waits for the block), and the next one's rotation to registers.  The quotient is x r + (x - x r s) r with r = 1/s rounded (P. Markstein,
 // "Computation of elementary functions on the IBM RISC System/6000 processor",
 // 1990): three operations an element instead of a division's, and the same
 // e4m3 codes as the division for 1.4e11 quotients, half of them around the codes' midpoints.
@@ -29,7 +31,9 @@ namespace mxq {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kUnroll = 3;   // heads in flight per thread
+constexpr int kUnroll = 3;   // heads of a thread in a step
+constexpr int kStages = 3;   // steps in shared memory
+constexpr int kBlocks = 5;   // per SM
 
 __device__ __forceinline__ void unpack8(const uint4& w, float* v) {
   const uint32_t a[4] = {w.x, w.y, w.z, w.w};
@@ -83,8 +87,14 @@ __device__ __forceinline__ void rotate(float* a, float* b, const float* c, const
   }
 }
 
+__device__ __forceinline__ void copy16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src)
+               : "memory");
+}
+
 template <bool FP8>
-__global__ void __launch_bounds__(kThreads) rope_append_kernel(const RopeAppendParams p) {
+__global__ void __launch_bounds__(kThreads, kBlocks) rope_append_kernel(const RopeAppendParams p) {
+  __shared__ uint4 ring[kStages][kUnroll][2][kThreads];
   const int nchunk = p.D / 16;
   const int lanes = kThreads / nchunk;         // heads a block takes at once
   const int c = threadIdx.x % nchunk;
@@ -93,121 +103,152 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const RopeAppendP
   pdl_launch_dependents();
   if (h0 >= lanes) return;
   const int heads = p.Hq + 2 * p.Hkv;          // q heads, then k, then v
+  const int steps = (heads + lanes * kUnroll - 1) / (lanes * kUnroll);   // of a token
   const bool turn = c < p.rot / 16;
   // offsets of the thread's two groups of 8 elements in a head of q or k
   const int e0 = turn && !p.interleaved ? 8 * c : 16 * c;
   const int e1 = turn && !p.interleaved ? p.rot / 2 + 8 * c : 16 * c + 8;
-  for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x) {
-    // the first heads' elements are on their way before the slot, the position and
-    // (which depends on it) the rotation's row are looked at
-    uint4 lo[kUnroll], hi[kUnroll];
-    auto load = [&](int hb) {
+
+  // a step: token, its first head, its slot and position
+  struct Step {
+    int64_t t, slot;
+    int64_t pos;
+    int k;
+  };
+  auto next = [&](Step& s) {
+    if (++s.k == steps) {
+      s.k = 0;
+      s.t += gridDim.x;
+    }
+  };
+  int fill = 0;
+  auto copy = [&](Step& s) {
+    if (s.t < p.T) {
+      s.slot = p.slots[s.t];
+      s.pos = p.rot > 0 ? p.positions[s.t] : 0;
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
-        const int h = hb + u * lanes;
+        const int h = h0 + (s.k * kUnroll + u) * lanes;
         if (h >= heads) continue;
         const __nv_bfloat16* src;
         int a = e0, b = e1;
         if (h < p.Hq) {
-          src = static_cast<const __nv_bfloat16*>(p.q) + t * p.q_t + h * p.q_h;
+          src = static_cast<const __nv_bfloat16*>(p.q) + s.t * p.q_t + h * p.q_h;
         } else if (h < p.Hq + p.Hkv) {
-          src = static_cast<const __nv_bfloat16*>(p.k) + t * p.k_t + (h - p.Hq) * p.k_h;
+          src = static_cast<const __nv_bfloat16*>(p.k) + s.t * p.k_t + (h - p.Hq) * p.k_h;
         } else {
-          src = static_cast<const __nv_bfloat16*>(p.v) + t * p.v_t + (h - p.Hq - p.Hkv) * p.v_h;
+          src = static_cast<const __nv_bfloat16*>(p.v) + s.t * p.v_t + (h - p.Hq - p.Hkv) * p.v_h;
           a = 16 * c, b = 16 * c + 8;
         }
-        // plain loads: q may be rotated in place
-        lo[u] = *reinterpret_cast<const uint4*>(src + a);
-        hi[u] = *reinterpret_cast<const uint4*>(src + b);
-      }
-    };
-    load(h0);
-    const int64_t slot = p.slots[t];
-    const int64_t pos = p.rot > 0 ? p.positions[t] : 0;
-    const bool rows = p.rot == 0 || (pos >= 0 && pos < p.max_pos);   // the table has this row
-    float cs[8], sn[8];
-    if (turn && rows) {
-      const float4* cp = reinterpret_cast<const float4*>(p.cos_sin + pos * p.rot + 8 * c);
-      const float4* sp =
-          reinterpret_cast<const float4*>(p.cos_sin + pos * p.rot + p.rot / 2 + 8 * c);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float4 a = __ldg(cp + i), b = __ldg(sp + i);
-        cs[4 * i] = a.x, cs[4 * i + 1] = a.y, cs[4 * i + 2] = a.z, cs[4 * i + 3] = a.w;
-        sn[4 * i] = b.x, sn[4 * i + 1] = b.y, sn[4 * i + 2] = b.z, sn[4 * i + 3] = b.w;
+        copy16(&ring[fill][u][0][threadIdx.x], src + a);
+        copy16(&ring[fill][u][1][threadIdx.x], src + b);
       }
     }
-    const bool stored = slot >= 0 && slot < p.slots_total;   // negative: a token not cached
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    fill = fill + 1 == kStages ? 0 : fill + 1;
+  };
+  float cs[8], sn[8], cs_next[8], sn_next[8];
+  auto rotation = [&](const Step& s, float* co, float* si) {
+    if (!turn || s.t >= p.T || s.pos < 0 || s.pos >= p.max_pos) return;
+    const float4* cp = reinterpret_cast<const float4*>(p.cos_sin + s.pos * p.rot + 8 * c);
+    const float4* sp =
+        reinterpret_cast<const float4*>(p.cos_sin + s.pos * p.rot + p.rot / 2 + 8 * c);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float4 a = __ldg(cp + i), b = __ldg(sp + i);
+      co[4 * i] = a.x, co[4 * i + 1] = a.y, co[4 * i + 2] = a.z, co[4 * i + 3] = a.w;
+      si[4 * i] = b.x, si[4 * i + 1] = b.y, si[4 * i + 2] = b.z, si[4 * i + 3] = b.w;
+    }
+  };
+  static_assert(kStages == 3, "the steps ahead are named one by one");
+  Step now = {static_cast<int64_t>(blockIdx.x), 0, 0, 0}, ahead, far;
+  copy(now);
+  ahead = now;
+  next(ahead);
+  copy(ahead);
+  rotation(now, cs_next, sn_next);
+  int use = 0;
+  while (now.t < p.T) {
+    far = ahead;
+    next(far);
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 8; ++i) cs[i] = cs_next[i], sn[i] = sn_next[i];
+    copy(far);                                         // into the stage used one step ago
+    rotation(ahead, cs_next, sn_next);
+    const bool rows = p.rot == 0 || (now.pos >= 0 && now.pos < p.max_pos);   // the table's
+    const bool stored = now.slot >= 0 && now.slot < p.slots_total;   // negative: not cached
     int64_t page = 0, off = 0;
     if (stored) {
       if (p.slots_total <= 0x7fffffff) {               // 32-bit division where it is enough
-        const uint32_t s32 = static_cast<uint32_t>(slot);
+        const uint32_t s32 = static_cast<uint32_t>(now.slot);
         page = s32 / static_cast<uint32_t>(p.page_size);
         off = s32 - static_cast<uint32_t>(page) * static_cast<uint32_t>(p.page_size);
       } else {
-        page = slot / p.page_size;
-        off = slot - page * p.page_size;
+        page = now.slot / p.page_size;
+        off = now.slot - page * p.page_size;
       }
     }
-    if ((!rows || slot >= p.slots_total) && threadIdx.x == 0)
+    if ((!rows || now.slot >= p.slots_total) && threadIdx.x == 0)
       atomicOr(p.status, kStatusBadIndex);
-    if (!rows) continue;                               // flagged: nothing is written
-    for (int hb = h0; hb < heads; hb += lanes * kUnroll) {
-      if (hb != h0) load(hb);
 #pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        const int h = hb + u * lanes;
-        if (h >= heads || (h >= p.Hq && !stored)) continue;
-        const bool is_q = h < p.Hq, is_v = h >= p.Hq + p.Hkv;
-        float x[16];
-        unpack8(lo[u], x);
-        unpack8(hi[u], x + 8);
-        int a = e0, b = e1;
-        if (is_v) {
-          a = 16 * c, b = 16 * c + 8;
-        } else if (turn) {
-          if (p.interleaved) {
-            float y[16];
+    for (int u = 0; u < kUnroll; ++u) {
+      const int h = h0 + (now.k * kUnroll + u) * lanes;
+      // a position without a row was flagged: nothing of the token is written
+      if (!rows || h >= heads || (h >= p.Hq && !stored)) continue;
+      const bool is_q = h < p.Hq, is_v = h >= p.Hq + p.Hkv;
+      float x[16];
+      unpack8(ring[use][u][0][threadIdx.x], x);
+      unpack8(ring[use][u][1][threadIdx.x], x + 8);
+      int a = e0, b = e1;
+      if (is_v) {
+        a = 16 * c, b = 16 * c + 8;
+      } else if (turn) {
+        if (p.interleaved) {
+          float y[16];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = x[2 * i], y[8 + i] = x[2 * i + 1];
-            rotate(y, y + 8, cs, sn);
+          for (int i = 0; i < 8; ++i) y[i] = x[2 * i], y[8 + i] = x[2 * i + 1];
+          rotate(y, y + 8, cs, sn);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[2 * i] = y[i], x[2 * i + 1] = y[8 + i];
-          } else {
-            rotate(x, x + 8, cs, sn);
-          }
-        }
-        if (is_q) {
-          __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.q_out) + t * p.o_t + h * p.o_h;
-          *reinterpret_cast<uint4*>(dst + a) = pack8_bf16(x);
-          *reinterpret_cast<uint4*>(dst + b) = pack8_bf16(x + 8);
-          continue;
-        }
-        const int hk = h - p.Hq - (is_v ? p.Hkv : 0);
-        const int64_t at = is_v ? page * p.cv_p + off * p.cv_t + hk * p.cv_h
-                                : page * p.ck_p + off * p.ck_t + hk * p.ck_h;
-        void* cache = is_v ? p.v_cache : p.k_cache;
-        if (FP8) {
-          const float* sc = is_v ? p.v_scale : p.k_scale;
-          const float s = sc ? __ldg(sc + hk) : 1.f;
-          const float r = fabsf(s) > 0x1p-60f && fabsf(s) < 0x1p60f ? __frcp_rn(s) : 0.f;
-          uint8_t* dst = static_cast<uint8_t*>(cache) + at;
-          *reinterpret_cast<uint2*>(dst + a) = pack8_e4m3(x, s, r);
-          *reinterpret_cast<uint2*>(dst + b) = pack8_e4m3(x + 8, s, r);
+          for (int i = 0; i < 8; ++i) x[2 * i] = y[i], x[2 * i + 1] = y[8 + i];
         } else {
-          __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(cache) + at;
-          *reinterpret_cast<uint4*>(dst + a) = pack8_bf16(x);
-          *reinterpret_cast<uint4*>(dst + b) = pack8_bf16(x + 8);
+          rotate(x, x + 8, cs, sn);
         }
       }
+      if (is_q) {
+        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.q_out) + now.t * p.o_t + h * p.o_h;
+        *reinterpret_cast<uint4*>(dst + a) = pack8_bf16(x);
+        *reinterpret_cast<uint4*>(dst + b) = pack8_bf16(x + 8);
+        continue;
+      }
+      const int hk = h - p.Hq - (is_v ? p.Hkv : 0);
+      const int64_t at = is_v ? page * p.cv_p + off * p.cv_t + hk * p.cv_h
+                              : page * p.ck_p + off * p.ck_t + hk * p.ck_h;
+      void* cache = is_v ? p.v_cache : p.k_cache;
+      if (FP8) {
+        const float* sc = is_v ? p.v_scale : p.k_scale;
+        const float s = sc ? __ldg(sc + hk) : 1.f;
+        const float r = fabsf(s) > 0x1p-60f && fabsf(s) < 0x1p60f ? __frcp_rn(s) : 0.f;
+        uint8_t* dst = static_cast<uint8_t*>(cache) + at;
+        *reinterpret_cast<uint2*>(dst + a) = pack8_e4m3(x, s, r);
+        *reinterpret_cast<uint2*>(dst + b) = pack8_e4m3(x + 8, s, r);
+      } else {
+        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(cache) + at;
+        *reinterpret_cast<uint4*>(dst + a) = pack8_bf16(x);
+        *reinterpret_cast<uint4*>(dst + b) = pack8_bf16(x + 8);
+      }
     }
+    use = use + 1 == kStages ? 0 : use + 1;
+    now = ahead;
+    ahead = far;
   }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
 }  // namespace
 
 cudaError_t launch_rope_append(const RopeAppendParams& p, int num_sms, cudaStream_t stream) {
-  const int64_t cap = static_cast<int64_t>(num_sms) * 64;
+  const int64_t cap = static_cast<int64_t>(num_sms) * kBlocks;
   const unsigned blocks = static_cast<unsigned>(p.T < cap ? p.T : cap);
   if (p.fp8)
     return launch_k(rope_append_kernel<true>, dim3(blocks), dim3(kThreads), 0, stream, p);
