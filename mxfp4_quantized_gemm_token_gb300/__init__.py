@@ -529,7 +529,8 @@ def rope_append_kv(k, v, k_cache, v_cache, slots, cos_sin=None, positions=None, 
     no rotation); positions: int32 [T]; k_scale, v_scale: fp32 [Hkv] of an
     e4m3 cache (None: 1).  interleaved: the pairs are adjacent elements
     instead of (i, i + R/2).  Returns the rotated q (q_out if given; it may be
-    q itself), or None without q."""
+    q itself), or None without q.  q may hold k's heads too, where the rotated
+    k is needed outside the cache (not in place then)."""
     dev = _one_device(k, v, k_cache, v_cache, slots, cos_sin, positions, q, q_out, k_scale,
                       v_scale)
     T, Hkv, D = shape = k.shape

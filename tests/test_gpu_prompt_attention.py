@@ -99,7 +99,8 @@ def test_long():
 
 
 @pytest.mark.parametrize("nq,nk,H,KV,D,window", [
-    ([5], [1025], 2, 1, 128, 0), ([64], [1153], 8, 8, 64, 0), ([300, 9], [5000, 2111], 8, 2, 128, 0),
+    ([5], [1025], 2, 1, 128, 0), ([64], [1153], 8, 8, 64, 0),
+    ([300, 9], [5000, 2111], 8, 2, 128, 0),
     ([1, 1, 0, 7], [3000, 129, 50, 4001], 6, 2, 64, 0), ([30], [6000], 4, 1, 64, 3000),
     ([700], [3500], 3, 1, 128, 0), ([16, 16], [0, 9000], 128, 1, 64, 0)])
 @pytest.mark.parametrize("sinks", [False, True])
