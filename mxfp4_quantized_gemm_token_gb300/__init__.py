@@ -450,32 +450,32 @@ _raw_stream = torch._C._cuda_getCurrentRawStream
 _bf16, _fp8, _f32, _i32 = torch.bfloat16, torch.float8_e4m3fn, torch.float32, torch.int32
 
 
-def _one_device(*ts):
-    """The index of the one CUDA device of all tensors (None: not given)."""
-    dev = ts[0].get_device()
+def _devices_differ(*ts):
     for t in ts:
-        if t is not None and (t.get_device() != dev or dev < 0):
+        if t is not None and t.get_device() != ts[0].get_device() or ts[0].get_device() < 0:
             raise ValueError("mxq operates on CUDA tensors of one device (got %s and %s)"
                              % (ts[0].device, t.device))
-    return dev
 
 
 def _heads3(name, t):
     """t [n, heads, D] as the kernels read it, with unit inner stride, outer
     strides of 16-byte multiples and at least D (copied only if needed):
     (tensor, address, stride 0, stride 1)."""
-    if t.dim() != 3:
-        raise ValueError("%s must be [tokens, heads, head_dim], got %d dimensions"
-                         % (name, t.dim()))
-    if t.dtype != _bf16:
+    if t.dtype is not _bf16:
         raise TypeError("%s must be bf16" % name)
-    s0, s1, s2 = t.stride()
-    n0, n1, D = t.shape
+    strides = t.stride()
+    if len(strides) != 3:
+        raise ValueError("%s must be [tokens, heads, head_dim], got %d dimensions"
+                         % (name, len(strides)))
+    s0, s1, s2 = strides
     p = t.data_ptr()
-    if s2 != 1 or (n0 > 1 and (s0 < D or s0 & 7)) or (n1 > 1 and (s1 < D or s1 & 7)) or p & 15:
-        t = t.clone(memory_format=torch.contiguous_format)
-        s0, s1, _ = t.stride()
-        p = t.data_ptr()
+    # (the usual case in one test: all strides positive, 8 | s0, s1, 16 | p)
+    if s2 != 1 or p & 15 or (s0 | s1) & 7 or s1 < t.shape[2] or s0 < s1:
+        n0, n1, D = t.shape
+        if s2 != 1 or (n0 > 1 and (s0 < D or s0 & 7)) or (n1 > 1 and (s1 < D or s1 & 7)) or p & 15:
+            t = t.clone(memory_format=torch.contiguous_format)
+            s0, s1, _ = t.stride()
+            p = t.data_ptr()
     return t, p, s0, s1
 
 
@@ -486,15 +486,15 @@ def _caches(k, v, kv_heads, D):
         raise ValueError("k_cache must be [pages, page_size, %s, %d], got %s"
                          % ("kv_heads" if kv_heads is None else kv_heads, D, list(shape)))
     dtype = k.dtype
-    if v.shape != shape or v.dtype != dtype:
+    if v.shape != shape or v.dtype is not dtype:
         raise ValueError("k_cache and v_cache must have the same shape and dtype")
-    if dtype != _bf16 and dtype != _fp8:
+    if dtype is not _bf16 and dtype is not _fp8:
         raise TypeError("k_cache and v_cache must be bf16 or float8_e4m3fn")
     k0, k1, k2, k3 = k.stride()
     v0, v1, v2, v3 = v.stride()
     if k3 != 1 or v3 != 1:
         raise ValueError("k_cache and v_cache need a unit stride along the head dimension")
-    return (_lib.BF16 if dtype == _bf16 else _lib.E4M3, shape[0], shape[1], k0, k1, k2, v0, v1,
+    return (_lib.BF16 if dtype is _bf16 else _lib.E4M3, shape[0], shape[1], k0, k1, k2, v0, v1,
             v2, shape[2])
 
 
@@ -502,7 +502,7 @@ def _vec(name, t, dtype, n):
     """The address of a contiguous vector of n elements (None for None)."""
     if t is None:
         return None
-    if t.dtype != dtype or t.numel() != n or not t.is_contiguous():
+    if t.dtype is not dtype or t.numel() != n or not t.is_contiguous():
         raise ValueError("%s must be contiguous %s of %d elements" % (name, dtype, n))
     return t.data_ptr()
 
@@ -511,7 +511,7 @@ def _output(name, t, shape, dev):
     """(tensor, address, stride 0, stride 1) of a given output or a new one."""
     if t is None:
         t = torch.empty(shape, dtype=_bf16, device=dev)
-    elif t.dtype != _bf16 or t.shape != shape or t.stride(2) != 1:
+    elif t.dtype is not _bf16 or t.shape != shape or t.stride(2) != 1:
         raise ValueError("%s must be bf16 %s with a unit inner stride" % (name, list(shape)))
     s0, s1, _ = t.stride()
     return t, t.data_ptr(), s0, s1
@@ -531,8 +531,17 @@ def rope_append_kv(k, v, k_cache, v_cache, slots, cos_sin=None, positions=None, 
     instead of (i, i + R/2).  Returns the rotated q (q_out if given; it may be
     q itself), or None without q.  q may hold k's heads too, where the rotated
     k is needed outside the cache (not in place then)."""
-    dev = _one_device(k, v, k_cache, v_cache, slots, cos_sin, positions, q, q_out, k_scale,
-                      v_scale)
+    dev = k.get_device()
+    if not (dev >= 0 and v.get_device() == dev and k_cache.get_device() == dev
+            and v_cache.get_device() == dev and slots.get_device() == dev
+            and (cos_sin is None or cos_sin.get_device() == dev)
+            and (positions is None or positions.get_device() == dev)
+            and (q is None or q.get_device() == dev)
+            and (q_out is None or q_out.get_device() == dev)
+            and (k_scale is None or k_scale.get_device() == dev)
+            and (v_scale is None or v_scale.get_device() == dev)):
+        _devices_differ(k, v, k_cache, v_cache, slots, cos_sin, positions, q, q_out, k_scale,
+                        v_scale)
     T, Hkv, D = shape = k.shape
     if v.shape != shape:
         raise ValueError("k and v must have the same shape")
@@ -587,14 +596,22 @@ def paged_attention_decode(q, k_cache, v_cache, page_table, seq_lens, scale=None
     [B, Hq, D], with return_lse also the fp32 [B, Hq] log-sum-exp.  workspace:
     a caller's buffer of paged_attention_decode_workspace_size bytes (None:
     allocated here)."""
-    dev = _one_device(q, k_cache, v_cache, page_table, seq_lens, sinks, k_scale, v_scale, out,
-                      workspace)
+    dev = q.get_device()
+    if not (dev >= 0 and k_cache.get_device() == dev and v_cache.get_device() == dev
+            and page_table.get_device() == dev and seq_lens.get_device() == dev
+            and (sinks is None or sinks.get_device() == dev)
+            and (k_scale is None or k_scale.get_device() == dev)
+            and (v_scale is None or v_scale.get_device() == dev)
+            and (out is None or out.get_device() == dev)
+            and (workspace is None or workspace.get_device() == dev)):
+        _devices_differ(q, k_cache, v_cache, page_table, seq_lens, sinks, k_scale, v_scale, out,
+                        workspace)
     shape = q.shape
     q, qp, q0, q1 = _heads3("q", q)
     B, Hq, D = shape
     cache = _caches(k_cache, v_cache, None, D)
     Hkv = cache[9]
-    if page_table.dim() != 2 or page_table.dtype != _i32:
+    if page_table.dim() != 2 or page_table.dtype is not _i32:
         raise ValueError("page_table must be int32 [%d, max_pages]" % B)
     rows, width = page_table.shape
     t0, t1 = page_table.stride()
@@ -638,7 +655,14 @@ def attention_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k=None, scale=None, causa
     [Tq, Hq, D], with return_lse also the fp32 [Tq, Hq] log-sum-exp.
     workspace: a caller's buffer of attention_varlen_workspace_size bytes
     (None: allocated here)."""
-    dev = _one_device(q, k, v, cu_seqlens_q, cu_seqlens_k, sinks, out, workspace)
+    dev = q.get_device()
+    if not (dev >= 0 and k.get_device() == dev and v.get_device() == dev
+            and cu_seqlens_q.get_device() == dev
+            and (cu_seqlens_k is None or cu_seqlens_k.get_device() == dev)
+            and (sinks is None or sinks.get_device() == dev)
+            and (out is None or out.get_device() == dev)
+            and (workspace is None or workspace.get_device() == dev)):
+        _devices_differ(q, k, v, cu_seqlens_q, cu_seqlens_k, sinks, out, workspace)
     shape, kshape = q.shape, k.shape
     q, qp, q0, q1 = _heads3("q", q)
     k, kp, k0, k1 = _heads3("k", k)
