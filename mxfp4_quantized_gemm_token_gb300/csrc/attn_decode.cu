@@ -52,6 +52,7 @@ struct DecodeArgs {
   int G, tiles, rows;               // query heads per kv head, units per kv head, rows stored
   int chunk, entries;               // sequences per entry of the prefix table, its entries
   int min_steps;
+  int join_rows;                    // rows of a block of the join: 8, or 1
   bool alike;                       // both caches have the same page and token strides
   int64_t* cum;                     // workspace: steps before each sequence [B + 1], then `per`
   float2* part_ml;                  // [warps][2][rows]
@@ -65,22 +66,20 @@ struct DecodeShape {
   static constexpr int kTile = KS * kRowBytes;                 // K (or V) of a step
   static constexpr int kStages = kTile == 4096 ? 3 : 6;
   static constexpr int kLPR = kRowBytes / 16;                  // lanes per row
-  static constexpr int kSmem = kWarps * kStages * 2 * kTile + 8 * kEntries + 4 * kWarps * kStages;
+  static constexpr int kSmem =
+      kWarps * kStages * 2 * kTile + 12 * kEntries + 4 * kWarps * kStages;
 };
 
 struct SeqRange {
   int lo, len, first, steps;        // visible keys [lo, len); the first step's key; its steps
 };
 
-// The visible keys of sequence b, in steps from a multiple of 16; at least one
-// step (without keys), so that every output is written.
+// The visible keys of a sequence of `len` keys, in steps from a multiple of 16; at
+// least one step (without keys), so that every output is written.
 template <int KS>
-__device__ __forceinline__ SeqRange seq_steps(const DecodeParams& p, int b, bool* bad) {
+__device__ __forceinline__ SeqRange seq_steps(const DecodeParams& p, int len) {
   SeqRange r;
-  const int cap = static_cast<int>(p.max_pages * p.page_size);
-  const int len = p.seq_lens[b];
-  *bad = len < 0 || len > cap;
-  r.len = min(max(len, 0), cap);
+  r.len = min(max(len, 0), static_cast<int>(p.max_pages * p.page_size));
   r.lo = p.window > 0 ? max(0, r.len - p.window) : 0;
   r.first = r.lo & ~15;
   r.steps = max(1, (r.len - r.first + KS - 1) / KS);
@@ -156,16 +155,18 @@ __device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
   return a / b;
 }
 
+// lens: the lengths in shared memory, where the prefix table has an entry for each sequence
+__device__ __forceinline__ int length_of(const DecodeArgs& a, const int* lens, int b) {
+  return a.chunk == 1 ? lens[b] : a.p.seq_lens[b];
+}
+
 template <int KS>
-__device__ __forceinline__ void advance(Cursor& c, const DecodeArgs& a) {
+__device__ __forceinline__ void advance(Cursor& c, const DecodeArgs& a, const int* lens) {
   if (++c.step < c.s.steps) return;
   c.step = 0;
   if (++c.head < a.p.Hkv * a.tiles) return;
   c.head = 0;
-  if (++c.b < a.p.B) {
-    bool bad;
-    c.s = seq_steps<KS>(a.p, c.b, &bad);
-  }
+  if (++c.b < a.p.B) c.s = seq_steps<KS>(a.p, length_of(a, lens, c.b));
 }
 
 template <int D, bool FP8>
@@ -179,8 +180,10 @@ __global__ void __launch_bounds__(32 * kWarps, 1) decode_kernel(const DecodeArgs
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int quad = lane & 3, r0 = lane >> 2;
   int64_t* table = reinterpret_cast<int64_t*>(smem + kWarps * ST * 2 * S::kTile);
-  uint32_t* masks = reinterpret_cast<uint32_t*>(table + kEntries) + warp * ST;
+  int* lens = reinterpret_cast<int*>(table + kEntries);
+  uint32_t* masks = reinterpret_cast<uint32_t*>(lens + kEntries) + warp * ST;
   __shared__ int64_t warp_sum[kWarps];
+  __shared__ int warp_longest[kWarps];
   pdl_wait();
   pdl_launch_dependents();
 
@@ -188,38 +191,44 @@ __global__ void __launch_bounds__(32 * kWarps, 1) decode_kernel(const DecodeArgs
   const int per_thread = (a.entries + 32 * kWarps - 1) / (32 * kWarps);
   const int e0 = threadIdx.x * per_thread;
   int64_t mine = 0;
+  int longest = 0;
   for (int e = e0; e < min(a.entries, e0 + per_thread); ++e)
     for (int b = e * a.chunk; b < min(p.B, (e + 1) * a.chunk); ++b) {
-      bool bad;
-      mine += seq_steps<KS>(p, b, &bad).steps;
-      if (bad && blockIdx.x == 0) atomicOr(p.status, kStatusBadIndex);
+      const int len = p.seq_lens[b];
+      if (a.chunk == 1) lens[b] = len;
+      const SeqRange r = seq_steps<KS>(p, len);
+      if (len != r.len && blockIdx.x == 0) atomicOr(p.status, kStatusBadIndex);
+      mine += r.steps;
+      longest = max(longest, r.steps);
     }
+  longest = __reduce_max_sync(0xffffffffu, longest);
   int64_t incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += y;
   }
-  if (lane == 31) warp_sum[warp] = incl;
+  if (lane == 31) warp_sum[warp] = incl, warp_longest[warp] = longest;
   __syncthreads();
   int64_t before = incl - mine, total = 0;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
     if (w < warp) before += warp_sum[w];
     total += warp_sum[w];
+    longest = max(longest, warp_longest[w]);
   }
   const int heads = p.Hkv * a.tiles;
   const int64_t workers = static_cast<int64_t>(gridDim.x) * kWarps;
   int64_t per = divide(total * heads + workers - 1, workers);
   if (per < a.min_steps) per = a.min_steps;
+  // units that stay whole: a part has room for the longest, or some get two
+  if (longest <= kWhole && per < longest) per = longest;
   for (int e = e0; e < min(a.entries, e0 + per_thread); ++e) {
     table[e] = before;
     for (int b = e * a.chunk; b < min(p.B, (e + 1) * a.chunk); ++b) {
       if (blockIdx.x == 0) a.cum[b] = before;
-      if (blockIdx.x == 0 || a.chunk * per_thread > 1) {
-        bool bad;
-        before += seq_steps<KS>(p, b, &bad).steps;
-      }
+      if (blockIdx.x == 0 || a.chunk * per_thread > 1)
+        before += seq_steps<KS>(p, length_of(a, lens, b)).steps;
     }
   }
   if (blockIdx.x == 0 && threadIdx.x == 0) {
@@ -232,22 +241,14 @@ __global__ void __launch_bounds__(32 * kWarps, 1) decode_kernel(const DecodeArgs
   const int64_t worker = static_cast<int64_t>(warp) * gridDim.x + blockIdx.x;
   const int64_t raw0 = worker * per;
   if (raw0 >= total * heads) return;
-  // the part's end `pos` on the line, moved out of a short unit, and where that is
-  auto locate = [&](int64_t pos, Cursor* c) {
+  // the part's end `pos` on the line, moved out of a short unit, and where that
+  // is; `at`: steps before sequence c->b
+  auto locate = [&](int64_t pos, Cursor* c, int64_t at) {
     if (pos >= total * heads) return total * heads;
-    int lo = 0, hi = a.entries - 1;                    // the last entry at or before pos
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (table[mid] * heads <= pos) lo = mid;
-      else hi = mid - 1;
-    }
-    bool bad;
-    int64_t at = table[lo] * heads;
-    c->b = lo * a.chunk;
-    c->s = seq_steps<KS>(p, c->b, &bad);
     while (at + static_cast<int64_t>(c->s.steps) * heads <= pos) {
       at += static_cast<int64_t>(c->s.steps) * heads;
-      c->s = seq_steps<KS>(p, ++c->b, &bad);
+      ++c->b;
+      c->s = seq_steps<KS>(p, length_of(a, lens, c->b));
     }
     const int n = c->s.steps;
     c->head = static_cast<int>(divide(pos - at, n));
@@ -258,13 +259,36 @@ __global__ void __launch_bounds__(32 * kWarps, 1) decode_kernel(const DecodeArgs
       c->step = up ? n - 1 : 0;
       if (up) {
         pos += n;
-        advance<KS>(*c, a);
+        advance<KS>(*c, a, lens);
       }
     }
     return pos;
   };
+  // the last entry of the prefix table at or before a position
+  auto entry = [&](int64_t pos, int lo) {
+    int hi = a.entries - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (table[mid] * heads <= pos) lo = mid;
+      else hi = mid - 1;
+    }
+    return lo;
+  };
   Cursor in, end;                                      // of the copies
-  const int64_t s0 = locate(raw0, &in), s1 = locate(raw0 + per, &end);
+  const int e_in = entry(raw0, 0);
+  in.b = e_in * a.chunk;
+  in.s = seq_steps<KS>(p, length_of(a, lens, in.b));
+  end.b = in.b, end.s = in.s;
+  int64_t at_end = table[e_in] * heads;
+  const int64_t s0 = locate(raw0, &in, at_end);
+  const int64_t raw1 = min(raw0 + per, total * heads - 1);
+  if (e_in + 1 < a.entries && table[e_in + 1] * heads <= raw1) {
+    const int e = entry(raw1, e_in + 1);
+    end.b = e * a.chunk;
+    end.s = seq_steps<KS>(p, length_of(a, lens, end.b));
+    at_end = table[e] * heads;
+  }
+  const int64_t s1 = locate(raw0 + per, &end, at_end);
   if (s0 >= s1) return;
   Cursor at = in;                                      // of the arithmetic
 
@@ -273,32 +297,37 @@ __global__ void __launch_bounds__(32 * kWarps, 1) decode_kernel(const DecodeArgs
   const int row_in = lane / S::kLPR, ch_in = lane % S::kLPR;
   constexpr int kRPI = 32 / S::kLPR;                   // rows per copy instruction
 
-  // the page of this lane's key of the step at `in`: read one step ahead
-  int page = 0, off = 0;
-  bool seen = false;
+  // the page of this lane's key of a step: looked up two steps before it is copied
+  struct Spot {
+    int page, off, head;
+    bool seen;
+  };
   auto look_up = [&]() {
+    Spot r = {0, 0, in.head, false};
     const int key = in.s.first + in.step * KS + lane;
-    seen = lane < KS && key >= in.s.lo && key < in.s.len;
-    page = off = 0;
-    if (seen) {
+    r.seen = lane < KS && key >= in.s.lo && key < in.s.len;
+    if (r.seen) {
       const uint32_t n = static_cast<uint32_t>(key) / static_cast<uint32_t>(p.page_size);
-      off = key - static_cast<int>(n) * p.page_size;
-      page = __ldg(p.page_table + in.b * p.ld_table + n);
+      r.off = key - static_cast<int>(n) * p.page_size;
+      r.page = __ldg(p.page_table + in.b * p.ld_table + n);
     }
+    return r;
   };
   int64_t left = s1 - s0;                              // steps still to be copied
   uint32_t fill = 0;
+  Spot now = {0, 0, 0, false}, next = now;
   auto copy_step = [&]() {
     if (left > 0) {
-      const bool ok = seen && static_cast<uint32_t>(page) < static_cast<uint32_t>(p.pages);
-      if (seen && !ok) {
+      int page = now.page, off = now.off;
+      const bool ok = now.seen && static_cast<uint32_t>(page) < static_cast<uint32_t>(p.pages);
+      if (now.seen && !ok) {
         atomicOr(p.status, kStatusBadIndex);
         page = off = 0;
       }
       const uint32_t mask = __ballot_sync(0xffffffffu, ok);
       const int st = fill % ST;
       if (lane == 0) masks[st] = mask;
-      const int hk = in.head / a.tiles;
+      const int hk = now.head / a.tiles;
       const char* kb = static_cast<const char*>(p.k_cache) + (hk * p.ck_h) * es + ch_in * 16;
       const char* vb = static_cast<const char*>(p.v_cache) + (hk * p.cv_h) * es + ch_in * 16;
       const uint32_t dst = ring + st * 2 * S::kTile;
@@ -324,14 +353,19 @@ __global__ void __launch_bounds__(32 * kWarps, 1) decode_kernel(const DecodeArgs
         }
       }
       ++fill;
-      if (--left > 0) {
-        advance<KS>(in, a);
-        look_up();
+      now = next;
+      if (--left > 1) {
+        advance<KS>(in, a, lens);
+        next = look_up();
       }
     }
     cp_commit();
   };
-  look_up();
+  now = look_up();
+  if (left > 1) {
+    advance<KS>(in, a, lens);
+    next = look_up();
+  }
 #pragma unroll 1
   for (int i = 0; i < ST - 1; ++i) copy_step();
 
@@ -569,15 +603,16 @@ __global__ void __launch_bounds__(32 * kWarps, 1) decode_kernel(const DecodeArgs
       }
     }
     fresh = true;
-    advance<KS>(at, a);
+    advance<KS>(at, a, lens);
   }
   cp_wait<0>();
 }
 
 // Joins the partial results of the rows of units that several parts share, in the parts'
 // order: out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i.  A warp takes a row,
-// reading eight parts at a time; a row of more than 32 parts is shared by the
-// block's eight warps.
+// reading eight parts at a time; a row of more than 32 parts, and of more than four
+// where there are too few rows to fill the SMs with warps, is shared by a
+// block's eight warps (24 parts of each of 32 rows: 4.9 us by one warp a row).
 template <int D>
 struct JoinRow {
   static constexpr int N = D / 32;
@@ -629,7 +664,7 @@ struct JoinRow {
 template <int D>
 __global__ void __launch_bounds__(32 * kWarps) decode_join_kernel(const DecodeArgs a) {
   constexpr int N = D / 32;
-  constexpr int kAlone = 32;                           // parts that one warp reads
+  const int alone = a.join_rows == 1 ? 4 : 32;         // parts that one warp reads
   const DecodeParams& p = a.p;
   __shared__ float so[kWarps][D];
   __shared__ float2 sml[kWarps];
@@ -662,19 +697,19 @@ __global__ void __launch_bounds__(32 * kWarps) decode_join_kernel(const DecodeAr
     r.split = steps > kWhole && r.w0 < r.w1 && r.gr < a.G;
     return r;
   };
-  const int64_t first = static_cast<int64_t>(blockIdx.x) * kWarps;
-  const Where mine = where(first + warp);
-  if (mine.split) {
-    if (mine.w1 - mine.w0 < kAlone) {
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * a.join_rows;
+  if (warp < a.join_rows) {
+    const Where mine = where(first + warp);
+    if (mine.split && mine.w1 - mine.w0 < alone) {
       JoinRow<D> r;
       r.read(a, mine.w0, mine.w1, 1, per, mine.u0, mine.row, lane);
       r.write(a, mine.b, mine.hk, mine.gr, lane);
-    } else if (lane == 0) {
+    } else if (mine.split && lane == 0) {
       atomicOr(&shared_rows, 1 << warp);
     }
   }
   __syncthreads();
-  for (int k = 0; k < kWarps; ++k) {
+  for (int k = 0; k < a.join_rows; ++k) {
     if (!((shared_rows >> k) & 1)) continue;
     const Where at = where(first + k);
     JoinRow<D> r;
@@ -728,7 +763,9 @@ cudaError_t launch(const DecodeArgs& a, int grid, cudaStream_t stream) {
                static_cast<size_t>(S::kSmem), stream, b);
   if (e != cudaSuccess) return e;
   const int64_t rows = static_cast<int64_t>(a.p.B) * a.p.Hkv * a.tiles * a.rows;
-  return launch_k(decode_join_kernel<D>, dim3(static_cast<unsigned>((rows + kWarps - 1) / kWarps)),
+  b.join_rows = rows <= 4 * grid ? 1 : kWarps;
+  return launch_k(decode_join_kernel<D>,
+                  dim3(static_cast<unsigned>((rows + b.join_rows - 1) / b.join_rows)),
                   dim3(32 * kWarps), 0, stream, b);
 }
 
