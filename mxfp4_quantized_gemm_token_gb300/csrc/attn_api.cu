@@ -31,8 +31,8 @@ mxq_status check_rows(const char* name, const void* p, int64_t n0, int64_t n1, i
     return fail(MXQ_ERR_INVALID_ARG, std::string(name) + ": strides below the head dimension");
   if (!aligned(p, bytes) || (n0 > 1 && s0 * es % static_cast<int64_t>(bytes) != 0) ||
       (n1 > 1 && s1 * es % static_cast<int64_t>(bytes) != 0))
-    return fail(MXQ_ERR_UNSUPPORTED, std::string(name) + " needs a base and strides of multiples of " +
-                                         std::to_string(bytes) + " bytes");
+    return fail(MXQ_ERR_UNSUPPORTED, std::string(name) + " needs a base and strides of " +
+                                         std::to_string(bytes) + "-byte multiples");
   return MXQ_OK;
 }
 
@@ -49,8 +49,8 @@ mxq_status check_cache(const char* name, const void* p, int32_t dtype, int64_t p
   if (pages > 1 && sp < D)
     return fail(MXQ_ERR_INVALID_ARG, std::string(name) + ": strides below the head dimension");
   if (pages > 1 && sp * es % static_cast<int64_t>(bytes) != 0)
-    return fail(MXQ_ERR_UNSUPPORTED, std::string(name) + " needs a base and strides of multiples of " +
-                                         std::to_string(bytes) + " bytes");
+    return fail(MXQ_ERR_UNSUPPORTED, std::string(name) + " needs a base and strides of " +
+                                         std::to_string(bytes) + "-byte multiples");
   return MXQ_OK;
 }
 
@@ -120,7 +120,8 @@ extern "C" mxq_status mxq_rope_append_kv(
     if (!cos_sin || !positions || max_pos <= 0)
       return fail(MXQ_ERR_INVALID_ARG, "a rotation needs cos_sin, max_pos > 0 and positions");
     if (!aligned(cos_sin, 16) || !aligned(positions, 4))
-      return fail(MXQ_ERR_UNSUPPORTED, "cos_sin needs a 16-byte aligned base, positions a 4-byte one");
+      return fail(MXQ_ERR_UNSUPPORTED,
+                  "cos_sin needs a 16-byte aligned base, positions a 4-byte one");
   }
   if (q) {
     MXQ_TRY(check_rows("q", q, T, Hq, sq_t, sq_h, D, 2, 16));
@@ -211,7 +212,8 @@ extern "C" mxq_status mxq_paged_attention_decode(
   p.pages = pages, p.page_size = page_size;
   p.ck_p = sck_p, p.ck_t = sck_t, p.ck_h = sck_h, p.cv_p = scv_p, p.cv_t = scv_t, p.cv_h = scv_h;
   p.page_table = page_table, p.ld_table = ld_table, p.max_pages = max_pages, p.seq_lens = seq_lens;
-  p.scale = scale, p.window = std::min(window, 1 << 30), p.sinks = sinks, p.k_scale = k_scale, p.v_scale = v_scale;
+  p.scale = scale, p.window = std::min(window, 1 << 30);
+  p.sinks = sinks, p.k_scale = k_scale, p.v_scale = v_scale;
   p.out = out, p.o_b = so_b, p.o_h = so_h, p.lse = lse, p.workspace = workspace;
   p.status = d.status;
   const cudaError_t e = launch_decode(p, d.num_sms, reinterpret_cast<cudaStream_t>(stream));

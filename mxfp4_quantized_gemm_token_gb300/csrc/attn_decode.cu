@@ -6,20 +6,23 @@
 // around keeping loads in flight.
 //
 // Work.  A sequence's visible keys are cut into steps of KS keys; the steps of
-// all (sequence, key/value head) units form one line, cut into equal parts, one
-// per warp of the grid, whatever the lengths.  A warp is on its own: its
+// all sequences form one line, cut into equal parts whatever the lengths, and a
+// (part, key/value head) pair is one warp's.  The heads of a part are at work at
+// the same time: their rows of a key are adjacent in memory.  (With all heads' steps on
+// one line, each head at another place of a sequence, the 128-byte rows of an e4m3
+// cache came at 4.8 TB/s on some devices.)  A warp is on its own: its
 // ring of shared-memory stages filled with 16-byte asynchronous copies, its own
 // running maximum, sum and accumulators, no block-wide barrier.  A
-// unit that lies inside one part is written out by its warp; the others
+// sequence that lies inside one part is written out by its warp; the others
 // leave at most two partial results per warp in the workspace, which
 // a second kernel joins in a fixed order.  A part's end that falls into a short
-// unit moves to the nearer end of it: splitting a few steps costs more than it balances.
+// sequence moves to the nearer end of it: splitting a few steps costs more than it balances.
 //
 // Arithmetic.  The G query heads of a key/value head are the rows of 16-row
-// tensor-core products (mma.sync m16n8k16: with at most 16 rows per 64 KB of
-// keys the products take a fraction of the load time, and their operands come from
-// registers and ldmatrix without a pass through tensor memory); G above 16 makes
-// further units.  Scores and outputs accumulate in fp32.  The reference a
+// tensor-core products (mma.sync m16n8k16: with at most 16 rows to a key the
+// products take a fraction of the load time, and their operands come from
+// registers and ldmatrix without a pass through tensor memory); every 16 query heads of
+// a larger G count as a head of their own above.  Scores and outputs accumulate in fp32.  The reference a
 // row's weights are relative to is raised only when a score exceeds it by 2^8
 // in the exponent, so most steps need no exchange between lanes.
 //   bf16 cache: bf16 products, weights rounded to bf16.
@@ -45,18 +48,18 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kEntries = 2048;      // entries of the shared prefix table
 constexpr int kRows = 16;           // rows of a product
-constexpr int kWhole = 8;           // units of at most this many steps stay whole
+constexpr int kWhole = 8;           // sequences of at most this many steps stay whole
 
 struct DecodeArgs {
   DecodeParams p;
-  int G, tiles, rows;               // query heads per kv head, units per kv head, rows stored
+  int G, tiles, rows;               // per kv head: query heads, 16-row tiles; rows stored
   int chunk, entries;               // sequences per entry of the prefix table, its entries
   int min_steps;
   int join_rows;                    // rows of a block of the join: 8, or 1
   bool alike;                       // both caches have the same page and token strides
   int64_t* cum;                     // workspace: steps before each sequence [B + 1], then `per`
-  float2* part_ml;                  // [warps][2][rows]
-  float* part_o;                    // [warps][2][rows][D]
+  float2* part_ml;                  // [task][2][rows]
+  float* part_o;                    // [task][2][rows][D]
 };
 
 template <int D, bool FP8>
@@ -126,7 +129,8 @@ __device__ __forceinline__ void mma16816(float* d, const uint32_t* a, uint32_t b
 
 // four e4m3 -> two f16x2
 __device__ __forceinline__ void e4m3x4_f16(uint32_t x, uint32_t* lo, uint32_t* hi) {
-  asm("{ .reg .b16 a, b; mov.b32 {a, b}, %2; cvt.rn.f16x2.e4m3x2 %0, a; cvt.rn.f16x2.e4m3x2 %1, b; }"
+  asm("{ .reg .b16 a, b; mov.b32 {a, b}, %2;"
+      " cvt.rn.f16x2.e4m3x2 %0, a; cvt.rn.f16x2.e4m3x2 %1, b; }"
       : "=r"(*lo), "=r"(*hi)
       : "r"(x));
 }
@@ -145,7 +149,7 @@ __device__ __forceinline__ void cp_wait() {
 
 // A place on the line of steps.
 struct Cursor {
-  int b, head, step;                // head: key/value head * tiles + tile
+  int b, step;
   SeqRange s;
 };
 
@@ -164,8 +168,6 @@ template <int KS>
 __device__ __forceinline__ void advance(Cursor& c, const DecodeArgs& a, const int* lens) {
   if (++c.step < c.s.steps) return;
   c.step = 0;
-  if (++c.head < a.p.Hkv * a.tiles) return;
-  c.head = 0;
   if (++c.b < a.p.B) c.s = seq_steps<KS>(a.p, length_of(a, lens, c.b));
 }
 
@@ -219,9 +221,9 @@ __global__ void __launch_bounds__(32 * kWarps, 1) decode_kernel(const DecodeArgs
   }
   const int heads = p.Hkv * a.tiles;
   const int64_t workers = static_cast<int64_t>(gridDim.x) * kWarps;
-  int64_t per = divide(total * heads + workers - 1, workers);
-  if (per < a.min_steps) per = a.min_steps;
-  // units that stay whole: a part has room for the longest, or some get two
+  const int64_t parts = max(static_cast<int64_t>(1), divide(workers, heads));
+  int64_t per = max(divide(total + parts - 1, parts), static_cast<int64_t>(a.min_steps));
+  // sequences that stay whole: a part has room for the longest, or some get two
   if (longest <= kWhole && per < longest) per = longest;
   for (int e = e0; e < min(a.entries, e0 + per_thread); ++e) {
     table[e] = before;
@@ -237,22 +239,17 @@ __global__ void __launch_bounds__(32 * kWarps, 1) decode_kernel(const DecodeArgs
   }
   __syncthreads();
 
-  // ---- this warp's part; few parts are spread over the SMs
-  const int64_t worker = static_cast<int64_t>(warp) * gridDim.x + blockIdx.x;
-  const int64_t raw0 = worker * per;
-  if (raw0 >= total * heads) return;
-  // the part's end `pos` on the line, moved out of a short unit, and where that
+  // the part's end `pos` on the line, moved out of a short sequence, and where that
   // is; `at`: steps before sequence c->b
   auto locate = [&](int64_t pos, Cursor* c, int64_t at) {
-    if (pos >= total * heads) return total * heads;
-    while (at + static_cast<int64_t>(c->s.steps) * heads <= pos) {
-      at += static_cast<int64_t>(c->s.steps) * heads;
+    if (pos >= total) return total;
+    while (at + c->s.steps <= pos) {
+      at += c->s.steps;
       ++c->b;
       c->s = seq_steps<KS>(p, length_of(a, lens, c->b));
     }
     const int n = c->s.steps;
-    c->head = static_cast<int>(divide(pos - at, n));
-    c->step = static_cast<int>((pos - at) - static_cast<int64_t>(c->head) * n);
+    c->step = static_cast<int>(pos - at);
     if (n <= kWhole && c->step > 0) {
       pos -= c->step;
       const bool up = 2 * c->step >= n;
@@ -269,347 +266,360 @@ __global__ void __launch_bounds__(32 * kWarps, 1) decode_kernel(const DecodeArgs
     int hi = a.entries - 1;
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (table[mid] * heads <= pos) lo = mid;
+      if (table[mid] <= pos) lo = mid;
       else hi = mid - 1;
     }
     return lo;
   };
-  Cursor in, end;                                      // of the copies
-  const int e_in = entry(raw0, 0);
-  in.b = e_in * a.chunk;
-  in.s = seq_steps<KS>(p, length_of(a, lens, in.b));
-  end.b = in.b, end.s = in.s;
-  int64_t at_end = table[e_in] * heads;
-  const int64_t s0 = locate(raw0, &in, at_end);
-  const int64_t raw1 = min(raw0 + per, total * heads - 1);
-  if (e_in + 1 < a.entries && table[e_in + 1] * heads <= raw1) {
-    const int e = entry(raw1, e_in + 1);
-    end.b = e * a.chunk;
-    end.s = seq_steps<KS>(p, length_of(a, lens, end.b));
-    at_end = table[e] * heads;
-  }
-  const int64_t s1 = locate(raw0 + per, &end, at_end);
-  if (s0 >= s1) return;
-  Cursor at = in;                                      // of the arithmetic
-
   const uint32_t ring = smem_u32(smem) + warp * ST * 2 * S::kTile;
   constexpr int es = FP8 ? 1 : 2;
   const int row_in = lane / S::kLPR, ch_in = lane % S::kLPR;
   constexpr int kRPI = 32 / S::kLPR;                   // rows per copy instruction
+  const int64_t tasks = divide(total + per - 1, per) * heads;
 
-  // the page of this lane's key of a step: looked up two steps before it is copied
-  struct Spot {
-    int page, off, head;
-    bool seen;
-  };
-  auto look_up = [&]() {
-    Spot r = {0, 0, in.head, false};
-    const int key = in.s.first + in.step * KS + lane;
-    r.seen = lane < KS && key >= in.s.lo && key < in.s.len;
-    if (r.seen) {
-      const uint32_t n = static_cast<uint32_t>(key) / static_cast<uint32_t>(p.page_size);
-      r.off = key - static_cast<int>(n) * p.page_size;
-      r.page = __ldg(p.page_table + in.b * p.ld_table + n);
+  // ---- this warp's tasks (one, unless there are more heads than warps); where
+  // there are few they are spread over the SMs
+  for (int64_t task = static_cast<int64_t>(warp) * gridDim.x + blockIdx.x; task < tasks;
+       task += workers) {
+    const int64_t part = divide(task, heads);
+    const int head = static_cast<int>(task - part * heads);
+    const int hk = head / a.tiles, tile = head - hk * a.tiles;
+    const int64_t raw0 = part * per;
+    Cursor in, end;                                      // of the copies
+    const int e_in = entry(raw0, 0);
+    in.b = e_in * a.chunk;
+    in.s = seq_steps<KS>(p, length_of(a, lens, in.b));
+    end.b = in.b, end.s = in.s;
+    int64_t at_end = table[e_in];
+    const int64_t s0 = locate(raw0, &in, at_end);
+    const int64_t raw1 = min(raw0 + per, total - 1);
+    if (e_in + 1 < a.entries && table[e_in + 1] <= raw1) {
+      const int e = entry(raw1, e_in + 1);
+      end.b = e * a.chunk;
+      end.s = seq_steps<KS>(p, length_of(a, lens, end.b));
+      at_end = table[e];
     }
-    return r;
-  };
-  int64_t left = s1 - s0;                              // steps still to be copied
-  uint32_t fill = 0;
-  Spot now = {0, 0, 0, false}, next = now;
-  auto copy_step = [&]() {
-    if (left > 0) {
-      int page = now.page, off = now.off;
-      const bool ok = now.seen && static_cast<uint32_t>(page) < static_cast<uint32_t>(p.pages);
-      if (now.seen && !ok) {
-        atomicOr(p.status, kStatusBadIndex);
-        page = off = 0;
+    const int64_t s1 = locate(raw0 + per, &end, at_end);
+    if (s0 >= s1) continue;
+    Cursor at = in;                                      // of the arithmetic
+    const char* k_base =
+        static_cast<const char*>(p.k_cache) + (hk * p.ck_h) * es + ch_in * 16;
+    const char* v_base =
+        static_cast<const char*>(p.v_cache) + (hk * p.cv_h) * es + ch_in * 16;
+
+    // the page of this lane's key of a step: looked up two steps before it is copied
+    struct Spot {
+      int page, off;
+      bool seen;
+    };
+    auto look_up = [&]() {
+      Spot r = {0, 0, false};
+      const int key = in.s.first + in.step * KS + lane;
+      r.seen = lane < KS && key >= in.s.lo && key < in.s.len;
+      if (r.seen) {
+        const uint32_t n = static_cast<uint32_t>(key) / static_cast<uint32_t>(p.page_size);
+        r.off = key - static_cast<int>(n) * p.page_size;
+        r.page = __ldg(p.page_table + in.b * p.ld_table + n);
       }
-      const uint32_t mask = __ballot_sync(0xffffffffu, ok);
-      const int st = fill % ST;
-      if (lane == 0) masks[st] = mask;
-      const int hk = now.head / a.tiles;
-      const char* kb = static_cast<const char*>(p.k_cache) + (hk * p.ck_h) * es + ch_in * 16;
-      const char* vb = static_cast<const char*>(p.v_cache) + (hk * p.cv_h) * es + ch_in * 16;
-      const uint32_t dst = ring + st * 2 * S::kTile;
-      // the lane's key's row, in both caches if they are laid out alike
-      const int64_t ko = (page * p.ck_p + off * p.ck_t) * es;
-      if (a.alike) {
-#pragma unroll
-        for (int i = 0; i < KS / kRPI; ++i) {
-          const int r = i * kRPI + row_in;
-          const int64_t from = __shfl_sync(0xffffffffu, ko, r);
-          const uint32_t d = dst + tile_off<ROWB>(r, ch_in);
-          cp16(d, kb + from, (mask >> r) & 1);
-          cp16(d + S::kTile, vb + from, (mask >> r) & 1);
+      return r;
+    };
+    int64_t left = s1 - s0;                              // steps still to be copied
+    uint32_t fill = 0;
+    Spot now = {0, 0, false}, next = now;
+    auto copy_step = [&]() {
+      if (left > 0) {
+        int page = now.page, off = now.off;
+        const bool ok = now.seen && static_cast<uint32_t>(page) < static_cast<uint32_t>(p.pages);
+        if (now.seen && !ok) {
+          atomicOr(p.status, kStatusBadIndex);
+          page = off = 0;
         }
-      } else {
-        const int64_t vo = (page * p.cv_p + off * p.cv_t) * es;
+        const uint32_t mask = __ballot_sync(0xffffffffu, ok);
+        const int st = fill % ST;
+        if (lane == 0) masks[st] = mask;
+        const uint32_t dst = ring + st * 2 * S::kTile;
+        // the lane's key's row, in both caches if they are laid out alike
+        const int64_t ko = (page * p.ck_p + off * p.ck_t) * es;
+        if (a.alike) {
 #pragma unroll
-        for (int i = 0; i < KS / kRPI; ++i) {
-          const int r = i * kRPI + row_in;
-          const uint32_t d = dst + tile_off<ROWB>(r, ch_in);
-          cp16(d, kb + __shfl_sync(0xffffffffu, ko, r), (mask >> r) & 1);
-          cp16(d + S::kTile, vb + __shfl_sync(0xffffffffu, vo, r), (mask >> r) & 1);
+          for (int i = 0; i < KS / kRPI; ++i) {
+            const int r = i * kRPI + row_in;
+            const int64_t from = __shfl_sync(0xffffffffu, ko, r);
+            const uint32_t d = dst + tile_off<ROWB>(r, ch_in);
+            cp16(d, k_base + from, (mask >> r) & 1);
+            cp16(d + S::kTile, v_base + from, (mask >> r) & 1);
+          }
+        } else {
+          const int64_t vo = (page * p.cv_p + off * p.cv_t) * es;
+#pragma unroll
+          for (int i = 0; i < KS / kRPI; ++i) {
+            const int r = i * kRPI + row_in;
+            const uint32_t d = dst + tile_off<ROWB>(r, ch_in);
+            cp16(d, k_base + __shfl_sync(0xffffffffu, ko, r), (mask >> r) & 1);
+            cp16(d + S::kTile, v_base + __shfl_sync(0xffffffffu, vo, r), (mask >> r) & 1);
+          }
+        }
+        ++fill;
+        now = next;
+        if (--left > 1) {
+          advance<KS>(in, a, lens);
+          next = look_up();
         }
       }
-      ++fill;
-      now = next;
-      if (--left > 1) {
-        advance<KS>(in, a, lens);
-        next = look_up();
-      }
+      cp_commit();
+    };
+    now = look_up();
+    if (left > 1) {
+      advance<KS>(in, a, lens);
+      next = look_up();
     }
-    cp_commit();
-  };
-  now = look_up();
-  if (left > 1) {
-    advance<KS>(in, a, lens);
-    next = look_up();
-  }
 #pragma unroll 1
-  for (int i = 0; i < ST - 1; ++i) copy_step();
+    for (int i = 0; i < ST - 1; ++i) copy_step();
 
-  uint32_t qf[D / 16][4];                              // rows r0, r0 + 8 of q
-  float o[DT][4];
-  float m[2], l[2], cs[2];
-  uint32_t use = 0;
-  bool fresh = true, opened = false;                   // opened: the unit began in this part
-  for (int64_t s = s0; s < s1; ++s, ++use) {
-    const int hk = at.head / a.tiles, tile = at.head - hk * a.tiles;
-    if (fresh) {
-      // a new unit: its q, and nothing summed yet
-      fresh = false;
-      opened = at.step == 0;
-      const float ks = p.k_scale != nullptr ? __ldg(p.k_scale + hk) : 1.f;
+    uint32_t qf[D / 16][4];                              // rows r0, r0 + 8 of q
+    float o[DT][4];
+    float m[2], l[2], cs[2];
+    uint32_t use = 0;
+    bool fresh = true, opened = false;                   // opened: the sequence began in this part
+    for (int64_t s = s0; s < s1; ++s, ++use) {
+      if (fresh) {
+        // a new sequence: its q, and nothing summed yet
+        fresh = false;
+        opened = at.step == 0;
+        const float ks = p.k_scale != nullptr ? __ldg(p.k_scale + hk) : 1.f;
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const int gr = tile * kRows + r0 + 8 * half;
-        const bool in_group = gr < a.G;
-        const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + at.b * p.q_b +
-                                 static_cast<int64_t>(hk * a.G + gr) * p.q_h;
-        float unscale = 1.f;
-        if constexpr (FP8) {
-          float big = 0.f;
-          uint2 raw[D / 16];
+        for (int half = 0; half < 2; ++half) {
+          const int gr = tile * kRows + r0 + 8 * half;
+          const bool in_group = gr < a.G;
+          const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + at.b * p.q_b +
+                                   static_cast<int64_t>(hk * a.G + gr) * p.q_h;
+          float unscale = 1.f;
+          if constexpr (FP8) {
+            float big = 0.f;
+            uint2 raw[D / 16];
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            raw[k] = in_group ? __ldg(reinterpret_cast<const uint2*>(q + 16 * k + 4 * quad))
-                              : make_uint2(0u, 0u);
-            const uint32_t w[2] = {raw[k].x, raw[k].y};
+            for (int k = 0; k < D / 16; ++k) {
+              raw[k] = in_group ? __ldg(reinterpret_cast<const uint2*>(q + 16 * k + 4 * quad))
+                                : make_uint2(0u, 0u);
+              const uint32_t w[2] = {raw[k].x, raw[k].y};
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              big = fmaxf(big, fabsf(__uint_as_float(w[i] << 16)));
-              big = fmaxf(big, fabsf(__uint_as_float(w[i] & 0xFFFF0000u)));
+              for (int i = 0; i < 2; ++i) {
+                big = fmaxf(big, fabsf(__uint_as_float(w[i] << 16)));
+                big = fmaxf(big, fabsf(__uint_as_float(w[i] & 0xFFFF0000u)));
+              }
             }
+            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+            // the power of two that brings the largest to [2^14, 2^15)
+            const int e = big > 0.f && big < INFINITY ? min(max(14 - ilogbf(big), -100), 100) : 0;
+            const float up = copysignf(ldexpf(1.f, e), ks);
+            unscale = ldexpf(1.f, -e);
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+              const uint32_t w[2] = {raw[k].x, raw[k].y};
+#pragma unroll
+              for (int i = 0; i < 2; ++i)
+                qf[k][half + 2 * i] = f16x2(__uint_as_float(w[i] << 16) * up,
+                                            __uint_as_float(w[i] & 0xFFFF0000u) * up);
+            }
+          } else {
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+              for (int i = 0; i < 2; ++i)
+                qf[k][half + 2 * i] =
+                    in_group
+                        ? __ldg(reinterpret_cast<const uint32_t*>(q + 16 * k + 8 * i + 2 * quad))
+                        : 0u;
           }
-          big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
-          big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
-          // the power of two that brings the largest to [2^14, 2^15)
-          const int e = big > 0.f && big < INFINITY ? min(max(14 - ilogbf(big), -100), 100) : 0;
-          const float up = copysignf(ldexpf(1.f, e), ks);
-          unscale = ldexpf(1.f, -e);
-#pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const uint32_t w[2] = {raw[k].x, raw[k].y};
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-              qf[k][half + 2 * i] = f16x2(__uint_as_float(w[i] << 16) * up,
-                                          __uint_as_float(w[i] & 0xFFFF0000u) * up);
-          }
-        } else {
-#pragma unroll
-          for (int k = 0; k < D / 16; ++k)
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-              qf[k][half + 2 * i] =
-                  in_group ? __ldg(reinterpret_cast<const uint32_t*>(q + 16 * k + 8 * i + 2 * quad))
-                           : 0u;
+          // > 0: the sign of a key scale goes into q, and a scale of 0 counts as next to
+          // nothing, so that it keeps a masked key's -inf
+          cs[half] = fmaxf(p.scale * fabsf(ks) * kLog2e * unscale, 1e-30f);
+          m[half] = -INFINITY;
+          l[half] = 0.f;
         }
-        // > 0: the sign of a key scale goes into q, and a scale of 0 counts as next to
-        // nothing, so that it keeps a masked key's -inf
-        cs[half] = fmaxf(p.scale * fabsf(ks) * kLog2e * unscale, 1e-30f);
-        m[half] = -INFINITY;
-        l[half] = 0.f;
+#pragma unroll
+        for (int t = 0; t < DT; ++t)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[t][i] = 0.f;
       }
-#pragma unroll
-      for (int t = 0; t < DT; ++t)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) o[t][i] = 0.f;
-    }
-    cp_wait<ST - 2>();
-    __syncwarp();
-    copy_step();                                       // into the stage used one step ago
-    const int st = use % ST;
-    const uint32_t mask = masks[st];
-    const uint32_t kt = ring + st * 2 * S::kTile, vt = kt + S::kTile;
+      cp_wait<ST - 2>();
+      __syncwarp();
+      copy_step();                                       // into the stage used one step ago
+      const int st = use % ST;
+      const uint32_t mask = masks[st];
+      const uint32_t kt = ring + st * 2 * S::kTile, vt = kt + S::kTile;
 
-    // ---- scores: rows x keys
-    float x[NT][4];
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) x[n][i] = 0.f;
-    // (elements outside, keys inside: the products that follow one another are independent)
-#pragma unroll
-    for (int k = 0; k < D / 16; k += FP8 ? 2 : 1) {
-#pragma unroll
-      for (int n = 0; n < NT; n += 2) {
-        uint32_t f[4];
-        if constexpr (FP8) {
-          // matrices: keys 8n.. and 8(n+1).. of chunk k (16 elements), then of k + 1
-          ldsm4(kt + tile_off<ROWB>(8 * n + (lane & 15), k + (lane >> 4)), f);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t b0, b1;
-            e4m3x4_f16(f[i], &b0, &b1);
-            mma16816<true>(x[n + (i & 1)], qf[k + (i >> 1)], b0, b1);
-          }
-        } else {
-          // matrices: (keys 8n.., chunks 2k and 2k + 1), (keys 8(n+1).., the same)
-          ldsm4(kt + tile_off<ROWB>(8 * n + ((lane >> 4) << 3) + (lane & 7),
-                                    2 * k + ((lane >> 3) & 1)), f);
-          mma16816<false>(x[n], qf[k], f[0], f[1]);
-          mma16816<false>(x[n + 1], qf[k], f[2], f[3]);
-        }
-      }
-    }
-
-    // ---- weights, relative to the reference m (of the unscaled scores)
-    constexpr uint32_t kAll = KS == 32 ? 0xffffffffu : (1u << KS) - 1;
-    if (mask != kAll) {
+      // ---- scores: rows x keys
+      float x[NT][4];
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (!((mask >> (8 * n + 2 * quad + (i & 1))) & 1)) x[n][i] = -INFINITY;
-    }
-    float mx[2] = {-INFINITY, -INFINITY};
+        for (int i = 0; i < 4; ++i) x[n][i] = 0.f;
+      // (elements outside, keys inside: the products that follow one another are independent)
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+      for (int k = 0; k < D / 16; k += FP8 ? 2 : 1) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) mx[h] = fmaxf(mx[h], fmaxf(x[n][2 * h], x[n][2 * h + 1]));
-    if (__any_sync(0xffffffffu, (mx[0] - m[0]) * cs[0] > 8.f || (mx[1] - m[1]) * cs[1] > 8.f ||
-                                    (m[0] == -INFINITY && mx[0] > m[0]) ||
-                                    (m[1] == -INFINITY && mx[1] > m[1]))) {
+        for (int n = 0; n < NT; n += 2) {
+          uint32_t f[4];
+          if constexpr (FP8) {
+            // matrices: keys 8n.. and 8(n+1).. of chunk k (16 elements), then of k + 1
+            ldsm4(kt + tile_off<ROWB>(8 * n + (lane & 15), k + (lane >> 4)), f);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint32_t b0, b1;
+              e4m3x4_f16(f[i], &b0, &b1);
+              mma16816<true>(x[n + (i & 1)], qf[k + (i >> 1)], b0, b1);
+            }
+          } else {
+            // matrices: (keys 8n.., chunks 2k and 2k + 1), (keys 8(n+1).., the same)
+            ldsm4(kt + tile_off<ROWB>(8 * n + ((lane >> 4) << 3) + (lane & 7),
+                                      2 * k + ((lane >> 3) & 1)), f);
+            mma16816<false>(x[n], qf[k], f[0], f[1]);
+            mma16816<false>(x[n + 1], qf[k], f[2], f[3]);
+          }
+        }
+      }
+
+      // ---- weights, relative to the reference m (of the unscaled scores)
+      constexpr uint32_t kAll = KS == 32 ? 0xffffffffu : (1u << KS) - 1;
+      if (mask != kAll) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (!((mask >> (8 * n + 2 * quad + (i & 1))) & 1)) x[n][i] = -INFINITY;
+      }
+      float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) mx[h] = fmaxf(mx[h], fmaxf(x[n][2 * h], x[n][2 * h + 1]));
+      if (__any_sync(0xffffffffu, (mx[0] - m[0]) * cs[0] > 8.f || (mx[1] - m[1]) * cs[1] > 8.f ||
+                                      (m[0] == -INFINITY && mx[0] > m[0]) ||
+                                      (m[1] == -INFINITY && mx[1] > m[1]))) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
+          mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
+          const float n = fmaxf(m[h], mx[h]);
+          const float f = m[h] == -INFINITY ? 0.f : ex2((m[h] - n) * cs[h]);
+          m[h] = n;
+          l[h] *= f;
+#pragma unroll
+          for (int t = 0; t < DT; ++t) {
+            o[t][2 * h] *= f;
+            o[t][2 * h + 1] *= f;
+          }
+        }
+      }
+      const float ref[2] = {m[0] == -INFINITY ? 0.f : m[0] * cs[0],
+                            m[1] == -INFINITY ? 0.f : m[1] * cs[1]};
+      uint32_t pf[KS / 16][4];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          x[n][i] = ex2(fmaf(x[n][i], cs[i >> 1], -ref[i >> 1]));
+          l[i >> 1] += x[n][i];
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          pf[n / 2][h + 2 * (n & 1)] = FP8 ? f16x2(x[n][2 * h], x[n][2 * h + 1])
+                                           : bf16x2(x[n][2 * h], x[n][2 * h + 1]);
+      }
+
+      // ---- values
+#pragma unroll
+      for (int kk = 0; kk < KS / 16; ++kk) {
+        // matrices: keys 16kk.. and 16kk + 8.. of chunk c, then of c + 1
+        const int r = 16 * kk + (lane & 15);
+        constexpr int kChunks = ROWB / 16;
+#pragma unroll
+        for (int c = 0; c < kChunks; c += 2) {
+          uint32_t f[4];
+          ldsm4_t(vt + tile_off<ROWB>(r, c + (lane >> 4)), f);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            if constexpr (FP8) {
+              // a register holds keys 2q, 2q + 1 of two elements: even elements
+              // make one output tile, odd ones the next
+              uint32_t e0, o0, e1, o1;
+              e4m3x4_f16(__byte_perm(f[2 * i], 0, 0x3120), &e0, &o0);
+              e4m3x4_f16(__byte_perm(f[2 * i + 1], 0, 0x3120), &e1, &o1);
+              mma16816<true>(o[2 * (c + i)], pf[kk], e0, e1);
+              mma16816<true>(o[2 * (c + i) + 1], pf[kk], o0, o1);
+            } else {
+              mma16816<false>(o[c + i], pf[kk], f[2 * i], f[2 * i + 1]);
+            }
+          }
+        }
+      }
+
+      // ---- the sequence's or the part's end
+      const bool closed = at.step + 1 == at.s.steps;
+      if (!closed && s + 1 < s1) {
+        ++at.step;
+        continue;
+      }
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
-        mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
-        const float n = fmaxf(m[h], mx[h]);
-        const float f = m[h] == -INFINITY ? 0.f : ex2((m[h] - n) * cs[h]);
-        m[h] = n;
-        l[h] *= f;
+        l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+        l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+        const int gl = r0 + 8 * h, gr = tile * kRows + gl;
+        if (gr >= a.G) continue;
+        const float top = m[h] == -INFINITY ? m[h] : m[h] * cs[h];
+        if (opened && closed) {
+          const int hq = hk * a.G + gr;
+          const RowEnd end = finish_row(top * kLn2, l[h], p.sinks ? p.sinks + hq : nullptr);
+          const float f = end.factor * (p.v_scale != nullptr ? __ldg(p.v_scale + hk) : 1.f);
+          __nv_bfloat16* dst =
+              static_cast<__nv_bfloat16*>(p.out) + at.b * p.o_b + static_cast<int64_t>(hq) * p.o_h;
 #pragma unroll
-        for (int t = 0; t < DT; ++t) {
-          o[t][2 * h] *= f;
-          o[t][2 * h + 1] *= f;
-        }
-      }
-    }
-    const float ref[2] = {m[0] == -INFINITY ? 0.f : m[0] * cs[0],
-                          m[1] == -INFINITY ? 0.f : m[1] * cs[1]};
-    uint32_t pf[KS / 16][4];
+          for (int t = 0; t < DT; t += 2) {
+            if constexpr (FP8) {
+              *reinterpret_cast<uint2*>(dst + 8 * t + 4 * quad) =
+                  make_uint2(bf16x2(o[t][2 * h] * f, o[t + 1][2 * h] * f),
+                             bf16x2(o[t][2 * h + 1] * f, o[t + 1][2 * h + 1] * f));
+            } else {
+              *reinterpret_cast<uint32_t*>(dst + 8 * t + 2 * quad) =
+                  bf16x2(o[t][2 * h] * f, o[t][2 * h + 1] * f);
+              *reinterpret_cast<uint32_t*>(dst + 8 * t + 8 + 2 * quad) =
+                  bf16x2(o[t + 1][2 * h] * f, o[t + 1][2 * h + 1] * f);
+            }
+          }
+          if (p.lse != nullptr && quad == 0)
+            p.lse[static_cast<int64_t>(at.b) * p.Hq + hq] = end.lse;
+        } else {
+          // a sequence that begins after the part's (unmoved) begin goes to slot 1 (parts
+          // are split at all only with a warp for each task)
+          const int64_t slot = (task * 2 + (opened && raw0 < s - at.step ? 1 : 0)) * a.rows + gl;
+          if (quad == 0) a.part_ml[slot] = make_float2(top, l[h]);
+          float* dst = a.part_o + slot * D;
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        x[n][i] = ex2(fmaf(x[n][i], cs[i >> 1], -ref[i >> 1]));
-        l[i >> 1] += x[n][i];
-      }
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        pf[n / 2][h + 2 * (n & 1)] = FP8 ? f16x2(x[n][2 * h], x[n][2 * h + 1])
-                                         : bf16x2(x[n][2 * h], x[n][2 * h + 1]);
-    }
-
-    // ---- values
-#pragma unroll
-    for (int kk = 0; kk < KS / 16; ++kk) {
-      // matrices: keys 16kk.. and 16kk + 8.. of chunk c, then of c + 1
-      const int r = 16 * kk + (lane & 15);
-      constexpr int kChunks = ROWB / 16;
-#pragma unroll
-      for (int c = 0; c < kChunks; c += 2) {
-        uint32_t f[4];
-        ldsm4_t(vt + tile_off<ROWB>(r, c + (lane >> 4)), f);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          if constexpr (FP8) {
-            // a register holds keys 2q, 2q + 1 of two elements: even elements
-            // make one output tile, odd ones the next
-            uint32_t e0, o0, e1, o1;
-            e4m3x4_f16(__byte_perm(f[2 * i], 0, 0x3120), &e0, &o0);
-            e4m3x4_f16(__byte_perm(f[2 * i + 1], 0, 0x3120), &e1, &o1);
-            mma16816<true>(o[2 * (c + i)], pf[kk], e0, e1);
-            mma16816<true>(o[2 * (c + i) + 1], pf[kk], o0, o1);
-          } else {
-            mma16816<false>(o[c + i], pf[kk], f[2 * i], f[2 * i + 1]);
+          for (int t = 0; t < DT; t += 2) {
+            if constexpr (FP8) {
+              *reinterpret_cast<float4*>(dst + 8 * t + 4 * quad) = make_float4(
+                  o[t][2 * h], o[t + 1][2 * h], o[t][2 * h + 1], o[t + 1][2 * h + 1]);
+            } else {
+              *reinterpret_cast<float2*>(dst + 8 * t + 2 * quad) =
+                  make_float2(o[t][2 * h], o[t][2 * h + 1]);
+              *reinterpret_cast<float2*>(dst + 8 * t + 8 + 2 * quad) =
+                  make_float2(o[t + 1][2 * h], o[t + 1][2 * h + 1]);
+            }
           }
         }
       }
+      fresh = true;
+      advance<KS>(at, a, lens);
     }
-
-    // ---- the unit's or the part's end
-    const bool closed = at.step + 1 == at.s.steps;
-    if (!closed && s + 1 < s1) {
-      ++at.step;
-      continue;
-    }
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
-      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
-      const int gl = r0 + 8 * h, gr = tile * kRows + gl;
-      if (gr >= a.G) continue;
-      const float top = m[h] == -INFINITY ? m[h] : m[h] * cs[h];
-      if (opened && closed) {
-        const int hq = hk * a.G + gr;
-        const RowEnd end = finish_row(top * kLn2, l[h], p.sinks ? p.sinks + hq : nullptr);
-        const float f = end.factor * (p.v_scale != nullptr ? __ldg(p.v_scale + hk) : 1.f);
-        __nv_bfloat16* dst =
-            static_cast<__nv_bfloat16*>(p.out) + at.b * p.o_b + static_cast<int64_t>(hq) * p.o_h;
-#pragma unroll
-        for (int t = 0; t < DT; t += 2) {
-          if constexpr (FP8) {
-            *reinterpret_cast<uint2*>(dst + 8 * t + 4 * quad) =
-                make_uint2(bf16x2(o[t][2 * h] * f, o[t + 1][2 * h] * f),
-                           bf16x2(o[t][2 * h + 1] * f, o[t + 1][2 * h + 1] * f));
-          } else {
-            *reinterpret_cast<uint32_t*>(dst + 8 * t + 2 * quad) =
-                bf16x2(o[t][2 * h] * f, o[t][2 * h + 1] * f);
-            *reinterpret_cast<uint32_t*>(dst + 8 * t + 8 + 2 * quad) =
-                bf16x2(o[t + 1][2 * h] * f, o[t + 1][2 * h + 1] * f);
-          }
-        }
-        if (p.lse != nullptr && quad == 0)
-          p.lse[static_cast<int64_t>(at.b) * p.Hq + hq] = end.lse;
-      } else {
-        // a unit that begins after the part's (unmoved) begin goes to slot 1
-        const int64_t slot = (worker * 2 + (opened && raw0 < s - at.step ? 1 : 0)) * a.rows + gl;
-        if (quad == 0) a.part_ml[slot] = make_float2(top, l[h]);
-        float* dst = a.part_o + slot * D;
-#pragma unroll
-        for (int t = 0; t < DT; t += 2) {
-          if constexpr (FP8) {
-            *reinterpret_cast<float4*>(dst + 8 * t + 4 * quad) = make_float4(
-                o[t][2 * h], o[t + 1][2 * h], o[t][2 * h + 1], o[t + 1][2 * h + 1]);
-          } else {
-            *reinterpret_cast<float2*>(dst + 8 * t + 2 * quad) =
-                make_float2(o[t][2 * h], o[t][2 * h + 1]);
-            *reinterpret_cast<float2*>(dst + 8 * t + 8 + 2 * quad) =
-                make_float2(o[t + 1][2 * h], o[t + 1][2 * h + 1]);
-          }
-        }
-      }
-    }
-    fresh = true;
-    advance<KS>(at, a, lens);
+    cp_wait<0>();
+    __syncwarp();
   }
-  cp_wait<0>();
 }
 
-// Joins the partial results of the rows of units that several parts share, in the parts'
-// order: out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i.  A warp takes a row,
+// Joins the partial results of the rows of sequences that several parts share, in the
+// parts' order: out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i.  A warp takes a row,
 // reading eight parts at a time; a row of more than 32 parts, and of more than four
 // where there are too few rows to fill the SMs with warps, is shared by a
 // block's eight warps (24 parts of each of 32 rows: 4.9 us by one warp a row).
@@ -626,9 +636,10 @@ struct JoinRow {
     for (int i = 0; i < N; ++i) o[i] = o[i] * f + v[i] * g;
     m = n;
   }
-  // parts w, w + stride, ... up to w1 of the unit that begins at u0
+  // parts w, w + stride, ... up to w1 of the sequence that begins at u0
   __device__ __forceinline__ void read(const DecodeArgs& a, int64_t w, int64_t w1, int stride,
-                                       int64_t per, int64_t u0, int row, int lane) {
+                                       int64_t per, int64_t u0, int head, int row, int lane) {
+    const int heads = a.p.Hkv * a.tiles;
     constexpr int U = 8;
     for (; w <= w1; w += U * stride) {
       float2 ml[U];
@@ -638,7 +649,7 @@ struct JoinRow {
         const int64_t k = w + u * stride;
         ml[u] = make_float2(-INFINITY, 0.f);
         if (k > w1) continue;
-        const int64_t slot = (k * 2 + (k * per < u0 ? 1 : 0)) * a.rows + row;
+        const int64_t slot = ((k * heads + head) * 2 + (k * per < u0 ? 1 : 0)) * a.rows + row;
         ml[u] = a.part_ml[slot];
 #pragma unroll
         for (int i = 0; i < N; ++i) v[u][i] = a.part_o[slot * D + lane + 32 * i];
@@ -677,7 +688,7 @@ __global__ void __launch_bounds__(32 * kWarps) decode_join_kernel(const DecodeAr
   const int heads = p.Hkv * a.tiles;
   const int64_t per = a.cum[p.B + 1];
   struct Where {
-    int b, hk, gr, row;
+    int b, head, hk, gr, row;
     int64_t u0, w0, w1;
     bool split;
   };
@@ -687,11 +698,11 @@ __global__ void __launch_bounds__(32 * kWarps) decode_join_kernel(const DecodeAr
     const int64_t unit = divide(item, a.rows);
     r.row = static_cast<int>(item - unit * a.rows);
     r.b = static_cast<int>(divide(unit, heads));
-    const int head = static_cast<int>(unit - static_cast<int64_t>(r.b) * heads);
-    r.hk = head / a.tiles;
-    r.gr = (head - r.hk * a.tiles) * kRows + r.row;
-    const int64_t before = a.cum[r.b], steps = a.cum[r.b + 1] - before;
-    r.u0 = before * heads + head * steps;
+    r.head = static_cast<int>(unit - static_cast<int64_t>(r.b) * heads);
+    r.hk = r.head / a.tiles;
+    r.gr = (r.head - r.hk * a.tiles) * kRows + r.row;
+    r.u0 = a.cum[r.b];
+    const int64_t steps = a.cum[r.b + 1] - r.u0;
     r.w0 = divide(r.u0, per);
     r.w1 = divide(r.u0 + steps - 1, per);
     r.split = steps > kWhole && r.w0 < r.w1 && r.gr < a.G;
@@ -702,7 +713,7 @@ __global__ void __launch_bounds__(32 * kWarps) decode_join_kernel(const DecodeAr
     const Where mine = where(first + warp);
     if (mine.split && mine.w1 - mine.w0 < alone) {
       JoinRow<D> r;
-      r.read(a, mine.w0, mine.w1, 1, per, mine.u0, mine.row, lane);
+      r.read(a, mine.w0, mine.w1, 1, per, mine.u0, mine.head, mine.row, lane);
       r.write(a, mine.b, mine.hk, mine.gr, lane);
     } else if (mine.split && lane == 0) {
       atomicOr(&shared_rows, 1 << warp);
@@ -713,7 +724,7 @@ __global__ void __launch_bounds__(32 * kWarps) decode_join_kernel(const DecodeAr
     if (!((shared_rows >> k) & 1)) continue;
     const Where at = where(first + k);
     JoinRow<D> r;
-    r.read(a, at.w0 + warp, at.w1, kWarps, per, at.u0, at.row, lane);
+    r.read(a, at.w0 + warp, at.w1, kWarps, per, at.u0, at.head, at.row, lane);
     if (lane == 0) sml[warp] = make_float2(r.m, r.l);
 #pragma unroll
     for (int i = 0; i < N; ++i) so[warp][lane + 32 * i] = r.o[i];
