@@ -21,9 +21,9 @@
 // Arithmetic.  The G query heads of a key/value head are the rows of 16-row
 // tensor-core products (mma.sync m16n8k16: with at most 16 rows to a key the
 // products take a fraction of the load time, and their operands come from
-// registers and ldmatrix without a pass through tensor memory); every 16 query heads of
-// a larger G count as a head of their own above.  Scores and outputs accumulate in fp32.  The reference a
-// row's weights are relative to is raised only when a score exceeds it by 2^8
+// registers and ldmatrix without a pass through tensor memory); every 16 query
+// heads of a larger G count as a head of their own above.  Scores and outputs
+// accumulate in fp32.  The reference a row's weights are relative to is raised only when a score exceeds it by 2^8
 // in the exponent, so most steps need no exchange between lanes.
 //   bf16 cache: bf16 products, weights rounded to bf16.
 //   e4m3 cache: keys and values converted to f16 (exact), q scaled per row by

@@ -414,7 +414,8 @@ __device__ __forceinline__ void join_rows(const PromptArgs& a, const PromptPiece
       if ((stored >> rw) & 1)
         *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + to + col) =
             none ? make_uint2(0u, 0u)
-                 : make_uint2(bf16x2(acc[k].x * f, acc[k].y * f), bf16x2(acc[k].z * f, acc[k].w * f));
+                 : make_uint2(bf16x2(acc[k].x * f, acc[k].y * f),
+                              bf16x2(acc[k].z * f, acc[k].w * f));
     }
   }
 }
