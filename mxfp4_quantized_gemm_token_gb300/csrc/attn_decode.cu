@@ -23,7 +23,8 @@
 // products take a fraction of the load time, and their operands come from
 // registers and ldmatrix without a pass through tensor memory); every 16 query
 // heads of a larger G count as a head of their own above.  Scores and outputs
-// accumulate in fp32.  The reference a row's weights are relative to is raised only when a score exceeds it by 2^8
+// accumulate in fp32.  The reference a row's weights are relative to is raised only
+// when a score exceeds it by 2^8
 // in the exponent, so most steps need no exchange between lanes.
 //   bf16 cache: bf16 products, weights rounded to bf16.
 //   e4m3 cache: keys and values converted to f16 (exact), q scaled per row by

@@ -235,3 +235,24 @@ def test_refusals():
     size = ctypes.c_size_t(0)
     assert lib.mxq_attention_varlen_workspace_size(5, 1, 4, 2, 32, ctypes.byref(size)) == \
         _lib.ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("nq,nk", [([300], [300]), ([70, 20], [70, 3000])])
+def test_stalled_loads_time_out_and_recover(nq, nk):
+    """With the test-only switch no tile is loaded: every wait runs out, the status
+    says so, and the next call is right."""
+    g = gen(22)
+    q, k, v = randn(g, sum(nq), 8, 128), randn(g, sum(nk), 2, 128), randn(g, sum(nk), 2, 128)
+    mxq.sync_status()
+    old = mxq.get_option(_lib.OPT_WAIT_BUDGET_NS)
+    try:
+        mxq.set_option(_lib.OPT_WAIT_BUDGET_NS, 20_000_000)
+        mxq.set_option(_lib.OPT_INJECT_STALL, 1)
+        mxq.attention_varlen(q, k, v, offsets(nq), offsets(nk))
+        with pytest.raises(mxq.MxqError) as e:
+            mxq.sync_status()
+        assert e.value.status == _lib.ERR_TIMEOUT
+    finally:
+        mxq.set_option(_lib.OPT_INJECT_STALL, 0)
+        mxq.set_option(_lib.OPT_WAIT_BUDGET_NS, old)
+    check(nq, nk, 8, 2, 128, seed=23)
