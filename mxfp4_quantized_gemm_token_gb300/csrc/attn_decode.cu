@@ -55,6 +55,7 @@ struct DecodeArgs {
   DecodeParams p;
   int G, tiles, rows;               // per kv head: query heads, 16-row tiles; rows stored
   int chunk, entries;               // sequences per entry of the prefix table, its entries
+  int parts;                        // of the line, at most
   int min_steps;
   int join_rows;                    // rows of a block of the join: 8, or 1
   bool alike;                       // both caches have the same page and token strides
@@ -148,6 +149,10 @@ __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+__device__ __forceinline__ void prefetch(const void* at) {
+  asm volatile("prefetch.global.L1 [%0];" ::"l"(at));
+}
+
 // A place on the line of steps.
 struct Cursor {
   int b, step;
@@ -221,9 +226,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1) decode_kernel(const DecodeArgs
     longest = max(longest, warp_longest[w]);
   }
   const int heads = p.Hkv * a.tiles;
-  const int64_t workers = static_cast<int64_t>(gridDim.x) * kWarps;
-  const int64_t parts = max(static_cast<int64_t>(1), divide(workers, heads));
-  int64_t per = max(divide(total + parts - 1, parts), static_cast<int64_t>(a.min_steps));
+  const int workers = gridDim.x * kWarps;
+  int64_t per = max(divide(total + a.parts - 1, a.parts), static_cast<int64_t>(a.min_steps));
   // sequences that stay whole: a part has room for the longest, or some get two
   if (longest <= kWhole && per < longest) per = longest;
   for (int e = e0; e < min(a.entries, e0 + per_thread); ++e) {
@@ -262,13 +266,14 @@ __global__ void __launch_bounds__(32 * kWarps, 1) decode_kernel(const DecodeArgs
     }
     return pos;
   };
-  // the last entry of the prefix table at or before a position
+  // the last entry of the prefix table at or before a position, 32 candidates at a time
   auto entry = [&](int64_t pos, int lo) {
-    int hi = a.entries - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (table[mid] <= pos) lo = mid;
-      else hi = mid - 1;
+    for (int n = a.entries - lo; n > 1;) {
+      const int step = (n + 31) >> 5, k = lane * step;
+      const uint32_t at = __ballot_sync(0xffffffffu, k < n && table[lo + k] <= pos);
+      const int skip = max(0, __popc(at) - 1) * step;
+      lo += skip;
+      n = min(step, n - skip);
     }
     return lo;
   };
@@ -302,6 +307,17 @@ __global__ void __launch_bounds__(32 * kWarps, 1) decode_kernel(const DecodeArgs
     }
     const int64_t s1 = locate(raw0 + per, &end, at_end);
     if (s0 >= s1) continue;
+    {
+      // on their way while the pages are looked up: q and what its output needs
+      const int gr = tile * kRows + (lane & 15);
+      if (gr < a.G) {
+        const int hq = hk * a.G + gr;
+        if ((lane >> 4) * 64 < D)
+          prefetch(static_cast<const __nv_bfloat16*>(p.q) + in.b * p.q_b +
+                   static_cast<int64_t>(hq) * p.q_h + (lane >> 4) * 64);
+        if (lane < 16 && p.sinks != nullptr) prefetch(p.sinks + hq);
+      }
+    }
     Cursor at = in;                                      // of the arithmetic
     const char* k_base =
         static_cast<const char*>(p.k_cache) + (hk * p.ck_h) * es + ch_in * 16;
@@ -771,9 +787,14 @@ cudaError_t launch(const DecodeArgs& a, int grid, cudaStream_t stream) {
   }
   DecodeArgs b = a;
   b.min_steps = 64 / S::KS;
+  b.parts = std::max(1, grid * kWarps / (a.p.Hkv * a.tiles));
   e = launch_k(decode_kernel<D, FP8>, dim3(grid), dim3(32 * kWarps),
                static_cast<size_t>(S::kSmem), stream, b);
   if (e != cudaSuccess) return e;
+  // where every sequence stays whole, whatever the lengths, there is nothing to join
+  int64_t keys = a.p.max_pages * a.p.page_size;
+  if (a.p.window > 0) keys = std::min<int64_t>(keys, static_cast<int64_t>(a.p.window) + 15);
+  if (keys <= kWhole * S::KS) return cudaSuccess;
   const int64_t rows = static_cast<int64_t>(a.p.B) * a.p.Hkv * a.tiles * a.rows;
   b.join_rows = rows <= 4 * grid ? 1 : kWarps;
   return launch_k(decode_join_kernel<D>,

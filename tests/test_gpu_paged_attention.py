@@ -204,6 +204,21 @@ def test_decode_window_and_sinks(window, fp8):
     run_decode(c, lens, window, None)
 
 
+@pytest.mark.parametrize("D,fp8,limit", [(64, False, 256), (64, True, 256), (128, False, 128),
+                                         (128, True, 256)])
+def test_decode_where_sequences_stay_whole(D, fp8, limit):
+    """Calls whose longest possible sequence is just short enough to be one
+    warp's, and calls just past that: bounded by the page table, by the window."""
+    for n in (limit - 1, limit, limit + 1, limit + 16):
+        q, kc, vc, table, lens, g = decode_case(n, [n, 3, n], 8, 2, D, 16, fp8)
+        table = table[:, :-(-n // 16)]
+        run_decode((q, kc, vc, table, lens, g), [n, 3, n])
+    lens = [1000, limit, 1007]
+    c = decode_case(D, lens, 8, 2, D, 16, fp8)
+    for window in (limit - 16, limit - 15, limit - 14, limit):
+        run_decode(c, lens, window)
+
+
 def test_decode_scales_and_large_scores():
     """Per-head scales of an e4m3 cache; scores of several hundred."""
     lens = [1, 200, 3333]
