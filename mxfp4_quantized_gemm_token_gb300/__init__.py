@@ -444,77 +444,16 @@ def fused_experts(hidden, w1, w1_scale, w2, w2_scale, topk_weights, topk_ids,
 
 # ------------------------------------------------- paged cache and attention
 # A decode step makes these calls for every layer, with kernels of a few
-# microseconds: the helpers below read each property of a tensor once.
+# microseconds: their arguments are read and checked in csrc/attn_calls.cpp.
 
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_bf16, _fp8, _f32, _i32 = torch.bfloat16, torch.float8_e4m3fn, torch.float32, torch.int32
-
-
-def _devices_differ(*ts):
-    for t in ts:
-        if t is not None and t.get_device() != ts[0].get_device() or ts[0].get_device() < 0:
-            raise ValueError("mxq operates on CUDA tensors of one device (got %s and %s)"
-                             % (ts[0].device, t.device))
+_calls = None
 
 
-def _heads3(name, t):
-    """t [n, heads, D] as the kernels read it, with unit inner stride, outer
-    strides of 16-byte multiples and at least D (copied only if needed):
-    (tensor, address, stride 0, stride 1)."""
-    if t.dtype is not _bf16:
-        raise TypeError("%s must be bf16" % name)
-    strides = t.stride()
-    if len(strides) != 3:
-        raise ValueError("%s must be [tokens, heads, head_dim], got %d dimensions"
-                         % (name, len(strides)))
-    s0, s1, s2 = strides
-    p = t.data_ptr()
-    # (the usual case in one test: all strides positive, 8 | s0, s1, 16 | p)
-    if s2 != 1 or p & 15 or (s0 | s1) & 7 or s1 < t.shape[2] or s0 < s1:
-        n0, n1, D = t.shape
-        if s2 != 1 or (n0 > 1 and (s0 < D or s0 & 7)) or (n1 > 1 and (s1 < D or s1 & 7)) or p & 15:
-            t = t.clone(memory_format=torch.contiguous_format)
-            s0, s1, _ = t.stride()
-            p = t.data_ptr()
-    return t, p, s0, s1
-
-
-def _caches(k, v, kv_heads, D):
-    """Tag, pages, page size, and the strides of k and v of a cache."""
-    shape = k.shape
-    if len(shape) != 4 or shape[3] != D or (kv_heads is not None and shape[2] != kv_heads):
-        raise ValueError("k_cache must be [pages, page_size, %s, %d], got %s"
-                         % ("kv_heads" if kv_heads is None else kv_heads, D, list(shape)))
-    dtype = k.dtype
-    if v.shape != shape or v.dtype is not dtype:
-        raise ValueError("k_cache and v_cache must have the same shape and dtype")
-    if dtype is not _bf16 and dtype is not _fp8:
-        raise TypeError("k_cache and v_cache must be bf16 or float8_e4m3fn")
-    k0, k1, k2, k3 = k.stride()
-    v0, v1, v2, v3 = v.stride()
-    if k3 != 1 or v3 != 1:
-        raise ValueError("k_cache and v_cache need a unit stride along the head dimension")
-    return (_lib.BF16 if dtype is _bf16 else _lib.E4M3, shape[0], shape[1], k0, k1, k2, v0, v1,
-            v2, shape[2])
-
-
-def _vec(name, t, dtype, n):
-    """The address of a contiguous vector of n elements (None for None)."""
-    if t is None:
-        return None
-    if t.dtype is not dtype or t.numel() != n or not t.is_contiguous():
-        raise ValueError("%s must be contiguous %s of %d elements" % (name, dtype, n))
-    return t.data_ptr()
-
-
-def _output(name, t, shape, dev):
-    """(tensor, address, stride 0, stride 1) of a given output or a new one."""
-    if t is None:
-        t = torch.empty(shape, dtype=_bf16, device=dev)
-    elif t.dtype is not _bf16 or t.shape != shape or t.stride(2) != 1:
-        raise ValueError("%s must be bf16 %s with a unit inner stride" % (name, list(shape)))
-    s0, s1, _ = t.stride()
-    return t, t.data_ptr(), s0, s1
+def _attn():
+    global _calls
+    if _calls is None:
+        _calls = _lib.load_calls(torch._C._cuda_getCurrentRawStream)
+    return _calls
 
 
 def rope_append_kv(k, v, k_cache, v_cache, slots, cos_sin=None, positions=None, q=None,
@@ -531,48 +470,8 @@ def rope_append_kv(k, v, k_cache, v_cache, slots, cos_sin=None, positions=None, 
     instead of (i, i + R/2).  Returns the rotated q (q_out if given; it may be
     q itself), or None without q.  q may hold k's heads too, where the rotated
     k is needed outside the cache (not in place then)."""
-    dev = k.get_device()
-    if not (dev >= 0 and v.get_device() == dev and k_cache.get_device() == dev
-            and v_cache.get_device() == dev and slots.get_device() == dev
-            and (cos_sin is None or cos_sin.get_device() == dev)
-            and (positions is None or positions.get_device() == dev)
-            and (q is None or q.get_device() == dev)
-            and (q_out is None or q_out.get_device() == dev)
-            and (k_scale is None or k_scale.get_device() == dev)
-            and (v_scale is None or v_scale.get_device() == dev)):
-        _devices_differ(k, v, k_cache, v_cache, slots, cos_sin, positions, q, q_out, k_scale,
-                        v_scale)
-    T, Hkv, D = shape = k.shape
-    if v.shape != shape:
-        raise ValueError("k and v must have the same shape")
-    k, kp, k0, k1 = _heads3("k", k)
-    v, vp, v0, v1 = _heads3("v", v)
-    cache = _caches(k_cache, v_cache, Hkv, D)
-    cp, rot, max_pos, pos = None, 0, 0, None
-    if cos_sin is not None:
-        if cos_sin.dim() != 2 or cos_sin.dtype != _f32 or not cos_sin.is_contiguous():
-            raise ValueError("cos_sin must be contiguous fp32 [max_pos, R]")
-        if positions is None:
-            raise ValueError("a rotation needs positions")
-        max_pos, rot = cos_sin.shape
-        cp, pos = cos_sin.data_ptr(), _vec("positions", positions, _i32, T)
-    qp = op = None
-    Hq = q0 = q1 = o0 = o1 = 0
-    if q is not None:
-        given = q.shape
-        if len(given) != 3 or given[0] != T or given[2] != D:
-            raise ValueError("q must be [%d, heads, %d]" % (T, D))
-        Hq = given[1]
-        q_in, qp, q0, q1 = _heads3("q", q)
-        q_out, op, o0, o1 = _output("q_out", q_out, given, k.device)
-    elif q_out is not None:
-        raise ValueError("q_out without q")
-    check(_lib.load().mxq_rope_append_kv(
-        qp, q0, q1, Hq, op, o0, o1, kp, k0, k1, vp, v0, v1, T, Hkv, D, cp, max_pos, rot, pos,
-        1 if interleaved else 0, _vec("slots", slots, torch.int64, T), k_cache.data_ptr(),
-        v_cache.data_ptr(), *cache[:9], _vec("k_scale", k_scale, _f32, Hkv),
-        _vec("v_scale", v_scale, _f32, Hkv), _raw_stream(dev)))
-    return q_out
+    return _attn().append(k, v, k_cache, v_cache, slots, cos_sin, positions, q, q_out, k_scale,
+                          v_scale, interleaved)
 
 
 def paged_attention_decode_workspace_size(batch: int, heads: int, kv_heads: int,
@@ -596,41 +495,8 @@ def paged_attention_decode(q, k_cache, v_cache, page_table, seq_lens, scale=None
     [B, Hq, D], with return_lse also the fp32 [B, Hq] log-sum-exp.  workspace:
     a caller's buffer of paged_attention_decode_workspace_size bytes (None:
     allocated here)."""
-    dev = q.get_device()
-    if not (dev >= 0 and k_cache.get_device() == dev and v_cache.get_device() == dev
-            and page_table.get_device() == dev and seq_lens.get_device() == dev
-            and (sinks is None or sinks.get_device() == dev)
-            and (k_scale is None or k_scale.get_device() == dev)
-            and (v_scale is None or v_scale.get_device() == dev)
-            and (out is None or out.get_device() == dev)
-            and (workspace is None or workspace.get_device() == dev)):
-        _devices_differ(q, k_cache, v_cache, page_table, seq_lens, sinks, k_scale, v_scale, out,
-                        workspace)
-    shape = q.shape
-    q, qp, q0, q1 = _heads3("q", q)
-    B, Hq, D = shape
-    cache = _caches(k_cache, v_cache, None, D)
-    Hkv = cache[9]
-    if page_table.dim() != 2 or page_table.dtype is not _i32:
-        raise ValueError("page_table must be int32 [%d, max_pages]" % B)
-    rows, width = page_table.shape
-    t0, t1 = page_table.stride()
-    if rows != B or (width > 1 and t1 != 1) or (rows > 1 and t0 < width):
-        raise ValueError("page_table must be int32 [%d, max_pages] with a unit inner stride" % B)
-    out, op, o0, o1 = _output("out", out, shape, q.device)
-    lse = torch.empty((B, Hq), dtype=_f32, device=q.device) if return_lse else None
-    if workspace is None:
-        workspace = torch.empty(paged_attention_decode_workspace_size(B, Hq, Hkv, D),
-                                dtype=torch.uint8, device=q.device)
-    check(_lib.load().mxq_paged_attention_decode(
-        qp, q0, q1, B, Hq, Hkv, D, k_cache.data_ptr(), v_cache.data_ptr(), *cache[:9],
-        page_table.data_ptr(), t0 if rows > 1 else width, width,
-        _vec("seq_lens", seq_lens, _i32, B), D ** -0.5 if scale is None else scale, window,
-        _vec("sinks", sinks, _f32, Hq), _vec("k_scale", k_scale, _f32, Hkv),
-        _vec("v_scale", v_scale, _f32, Hkv), op, o0, o1,
-        None if lse is None else lse.data_ptr(), workspace.data_ptr(), workspace.nbytes,
-        _raw_stream(dev)))
-    return (out, lse) if return_lse else out
+    return _attn().decode(q, k_cache, v_cache, page_table, seq_lens, scale, window, sinks, k_scale,
+                          v_scale, return_lse, out, workspace)
 
 
 def attention_varlen_workspace_size(tokens: int, batch: int, heads: int, kv_heads: int,
@@ -655,33 +521,5 @@ def attention_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k=None, scale=None, causa
     [Tq, Hq, D], with return_lse also the fp32 [Tq, Hq] log-sum-exp.
     workspace: a caller's buffer of attention_varlen_workspace_size bytes
     (None: allocated here)."""
-    dev = q.get_device()
-    if not (dev >= 0 and k.get_device() == dev and v.get_device() == dev
-            and cu_seqlens_q.get_device() == dev
-            and (cu_seqlens_k is None or cu_seqlens_k.get_device() == dev)
-            and (sinks is None or sinks.get_device() == dev)
-            and (out is None or out.get_device() == dev)
-            and (workspace is None or workspace.get_device() == dev)):
-        _devices_differ(q, k, v, cu_seqlens_q, cu_seqlens_k, sinks, out, workspace)
-    shape, kshape = q.shape, k.shape
-    q, qp, q0, q1 = _heads3("q", q)
-    k, kp, k0, k1 = _heads3("k", k)
-    v, vp, v0, v1 = _heads3("v", v)
-    Tq, Hq, D = shape
-    Tk, Hkv, Dk = kshape
-    if Dk != D or v.shape != kshape:
-        raise ValueError("k and v must be [tokens, kv_heads, %d] alike" % D)
-    B = cu_seqlens_q.numel() - 1
-    cq = _vec("cu_seqlens_q", cu_seqlens_q, _i32, B + 1)
-    ck = cq if cu_seqlens_k is None else _vec("cu_seqlens_k", cu_seqlens_k, _i32, B + 1)
-    out, op, o0, o1 = _output("out", out, shape, q.device)
-    lse = torch.empty((Tq, Hq), dtype=_f32, device=q.device) if return_lse else None
-    if workspace is None:
-        workspace = torch.empty(attention_varlen_workspace_size(Tq, B, Hq, Hkv, D),
-                                dtype=torch.uint8, device=q.device)
-    check(_lib.load().mxq_attention_varlen(
-        qp, q0, q1, kp, k0, k1, vp, v0, v1, cq, ck, B, Tq, Tk, Hq, Hkv, D,
-        D ** -0.5 if scale is None else scale, 1 if causal else 0, window,
-        _vec("sinks", sinks, _f32, Hq), op, o0, o1, None if lse is None else lse.data_ptr(),
-        workspace.data_ptr(), workspace.nbytes, _raw_stream(dev)))
-    return (out, lse) if return_lse else out
+    return _attn().prompt(q, k, v, cu_seqlens_q, cu_seqlens_k, scale, causal, window, sinks,
+                          return_lse, out, workspace)

@@ -7,6 +7,7 @@ libmxq.so``) by ``build.build()``.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 import threading
 
@@ -14,6 +15,7 @@ from . import build as _build
 
 _lock = threading.Lock()
 _lib = None
+_calls = None
 
 # status codes and tags (mirror include/mxq.h)
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_CUDA, ERR_TIMEOUT, ERR_DEVICE = range(6)
@@ -123,6 +125,27 @@ def load(build_if_missing: bool = True):
         _declare(lib)
         _lib = lib
         return lib
+
+
+def load_calls(raw_stream):
+    """Load _attn_calls.so (building it first if it does not exist) and give it
+    the library's entry points.  raw_stream: device index -> the current
+    stream's address."""
+    global _calls
+    lib = load()
+    with _lock:
+        if _calls is None:
+            if not os.path.exists(_build.CALLS):
+                _build.build()
+            spec = importlib.util.spec_from_file_location("_attn_calls", _build.CALLS)
+            mod = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(mod)
+            mod.connect(*[ctypes.cast(f, ctypes.c_void_p).value for f in (
+                lib.mxq_rope_append_kv, lib.mxq_paged_attention_decode,
+                lib.mxq_paged_attention_decode_workspace_size, lib.mxq_attention_varlen,
+                lib.mxq_attention_varlen_workspace_size)], check, raw_stream)
+            _calls = mod
+        return _calls
 
 
 def check(status: int) -> None:

@@ -3,6 +3,8 @@
 The translation units compile in parallel, then link into one shared library
 with the CUDA runtime linked statically.  The driver API (tensor-map encode)
 is reached through cudaGetDriverEntryPointByVersion, so no -lcuda is needed.
+Beside it goes _attn_calls.so, the Python calls of the attention operators
+(host code against torch's headers; it reaches libmxq.so by address).
 """
 from __future__ import annotations
 
@@ -11,6 +13,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -18,6 +21,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmxq.so")
+CALLS = os.path.join(PKG, "_attn_calls.so")
 
 SOURCES = ["api.cu", "quant.cu", "moe_aux.cu", "gemm_dense.cu", "gemm_moe.cu", "noalloc.cu",
            "prepack.cu", "attn_api.cu", "rope_append.cu", "attn_decode.cu", "attn_prompt.cu"]
@@ -39,9 +43,9 @@ def _inputs():
 
 
 def _stale() -> bool:
-    if not os.path.exists(LIB):
+    if not (os.path.exists(LIB) and os.path.exists(CALLS)):
         return True
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(CALLS))
     return any(os.path.getmtime(f) > t for f in _inputs())
 
 
@@ -55,13 +59,31 @@ def _compile(src: str, extra) -> str:
     return obj
 
 
+def _compile_calls() -> str:
+    import torch
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = CALLS + ".tmp%d" % os.getpid()
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+           "-fvisibility=hidden", "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI,
+           "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
+           "-I", sysconfig.get_paths()["include"], "-I", INCLUDE,
+           os.path.join(CSRC, "attn_calls.cpp"), "-o", tmp,
+           "-L", lib, "-lc10", "-ltorch_cpu", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("%s failed:\n%s\n%s" % (cmd[0], " ".join(cmd), r.stderr))
+    return tmp
+
+
 def build(force: bool = False, extra=(), verbose: bool = False) -> str:
     """Compile (if stale) and return the path of libmxq.so."""
     if not force and not _stale():
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     srcs = [os.path.join(CSRC, s) for s in SOURCES]
-    with cf.ThreadPoolExecutor(max_workers=len(srcs)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(srcs) + 1) as ex:
+        calls = ex.submit(_compile_calls)
         objs = list(ex.map(lambda s: _compile(s, list(extra)), srcs))
     tmp = LIB + ".tmp%d" % os.getpid()
     cmd = [nvcc(), *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
@@ -69,6 +91,7 @@ def build(force: bool = False, extra=(), verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError("link failed:\n%s\n%s" % (" ".join(cmd), r.stderr))
     os.replace(tmp, LIB)
+    os.replace(calls.result(), CALLS)
     if verbose:
         print("built", LIB, file=sys.stderr)
     return LIB
