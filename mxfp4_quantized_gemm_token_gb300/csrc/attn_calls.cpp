@@ -110,8 +110,8 @@ struct Heads {
     n = t.size(0), heads = t.size(1), D = t.size(2);
     s0 = t.stride(0), s1 = t.stride(1);
     p = t.data_ptr();
-    if (t.stride(2) != 1 || (n > 1 && (s0 < D || (s0 & 7))) || (heads > 1 && (s1 < D || (s1 & 7))) ||
-        (reinterpret_cast<uintptr_t>(p) & 15)) {
+    if (t.stride(2) != 1 || (n > 1 && (s0 < D || (s0 & 7))) ||
+        (heads > 1 && (s1 < D || (s1 & 7))) || (reinterpret_cast<uintptr_t>(p) & 15)) {
       copy = t.clone(at::MemoryFormat::Contiguous);
       s0 = copy.stride(0), s1 = copy.stride(1);
       p = copy.data_ptr();

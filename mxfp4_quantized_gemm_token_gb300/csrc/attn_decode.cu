@@ -15,8 +15,11 @@
 // running maximum, sum and accumulators, no block-wide barrier.  A
 // sequence that lies inside one part is written out by its warp; the others
 // leave at most two partial results per warp in the workspace, which
-// a second kernel joins in a fixed order.  A part's end that falls into a short
-// sequence moves to the nearer end of it: splitting a few steps costs more than it balances.
+// a second kernel joins in a fixed order.  A part's end that falls into a
+// sequence no longer than a part moves to the nearer end of it: splitting a few steps
+// costs more than it balances (24 sequences of 50-250 keys: 12.3 us; whole up to two
+// parts' steps 13.1, up to eight steps whatever the parts 16.0).  Where no sequence can be long, by
+// the page table's width or the window, all stay whole and there is no join.
 //
 // Arithmetic.  The G query heads of a key/value head are the rows of 16-row
 // tensor-core products (mma.sync m16n8k16: with at most 16 rows to a key the
@@ -49,7 +52,8 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kEntries = 2048;      // entries of the shared prefix table
 constexpr int kRows = 16;           // rows of a product
-constexpr int kWhole = 8;           // sequences of at most this many steps stay whole
+constexpr int kAllWhole = 9;        // calls whose sequences have at most this many steps: all whole
+constexpr int kWhole = 8;           // others: sequences of at most this many steps and a part's
 
 struct DecodeArgs {
   DecodeParams p;
@@ -58,6 +62,7 @@ struct DecodeArgs {
   int parts;                        // of the line, at most
   int min_steps;
   int join_rows;                    // rows of a block of the join: 8, or 1
+  bool all_whole;                   // no sequence is split
   bool alike;                       // both caches have the same page and token strides
   int64_t* cum;                     // workspace: steps before each sequence [B + 1], then `per`
   float2* part_ml;                  // [task][2][rows]
@@ -165,6 +170,11 @@ __device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
   return a / b;
 }
 
+// steps of the longest sequence that stays whole, with `per` steps a part
+__device__ __forceinline__ int whole_steps(int64_t per) {
+  return static_cast<int>(min(static_cast<int64_t>(kWhole), per));
+}
+
 // lens: the lengths in shared memory, where the prefix table has an entry for each sequence
 __device__ __forceinline__ int length_of(const DecodeArgs& a, const int* lens, int b) {
   return a.chunk == 1 ? lens[b] : a.p.seq_lens[b];
@@ -229,7 +239,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1) decode_kernel(const DecodeArgs
   const int workers = gridDim.x * kWarps;
   int64_t per = max(divide(total + a.parts - 1, a.parts), static_cast<int64_t>(a.min_steps));
   // sequences that stay whole: a part has room for the longest, or some get two
-  if (longest <= kWhole && per < longest) per = longest;
+  if ((a.all_whole || longest <= whole_steps(per)) && per < longest) per = longest;
+  const int whole = a.all_whole ? longest : whole_steps(per);
   for (int e = e0; e < min(a.entries, e0 + per_thread); ++e) {
     table[e] = before;
     for (int b = e * a.chunk; b < min(p.B, (e + 1) * a.chunk); ++b) {
@@ -255,7 +266,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) decode_kernel(const DecodeArgs
     }
     const int n = c->s.steps;
     c->step = static_cast<int>(pos - at);
-    if (n <= kWhole && c->step > 0) {
+    if (n <= whole && c->step > 0) {
       pos -= c->step;
       const bool up = 2 * c->step >= n;
       c->step = up ? n - 1 : 0;
@@ -722,7 +733,7 @@ __global__ void __launch_bounds__(32 * kWarps) decode_join_kernel(const DecodeAr
     const int64_t steps = a.cum[r.b + 1] - r.u0;
     r.w0 = divide(r.u0, per);
     r.w1 = divide(r.u0 + steps - 1, per);
-    r.split = steps > kWhole && r.w0 < r.w1 && r.gr < a.G;
+    r.split = steps > whole_steps(per) && r.w0 < r.w1 && r.gr < a.G;
     return r;
   };
   const int64_t first = static_cast<int64_t>(blockIdx.x) * a.join_rows;
@@ -786,15 +797,17 @@ cudaError_t launch(const DecodeArgs& a, int grid, cudaStream_t stream) {
     configured[dev] = true;
   }
   DecodeArgs b = a;
-  b.min_steps = 64 / S::KS;
+  b.min_steps = std::max(1, 32 / S::KS);
   b.parts = std::max(1, grid * kWarps / (a.p.Hkv * a.tiles));
-  e = launch_k(decode_kernel<D, FP8>, dim3(grid), dim3(32 * kWarps),
-               static_cast<size_t>(S::kSmem), stream, b);
-  if (e != cudaSuccess) return e;
-  // where every sequence stays whole, whatever the lengths, there is nothing to join
+  // Where no sequence can have more steps there is nothing to join, and a join's launch takes
+  // as long as eight steps (a window of 128 keys, D 128, 128 sequences: 32.0 us split and
+  // joined, 23.1 whole; 4 sequences: 10.0 and 10.8).
   int64_t keys = a.p.max_pages * a.p.page_size;
   if (a.p.window > 0) keys = std::min<int64_t>(keys, static_cast<int64_t>(a.p.window) + 15);
-  if (keys <= kWhole * S::KS) return cudaSuccess;
+  b.all_whole = keys <= kAllWhole * S::KS;
+  e = launch_k(decode_kernel<D, FP8>, dim3(grid), dim3(32 * kWarps),
+               static_cast<size_t>(S::kSmem), stream, b);
+  if (e != cudaSuccess || b.all_whole) return e;
   const int64_t rows = static_cast<int64_t>(a.p.B) * a.p.Hkv * a.tiles * a.rows;
   b.join_rows = rows <= 4 * grid ? 1 : kWarps;
   return launch_k(decode_join_kernel<D>,

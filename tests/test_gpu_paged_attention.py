@@ -204,12 +204,12 @@ def test_decode_window_and_sinks(window, fp8):
     run_decode(c, lens, window, None)
 
 
-@pytest.mark.parametrize("D,fp8,limit", [(64, False, 256), (64, True, 256), (128, False, 128),
-                                         (128, True, 256)])
+@pytest.mark.parametrize("D,fp8,limit", [(64, False, 288), (64, True, 288), (128, False, 144),
+                                         (128, True, 288)])
 def test_decode_where_sequences_stay_whole(D, fp8, limit):
     """Calls whose longest possible sequence is just short enough to be one
     warp's, and calls just past that: bounded by the page table, by the window."""
-    for n in (limit - 1, limit, limit + 1, limit + 16):
+    for n in (limit - 17, limit - 1, limit, limit + 1, limit + 16):
         q, kc, vc, table, lens, g = decode_case(n, [n, 3, n], 8, 2, D, 16, fp8)
         table = table[:, :-(-n // 16)]
         run_decode((q, kc, vc, table, lens, g), [n, 3, n])
@@ -217,6 +217,14 @@ def test_decode_where_sequences_stay_whole(D, fp8, limit):
     c = decode_case(D, lens, 8, 2, D, 16, fp8)
     for window in (limit - 16, limit - 15, limit - 14, limit):
         run_decode(c, lens, window)
+
+
+@pytest.mark.parametrize("D,fp8", [(64, False), (64, True), (128, False), (128, True)])
+def test_decode_many_short_among_long(D, fp8):
+    """Parts of one step and more, with sequences around a part's length."""
+    for B, longest in [(3, 400), (24, 250), (40, 90), (150, 333)]:
+        lens = [1 + (i * 97) % longest for i in range(B)]
+        run_decode(decode_case(B, lens, 8, 2, D, 16, fp8), lens)
 
 
 def test_decode_scales_and_large_scores():
