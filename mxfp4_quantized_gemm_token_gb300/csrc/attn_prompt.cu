@@ -86,14 +86,14 @@ struct __align__(8) PromptHeader {
 constexpr int kRowsPerItem = 2 * kBM;
 constexpr int kMinSplit = 8;         // items of at most this many blocks stay whole
 constexpr int kMaxSplitItems = 16;   // items per SM above which all do
+constexpr int kRankItems = 512;      // items of a call, before their heads, above which all do
 
 struct PromptArgs {
   PromptParams p;
   PromptHeader* header;              // in the workspace; null: one sequence, no list
   PromptItem* list;                  // what the CTAs work on
-  PromptItem* items;                 // the plan's own; null: items stay whole
-  PromptPiece* pieces;               // for the list's entries
-  int* start;                        // each part's first entry
+  PromptPiece* pieces;               // for the list's entries; null: items stay whole
+  int2* part;                        // each part's first entry, and one past its last
   int* done;                         // [item][8 warps]: finished pieces
   float2* part_ml;                   // [slot][256]: reference and sum
   float* part_o;                     // [slot][256][D]
@@ -135,43 +135,140 @@ __device__ __forceinline__ PromptItem make_item(const PromptParams& p, int token
   return it;
 }
 
-// Exclusive prefix sum over the block's 1024 threads, and the sum of all.
-__device__ __forceinline__ int block_scan(int v, int* sums, int* all) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int x = v;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
+// Writes the list's entries of one item, for its heads first, first + step, ...: whole at
+// rank * Hkv + head, or, with `per` blocks to a part, its pieces.  The line holds all
+// items' blocks, heads inside items (an item without keys counts as one block); `before`
+// of them, of one head, come before this item's.  The piece of item and head idx that
+// lies in part w is entry idx + w: a part's are adjacent, and each is placed without the others.
+__device__ __forceinline__ void list_item(const PromptArgs& a, PromptItem it, int rank, int before,
+                                          int total, int per, int first, int step) {
+  const int Hkv = a.p.Hkv;
+  if (per == 0) {
+    for (it.head = first; it.head < Hkv; it.head += step) a.list[rank * Hkv + it.head] = it;
+    return;
   }
-  if (lane == 31) sums[warp] = x;
-  __syncthreads();
-  int before = 0, total = 0;
-#pragma unroll
-  for (int w = 0; w < 32; ++w) {
-    if (w < warp) before += sums[w];
-    total += sums[w];
+  const int n = item_blocks(it), kb1 = it.kb1, line = total * Hkv;
+  const bool keys = it.kb1 > it.kb0;
+  for (int h = first; h < Hkv; h += step) {
+    const int idx = rank * Hkv + h, p0 = before * Hkv + h * n, p1 = p0 + n;
+    const int w0 = p0 / per, w1 = (p1 - 1) / per;
+    const bool whole = w0 == w1;
+    if (!whole)
+      for (int k = 0; k < 2; ++k) reinterpret_cast<int4*>(a.done)[idx * 2 + k] = {0, 0, 0, 0};
+    it.head = h + (whole ? 0 : kPiece);
+    for (int w = w0; w <= w1; ++w) {
+      const int from = max(p0, w * per), to = min(p1, (w + 1) * per);
+      if (keys) {
+        it.kb1 = kb1 - (from - p0);
+        it.kb0 = it.kb1 - (to - from);
+      }
+      a.list[idx + w] = it;
+      if (!whole)
+        a.pieces[idx + w] = {2 * w + (from == w * per ? 0 : 1), w0, w1,
+                             2 * idx + (w0 * per < p0 ? 1 : 0)};
+      if (from == w * per) a.part[w].x = idx + w;
+      if (to == min(line, (w + 1) * per)) a.part[w].y = idx + w + 1;
+    }
   }
-  __syncthreads();
-  *all = total;
-  return before + x - v;
 }
 
-// Lists the items, ordered by falling number of key blocks (a counting sort; more than
-// 511 blocks count as 511), and cuts them into pieces where one is too long.
+// Lists the items, ordered by falling number of key blocks, and cuts them into pieces
+// where one is too long.  An item's place is the number of items before it, by
+// comparison with each: for up to kRankItems of them no longer than the passes and
+// barriers of a sort, and the order, and with it the cuts, is always the same.  Bound by
+// the latency of one block's few steps, a call's first use of each instruction among
+// them: 5 us from the offsets to the kernel's first item (130 items; or 10 items cut into
+// pieces, which took 9 us by a counting sort and three prefix sums).
+__global__ void __launch_bounds__(1024) prompt_rank_kernel(const PromptArgs a) {
+  const PromptParams& p = a.p;
+  __shared__ __align__(16) unsigned long long keys[kRankItems];
+  __shared__ PromptItem items[kRankItems];
+  __shared__ int count, longest, all_blocks;
+  for (int i = threadIdx.x; i < kRankItems; i += 1024) keys[i] = 0;
+  if (threadIdx.x == 0) count = longest = all_blocks = 0;
+  pdl_wait();
+  pdl_launch_dependents();
+  __syncthreads();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int b = warp; b < p.B; b += 32) {
+    int q0, nq, k0, nk;
+    const bool okq = seq_range(p.cu_q, b, p.Tq, &q0, &nq);
+    const bool okk = seq_range(p.cu_k, b, p.Tk, &k0, &nk);
+    if (!(okq && okk)) {
+      if (lane == 0) atomicOr(p.status, kStatusBadIndex);
+      continue;
+    }
+    const int n = (nq + 2 * a.TB - 1) / (2 * a.TB);
+    int at = 0, sum = 0, most = 0;
+    if (lane == 0) at = atomicAdd(&count, n);
+    at = __shfl_sync(0xffffffffu, at, 0);
+    for (int i = lane; i < n && at + i < a.cap; i += 32) {
+      const PromptItem it = make_item(p, 2 * a.TB, q0, nq, k0, nk, i);
+      const int blocks = item_blocks(it);
+      items[at + i] = it;
+      keys[at + i] =
+          static_cast<unsigned long long>(blocks) << 32 | ~static_cast<uint32_t>(it.q_row);
+      sum += blocks;
+      most = max(most, blocks);
+    }
+    sum = __reduce_add_sync(0xffffffffu, sum);
+    most = __reduce_max_sync(0xffffffffu, most);
+    if (lane == 0) {
+      atomicAdd(&all_blocks, sum);
+      atomicMax(&longest, most);
+    }
+  }
+  __syncthreads();
+  const int n = min(count, a.cap), total = all_blocks;
+  const int share = (total * p.Hkv + a.grid - 1) / a.grid;    // of a CTA
+  const bool split =
+      a.pieces != nullptr && count <= a.cap && longest > kMinSplit && longest > share;
+  const int per = split ? max(kMinSplit / 2, share) : 0;
+  if (threadIdx.x == 0) {
+    // only offsets that run backwards give more items than there is room for
+    if (count > a.cap) atomicOr(p.status, kStatusBadIndex);
+    *a.header = {n * p.Hkv, per};
+  }
+  // eight, four or two threads compare an item with the others
+  const int threads = n <= 128 ? 8 : n <= 256 ? 4 : 2;
+  const int i = threadIdx.x / threads, sub = threadIdx.x & (threads - 1);
+  int rank = 0, before = 0;
+  if (i < n) {
+    const unsigned long long mine = keys[i];
+    // the keys of sequences that overlap, of offsets that run backwards, may be equal
+    auto count_key = [&](unsigned long long k, int j) {
+      const int first = (k > mine) | ((k == mine) & (j < i));
+      rank += first;
+      before += static_cast<int>(k >> 32) & -first;
+    };
+    for (int j = 2 * sub; j < n; j += 2 * threads) {
+      const ulonglong2 k = *reinterpret_cast<const ulonglong2*>(keys + j);
+      count_key(k.x, j);
+      count_key(k.y, j + 1);
+    }
+  }
+  for (int o = 1; o < threads; o <<= 1) {
+    rank += __shfl_xor_sync(0xffffffffu, rank, o);
+    before += __shfl_xor_sync(0xffffffffu, before, o);
+  }
+  if (i < n) list_item(a, items[i], rank, before, total, per, sub, threads);
+  // parts past the line's end are empty
+  if (split)
+    for (int w = (total * p.Hkv + per - 1) / per + threadIdx.x; w < a.grid; w += 1024)
+      a.part[w] = {0, 0};
+}
+
+// The list for more items: a counting sort (more than 511 blocks count as 511), whole items
+// only.
 __global__ void __launch_bounds__(1024) prompt_plan_kernel(const PromptArgs a) {
   const PromptParams& p = a.p;
-  const int tokens_per_item = 2 * a.TB;
   __shared__ int count[kBuckets];
-  __shared__ int sums[32], longest, all_blocks;
+  __shared__ int sums[kBuckets / 32];
   pdl_wait();
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   for (int i = threadIdx.x; i < kBuckets; i += blockDim.x) count[i] = 0;
-  if (threadIdx.x == 0) longest = all_blocks = 0;
   __syncthreads();
-  bool split = false;
-  int n_items = 0;
   for (int pass = 0; pass < 2; ++pass) {
     for (int b = warp; b < p.B; b += 32) {
       int q0, nq, k0, nk;
@@ -181,82 +278,39 @@ __global__ void __launch_bounds__(1024) prompt_plan_kernel(const PromptArgs a) {
         if (lane == 0) atomicOr(p.status, kStatusBadIndex);
         continue;
       }
-      const int pairs = (nq + tokens_per_item - 1) / tokens_per_item;
-      for (int i = lane; i < pairs; i += 32) {
-        PromptItem it = make_item(p, tokens_per_item, q0, nq, k0, nk, i);
-        const int bucket = kBuckets - 1 - min(kBuckets - 1, max(0, it.kb1 - it.kb0));
-        if (pass == 0) {
-          atomicAdd(&count[bucket], 1);
-          if (a.items != nullptr) {
-            atomicMax(&longest, item_blocks(it));
-            atomicAdd(&all_blocks, item_blocks(it));
-          }
-          continue;
-        }
-        const int at = atomicAdd(&count[bucket], 1);
-        if (at >= a.cap) continue;
-        if (split) {
-          a.items[at] = it;
-        } else {
-          for (; it.head < p.Hkv; ++it.head)
-            a.list[static_cast<int64_t>(at) * p.Hkv + it.head] = it;
-        }
+      const int n = (nq + 2 * a.TB - 1) / (2 * a.TB);
+      for (int i = lane; i < n; i += 32) {
+        PromptItem it = make_item(p, 2 * a.TB, q0, nq, k0, nk, i);
+        const int at = atomicAdd(
+            &count[kBuckets - 1 - min(kBuckets - 1, max(0, it.kb1 - it.kb0))], 1);
+        if (pass == 0 || at >= a.cap) continue;
+        for (; it.head < p.Hkv; ++it.head) a.list[static_cast<int64_t>(at) * p.Hkv + it.head] = it;
       }
     }
     __syncthreads();
-    if (pass == 0) {
-      int run;
-      const int c = threadIdx.x < kBuckets ? count[threadIdx.x] : 0;
-      const int at = block_scan(c, sums, &run);
-      if (threadIdx.x < kBuckets) count[threadIdx.x] = at;
-      n_items = min(run, a.cap);
-      if (threadIdx.x == 0) {
-        // only offsets that run backwards give more items than there is room for
-        if (run > a.cap) atomicOr(p.status, kStatusBadIndex);
-        *a.header = {n_items * p.Hkv, 0};
+    if (pass == 1) break;
+    // items before each bucket
+    int x = 0, c = 0;
+    if (threadIdx.x < kBuckets) {
+      x = c = count[threadIdx.x];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
       }
-      __syncthreads();
-      split = a.items != nullptr && run <= a.cap && longest > kMinSplit &&
-              longest > (all_blocks * p.Hkv + a.grid - 1) / a.grid;
+      if (lane == 31) sums[warp] = x;
     }
-  }
-  if (!split) return;
-  // the line of all items' blocks, heads inside items; an item without keys
-  // counts as one block
-  const int per = max(kMinSplit / 2, (all_blocks * p.Hkv + a.grid - 1) / a.grid);
-  int line = 0, entries = 0;
-  for (int i0 = 0; i0 < n_items * p.Hkv; i0 += 1024) {
-    const int idx = i0 + threadIdx.x, i = idx / p.Hkv;
-    const bool in = i < n_items;
-    PromptItem it = {};
-    if (in) it = a.items[i];
-    const int n = in ? item_blocks(it) : 0;
-    int sum;
-    const int p0 = line + block_scan(n, sums, &sum), p1 = p0 + n;
-    line += sum;
-    const int w0 = p0 / per, w1 = in ? (p1 - 1) / per : w0 - 1;
-    int e = entries + block_scan(w1 - w0 + 1, sums, &sum);
-    entries += sum;
-    if (!in) continue;
-    for (int k = 0; k < 8; ++k) a.done[idx * 8 + k] = 0;
-    const int kb1 = it.kb1;
-    const bool whole = w0 == w1, keys = it.kb1 > it.kb0;
-    it.head = idx - i * p.Hkv + (whole ? 0 : kPiece);
-    for (int w = w0; w <= w1; ++w, ++e) {
-      const int from = max(p0, w * per), to = min(p1, (w + 1) * per);
-      if (keys) {
-        it.kb1 = kb1 - (from - p0);
-        it.kb0 = it.kb1 - (to - from);
+    __syncthreads();
+    if (threadIdx.x < kBuckets) {
+      for (int w = 0; w < warp; ++w) x += sums[w];
+      count[threadIdx.x] = x - c;
+      if (threadIdx.x == kBuckets - 1) {
+        if (x > a.cap) atomicOr(p.status, kStatusBadIndex);
+        *a.header = {min(x, a.cap) * p.Hkv, 0};
       }
-      a.list[e] = it;
-      if (!whole) a.pieces[e] = {2 * w + (from == w * per ? 0 : 1), w0, w1,
-                                 2 * idx + (w0 * per < p0 ? 1 : 0)};
-      if (from == w * per) a.start[w] = e;
     }
+    __syncthreads();
   }
-  // parts past the line's end are empty
-  for (int w = (line + per - 1) / per + threadIdx.x; w <= a.grid; w += 1024) a.start[w] = entries;
-  if (threadIdx.x == 0) *a.header = {entries, per};
 }
 
 template <int D>
@@ -318,8 +372,9 @@ struct Items {
       else if (threadIdx.x == 0)
         atomicOr(a.p.status, kStatusBadIndex);
     } else {
-      // the first whole item's entry is read along with the header
+      // what the first entry needs is read along with the header
       const PromptItem guess = a.list[blockIdx.x];
+      const int2 part = a.pieces != nullptr ? a.part[blockIdx.x] : make_int2(0, 0);
       const PromptHeader head = *a.header;
       limit = head.n;
       parts = head.per > 0;
@@ -330,8 +385,8 @@ struct Items {
         ahead = guess;
         return;
       }
-      first = a.start[blockIdx.x];
-      limit = a.start[blockIdx.x + 1];
+      first = part.x;
+      limit = part.y;
     }
     fetch();
   }
@@ -844,26 +899,25 @@ int64_t max_items(int64_t Tq, int64_t B, int Hq, int Hkv) {
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
 struct PromptSpace {
-  size_t list, items, pieces, start, done, ml, o, total;   // offsets
+  size_t list, pieces, part, done, ml, o, total;   // offsets
   bool split;
 };
 PromptSpace prompt_space(int64_t Tq, int64_t B, int Hq, int Hkv, int D, int num_sms) {
   const size_t items = static_cast<size_t>(max_items(Tq, B, Hq, Hkv)), n = items * Hkv;
   PromptSpace s;
-  s.split = n <= static_cast<size_t>(kMaxSplitItems) * num_sms;
+  s.split = items <= kRankItems && n <= static_cast<size_t>(kMaxSplitItems) * num_sms;
   size_t at = 256;
   auto take = [&](size_t bytes) {
     const size_t here = at;
     at += round256(bytes);
     return here;
   };
-  // every part's end may cut an item
+  // with an entry more for each part
   s.list = take((n + (s.split ? num_sms : 0)) * sizeof(PromptItem));
-  s.items = s.pieces = s.start = s.done = s.ml = s.o = at;
+  s.pieces = s.part = s.done = s.ml = s.o = at;
   if (s.split) {
-    s.items = take(items * sizeof(PromptItem));
     s.pieces = take((n + num_sms) * sizeof(PromptPiece));
-    s.start = take((num_sms + 1) * sizeof(int));
+    s.part = take(num_sms * sizeof(int2));
     s.done = take(n * 8 * sizeof(int));
     const size_t rows = static_cast<size_t>(num_sms) * 2 * kRowsPerItem;
     s.ml = take(rows * sizeof(float2));
@@ -917,9 +971,8 @@ cudaError_t launch_prompt(const PromptParams& p, int num_sms, cudaStream_t strea
     a.list = reinterpret_cast<PromptItem*>(ws + space.list);
   }
   if (split) {
-    a.items = reinterpret_cast<PromptItem*>(ws + space.items);
     a.pieces = reinterpret_cast<PromptPiece*>(ws + space.pieces);
-    a.start = reinterpret_cast<int*>(ws + space.start);
+    a.part = reinterpret_cast<int2*>(ws + space.part);
     a.done = reinterpret_cast<int*>(ws + space.done);
     a.part_ml = reinterpret_cast<float2*>(ws + space.ml);
     a.part_o = reinterpret_cast<float*>(ws + space.o);
@@ -946,7 +999,8 @@ cudaError_t launch_prompt(const PromptParams& p, int num_sms, cudaStream_t strea
       !map3(&maps.v, keys ? p.v : p.q, p.Hkv, keys ? p.Tk : 1, p.v_t, keys ? p.v_h : p.D, 1, kBM))
     return cudaErrorInvalidValue;
   if (!alone) {
-    const cudaError_t e = launch_k(prompt_plan_kernel, dim3(1), dim3(1024), 0, stream, a);
+    const cudaError_t e = launch_k(most <= kRankItems ? prompt_rank_kernel : prompt_plan_kernel,
+                                   dim3(1), dim3(1024), 0, stream, a);
     if (e != cudaSuccess) return e;
   }
   return p.D == 128 ? launch<128>(maps, a, stream) : launch<64>(maps, a, stream);

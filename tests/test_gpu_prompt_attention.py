@@ -115,6 +115,37 @@ def test_many_sequences():
     check(lens, lens, 4, 2, 64, seed=12)
 
 
+@pytest.mark.parametrize("B", [128, 129, 256, 257, 505, 600])
+def test_any_number_of_items(B):
+    """The list's order, with each number of threads an item and by both ways."""
+    nq = [1 + (i * 7) % 3 for i in range(B)]
+    nk = [n + (i * 131) % 300 for i, n in enumerate(nq)]
+    check(nq, nk, 4, 2, 64, seed=13)
+
+
+def test_pieces_repeat_bit_for_bit():
+    """Items of equal length, cut and joined, in the same places each time."""
+    g = gen(23)
+    nq, nk = [90] * 5, [3000] * 5
+    q, k, v = randn(g, 450, 8, 128), randn(g, 15000, 2, 128), randn(g, 15000, 2, 128)
+    runs = [mxq.attention_varlen(q, k, v, offsets(nq), offsets(nk)) for _ in range(8)]
+    mxq.sync_status()
+    assert all(torch.equal(runs[0], r) for r in runs[1:])
+
+
+def test_offsets_that_run_backwards_are_reported():
+    """Sequences that overlap, in more items than there is room for."""
+    g = gen(24)
+    q, k, v = randn(g, 50, 32, 64), randn(g, 50, 1, 64), randn(g, 50, 1, 64)
+    cu = torch.tensor([0, 50] * 40, device="cuda", dtype=torch.int32)
+    mxq.sync_status()
+    mxq.attention_varlen(q, k, v, cu)
+    with pytest.raises(mxq.MxqError) as e:
+        mxq.sync_status()
+    assert e.value.status == _lib.ERR_DEVICE
+    check([50], [50], 32, 1, 64)
+
+
 def test_other_sequences_do_not_reach_in():
     """Neighbours and rows outside every sequence hold NaN and infinities."""
     g = gen(13)
