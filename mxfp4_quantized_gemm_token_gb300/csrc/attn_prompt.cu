@@ -35,6 +35,15 @@
 // CTA, and whichever warp is the last to finish its 32 rows of an item joins them,
 // in the parts' order, so the result does not depend on who was last.  One
 // sequence with enough rows needs no list: its items are in order as they stand.
+//
+// Bound.  Arithmetic: 4 D operations a visible (query head, key) pair, on the
+// tensor cores at best.  One causal prompt of 8192 tokens, 32 query and 8 key/value
+// heads of 128: 328 us, 1.67 PFLOP/s, 86 % of a plain bf16 product's burst rate (350 us
+// when run for seconds, 90 % of its sustained rate under the power limit); the tensor pipe is
+// busy 71 % of the time, the rest is the chain scores -> maximum -> weights -> product of each
+// tile, ~3000 cycles for a block of both against 2048 of products.  11 packed prompts of 8192
+// tokens: 81 us (42 at the burst rate); here an item's beginning and end count, ~2 us.
+// Two chunks of 300 rows over 7892 keys, in pieces: 71 us (40).
 #include <cuda_bf16.h>
 #include <math.h>
 
