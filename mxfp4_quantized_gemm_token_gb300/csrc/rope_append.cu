@@ -35,9 +35,13 @@ namespace mxq {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kUnroll = 3;   // heads of a thread in a step
 constexpr int kStages = 3;   // steps in shared memory
-constexpr int kBlocks = 5;   // per SM
+
+// Blocks per SM by the heads a thread takes in a step.  A token of few heads has a step
+// of one or two: more blocks, with fewer tokens each (1777 tokens of 24 + 2 x 3 heads of
+// 64: 5.0 us with one, 6.2 with steps of three; 3000 tokens of 16 + 2 x 4 heads of 128:
+// 8.2 with two, 8.5 with three).
+constexpr int blocks_of(int unroll) { return unroll == 1 ? 6 : 5; }
 
 __device__ __forceinline__ void unpack8(const uint4& w, float* v) {
   const uint32_t a[4] = {w.x, w.y, w.z, w.w};
@@ -96,8 +100,10 @@ __device__ __forceinline__ void copy16(void* dst, const void* src) {
                : "memory");
 }
 
-template <bool FP8>
-__global__ void __launch_bounds__(kThreads, kBlocks) rope_append_kernel(const RopeAppendParams p) {
+// kUnroll: heads of a thread in a step
+template <bool FP8, int kUnroll>
+__global__ void __launch_bounds__(kThreads, blocks_of(kUnroll))
+    rope_append_kernel(const RopeAppendParams p) {
   __shared__ uint4 ring[kStages][kUnroll][2][kThreads];
   const int nchunk = p.D / 16;
   const int lanes = kThreads / nchunk;         // heads a block takes at once
@@ -249,14 +255,25 @@ __global__ void __launch_bounds__(kThreads, kBlocks) rope_append_kernel(const Ro
   asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
+template <bool FP8, int kUnroll>
+cudaError_t launch(const RopeAppendParams& p, int num_sms, cudaStream_t stream) {
+  const int64_t cap = static_cast<int64_t>(num_sms) * blocks_of(kUnroll);
+  const unsigned blocks = static_cast<unsigned>(p.T < cap ? p.T : cap);
+  return launch_k(rope_append_kernel<FP8, kUnroll>, dim3(blocks), dim3(kThreads), 0, stream, p);
+}
+
+template <bool FP8>
+cudaError_t launch_unroll(const RopeAppendParams& p, int num_sms, cudaStream_t stream) {
+  const int64_t parts = (p.Hq + 2 * static_cast<int64_t>(p.Hkv)) * (p.D / 16);
+  if (parts <= kThreads) return launch<FP8, 1>(p, num_sms, stream);
+  if (parts <= 2 * kThreads) return launch<FP8, 2>(p, num_sms, stream);
+  return launch<FP8, 3>(p, num_sms, stream);
+}
+
 }  // namespace
 
 cudaError_t launch_rope_append(const RopeAppendParams& p, int num_sms, cudaStream_t stream) {
-  const int64_t cap = static_cast<int64_t>(num_sms) * kBlocks;
-  const unsigned blocks = static_cast<unsigned>(p.T < cap ? p.T : cap);
-  if (p.fp8)
-    return launch_k(rope_append_kernel<true>, dim3(blocks), dim3(kThreads), 0, stream, p);
-  return launch_k(rope_append_kernel<false>, dim3(blocks), dim3(kThreads), 0, stream, p);
+  return p.fp8 ? launch_unroll<true>(p, num_sms, stream) : launch_unroll<false>(p, num_sms, stream);
 }
 
 }  // namespace mxq

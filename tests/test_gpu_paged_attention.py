@@ -58,6 +58,9 @@ def rotate_ref(x, cs, rot, interleaved):
     (9, 20, 4, 192, 0, 16, True, False, False),      # no rotation
     (300, 12, 1, 512, 64, 64, False, False, False),
     (11, 7, 7, 48, 16, 3, True, False, False),       # threads per head not a power of two
+    (2000, 12, 2, 64, 64, 16, False, True, True),    # more tokens than blocks: few heads,
+    (1600, 16, 4, 128, 64, 16, True, False, False),  # more,
+    (1000, 32, 8, 128, 128, 32, False, False, False),    # many
 ])
 def test_append_bit_exact(T, H, KV, D, rot, page, fp8, inter, major):
     g = gen(T)
