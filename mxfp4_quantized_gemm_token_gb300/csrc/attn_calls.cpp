@@ -12,12 +12,13 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cmath>
 #include <cstdint>
+#include <exception>
 #include <initializer_list>
-#include <stdexcept>
 #include <string>
 
 #include "mxq.h"
@@ -206,8 +207,9 @@ PyObject* guarded(Py_ssize_t given, Py_ssize_t wanted, F f) {
     if (given != wanted) refuse(PyExc_TypeError, "wrong number of arguments");
     return f();
   } catch (const Raised&) {
-  } catch (const std::exception& e) {
-    PyErr_SetString(PyExc_RuntimeError, e.what());
+  } catch (const std::exception&) {
+    // torch's own, such as its out-of-memory error
+    torch::translate_exception_to_python(std::current_exception());
   }
   return nullptr;
 }
