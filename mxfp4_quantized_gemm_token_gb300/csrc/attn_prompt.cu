@@ -714,16 +714,22 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
 #pragma unroll
         for (int q = 0; q < 4; ++q) tmem_ld32_async(tS + 32 * q, x + 32 * q);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          float* v = x + 32 * q;
-          tmem_wait32(v);
-          const int kq = k0 + 32 * q;
-          if (kq + 32 > all_hi || kq < all_lo) {
-            // a warp's rows span few positions: most chunks need no mask
+        for (int q = 0; q < 4; ++q) tmem_wait32(x + 32 * q);
+        if (__builtin_expect(k0 + kBM > all_hi || k0 < all_lo, 0)) {
+          // a warp's rows span few positions: most blocks need no mask
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int kq = k0 + 32 * q;
+            if (kq + 32 <= all_hi && kq >= all_lo) continue;
             const uint32_t vis = low_bits(hi - kq) & ~low_bits(lo - kq);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) v[e] = (vis >> e) & 1 ? v[e] : -INFINITY;
+            for (int e = 0; e < 32; ++e)
+              x[32 * q + e] = (vis >> e) & 1 ? x[32 * q + e] : -INFINITY;
           }
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const float* v = x + 32 * q;
           mq[q] = fmaxf(v[0], v[1]);
 #pragma unroll
           for (int e = 2; e < 32; e += 2) mq[q] = fmaxf(mq[q], fmaxf(v[e], v[e + 1]));
