@@ -774,7 +774,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         }
         // weights, in two halves of 64 keys; the first is handed over a little
         // into the second, when its store is surely complete
-        uint64_t sum[4] = {};
+        uint64_t sum[4];
         auto weights = [&](uint32_t* w, int first, int last) {
 #pragma unroll
           for (int e = first; e < last; e += 2) {
@@ -782,7 +782,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             unpack2(fma2(pack2(x[e], x[e + 1]), c2, n2), &u, &v);
             u = ex2(u), v = ex2(v);
             w[(e & 63) / 2] = bf16x2(u, v);
-            sum[(e / 2) & 3] = add2(sum[(e / 2) & 3], pack2(u, v));
+            sum[(e / 2) & 3] = e < 8 ? pack2(u, v) : add2(sum[(e / 2) & 3], pack2(u, v));
           }
         };
         auto hand_over = [&](int part) {
