@@ -38,12 +38,12 @@
 //
 // Bound.  Arithmetic: 4 D operations a visible (query head, key) pair, on the
 // tensor cores at best.  One causal prompt of 8192 tokens, 32 query and 8 key/value
-// heads of 128: 328 us, 1.67 PFLOP/s, 86 % of a plain bf16 product's burst rate (350 us
-// when run for seconds, 90 % of its sustained rate under the power limit); the tensor pipe is
-// busy 71 % of the time, the rest is the chain scores -> maximum -> weights -> product of each
+// heads of 128: 323 us, 1.70 PFLOP/s, 87 % of a plain bf16 product's burst rate (346 us
+// when run for seconds, 92 % of its sustained rate under the power limit); the tensor pipe is
+// busy 72 % of the time, the rest is the chain scores -> maximum -> weights -> product of each
 // tile, ~3000 cycles for a block of both against 2048 of products.  11 packed prompts of 8192
-// tokens: 81 us (42 at the burst rate); here an item's beginning and end count, ~2 us.
-// Two chunks of 300 rows over 7892 keys, in pieces: 71 us (40).
+// tokens: 80 us (42 at the burst rate); here an item's beginning and end count, ~2 us.
+// Two chunks of 300 rows over 7892 keys, in pieces: 70 us (40).
 #include <cuda_bf16.h>
 #include <math.h>
 
@@ -716,7 +716,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
 #pragma unroll
         for (int q = 0; q < 4; ++q) tmem_wait32(x + 32 * q);
         if (__builtin_expect(k0 + kBM > all_hi || k0 < all_lo, 0)) {
-          // a warp's rows span few positions: most blocks need no mask
+          // A warp's rows span few positions: most blocks need no mask.  One test a block,
+          // out of line: the loop is short of instructions (a test for each 32 keys: D 128 1 %
+          // slower, D 64 6 %).
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             const int kq = k0 + 32 * q;

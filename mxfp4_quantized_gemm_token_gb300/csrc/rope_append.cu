@@ -39,7 +39,7 @@ constexpr int kStages = 3;   // steps in shared memory
 
 // Blocks per SM by the heads a thread takes in a step.  A token of few heads has a step
 // of one or two: more blocks, with fewer tokens each (1777 tokens of 24 + 2 x 3 heads of
-// 64: 5.0 us with one, 6.2 with steps of three; 3000 tokens of 16 + 2 x 4 heads of 128:
+// 64: 5.1 us with one, 6.2 with steps of three; 3000 tokens of 16 + 2 x 4 heads of 128:
 // 8.2 with two, 8.5 with three).
 constexpr int blocks_of(int unroll) { return unroll == 1 ? 6 : 5; }
 
