@@ -550,7 +550,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     if (warp == 9) {
       // ------------------------------------------------------------ loads
       if (lane == 0 && !a.inject_stall) {
-        uint32_t fill = 0, nq = 0;
+        uint32_t fill = 0, nq[2] = {0, 0};              // copies of K and V, of each tile's Q
         const uint32_t q_bytes = static_cast<uint32_t>(a.G * a.TB) * 128 * L::kChunks;
         bool ok = true;
         Items items(a);
@@ -559,11 +559,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           const int hk = it.head & ~kPiece;
           if (it.kb1 <= it.kb0) continue;
           auto load_q = [&](int s) {
-            if (!mbar_wait(&q_empty[s], (nq & 1) ^ 1, wc)) return false;
+            if (!mbar_wait(&q_empty[s], (nq[s] & 1) ^ 1, wc)) return false;
             mbar_expect_tx(&q_full[s], q_bytes);
             for (int c = 0; c < L::kChunks; ++c)
               tma_load_3d(sQ + s * L::kTileBytes + c * L::kChunkBytes, &maps.q, &q_full[s], c * 64,
                           hk * a.G, it.q_row + s * a.TB);
+            ++nq[s];
             return true;
           };
           auto load_kv = [&](const CUtensorMap* map, int kb) {
@@ -578,19 +579,17 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           };
           ok = load_q(0) && load_kv(&maps.k, it.kb1 - 1) && load_q(1) &&
                load_kv(&maps.v, it.kb1 - 1);
-          ++nq;
           for (int kb = it.kb1 - 2; ok && kb >= it.kb0; --kb)
             ok = load_kv(&maps.k, kb) && load_kv(&maps.v, kb);
         }
-        if (*abort_flag) {
-          // let every copy already issued land before the CTA goes away
-          volatile int zero = 0;
-          WaitCtx dw{p.status, &zero, 1000000000ull};
-          for (uint32_t i = fill > ST ? fill - ST : 0; i < fill; ++i)
-            mbar_wait(&kv_full[i % ST], (i / ST) & 1, dw);
-          for (int s = 0; s < 2; ++s)
-            if (nq > 0) mbar_wait(&q_full[s], (nq - 1) & 1, dw);
-        }
+        // Every copy issued lands before the CTA goes away, whichever wait of whichever warp
+        // gives up, and when.
+        volatile int zero = 0;
+        WaitCtx dw{p.status, &zero, 1000000000ull};
+        for (uint32_t i = fill > ST ? fill - ST : 0; i < fill; ++i)
+          mbar_wait(&kv_full[i % ST], (i / ST) & 1, dw);
+        for (int s = 0; s < 2; ++s)
+          if (nq[s] > 0) mbar_wait(&q_full[s], (nq[s] - 1) & 1, dw);
       }
     } else if (warp == 8) {
       // -------------------------------------------------------------- MMAs
@@ -671,13 +670,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         ++nq;
       }
     mma_done:
-      if (*abort_flag) {
-        // wait for the MMAs in flight before the tensor memory is freed
-        if (leader) mma_commit(drain);
-        volatile int zero = 0;
-        WaitCtx dw{p.status, &zero, 1000000000ull};
-        mbar_wait(drain, 0, dw);
-      }
+      // the products in flight end before the tensor memory is freed, as above
+      if (leader) mma_commit(drain);
+      volatile int zero = 0;
+      WaitCtx dw{p.status, &zero, 1000000000ull};
+      mbar_wait(drain, 0, dw);
     }
   } else {
     // ----------------------------------------------------------- softmax
