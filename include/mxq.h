@@ -504,7 +504,8 @@ mxq_status mxq_paged_attention_decode_workspace_size(int64_t B, int32_t Hq, int3
  * sequence never reach another's output, whatever they hold; within a
  * sequence a value that is not finite may reach any of its rows, as
  * 0 * inf is not 0.  Offsets that decrease or leave [0, Tq] or [0, Tk] make
- * their sequence empty and set MXQ_ERR_DEVICE for mxq_sync_status.
+ * their sequence empty and set MXQ_ERR_DEVICE for mxq_sync_status; where the
+ * others then overlap in more rows than Tq, it is not defined which are computed.
  * B == 0 or Tq == 0 is a no-op.
  */
 mxq_status mxq_attention_varlen(const void* q, int64_t sq_t, int64_t sq_h, const void* k,

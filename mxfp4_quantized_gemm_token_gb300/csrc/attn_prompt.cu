@@ -268,11 +268,15 @@ __global__ void __launch_bounds__(1024) prompt_rank_kernel(const PromptArgs a) {
 }
 
 // The list for more items: a counting sort (more than 511 blocks count as 511), whole items
-// only.
+// only.  Sequences that overlap, of offsets that run backwards, may have more items than there
+// is room for, up to 2^44: they are added up in 64 bits, none is counted past the room, and
+// then none is listed.
 __global__ void __launch_bounds__(1024) prompt_plan_kernel(const PromptArgs a) {
   const PromptParams& p = a.p;
   __shared__ int count[kBuckets];
   __shared__ int sums[kBuckets / 32];
+  __shared__ unsigned long long all_items;
+  if (threadIdx.x == 0) all_items = 0;
   pdl_wait();
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -288,16 +292,29 @@ __global__ void __launch_bounds__(1024) prompt_plan_kernel(const PromptArgs a) {
         continue;
       }
       const int n = (nq + 2 * a.TB - 1) / (2 * a.TB);
+      if (pass == 0) {
+        unsigned long long before = 0;
+        if (lane == 0) before = atomicAdd(&all_items, static_cast<unsigned long long>(n));
+        before = __shfl_sync(0xffffffffu, before, 0);
+        if (before + n > static_cast<unsigned long long>(a.cap)) continue;
+      }
       for (int i = lane; i < n; i += 32) {
         PromptItem it = make_item(p, 2 * a.TB, q0, nq, k0, nk, i);
         const int at = atomicAdd(
             &count[kBuckets - 1 - min(kBuckets - 1, max(0, it.kb1 - it.kb0))], 1);
-        if (pass == 0 || at >= a.cap) continue;
+        if (pass == 0) continue;
         for (; it.head < p.Hkv; ++it.head) a.list[static_cast<int64_t>(at) * p.Hkv + it.head] = it;
       }
     }
     __syncthreads();
     if (pass == 1) break;
+    if (all_items > static_cast<unsigned long long>(a.cap)) {
+      if (threadIdx.x == 0) {
+        atomicOr(p.status, kStatusBadIndex);
+        *a.header = {0, 0};
+      }
+      return;
+    }
     // items before each bucket
     int x = 0, c = 0;
     if (threadIdx.x < kBuckets) {
@@ -313,10 +330,7 @@ __global__ void __launch_bounds__(1024) prompt_plan_kernel(const PromptArgs a) {
     if (threadIdx.x < kBuckets) {
       for (int w = 0; w < warp; ++w) x += sums[w];
       count[threadIdx.x] = x - c;
-      if (threadIdx.x == kBuckets - 1) {
-        if (x > a.cap) atomicOr(p.status, kStatusBadIndex);
-        *a.header = {min(x, a.cap) * p.Hkv, 0};
-      }
+      if (threadIdx.x == kBuckets - 1) *a.header = {x * p.Hkv, 0};
     }
     __syncthreads();
   }
