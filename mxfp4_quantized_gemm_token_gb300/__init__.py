@@ -50,10 +50,23 @@ def _stream(device):
     return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
 
 
+def _need_current(index):
+    # the library launches on the current device, whatever the pointers' and the stream's is
+    current = torch.cuda.current_device()
+    if index != current:
+        raise ValueError("the tensors are on cuda:%d, the current device is cuda:%d"
+                         % (index, current))
+
+
 def _need_cuda(*ts):
+    devices = set()
     for t in ts:
-        if t is not None and not t.is_cuda:
-            raise ValueError("mxq operates on CUDA tensors only (got a %s tensor)" % t.device)
+        if t is not None:
+            if not t.is_cuda:
+                raise ValueError("mxq operates on CUDA tensors only (got a %s tensor)" % t.device)
+            devices.add(t.get_device())
+    for index in devices:
+        _need_current(index)
 
 
 def set_option(option: int, value: int) -> None:
@@ -68,8 +81,9 @@ def get_option(option: int) -> int:
 
 def sync_status(device=None) -> None:
     """Synchronize the current stream and raise if a kernel flagged an error."""
-    device = device if device is not None else torch.cuda.current_device()
-    check(_lib_handle().mxq_sync_status(_stream(device)))
+    stream = torch.cuda.current_stream(device)
+    _need_current(stream.device.index)
+    check(_lib_handle().mxq_sync_status(ctypes.c_void_p(stream.cuda_stream)))
 
 
 # ------------------------------------------------------------ quantization
@@ -452,7 +466,7 @@ _calls = None
 def _attn():
     global _calls
     if _calls is None:
-        _calls = _lib.load_calls(torch._C._cuda_getCurrentRawStream)
+        _calls = _lib.load_calls(torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice)
     return _calls
 
 

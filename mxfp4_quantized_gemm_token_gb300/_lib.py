@@ -127,10 +127,10 @@ def load(build_if_missing: bool = True):
         return lib
 
 
-def load_calls(raw_stream):
+def load_calls(raw_stream, current_device):
     """Load _attn_calls.so (building it first if it does not exist) and give it
     the library's entry points.  raw_stream: device index -> the current
-    stream's address."""
+    stream's address; current_device: -> the current device's index."""
     global _calls
     lib = load()
     with _lock:
@@ -143,7 +143,8 @@ def load_calls(raw_stream):
             mod.connect(*[ctypes.cast(f, ctypes.c_void_p).value for f in (
                 lib.mxq_rope_append_kv, lib.mxq_paged_attention_decode,
                 lib.mxq_paged_attention_decode_workspace_size, lib.mxq_attention_varlen,
-                lib.mxq_attention_varlen_workspace_size)], check, raw_stream)
+                lib.mxq_attention_varlen_workspace_size)], check, raw_stream,
+                current_device)
             _calls = mod
         return _calls
 

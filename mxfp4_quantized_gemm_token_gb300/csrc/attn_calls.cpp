@@ -32,6 +32,7 @@ decltype(&mxq_attention_varlen) prompt_fn;
 decltype(&mxq_attention_varlen_workspace_size) prompt_size_fn;
 PyObject* check_fn;        // raises for a status
 PyObject* stream_fn;       // device index -> the current stream's address
+PyObject* device_fn;       // the current device's index
 
 struct Raised {};          // a Python exception is set
 
@@ -60,12 +61,22 @@ const at::Tensor& needed(const char* name, PyObject* o) {
   return *t;
 }
 
+// The tensors are on one device, and it is the current one: the entry points launch
+// there, whatever device the pointers and the stream belong to.
 void same_device(std::initializer_list<const at::Tensor*> ts) {
   const at::Tensor& first = **ts.begin();
   for (const at::Tensor* t : ts)
     if (t != nullptr && (!t->is_cuda() || t->device() != first.device()))
       refuse(PyExc_ValueError, "mxq operates on CUDA tensors of one device (got " +
                                    first.device().str() + " and " + t->device().str() + ")");
+  PyObject* r = PyObject_CallNoArgs(device_fn);
+  if (r == nullptr) throw Raised();
+  const long current = PyLong_AsLong(r);
+  Py_DECREF(r);
+  if (current == -1 && PyErr_Occurred()) throw Raised();
+  if (first.device().index() != current)
+    refuse(PyExc_ValueError, "the tensors are on " + first.device().str() +
+                                 ", the current device is cuda:" + std::to_string(current));
 }
 
 std::string shape_of(at::IntArrayRef s) {
@@ -344,11 +355,11 @@ PyObject* prompt(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   });
 }
 
-// (addresses of the five entry points, check, stream): once, before any call
+// (addresses of the five entry points, check, stream, device): once, before any call
 PyObject* connect(PyObject*, PyObject* args) {
   unsigned long long fn[5];
-  PyObject *c, *s;
-  if (!PyArg_ParseTuple(args, "KKKKKOO", &fn[0], &fn[1], &fn[2], &fn[3], &fn[4], &c, &s))
+  PyObject *c, *s, *d;
+  if (!PyArg_ParseTuple(args, "KKKKKOOO", &fn[0], &fn[1], &fn[2], &fn[3], &fn[4], &c, &s, &d))
     return nullptr;
   append_fn = reinterpret_cast<decltype(append_fn)>(fn[0]);
   decode_fn = reinterpret_cast<decltype(decode_fn)>(fn[1]);
@@ -357,6 +368,7 @@ PyObject* connect(PyObject*, PyObject* args) {
   prompt_size_fn = reinterpret_cast<decltype(prompt_size_fn)>(fn[4]);
   Py_XSETREF(check_fn, Py_NewRef(c));
   Py_XSETREF(stream_fn, Py_NewRef(s));
+  Py_XSETREF(device_fn, Py_NewRef(d));
   Py_RETURN_NONE;
 }
 
