@@ -196,7 +196,11 @@ mxq_stream_t stream_of(const at::Tensor& t) {
 // a caller's workspace, or a new one of `bytes`
 template <typename Size>
 at::Tensor workspace_of(const at::Tensor* given, const at::Tensor& like, Size bytes) {
-  if (given != nullptr) return *given;
+  if (given != nullptr) {
+    // an expanded tensor counts bytes that it does not have
+    if (!given->is_contiguous()) refuse(PyExc_ValueError, "workspace must be contiguous");
+    return *given;
+  }
   size_t n = 0;
   check(bytes(&n));
   return fresh({static_cast<int64_t>(n)}, at::kByte, like);

@@ -27,3 +27,24 @@ def test_prompts_that_overlap_in_many_items_are_reported():
     got = mxq.attention_varlen(q, k, v, torch.tensor([0, 700, 701, T], device="cuda").int())
     ref, _, b, _ = prompt_ref(q, k, v, lens, lens, 0.125)
     assert_within(got, ref, b, "out")
+
+
+def test_a_workspace_that_is_not_one_piece_is_refused():
+    """An expanded tensor has the bytes of one row, a strided one somebody else's between."""
+    g = gen(41)
+    q, k, v = randn(g, 40, 8, 64), randn(g, 40, 2, 64), randn(g, 40, 2, 64)
+    cu = torch.tensor([0, 10, 40], device="cuda").int()
+    cache = randn(g, 3, 16, 2, 64)
+    table, lens = (torch.ones(n, device="cuda").int() for n in ((40, 2), (40,)))
+    need = max(mxq.attention_varlen_workspace_size(40, 2, 8, 2, 64),
+               mxq.paged_attention_decode_workspace_size(40, 8, 2, 64))
+    for ws in (torch.zeros(1, 256, dtype=torch.uint8, device="cuda").expand(need // 256 + 1, 256),
+               torch.zeros(2 * need, dtype=torch.uint8, device="cuda")[::2]):
+        assert ws.nbytes >= need
+        with pytest.raises(ValueError, match="contiguous"):
+            mxq.attention_varlen(q, k, v, cu, workspace=ws)
+        with pytest.raises(ValueError, match="contiguous"):
+            mxq.paged_attention_decode(q, cache, cache, table, lens, workspace=ws)
+    whole = torch.zeros(need // 64 + 1, 64, dtype=torch.uint8, device="cuda")
+    assert torch.equal(mxq.attention_varlen(q, k, v, cu, workspace=whole),
+                       mxq.attention_varlen(q, k, v, cu))
