@@ -69,6 +69,13 @@ def _need_cuda(*ts):
         _need_current(index)
 
 
+def _need_whole(workspace):
+    # an expanded tensor counts bytes that it does not have
+    _need_cuda(workspace)
+    if workspace is not None and not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+
+
 def set_option(option: int, value: int) -> None:
     check(_lib_handle().mxq_set_option(option, int(value)))
 
@@ -203,6 +210,7 @@ def fp8_scaled_mm(a, w, w_scale, block_size=None, a_scale=None, bias=None,
         _need_cuda(a, w.tiles, a_scale, bias)
     else:
         _need_cuda(a, w, w_scale, a_scale, bias)
+    _need_whole(workspace)
     lib = _lib_handle()
     K = a.shape[-1]
     a2 = _as_rows(a)
@@ -414,6 +422,7 @@ def fused_experts(hidden, w1, w1_scale, w2, w2_scale, topk_weights, topk_ids,
     if activation not in ("silu", "swiglu_clamp"):
         raise ValueError("activation must be 'silu' or 'swiglu_clamp'")
     _need_cuda(hidden, w1, w1_scale, w2, w2_scale, topk_weights, topk_ids, w1_bias, w2_bias)
+    _need_whole(workspace)
     lib = _lib_handle()
     T, K = hidden.shape
     if hidden.stride(-1) != 1:
