@@ -665,9 +665,9 @@ struct JoinRow {
   static constexpr int N = D / 32;
   float m = -INFINITY, l = 0.f, o[N] = {};
   __device__ __forceinline__ void add(float pm, float pl, const float* v) {
-    const float n = fmaxf(m, pm);
-    if (n == -INFINITY) return;
-    const float f = ex2(m - n), g = ex2(pm - n);
+    // a part whose scores are all NaN has no reference, but a sum: it counts
+    const float n = fmaxf(m, pm), ref = n == -INFINITY ? 0.f : n;
+    const float f = ex2(m - ref), g = ex2(pm - ref);
     l = l * f + pl * g;
 #pragma unroll
     for (int i = 0; i < N; ++i) o[i] = o[i] * f + v[i] * g;

@@ -5,10 +5,11 @@ import torch
 
 import mxfp4_quantized_gemm_token_gb300 as mxq
 from mxfp4_quantized_gemm_token_gb300 import _lib
-from attention_util import assert_within, prompt_ref
-from test_gpu_prompt_attention import gen, randn
+from attention_util import assert_within, decode_ref, prompt_ref
+from test_gpu_paged_attention import decode_case, gen, randn
 
 pytestmark = pytest.mark.gpu
+NAN, INF = float("nan"), float("inf")
 
 
 def test_prompts_that_overlap_in_many_items_are_reported():
@@ -48,3 +49,36 @@ def test_a_workspace_that_is_not_one_piece_is_refused():
     whole = torch.zeros(need // 64 + 1, 64, dtype=torch.uint8, device="cuda")
     assert torch.equal(mxq.attention_varlen(q, k, v, cu, workspace=whole),
                        mxq.attention_varlen(q, k, v, cu))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("lens", [[6000, 40], [300] * 30 + [9000]])
+def test_a_query_that_is_not_a_number_shows(lens, fp8):
+    """Every score of the head's row is NaN, in whole sequences and in those that several
+    parts share."""
+    c = decode_case(44, lens, 8, 2, 128, 16, fp8)
+    q, kc, vc, table, n, g = c
+    ref, rl, b, bl = decode_ref(q, kc, vc, table, lens, 128 ** -0.5)
+    q = q.clone()
+    q[:, 5, 77] = NAN
+    out, lse = mxq.paged_attention_decode(q, kc, vc, table, n, return_lse=True)
+    assert bool(torch.isnan(out[:, 5]).all()) and bool(torch.isnan(lse[:, 5]).all())
+    rest = [0, 1, 2, 3, 4, 6, 7]
+    assert_within(out[:, rest], ref[:, rest], b[:, rest], "out")
+    assert_within(lse[:, rest], rl[:, rest], bl[:, rest], "lse")
+
+
+@pytest.mark.parametrize("nq,nk", [([300], [300]), ([40, 9], [20000, 9])])
+def test_a_prompt_row_that_is_not_a_number_shows(nq, nk):
+    """The same in whole items and in pieces."""
+    g = gen(45)
+    q, k, v = randn(g, sum(nq), 8, 128), randn(g, sum(nk), 2, 128), randn(g, sum(nk), 2, 128)
+    ref, rl, b, bl = prompt_ref(q, k, v, nq, nk, 128 ** -0.5)
+    q[7, 5, 77] = NAN
+    cu = [torch.tensor([0, *n], device="cuda").cumsum(0).int() for n in (nq, nk)]
+    out, lse = mxq.attention_varlen(q, k, v, *cu, return_lse=True)
+    assert bool(torch.isnan(out[7, 5]).all()) and bool(torch.isnan(lse[7, 5]))
+    rest = torch.ones(sum(nq), 8, dtype=torch.bool, device="cuda")
+    rest[7, 5] = False
+    assert_within(out[rest], ref[rest], b[rest], "out")
+    assert_within(lse[rest], rl[rest], bl[rest], "lse")
