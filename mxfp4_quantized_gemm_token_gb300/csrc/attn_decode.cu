@@ -423,7 +423,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) decode_kernel(const DecodeArgs
         // a new sequence: its q, and nothing summed yet
         fresh = false;
         opened = at.step == 0;
-        const float ks = p.k_scale != nullptr ? __ldg(p.k_scale + hk) : 1.f;
+        const float ks = FP8 && p.k_scale != nullptr ? __ldg(p.k_scale + hk) : 1.f;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           const int gr = tile * kRows + r0 + 8 * half;
@@ -449,7 +449,9 @@ __global__ void __launch_bounds__(32 * kWarps, 1) decode_kernel(const DecodeArgs
             big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
             // the power of two that brings the largest to [2^14, 2^15)
             const int e = big > 0.f && big < INFINITY ? min(max(14 - ilogbf(big), -100), 100) : 0;
-            const float up = copysignf(ldexpf(1.f, e), ks);
+            // the key scale's sign goes into q, and so does a scale of 0 or NaN: what
+            // multiplies the scores below stays positive and keeps a masked key's -inf
+            const float up = (ks > 0.f ? 1.f : ks < 0.f ? -1.f : ks) * ldexpf(1.f, e);
             unscale = ldexpf(1.f, -e);
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
@@ -469,9 +471,11 @@ __global__ void __launch_bounds__(32 * kWarps, 1) decode_kernel(const DecodeArgs
                         ? __ldg(reinterpret_cast<const uint32_t*>(q + 16 * k + 8 * i + 2 * quad))
                         : 0u;
           }
-          // > 0: the sign of a key scale goes into q, and a scale of 0 counts as next to
-          // nothing, so that it keeps a masked key's -inf
-          cs[half] = fmaxf(p.scale * fabsf(ks) * kLog2e * unscale, 1e-30f);
+          if constexpr (FP8)
+            // the scores of the scaled q are below 2^32: 1e-30 of them is nothing
+            cs[half] = fmaxf(p.scale * fabsf(ks) * kLog2e * unscale, 1e-30f);
+          else
+            cs[half] = p.scale * kLog2e;
           m[half] = -INFINITY;
           l[half] = 0.f;
         }

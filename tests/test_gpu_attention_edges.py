@@ -6,7 +6,7 @@ import torch
 import mxfp4_quantized_gemm_token_gb300 as mxq
 from mxfp4_quantized_gemm_token_gb300 import _lib
 from attention_util import assert_within, decode_ref, prompt_ref
-from test_gpu_paged_attention import decode_case, gen, randn
+from test_gpu_paged_attention import decode_case, gen, randn, run_decode
 
 pytestmark = pytest.mark.gpu
 NAN, INF = float("nan"), float("inf")
@@ -82,3 +82,46 @@ def test_a_prompt_row_that_is_not_a_number_shows(nq, nk):
     rest[7, 5] = False
     assert_within(out[rest], ref[rest], b[rest], "out")
     assert_within(lse[rest], rl[rest], bl[rest], "lse")
+
+
+LENS = [0, 1, 40, 300, 5000]
+
+
+@pytest.mark.parametrize("bad", [NAN, INF])
+@pytest.mark.parametrize("with_sinks", [False, True])
+def test_a_key_scale_that_is_not_finite_shows(bad, with_sinks):
+    """Rows that see a key are NaN, those without keys stay what they are, and the other
+    key/value head is not touched."""
+    c = decode_case(41, LENS, 8, 2, 128, 16, True)
+    q, kc, vc, table, n, g = c
+    sinks = torch.randn(8, generator=g, device="cuda") if with_sinks else None
+    ks = torch.tensor([0.02, bad], device="cuda")
+    out, lse = mxq.paged_attention_decode(q, kc, vc, table, n, sinks=sinks, k_scale=ks,
+                                          return_lse=True)
+    assert bool(torch.isnan(out[1:, 4:]).all())
+    if bad != bad:
+        assert bool(torch.isnan(lse[1:, 4:]).all())
+    assert not out[0].any()
+    assert torch.equal(lse[0], sinks if with_sinks else torch.full_like(lse[0], -INF))
+    ref, rl, b, bl = decode_ref(q, kc, vc, table, LENS, 128 ** -0.5, 0, sinks,
+                                torch.full((2,), 0.02, device="cuda"))
+    assert_within(out[:, :4], ref[:, :4], b[:, :4], "out")
+    assert_within(lse[:, :4], rl[:, :4], bl[:, :4], "lse")
+
+
+@pytest.mark.parametrize("window", [0, 70])
+@pytest.mark.parametrize("scales", [(0.0, 0.02), (-0.02, 0.01), (-0.0, -0.02)])
+def test_zero_and_negative_key_scales(scales, window):
+    """A scale of zero weighs every visible key alike."""
+    c = decode_case(42, LENS, 8, 2, 64, 16, True)
+    run_decode(c, LENS, window, None, torch.tensor(scales, device="cuda"),
+               torch.tensor([0.02, -0.01], device="cuda"))
+
+
+def test_a_small_scale_of_large_scores():
+    """bf16 keys whose products with q come near 1e37, and the scale that brings them
+    back to a few units."""
+    lens = [1, 200, 3000]
+    q, kc, vc, table, n, g = decode_case(43, lens, 8, 2, 64, 16, poison=False)
+    q, kc = (q.float() * 2.0 ** 60).bfloat16(), (kc.float() * 2.0 ** 60).bfloat16()
+    run_decode((q, kc, vc, table, n, g), lens, scale=2.0 ** -123)
