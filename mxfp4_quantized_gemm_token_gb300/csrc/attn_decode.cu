@@ -447,8 +447,9 @@ __global__ void __launch_bounds__(32 * kWarps, 1) decode_kernel(const DecodeArgs
             }
             big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
             big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
-            // the power of two that brings the largest to [2^14, 2^15)
-            const int e = big > 0.f && big < INFINITY ? min(max(14 - ilogbf(big), -100), 100) : 0;
+            // the power of two that brings the largest to [2^14, 2^15) (a largest below
+            // 2^-86: nearer to it; both powers are normal numbers)
+            const int e = big > 0.f && big < INFINITY ? min(14 - ilogbf(big), 100) : 0;
             // the key scale's sign goes into q, and so does a scale of 0 or NaN: what
             // multiplies the scores below stays positive and keeps a masked key's -inf
             const float up = (ks > 0.f ? 1.f : ks < 0.f ? -1.f : ks) * ldexpf(1.f, e);

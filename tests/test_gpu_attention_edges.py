@@ -125,3 +125,12 @@ def test_a_small_scale_of_large_scores():
     q, kc, vc, table, n, g = decode_case(43, lens, 8, 2, 64, 16, poison=False)
     q, kc = (q.float() * 2.0 ** 60).bfloat16(), (kc.float() * 2.0 ** 60).bfloat16()
     run_decode((q, kc, vc, table, n, g), lens, scale=2.0 ** -123)
+
+
+@pytest.mark.parametrize("power", [100, 118])
+def test_large_queries_over_an_e4m3_cache(power):
+    """q is scaled into the range of f16 whatever its size."""
+    lens = [1, 200, 3000]
+    q, kc, vc, table, n, g = decode_case(45, lens, 8, 2, 64, 16, True)
+    q = (q.float() * 2.0 ** power).bfloat16()
+    run_decode((q, kc, vc, table, n, g), lens, scale=2.0 ** -(power + 7))
