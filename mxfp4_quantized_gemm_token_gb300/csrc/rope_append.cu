@@ -23,8 +23,8 @@
 // with a division an element 49 us).  The quotient is x r + (x - x r s) r with
 // r = 1/s rounded (P. Markstein, "Computation of elementary functions on the IBM
 // RISC System/6000 processor", 1990): three operations an element instead of a
-// division's, and the same e4m3 codes as the division for 1.4e11 quotients, half
-// of them around the codes' midpoints.
+// division's, and the same e4m3 codes (tests compare six million quotients on and next
+// to the codes' midpoints).
 #include <cuda_bf16.h>
 
 #include "attn.h"
@@ -63,13 +63,15 @@ __device__ __forceinline__ uint4 pack8_bf16(const float* v) {
 }
 
 // e4m3 codes of 8 elements over the scale s; r = 1/s, or 0 where the quotient
-// has to be a division (the conversion itself clamps to +-448, NaN stays NaN)
+// has to be a division (the conversion itself clamps to +-448, NaN stays NaN).  The
+// residual is formed so that a zero keeps its sign: over a positive s its correction is
+// -0.  (Copying the sign instead costs 3 % of 8192 tokens.)
 __device__ __forceinline__ uint2 pack8_e4m3(const float* v, float s, float r) {
   float q[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const float q0 = __fmul_rn(v[i], r);
-    const float q1 = fmaf(fmaf(-q0, s, v[i]), r, q0);
+    const float q1 = fmaf(-fmaf(q0, s, -v[i]), r, q0);
     q[i] = fabsf(q0) < 1024.f ? q1 : q0;
   }
   if (r == 0.f) {
@@ -238,7 +240,8 @@ __global__ void __launch_bounds__(kThreads, blocks_of(kUnroll))
       if (FP8) {
         const float* sc = is_v ? p.v_scale : p.k_scale;
         const float s = sc ? __ldg(sc + hk) : 1.f;
-        const float r = fabsf(s) > 0x1p-60f && fabsf(s) < 0x1p60f ? __frcp_rn(s) : 0.f;
+        // a negative scale divides: 40 us for 8192 tokens, 34 over a positive one
+        const float r = s > 0x1p-60f && s < 0x1p60f ? __frcp_rn(s) : 0.f;
         uint8_t* dst = static_cast<uint8_t*>(cache) + at;
         *reinterpret_cast<uint2*>(dst + a) = pack8_e4m3(x, s, r);
         *reinterpret_cast<uint2*>(dst + b) = pack8_e4m3(x + 8, s, r);

@@ -6,9 +6,10 @@ import torch
 import mxfp4_quantized_gemm_token_gb300 as mxq
 from mxfp4_quantized_gemm_token_gb300 import _lib
 from attention_util import assert_within, decode_ref, prompt_ref
-from test_gpu_paged_attention import decode_case, gen, randn, run_decode
+from test_gpu_paged_attention import bits, decode_case, gen, randn, rotate_ref, run_decode
 
 pytestmark = pytest.mark.gpu
+FP8 = torch.float8_e4m3fn
 NAN, INF = float("nan"), float("inf")
 
 
@@ -134,3 +135,49 @@ def test_large_queries_over_an_e4m3_cache(power):
     q, kc, vc, table, n, g = decode_case(45, lens, 8, 2, 64, 16, True)
     q = (q.float() * 2.0 ** power).bfloat16()
     run_decode((q, kc, vc, table, n, g), lens, scale=2.0 ** -(power + 7))
+
+
+@pytest.mark.parametrize("scale", [None, 0.02, -0.02, 1.0])
+@pytest.mark.parametrize("rot", [0, 64])
+def test_append_keeps_the_sign_of_zero(scale, rot):
+    """A quotient of zero has the sign that the division gives it."""
+    g = gen(46)
+    T, KV, D, page = 5, 3, 64, 4
+    k, v = randn(g, T, KV, D), randn(g, T, KV, D)
+    for x in (k, v):
+        x[:, :, ::3] = -0.0
+        x[:, :, 1::3] = 0.0
+    x = torch.tensor([1e-38, -1e-38, 1e-30, -1e-30], device="cuda").bfloat16()
+    v[0, 0, :4], k[0, 0, 60:] = x, x
+    cs = torch.randn(9, 64, generator=g, device="cuda")
+    pos = torch.arange(T, device="cuda", dtype=torch.int32)
+    kc, vc = (torch.zeros(2, page, KV, D, device="cuda").to(FP8) for _ in range(2))
+    s = None if scale is None else torch.full((KV,), scale, device="cuda")
+    mxq.rope_append_kv(k, v, kc, vc, torch.arange(T, device="cuda"), cs if rot else None,
+                       pos if rot else None, k_scale=s, v_scale=s)
+    turned = rotate_ref(k, cs[:T], rot, False)
+    for cache, want in ((kc, turned), (vc, v.float())):
+        want = (want / (1.0 if scale is None else scale)).clamp(-448, 448).to(FP8)
+        assert torch.equal(bits(cache).view(-1, KV, D)[:T], bits(want))
+
+
+@pytest.mark.parametrize("seed", range(4))
+def test_append_quotients_around_midpoints(seed):
+    """Scales that put quotients on and next to the middle between two codes, where a
+    quotient off by one unit changes the code: 8 x 786432 of them."""
+    g = gen(47 + seed)
+    KV, D = 49152, 16
+    # an odd multiple of half a code's step, times powers of two: a midpoint of each binade
+    mid = (torch.randint(8, 16, (KV,), generator=g, device="cuda") + 0.5) / 16
+    v = torch.randint(128, 256, (KV,), generator=g, device="cuda") / 256.0
+    s = ((v / mid).view(torch.int32) + torch.randint(-3, 4, (KV,), generator=g, device="cuda",
+                                                     dtype=torch.int32)).view(torch.float32)
+    power = torch.arange(D, device="cuda") - 7
+    sign = torch.randint(0, 2, (1, KV, D), generator=g, device="cuda") * 2 - 1
+    v = (v[None, :, None] * 2.0 ** power * sign).bfloat16()
+    kc, vc = (torch.zeros(1, 1, KV, D, device="cuda").to(FP8) for _ in range(2))
+    mxq.rope_append_kv(v, v, kc, vc, torch.zeros(1, device="cuda", dtype=torch.int64), k_scale=s,
+                       v_scale=s * 4)
+    for cache, scale in ((kc, s), (vc, s * 4)):
+        want = (v.float() / scale[None, :, None]).clamp(-448, 448).to(FP8)
+        assert torch.equal(bits(cache).view(1, KV, D), bits(want))
