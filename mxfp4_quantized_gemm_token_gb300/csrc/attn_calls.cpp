@@ -41,6 +41,20 @@ struct Raised {};          // a Python exception is set
   throw Raised();
 }
 
+// Other Python threads run meanwhile: while the entry point launches (a full queue makes it
+// wait), while torch allocates or copies.
+struct Unlocked {
+  PyThreadState* state = PyEval_SaveThread();
+  Unlocked() = default;
+  Unlocked(const Unlocked&) = delete;
+  ~Unlocked() { PyEval_RestoreThread(state); }
+};
+template <typename... P, typename... A>
+mxq_status unlocked(mxq_status (*fn)(P...), A... args) {
+  const Unlocked u;
+  return fn(args...);
+}
+
 void check(mxq_status status) {
   if (status == MXQ_OK) return;
   PyObject* r = PyObject_CallFunction(check_fn, "i", static_cast<int>(status));
@@ -124,6 +138,7 @@ struct Heads {
     p = t.data_ptr();
     if (t.stride(2) != 1 || (n > 1 && (s0 < D || (s0 & 7))) ||
         (heads > 1 && (s1 < D || (s1 & 7))) || (reinterpret_cast<uintptr_t>(p) & 15)) {
+      const Unlocked u;
       copy = t.clone(at::MemoryFormat::Contiguous);
       s0 = copy.stride(0), s1 = copy.stride(1);
       p = copy.data_ptr();
@@ -169,6 +184,7 @@ T* vec(const char* name, const at::Tensor* t, at::ScalarType type, int64_t n) {
 }
 
 at::Tensor fresh(at::IntArrayRef shape, at::ScalarType type, const at::Tensor& like) {
+  const Unlocked u;
   return at::empty(shape, at::TensorOptions().dtype(type).device(like.device()));
 }
 
@@ -270,13 +286,13 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     } else if (q_out != nullptr) {
       refuse(PyExc_ValueError, "q_out without q");
     }
-    check(append_fn(qp, q0, q1, narrow("heads", Hq), op, o0, o1, hk.p, hk.s0, hk.s1, hv.p, hv.s0,
-                    hv.s1, T, narrow("kv_heads", hk.heads), narrow("head_dim", D), rotation,
-                    max_pos, narrow("the rotation", rot), at_pos, truth(a[11]),
-                    vec<const int64_t>("slots", &slots, at::kLong, T), c.k, c.v, c.dtype, c.pages,
-                    c.page_size, c.k0, c.k1, c.k2, c.v0, c.v1, c.v2,
-                    vec<const float>("k_scale", ks, at::kFloat, hk.heads),
-                    vec<const float>("v_scale", vs, at::kFloat, hk.heads), stream_of(k)));
+    check(unlocked(
+        append_fn, qp, q0, q1, narrow("heads", Hq), op, o0, o1, hk.p, hk.s0, hk.s1, hv.p, hv.s0,
+        hv.s1, T, narrow("kv_heads", hk.heads), narrow("head_dim", D), rotation, max_pos,
+        narrow("the rotation", rot), at_pos, truth(a[11]),
+        vec<const int64_t>("slots", &slots, at::kLong, T), c.k, c.v, c.dtype, c.pages, c.page_size,
+        c.k0, c.k1, c.k2, c.v0, c.v1, c.v2, vec<const float>("k_scale", ks, at::kFloat, hk.heads),
+        vec<const float>("v_scale", vs, at::kFloat, hk.heads), stream_of(k)));
     if (q == nullptr) Py_RETURN_NONE;
     if (q_out != nullptr) return Py_NewRef(a[8]);
     return THPVariable_Wrap(out);
@@ -310,16 +326,16 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     const at::Tensor space = workspace_of(ws, q, [&](size_t* n) {
       return decode_size_fn(B, Hq, Hkv, narrow("head_dim", D), n);
     });
-    check(decode_fn(hq.p, hq.s0, hq.s1, B, Hq, Hkv, narrow("head_dim", D), c.k, c.v, c.dtype,
-                    c.pages, c.page_size, c.k0, c.k1, c.k2, c.v0, c.v1, c.v2,
-                    static_cast<const int32_t*>(table.data_ptr()), B > 1 ? table.stride(0) : width,
-                    width, vec<const int32_t>("seq_lens", &lens, at::kInt, B), scale_of(a[5], D),
-                    integer("window", a[6]), vec<const float>("sinks", sinks, at::kFloat, Hq),
-                    vec<const float>("k_scale", ks, at::kFloat, Hkv),
-                    vec<const float>("v_scale", vs, at::kFloat, Hkv), out.data_ptr(),
-                    out.stride(0), out.stride(1),
-                    lse.defined() ? static_cast<float*>(lse.data_ptr()) : nullptr,
-                    space.data_ptr(), space.nbytes(), stream_of(q)));
+    check(unlocked(
+        decode_fn, hq.p, hq.s0, hq.s1, B, Hq, Hkv, narrow("head_dim", D), c.k, c.v, c.dtype,
+        c.pages, c.page_size, c.k0, c.k1, c.k2, c.v0, c.v1, c.v2,
+        static_cast<const int32_t*>(table.data_ptr()), B > 1 ? table.stride(0) : width, width,
+        vec<const int32_t>("seq_lens", &lens, at::kInt, B), scale_of(a[5], D),
+        integer("window", a[6]), vec<const float>("sinks", sinks, at::kFloat, Hq),
+        vec<const float>("k_scale", ks, at::kFloat, Hkv),
+        vec<const float>("v_scale", vs, at::kFloat, Hkv), out.data_ptr(), out.stride(0),
+        out.stride(1), lse.defined() ? static_cast<float*>(lse.data_ptr()) : nullptr,
+        space.data_ptr(), space.nbytes(), stream_of(q)));
     return result(out, lse);
   });
 }
@@ -349,12 +365,12 @@ PyObject* prompt(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     const at::Tensor space = workspace_of(ws, q, [&](size_t* n) {
       return prompt_size_fn(hq.n, B, Hq, Hkv, D, n);
     });
-    check(prompt_fn(hq.p, hq.s0, hq.s1, hk.p, hk.s0, hk.s1, hv.p, hv.s0, hv.s1, cq, ck, B, hq.n,
-                    hk.n, Hq, Hkv, D, scale_of(a[5], D), truth(a[6]), integer("window", a[7]),
-                    vec<const float>("sinks", sinks, at::kFloat, Hq), out.data_ptr(),
-                    out.stride(0), out.stride(1),
-                    lse.defined() ? static_cast<float*>(lse.data_ptr()) : nullptr,
-                    space.data_ptr(), space.nbytes(), stream_of(q)));
+    check(unlocked(
+        prompt_fn, hq.p, hq.s0, hq.s1, hk.p, hk.s0, hk.s1, hv.p, hv.s0, hv.s1, cq, ck, B, hq.n,
+        hk.n, Hq, Hkv, D, scale_of(a[5], D), truth(a[6]), integer("window", a[7]),
+        vec<const float>("sinks", sinks, at::kFloat, Hq), out.data_ptr(), out.stride(0),
+        out.stride(1), lse.defined() ? static_cast<float*>(lse.data_ptr()) : nullptr,
+        space.data_ptr(), space.nbytes(), stream_of(q)));
     return result(out, lse);
   });
 }
