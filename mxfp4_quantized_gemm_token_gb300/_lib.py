@@ -128,7 +128,7 @@ def load(build_if_missing: bool = True):
 
 
 def load_calls(raw_stream, current_device):
-    """Load _attn_calls.so (building it first if it does not exist) and give it
+    """Load the compiled calls (building them first if they do not exist) and give them
     the library's entry points.  raw_stream: device index -> the current
     stream's address; current_device: -> the current device's index."""
     global _calls

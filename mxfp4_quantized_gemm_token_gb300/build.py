@@ -3,8 +3,9 @@
 The translation units compile in parallel, then link into one shared library
 with the CUDA runtime linked statically.  The driver API (tensor-map encode)
 is reached through cudaGetDriverEntryPointByVersion, so no -lcuda is needed.
-Beside it goes _attn_calls.so, the Python calls of the attention operators
-(host code against torch's headers; it reaches libmxq.so by address).
+Beside it goes _attn_calls.<torch version>.<Python ABI>.so, the Python calls of the
+attention operators (host code against torch's headers; it reaches libmxq.so by
+address).  Another torch or Python finds no file of its name and builds one.
 """
 from __future__ import annotations
 
@@ -21,7 +22,15 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmxq.so")
-CALLS = os.path.join(PKG, "_attn_calls.so")
+
+
+def calls_path() -> str:
+    import torch
+    return os.path.join(PKG, "_attn_calls.torch-%s%s" % (torch.__version__,
+                                                         sysconfig.get_config_var("EXT_SUFFIX")))
+
+
+CALLS = calls_path()
 
 SOURCES = ["api.cu", "quant.cu", "moe_aux.cu", "gemm_dense.cu", "gemm_moe.cu", "noalloc.cu",
            "prepack.cu", "attn_api.cu", "rope_append.cu", "attn_decode.cu", "attn_prompt.cu"]
