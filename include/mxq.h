@@ -464,6 +464,7 @@ mxq_status mxq_rope_append_kv(const void* q, int64_t sq_t, int64_t sq_h, int32_t
  *          either type; only the rows of visible keys are read
  *   page_table int32 [B, max_pages], row stride ld_table; entries past a
  *          sequence's pages are not read.  seq_lens int32 [B]
+ *   scale  positive, and finite times log2 e
  *   sinks  fp32 [Hq] or NULL: a logit per head without a value
  *   lse    fp32 [B, Hq] or NULL
  *   workspace mxq_paged_attention_decode_workspace_size bytes (NULL if 0),

@@ -1,6 +1,7 @@
 // attn_api.cu — the extern "C" entry points of the paged cache and attention
 // operators (declared in mxq.h): host-side checks, then one launch function.
 #include <algorithm>
+#include <cmath>
 #include <string>
 
 #include "attn.h"
@@ -69,8 +70,9 @@ mxq_status check_heads(int32_t Hq, int32_t Hkv, int32_t D) {
 }
 
 mxq_status check_scale(float scale, int32_t window) {
-  if (!(scale > 0.f) || !(scale < 3.4e38f))
-    return fail(MXQ_ERR_INVALID_ARG, "scale must be positive and finite");
+  // (the kernels multiply it by log2 e)
+  if (!(scale > 0.f) || !std::isfinite(scale * 1.44269504088896340736f))
+    return fail(MXQ_ERR_INVALID_ARG, "scale must be positive and finite, times log2 e as well");
   if (window < 0) return fail(MXQ_ERR_INVALID_ARG, "window must be >= 0 (0: none)");
   return MXQ_OK;
 }
@@ -111,6 +113,8 @@ extern "C" mxq_status mxq_rope_append_kv(
   if (Hq > 65535 || Hkv > 65535) return fail(MXQ_ERR_UNSUPPORTED, "more than 65535 heads");
   if (pages <= 0 || page_size <= 0 || pages > (int64_t(1) << 40))
     return fail(MXQ_ERR_INVALID_ARG, "need pages > 0 and page_size > 0");
+  if (pages > (int64_t(1) << 60) / page_size)
+    return fail(MXQ_ERR_INVALID_ARG, "more than 2^60 cache slots");
   if ((q == nullptr) != (Hq == 0) || (q && !q_out))
     return fail(MXQ_ERR_INVALID_ARG, "q, q_out and Hq > 0 go together");
   if (T == 0) return MXQ_OK;
@@ -185,7 +189,7 @@ extern "C" mxq_status mxq_paged_attention_decode(
     return fail(MXQ_ERR_INVALID_ARG, "need 0 < pages < 2^31 and page_size > 0");
   if (B == 0) return MXQ_OK;
   if (B > 65535) return fail(MXQ_ERR_UNSUPPORTED, "more than 65535 sequences");
-  if (max_pages * page_size > 0x7fffffff / 2)
+  if (max_pages > 0x7fffffff / 2 / page_size)
     return fail(MXQ_ERR_UNSUPPORTED, "sequences of more than 2^30 keys");
   if (!seq_lens || (max_pages > 0 && !page_table))
     return fail(MXQ_ERR_INVALID_ARG, "page_table and seq_lens must be non-NULL");
