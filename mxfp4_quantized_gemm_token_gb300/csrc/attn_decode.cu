@@ -244,8 +244,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1) decode_kernel(const DecodeArgs
   const int heads = p.Hkv * a.tiles;
   const int workers = gridDim.x * kWarps;
   int64_t per = max(divide(total + a.parts - 1, a.parts), static_cast<int64_t>(a.min_steps));
-  // sequences that stay whole: a part has room for the longest, or some get two
-  if ((a.all_whole || longest <= whole_steps(per)) && per < longest) per = longest;
+  // where all stay whole, a part has room for the longest, or some would get two
+  if (a.all_whole && per < longest) per = longest;
   const int whole = a.all_whole ? longest : whole_steps(per);
   for (int e = e0; e < min(a.entries, e0 + per_thread); ++e) {
     table[e] = before;
