@@ -127,6 +127,9 @@ const char* mxq_version(void);
 mxq_status mxq_set_option(int32_t option, int64_t value);
 mxq_status mxq_get_option(int32_t option, int64_t* value);
 
+/* The device that the calling thread's next call launches on. */
+mxq_status mxq_current_device(int32_t* device);
+
 /* Synchronizes `stream`, then reads and clears the device status word of the
  * current device: MXQ_OK, MXQ_ERR_TIMEOUT or MXQ_ERR_DEVICE. */
 mxq_status mxq_sync_status(mxq_stream_t stream);

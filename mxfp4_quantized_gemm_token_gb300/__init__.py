@@ -47,33 +47,40 @@ def _ptr(t):
 
 
 def _stream(device):
-    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+    return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(device.index))
+
+
+def _current_device():
+    return torch._C._cuda_getDevice()
 
 
 def _need_current(index):
     # the library launches on the current device, whatever the pointers' and the stream's is
-    current = torch.cuda.current_device()
+    current = _current_device()
     if index != current:
         raise ValueError("the tensors are on cuda:%d, the current device is cuda:%d"
                          % (index, current))
 
 
 def _need_cuda(*ts):
-    devices = set()
+    on = -1
     for t in ts:
         if t is not None:
-            if not t.is_cuda:
-                raise ValueError("mxq operates on CUDA tensors only (got a %s tensor)" % t.device)
-            devices.add(t.get_device())
-    for index in devices:
-        _need_current(index)
+            index = t.get_device()
+            if index != on or index < 0:
+                if not t.is_cuda:
+                    raise ValueError("mxq operates on CUDA tensors only (got a %s tensor)"
+                                     % t.device)
+                _need_current(index)
+                on = index
 
 
 def _need_whole(workspace):
-    # an expanded tensor counts bytes that it does not have
-    _need_cuda(workspace)
-    if workspace is not None and not workspace.is_contiguous():
-        raise ValueError("workspace must be contiguous")
+    if workspace is not None:
+        _need_cuda(workspace)
+        # an expanded tensor counts bytes that it does not have
+        if not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
 
 
 def set_option(option: int, value: int) -> None:
@@ -475,7 +482,7 @@ _calls = None
 def _attn():
     global _calls
     if _calls is None:
-        _calls = _lib.load_calls(torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice)
+        _calls = _lib.load_calls(torch._C._cuda_getCurrentRawStream)
     return _calls
 
 

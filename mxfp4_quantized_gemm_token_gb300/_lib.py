@@ -28,6 +28,7 @@ ACT_SILU, ACT_SWIGLU_CLAMP = 0, 1
 
 EXPORTED = [
     "mxq_last_error", "mxq_version", "mxq_set_option", "mxq_get_option", "mxq_sync_status",
+    "mxq_current_device",
     "mxq_per_token_group_quant_fp8", "mxq_fp8_scaled_mm", "mxq_fp8_scaled_mm_workspace_size",
     "mxq_moe_align_block", "mxq_fused_experts", "mxq_fused_experts_debug",
     "mxq_fused_experts_workspace_size", "mxq_fp8_scaled_mm_noalloc",
@@ -57,6 +58,7 @@ def _declare(lib):
         "mxq_set_option": (st, [I32, I64]),
         "mxq_get_option": (st, [I32, ctypes.POINTER(I64)]),
         "mxq_sync_status": (st, [P]),
+        "mxq_current_device": (st, [ctypes.POINTER(I32)]),
         "mxq_per_token_group_quant_fp8": (st, [P, I64, I64, I64, I32, F, P, P, P]),
         "mxq_fp8_scaled_mm": (st, [P, I32, I64, I64, I64, P, I64, I64, P, I64, I64, P, I32, I32,
                                    I64, I64, P, I32, P, I32, I64, P, SZ, P]),
@@ -127,10 +129,10 @@ def load(build_if_missing: bool = True):
         return lib
 
 
-def load_calls(raw_stream, current_device):
+def load_calls(raw_stream):
     """Load the compiled calls (building them first if they do not exist) and give them
     the library's entry points.  raw_stream: device index -> the current
-    stream's address; current_device: -> the current device's index."""
+    stream's address."""
     global _calls
     lib = load()
     with _lock:
@@ -143,8 +145,7 @@ def load_calls(raw_stream, current_device):
             mod.connect(*[ctypes.cast(f, ctypes.c_void_p).value for f in (
                 lib.mxq_rope_append_kv, lib.mxq_paged_attention_decode,
                 lib.mxq_paged_attention_decode_workspace_size, lib.mxq_attention_varlen,
-                lib.mxq_attention_varlen_workspace_size)], check, raw_stream,
-                current_device)
+                lib.mxq_attention_varlen_workspace_size, lib.mxq_current_device)], check, raw_stream)
             _calls = mod
         return _calls
 

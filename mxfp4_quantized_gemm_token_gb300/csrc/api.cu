@@ -180,6 +180,16 @@ extern "C" mxq_status mxq_get_option(int32_t opt, int64_t* value) {
   return MXQ_OK;
 }
 
+extern "C" mxq_status mxq_current_device(int32_t* device) {
+  if (!device) return fail(MXQ_ERR_INVALID_ARG, "device must be non-NULL");
+  int d = 0;
+  const cudaError_t e = cudaGetDevice(&d);
+  if (e != cudaSuccess)
+    return fail(MXQ_ERR_CUDA, std::string("cudaGetDevice: ") + cudaGetErrorString(e));
+  *device = d;
+  return MXQ_OK;
+}
+
 extern "C" mxq_status mxq_sync_status(mxq_stream_t stream) {
   DeviceInfo d;
   std::string err;

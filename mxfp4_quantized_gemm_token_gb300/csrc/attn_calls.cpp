@@ -30,9 +30,9 @@ decltype(&mxq_paged_attention_decode) decode_fn;
 decltype(&mxq_paged_attention_decode_workspace_size) decode_size_fn;
 decltype(&mxq_attention_varlen) prompt_fn;
 decltype(&mxq_attention_varlen_workspace_size) prompt_size_fn;
+decltype(&mxq_current_device) device_fn;
 PyObject* check_fn;        // raises for a status
 PyObject* stream_fn;       // device index -> the current stream's address
-PyObject* device_fn;       // the current device's index
 
 struct Raised {};          // a Python exception is set
 
@@ -41,18 +41,15 @@ struct Raised {};          // a Python exception is set
   throw Raised();
 }
 
-// Other Python threads run meanwhile: while the entry point launches (a full queue makes it
-// wait), while torch allocates or copies.
-struct Unlocked {
-  PyThreadState* state = PyEval_SaveThread();
-  Unlocked() = default;
-  Unlocked(const Unlocked&) = delete;
-  ~Unlocked() { PyEval_RestoreThread(state); }
-};
-template <typename... P, typename... A>
-mxq_status unlocked(mxq_status (*fn)(P...), A... args) {
-  const Unlocked u;
-  return fn(args...);
+// Other Python threads run while torch allocates or copies and while the entry point
+// launches (a full queue makes it wait).  Once a call: letting go costs 0.1 us.
+template <typename F>
+auto unlocked(F f) {
+  struct Unlocked {
+    PyThreadState* state = PyEval_SaveThread();
+    ~Unlocked() { PyEval_RestoreThread(state); }
+  } u;
+  return f();
 }
 
 void check(mxq_status status) {
@@ -83,11 +80,8 @@ void same_device(std::initializer_list<const at::Tensor*> ts) {
     if (t != nullptr && (!t->is_cuda() || t->device() != first.device()))
       refuse(PyExc_ValueError, "mxq operates on CUDA tensors of one device (got " +
                                    first.device().str() + " and " + t->device().str() + ")");
-  PyObject* r = PyObject_CallNoArgs(device_fn);
-  if (r == nullptr) throw Raised();
-  const long current = PyLong_AsLong(r);
-  Py_DECREF(r);
-  if (current == -1 && PyErr_Occurred()) throw Raised();
+  int32_t current = 0;
+  check(device_fn(&current));
   if (first.device().index() != current)
     refuse(PyExc_ValueError, "the tensors are on " + first.device().str() +
                                  ", the current device is cuda:" + std::to_string(current));
@@ -138,8 +132,7 @@ struct Heads {
     p = t.data_ptr();
     if (t.stride(2) != 1 || (n > 1 && (s0 < D || (s0 & 7))) ||
         (heads > 1 && (s1 < D || (s1 & 7))) || (reinterpret_cast<uintptr_t>(p) & 15)) {
-      const Unlocked u;
-      copy = t.clone(at::MemoryFormat::Contiguous);
+      copy = unlocked([&] { return t.clone(at::MemoryFormat::Contiguous); });
       s0 = copy.stride(0), s1 = copy.stride(1);
       p = copy.data_ptr();
     }
@@ -184,14 +177,12 @@ T* vec(const char* name, const at::Tensor* t, at::ScalarType type, int64_t n) {
 }
 
 at::Tensor fresh(at::IntArrayRef shape, at::ScalarType type, const at::Tensor& like) {
-  const Unlocked u;
   return at::empty(shape, at::TensorOptions().dtype(type).device(like.device()));
 }
 
-// a given output or a new one
-at::Tensor output(const char* name, const at::Tensor* given, at::IntArrayRef shape,
-                  const at::Tensor& like) {
-  if (given == nullptr) return fresh(shape, at::kBFloat16, like);
+// an output that the caller may have given
+at::Tensor output(const char* name, const at::Tensor* given, at::IntArrayRef shape) {
+  if (given == nullptr) return at::Tensor();
   if (given->scalar_type() != at::kBFloat16 || given->sizes() != shape || given->stride(2) != 1)
     refuse(PyExc_ValueError, std::string(name) + " must be bf16 " + shape_of(shape) +
                                  " with a unit inner stride");
@@ -209,17 +200,12 @@ mxq_stream_t stream_of(const at::Tensor& t) {
   return static_cast<mxq_stream_t>(p);
 }
 
-// a caller's workspace, or a new one of `bytes`
-template <typename Size>
-at::Tensor workspace_of(const at::Tensor* given, const at::Tensor& like, Size bytes) {
-  if (given != nullptr) {
-    // an expanded tensor counts bytes that it does not have
-    if (!given->is_contiguous()) refuse(PyExc_ValueError, "workspace must be contiguous");
-    return *given;
-  }
-  size_t n = 0;
-  check(bytes(&n));
-  return fresh({static_cast<int64_t>(n)}, at::kByte, like);
+// a workspace that the caller may have given
+at::Tensor workspace(const at::Tensor* given) {
+  if (given == nullptr) return at::Tensor();
+  // an expanded tensor counts bytes that it does not have
+  if (!given->is_contiguous()) refuse(PyExc_ValueError, "workspace must be contiguous");
+  return *given;
 }
 
 PyObject* result(const at::Tensor& out, const at::Tensor& lse) {
@@ -281,18 +267,27 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
       const Heads hq("q", *q);
       q_copy = hq.copy;
       Hq = hq.heads, qp = hq.p, q0 = hq.s0, q1 = hq.s1;
-      out = output("q_out", q_out, q->sizes(), k);
-      op = out.data_ptr(), o0 = out.stride(0), o1 = out.stride(1);
+      out = output("q_out", q_out, q->sizes());
     } else if (q_out != nullptr) {
       refuse(PyExc_ValueError, "q_out without q");
     }
-    check(unlocked(
-        append_fn, qp, q0, q1, narrow("heads", Hq), op, o0, o1, hk.p, hk.s0, hk.s1, hv.p, hv.s0,
-        hv.s1, T, narrow("kv_heads", hk.heads), narrow("head_dim", D), rotation, max_pos,
-        narrow("the rotation", rot), at_pos, truth(a[11]),
-        vec<const int64_t>("slots", &slots, at::kLong, T), c.k, c.v, c.dtype, c.pages, c.page_size,
-        c.k0, c.k1, c.k2, c.v0, c.v1, c.v2, vec<const float>("k_scale", ks, at::kFloat, hk.heads),
-        vec<const float>("v_scale", vs, at::kFloat, hk.heads), stream_of(k)));
+    const int32_t nq = narrow("heads", Hq), nkv = narrow("kv_heads", hk.heads);
+    const int32_t d = narrow("head_dim", D), r = narrow("the rotation", rot);
+    const int32_t interleaved = truth(a[11]);
+    const int64_t* at_slot = vec<const int64_t>("slots", &slots, at::kLong, T);
+    const float* k_scale = vec<const float>("k_scale", ks, at::kFloat, hk.heads);
+    const float* v_scale = vec<const float>("v_scale", vs, at::kFloat, hk.heads);
+    const mxq_stream_t stream = stream_of(k);
+    check(unlocked([&] {
+      if (q != nullptr) {
+        if (!out.defined()) out = fresh(q->sizes(), at::kBFloat16, k);
+        op = out.data_ptr(), o0 = out.stride(0), o1 = out.stride(1);
+      }
+      return append_fn(qp, q0, q1, nq, op, o0, o1, hk.p, hk.s0, hk.s1, hv.p, hv.s0, hv.s1, T, nkv,
+                       d, rotation, max_pos, r, at_pos, interleaved, at_slot, c.k, c.v, c.dtype,
+                       c.pages, c.page_size, c.k0, c.k1, c.k2, c.v0, c.v1, c.v2, k_scale, v_scale,
+                       stream);
+    }));
     if (q == nullptr) Py_RETURN_NONE;
     if (q_out != nullptr) return Py_NewRef(a[8]);
     return THPVariable_Wrap(out);
@@ -320,22 +315,32 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
       refuse(PyExc_ValueError, "page_table must be int32 [" + std::to_string(B) +
                                    ", max_pages] with a unit inner stride");
     const int64_t width = table.size(1);
-    const at::Tensor out = output("out", given, q.sizes(), q);
-    at::Tensor lse;
-    if (truth(a[10])) lse = fresh({B, hq.heads}, at::kFloat, q);
-    const at::Tensor space = workspace_of(ws, q, [&](size_t* n) {
-      return decode_size_fn(B, Hq, Hkv, narrow("head_dim", D), n);
-    });
-    check(unlocked(
-        decode_fn, hq.p, hq.s0, hq.s1, B, Hq, Hkv, narrow("head_dim", D), c.k, c.v, c.dtype,
-        c.pages, c.page_size, c.k0, c.k1, c.k2, c.v0, c.v1, c.v2,
-        static_cast<const int32_t*>(table.data_ptr()), B > 1 ? table.stride(0) : width, width,
-        vec<const int32_t>("seq_lens", &lens, at::kInt, B), scale_of(a[5], D),
-        integer("window", a[6]), vec<const float>("sinks", sinks, at::kFloat, Hq),
-        vec<const float>("k_scale", ks, at::kFloat, Hkv),
-        vec<const float>("v_scale", vs, at::kFloat, Hkv), out.data_ptr(), out.stride(0),
-        out.stride(1), lse.defined() ? static_cast<float*>(lse.data_ptr()) : nullptr,
-        space.data_ptr(), space.nbytes(), stream_of(q)));
+    at::Tensor out = output("out", given, q.sizes()), space = workspace(ws), lse;
+    const bool with_lse = truth(a[10]) != 0;
+    const int32_t d = narrow("head_dim", D), window = integer("window", a[6]);
+    const int32_t* at_len = vec<const int32_t>("seq_lens", &lens, at::kInt, B);
+    const float scale = scale_of(a[5], D);
+    const float* sink = vec<const float>("sinks", sinks, at::kFloat, Hq);
+    const float* k_scale = vec<const float>("k_scale", ks, at::kFloat, Hkv);
+    const float* v_scale = vec<const float>("v_scale", vs, at::kFloat, Hkv);
+    const mxq_stream_t stream = stream_of(q);
+    check(unlocked([&] {
+      if (!space.defined()) {
+        size_t n = 0;
+        const mxq_status st = decode_size_fn(B, Hq, Hkv, d, &n);
+        if (st != MXQ_OK) return st;
+        space = fresh({static_cast<int64_t>(n)}, at::kByte, q);
+      }
+      if (!out.defined()) out = fresh(q.sizes(), at::kBFloat16, q);
+      if (with_lse) lse = fresh({B, hq.heads}, at::kFloat, q);
+      return decode_fn(hq.p, hq.s0, hq.s1, B, Hq, Hkv, d, c.k, c.v, c.dtype, c.pages, c.page_size,
+                       c.k0, c.k1, c.k2, c.v0, c.v1, c.v2,
+                       static_cast<const int32_t*>(table.data_ptr()),
+                       B > 1 ? table.stride(0) : width, width, at_len, scale, window, sink, k_scale,
+                       v_scale, out.data_ptr(), out.stride(0), out.stride(1),
+                       with_lse ? static_cast<float*>(lse.data_ptr()) : nullptr, space.data_ptr(),
+                       space.nbytes(), stream);
+    }));
     return result(out, lse);
   });
 }
@@ -359,36 +364,45 @@ PyObject* prompt(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     const int32_t* cq = vec<const int32_t>("cu_seqlens_q", &cu_q, at::kInt, B + 1);
     const int32_t* ck =
         cu_k == nullptr ? cq : vec<const int32_t>("cu_seqlens_k", cu_k, at::kInt, B + 1);
-    const at::Tensor out = output("out", given, q.sizes(), q);
-    at::Tensor lse;
-    if (truth(a[9])) lse = fresh({hq.n, hq.heads}, at::kFloat, q);
-    const at::Tensor space = workspace_of(ws, q, [&](size_t* n) {
-      return prompt_size_fn(hq.n, B, Hq, Hkv, D, n);
-    });
-    check(unlocked(
-        prompt_fn, hq.p, hq.s0, hq.s1, hk.p, hk.s0, hk.s1, hv.p, hv.s0, hv.s1, cq, ck, B, hq.n,
-        hk.n, Hq, Hkv, D, scale_of(a[5], D), truth(a[6]), integer("window", a[7]),
-        vec<const float>("sinks", sinks, at::kFloat, Hq), out.data_ptr(), out.stride(0),
-        out.stride(1), lse.defined() ? static_cast<float*>(lse.data_ptr()) : nullptr,
-        space.data_ptr(), space.nbytes(), stream_of(q)));
+    at::Tensor out = output("out", given, q.sizes()), space = workspace(ws), lse;
+    const bool with_lse = truth(a[9]) != 0;
+    const float scale = scale_of(a[5], D);
+    const int32_t causal = truth(a[6]), window = integer("window", a[7]);
+    const float* sink = vec<const float>("sinks", sinks, at::kFloat, Hq);
+    const mxq_stream_t stream = stream_of(q);
+    check(unlocked([&] {
+      if (!space.defined()) {
+        size_t n = 0;
+        const mxq_status st = prompt_size_fn(hq.n, B, Hq, Hkv, D, &n);
+        if (st != MXQ_OK) return st;
+        space = fresh({static_cast<int64_t>(n)}, at::kByte, q);
+      }
+      if (!out.defined()) out = fresh(q.sizes(), at::kBFloat16, q);
+      if (with_lse) lse = fresh({hq.n, hq.heads}, at::kFloat, q);
+      return prompt_fn(hq.p, hq.s0, hq.s1, hk.p, hk.s0, hk.s1, hv.p, hv.s0, hv.s1, cq, ck, B, hq.n,
+                       hk.n, Hq, Hkv, D, scale, causal, window, sink, out.data_ptr(),
+                       out.stride(0), out.stride(1),
+                       with_lse ? static_cast<float*>(lse.data_ptr()) : nullptr, space.data_ptr(),
+                       space.nbytes(), stream);
+    }));
     return result(out, lse);
   });
 }
 
-// (addresses of the five entry points, check, stream, device): once, before any call
+// (addresses of the six entry points, check, stream): once, before any call
 PyObject* connect(PyObject*, PyObject* args) {
-  unsigned long long fn[5];
-  PyObject *c, *s, *d;
-  if (!PyArg_ParseTuple(args, "KKKKKOOO", &fn[0], &fn[1], &fn[2], &fn[3], &fn[4], &c, &s, &d))
+  unsigned long long fn[6];
+  PyObject *c, *s;
+  if (!PyArg_ParseTuple(args, "KKKKKKOO", &fn[0], &fn[1], &fn[2], &fn[3], &fn[4], &fn[5], &c, &s))
     return nullptr;
   append_fn = reinterpret_cast<decltype(append_fn)>(fn[0]);
   decode_fn = reinterpret_cast<decltype(decode_fn)>(fn[1]);
   decode_size_fn = reinterpret_cast<decltype(decode_size_fn)>(fn[2]);
   prompt_fn = reinterpret_cast<decltype(prompt_fn)>(fn[3]);
   prompt_size_fn = reinterpret_cast<decltype(prompt_size_fn)>(fn[4]);
+  device_fn = reinterpret_cast<decltype(device_fn)>(fn[5]);
   Py_XSETREF(check_fn, Py_NewRef(c));
   Py_XSETREF(stream_fn, Py_NewRef(s));
-  Py_XSETREF(device_fn, Py_NewRef(d));
   Py_RETURN_NONE;
 }
 

@@ -20,7 +20,7 @@ def on(index):
 
 
 def test_other_devices_are_refused(monkeypatch):
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    monkeypatch.setattr(mxq, "_current_device", lambda: 1)
     mxq._need_cuda(on(1), None, on(1))
     for tensors in ([on(0)], [on(1), on(0)], [None, on(2)]):
         with pytest.raises(ValueError, match="the current device is cuda:1"):
@@ -28,7 +28,7 @@ def test_other_devices_are_refused(monkeypatch):
 
 
 def test_status_of_another_device_is_refused(monkeypatch):
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    monkeypatch.setattr(mxq, "_current_device", lambda: 1)
     monkeypatch.setattr(torch.cuda, "current_stream",
                         lambda device=None: SimpleNamespace(device=torch.device("cuda", 0),
                                                             cuda_stream=0))
@@ -37,14 +37,21 @@ def test_status_of_another_device_is_refused(monkeypatch):
 
 
 def compiled_calls(tmp_path, entry, current_device):
-    """A copy of the compiled calls of its own, whose entry points are all `entry`."""
-    _lib.load_calls(torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice)
+    """A copy of the compiled calls of its own, whose entry points are all `entry`, with a
+    current device as told."""
+    def tell(at):
+        at[0] = current_device
+        return 0
+
+    device = ctypes.CFUNCTYPE(ctypes.c_int, ctypes.POINTER(ctypes.c_int32))(tell)
+    _lib.load_calls(torch._C._cuda_getCurrentRawStream)
     path = shutil.copy(build.CALLS, str(tmp_path / "_attn_calls.so"))
     spec = importlib.util.spec_from_file_location("_attn_calls", path)
     mod = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(mod)
-    mod.connect(*[ctypes.cast(entry, ctypes.c_void_p).value] * 5, _lib.check,
-                torch._C._cuda_getCurrentRawStream, current_device)
+    entries = [ctypes.cast(f, ctypes.c_void_p).value for f in [entry] * 5 + [device]]
+    mod.connect(*entries, _lib.check, torch._C._cuda_getCurrentRawStream)
+    mod.kept = entry, device
     return mod
 
 
@@ -54,7 +61,7 @@ def test_compiled_calls(tmp_path, current):
     """With entry points that only count, and a current device as told."""
     reached = []
     entry = ctypes.CFUNCTYPE(ctypes.c_int)(lambda: reached.append(1) or 0)
-    calls = compiled_calls(tmp_path, entry, lambda: current)
+    calls = compiled_calls(tmp_path, entry, current)
     d = "cuda:0"
     q, kv = torch.zeros(2, 4, 64, dtype=BF, device=d), torch.zeros(2, 2, 64, dtype=BF, device=d)
     cache = torch.zeros(3, 16, 2, 64, dtype=BF, device=d)

@@ -13,7 +13,7 @@ def on_gpu(t):
 
 
 def test_workspaces(monkeypatch):
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(mxq, "_current_device", lambda: 0)
     one = torch.zeros(1, 256, dtype=torch.uint8)
     mxq._need_whole(None)
     mxq._need_whole(on_gpu(one))
