@@ -13,7 +13,8 @@
  *     error nothing is launched, outputs are untouched, and
  *     mxq_last_error() (thread-local) describes the problem.
  *   - Problems detected on the device (an expert id outside [0, E), a cache slot
- *     or page outside its range, a bounded wait that expired) set a device status word that mxq_sync_status reads.
+ *     or page outside its range, a bounded wait that expired) set a device
+ *     status word that mxq_sync_status reads.
  *   - The device must be compute capability 10.3 (GB300, sm_103a); any other
  *     device gives MXQ_ERR_UNSUPPORTED.
  *   - Row strides (ld*) are in elements.  Operands read by the tensor-memory

@@ -3,7 +3,7 @@
 //
 // A decode step makes these calls for every layer, with kernels of a few
 // microseconds.  From Python alone (ctypes, and the tensors' properties read
-// one by one) the append of 64 tokens took 16.7 us a call, from here 4.8; the launch
+// one by one) the append of 64 tokens took 16.7 us a call, from here 4.9; the launch
 // itself is 2 to 3 of them, a new output tensor 1.5.
 // The checks here are those of shapes, types and devices; ranges, alignment and
 // the rest are the entry points' own, whose status the package's `check`

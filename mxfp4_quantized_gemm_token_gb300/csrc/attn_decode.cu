@@ -38,9 +38,11 @@
 //
 // Measured.  64 sequences of 5-8192 keys, 32 query and 8 key/value heads of 128, bf16:
 // 158 us, 6.6 TB/s of keys and values, 97 % of a plain copy's rate.  16 sequences
-// of 9000-32768 keys, 64 / 8 heads, e4m3: 110 us, 5.8 TB/s.  One sequence of 1500 keys:
-// 10.4 us; 128 sequences with a window of 128 keys, D 64: 13.8 us: there the chain length ->
-// page -> key, a load each, and the launches count.
+// of 9000-32768 keys, 64 / 8 heads, e4m3: 110 us, 5.8 TB/s.  D 64, 64 / 8 heads, whose rows
+// are half as long: the 64 sequences 91 us, 5.7 TB/s, in e4m3 66 us, 4.0 TB/s; the 16 in
+// e4m3 78 us, 4.2 TB/s.  One sequence of 1500 keys: 10.4 us; 128 sequences with a window
+// of 128 keys, D 64: 13.9 us: there the chain length -> page -> key, a load each, and the
+// launches count.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math.h>

@@ -24,7 +24,8 @@
 // The maximum a row subtracts is only raised when it grows by more than 2^8 in the
 // exponent: O is rescaled (by the row's own thread) in few blocks,
 // and l and O stay far from the range's ends.  l and O use the same reference, so
-// the result does not depend on it.
+// the result does not depend on it.  (Two tiles in turn and a reference that is seldom
+// raised are published techniques for attention on this generation.)
 //
 // Work.  A kernel of one block first lists the work items (sequence, pair of
 // tiles, its blocks of keys) with the costliest first; the persistent CTAs
@@ -38,12 +39,14 @@
 //
 // Bound.  Arithmetic: 4 D operations a visible (query head, key) pair, on the
 // tensor cores at best.  One causal prompt of 8192 tokens, 32 query and 8 key/value
-// heads of 128: 323 us, 1.70 PFLOP/s, 87 % of a plain bf16 product's burst rate (346 us
-// when run for seconds, 92 % of its sustained rate under the power limit); the tensor pipe is
-// busy 72 % of the time, the rest is the chain scores -> maximum -> weights -> product of each
-// tile, ~3000 cycles for a block of both against 2048 of products.  11 packed prompts of 8192
-// tokens: 80 us (42 at the burst rate); here an item's beginning and end count, ~2 us.
-// Two chunks of 300 rows over 7892 keys, in pieces: 70 us (40).
+// heads of 128: 323 us, 1.70 PFLOP/s, 87 % of a plain bf16 product's burst rate (342-364 us
+// when run for seconds, by the device: 87-93 % of its sustained rate under the power limit);
+// the tensor pipe is busy 72 % of the time, the rest is the chain scores -> maximum ->
+// weights -> product of each tile, ~3000 cycles for a block of both against 2048 of products;
+// at D 64 ~2500 against 1280, and the same prompt takes 276 us (141 at the burst rate).
+// 11 packed prompts of 8192 tokens: 80 us (42 at the burst rate), 65 at D 64 (21); here an
+// item's beginning and end count, ~2 us.  Two chunks of 300 rows over 7892 keys, in pieces:
+// 71 us (40).  One prompt of 2048 tokens is cut into pieces too: 65 us (18).
 #include <cuda_bf16.h>
 #include <math.h>
 
