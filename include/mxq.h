@@ -1,6 +1,7 @@
 /*
- * mxq.h — C ABI of libmxq: weight-quantized scaled GEMM, routed fused MoE and
- * attention with a paged key/value cache on one NVIDIA GB300 (sm_103a).
+ * mxq.h — C ABI of libmxq: weight-quantized scaled GEMM, routed fused MoE,
+ * attention with a paged key/value cache, and that cache's pages, on one NVIDIA
+ * GB300 (sm_103a).
  *
  * Conventions (all entry points):
  *   - The caller owns all memory.  Tensor arguments are DEVICE pointers on the
@@ -523,6 +524,84 @@ mxq_status mxq_attention_varlen(const void* q, int64_t sq_t, int64_t sq_h, const
                                 mxq_stream_t stream);
 mxq_status mxq_attention_varlen_workspace_size(int64_t Tq, int64_t B, int32_t Hq, int32_t Hkv,
                                                int32_t D, size_t* bytes);
+
+/*
+ * Pages of a paged cache.  page_refs[p] (int32 [pages], 16-byte aligned) is the
+ * number of page-table entries that hold page p; where it is 0 the page is free.
+ * A table's row holds the pages of its sequence's keys in order, -1 where a page
+ * was freed.  A call takes the lowest free pages, in the order of its rows; a page
+ * that a call frees is taken by a later call.  Where no page is left the entry
+ * becomes -1 and MXQ_ERR_DEVICE is set for mxq_sync_status, as for lengths outside
+ * [0, max_pages * page_size] (clamped), pages outside [0, pages) (skipped) and counts
+ * that fall below 0.
+ * workspace: mxq_cache_pages_workspace_size bytes (rows: the larger number of rows
+ * of the call's tables), 256-byte aligned, not read before it is written.
+ */
+mxq_status mxq_cache_pages_workspace_size(int64_t rows, int64_t pages, size_t* bytes);
+
+/*
+ * Sequences grow and shrink: row b of page_table (int32 [B, max_pages], row stride
+ * ld_table, changed in place) gets the pages of new_lens[b] keys where it had
+ * those of seq_lens[b]: entries are taken behind the old ones, or freed (-1) behind the
+ * new ones; new_lens[b] = 0 frees the row.  With window > 0, entries that the
+ * row at position new_lens[b] - 1 and later ones do not see are freed too: pages
+ * that had keys before the call, end at or before new_lens[b] - window and begin at or
+ * behind key `first`.  seq_lens, new_lens int32 [B].  B == 0 is a no-op.
+ */
+mxq_status mxq_cache_resize(int32_t* page_table, int64_t ld_table, int64_t B, int64_t max_pages,
+                            const int32_t* seq_lens, const int32_t* new_lens, int32_t* page_refs,
+                            int64_t pages, int32_t page_size, int32_t window, int32_t first,
+                            void* workspace, size_t ws_bytes, mxq_stream_t stream);
+
+/*
+ * Sequences fork: row b < n of new_table (int32 [n, max_pages], row stride ld_new, apart
+ * from page_table) continues row parents[b] of page_table (int32 [B, max_pages]);
+ * -1: an empty row.  new_lens[b] is its length.  Full pages are shared.  An open last
+ * page (a length that is no multiple of page_size) is kept by its row's first child
+ * if the page's count is 1 before the call; every other child gets a fresh page, and
+ * copies[b] (int32 [n, 3]) = source page, fresh page, tokens to copy
+ * (mxq_cache_copy_pages), for every layer of the cache; -1, -1, 0 for the rest.  Entries
+ * behind a row's pages are -1.  The counts lose the old rows and gain the new ones, so
+ * rows without children are freed.  parents int32 [n] outside [-1, B) count as -1 and
+ * set MXQ_ERR_DEVICE.
+ */
+mxq_status mxq_cache_fork(const int32_t* page_table, int64_t ld_table, int64_t B,
+                          int64_t max_pages, const int32_t* seq_lens, int32_t* page_refs,
+                          int64_t pages, int32_t page_size, const int32_t* parents, int64_t n,
+                          int32_t* new_table, int64_t ld_new, int32_t* new_lens, int32_t* copies,
+                          void* workspace, size_t ws_bytes, mxq_stream_t stream);
+
+/*
+ * Copies the first copies[i][2] tokens (at most page_size) of page copies[i][0] to page
+ * copies[i][1], keys and values.  Entries with a negative page or no tokens are
+ * skipped, pages outside the cache too, with MXQ_ERR_DEVICE.  Destinations are distinct and
+ * no copy's source.  Caches as in mxq_rope_append_kv with 16-byte bases and strides.
+ * n == 0 is a no-op.
+ */
+mxq_status mxq_cache_copy_pages(void* k_cache, void* v_cache, int32_t cache_dtype, int64_t pages,
+                                int32_t page_size, int32_t Hkv, int32_t D, int64_t sck_p,
+                                int64_t sck_t, int64_t sck_h, int64_t scv_p, int64_t scv_t,
+                                int64_t scv_h, const int32_t* copies, int64_t n,
+                                mxq_stream_t stream);
+
+/*
+ * Moves the rows that stay of every sequence together, in place: key starts[b] + kept[b][i]
+ * becomes key starts[b] + i for i < counts[b], as if all were read before any is
+ * written (the accepted tokens of a drafted tree, the keys that an eviction
+ * keeps).  kept int32 [B, most], row stride ld_kept, kept[b][i] >= i; starts, counts int32
+ * [B].  Rows behind the kept ones are left as they are, and so is the
+ * table (mxq_cache_resize frees what is no longer needed).  Pages from starts[b] on are the
+ * sequence's own.  An entry below its index, a key outside the table, a page outside the cache are
+ * skipped, a count outside [0, most] clamped, with MXQ_ERR_DEVICE.
+ * B == 0 or most == 0 is a no-op.
+ */
+mxq_status mxq_cache_compact(void* k_cache, void* v_cache, int32_t cache_dtype, int64_t pages,
+                             int32_t page_size, int32_t Hkv, int32_t D, int64_t sck_p,
+                             int64_t sck_t, int64_t sck_h, int64_t scv_p, int64_t scv_t,
+                             int64_t scv_h, const int32_t* page_table, int64_t ld_table, int64_t B,
+                             int64_t max_pages, const int32_t* starts, const int32_t* kept,
+                             int64_t ld_kept, int64_t most, const int32_t* counts,
+                             mxq_stream_t stream);
 
 #ifdef __cplusplus
 }

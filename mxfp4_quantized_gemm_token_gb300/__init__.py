@@ -15,6 +15,10 @@ arguments: shapes, strides, output/workspace allocation and the stream.
     rope_append_kv(k, v, k_cache, v_cache, slots, cos_sin, positions, q=None, ...)
     paged_attention_decode(q, k_cache, v_cache, page_table, seq_lens, ...)
     attention_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k=None, ...)
+    cache_resize(page_table, seq_lens, new_lens, page_refs, page_size, ...)
+    cache_fork(page_table, seq_lens, page_refs, parents, page_size, ...)
+    cache_copy_pages(k_cache, v_cache, copies)
+    cache_compact(k_cache, v_cache, page_table, starts, kept, counts)
 """
 from __future__ import annotations
 
@@ -31,6 +35,8 @@ __all__ = [
     "fp8_per_tensor_linear", "moe_align_block", "fused_experts", "align_capacity",
     "rope_append_kv", "paged_attention_decode", "paged_attention_decode_workspace_size",
     "attention_varlen", "attention_varlen_workspace_size",
+    "cache_resize", "cache_fork", "cache_copy_pages", "cache_compact",
+    "cache_pages_workspace_size",
     "set_option", "get_option", "sync_status", "W_FP8_BLOCK128", "W_MXFP4",
 ]
 
@@ -553,3 +559,62 @@ def attention_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k=None, scale=None, causa
     (None: allocated here)."""
     return _attn().prompt(q, k, v, cu_seqlens_q, cu_seqlens_k, scale, causal, window, sinks,
                           return_lse, out, workspace)
+
+
+# --------------------------------------------------------- the pages of a cache
+# page_refs[p] is the number of page-table entries that hold page p; 0: free.
+
+def cache_pages_workspace_size(rows: int, pages: int) -> int:
+    n = ctypes.c_size_t(0)
+    check(_lib.load().mxq_cache_pages_workspace_size(rows, pages, ctypes.byref(n)))
+    return n.value
+
+
+def cache_resize(page_table, seq_lens, new_lens, page_refs, page_size: int, window: int = 0,
+                 first: int = 0, workspace=None):
+    """Take and free pages as sequences grow and shrink.
+
+    page_table: int32 [B, max_pages], changed in place; seq_lens, new_lens:
+    int32 [B], keys before and after (0 frees a row); page_refs: int32
+    [pages], changed in place.  Rows take the lowest free pages in their
+    order; freed entries become -1, and so do those that no page is left for
+    (sync_status raises).  window: entries of pages that end before the last
+    `window` keys of new_lens and begin behind the first `first` are freed as
+    well: what paged_attention_decode with these arguments no longer reads.
+    workspace: a caller's buffer of cache_pages_workspace_size bytes (None:
+    allocated here).  Returns page_table."""
+    return _attn().resize(page_table, seq_lens, new_lens, page_refs, page_size, window, first,
+                          workspace)
+
+
+def cache_fork(page_table, seq_lens, page_refs, parents, page_size: int, out=None, workspace=None):
+    """Rows that continue other rows: beams, or samples of one prompt.
+
+    page_table: int32 [B, max_pages]; seq_lens: int32 [B]; page_refs: int32
+    [pages], changed in place; parents: int32 [n], the row of page_table that
+    each new row continues (-1: none).  Full pages are shared; an open last
+    page that nothing else holds stays with the row's first child, other
+    children get a fresh page.  Rows without children are freed.  Returns the new
+    table [n, max_pages] (out, if given), its lengths int32 [n] and copies
+    int32 [n, 3]: what cache_copy_pages has to copy in every layer."""
+    return _attn().fork(page_table, seq_lens, page_refs, parents, page_size, out, workspace)
+
+
+def cache_copy_pages(k_cache, v_cache, copies) -> None:
+    """Copy the first tokens of pages: copies int32 [n, 3] = source page,
+    destination page, tokens; entries with a negative page are skipped.
+    k_cache, v_cache as in rope_append_kv, any outer strides of 16-byte
+    multiples.  A destination is no other entry's page."""
+    return _attn().copy_pages(k_cache, v_cache, copies)
+
+
+def cache_compact(k_cache, v_cache, page_table, starts, kept, counts) -> None:
+    """Move the kept rows of every sequence together, in place.
+
+    Key starts[b] + kept[b, i] becomes key starts[b] + i for i < counts[b], as
+    if all were read before any is written: the accepted tokens of a drafted
+    tree (starts: the context's length), or what an eviction keeps.  page_table: int32
+    [B, max_pages]; starts, counts: int32 [B]; kept: int32 [B, most], kept[b, i] >= i.
+    The rows from starts on lie in pages of the sequence's own; cache_resize
+    then frees what is no longer needed."""
+    return _attn().compact(k_cache, v_cache, page_table, starts, kept, counts)

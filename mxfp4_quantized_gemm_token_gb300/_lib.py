@@ -37,7 +37,13 @@ EXPORTED = [
     "mxq_w8a8_block_fp8_linear", "mxq_w8a8_block_fp8_linear_workspace_size",
     "mxq_rope_append_kv", "mxq_paged_attention_decode", "mxq_paged_attention_decode_workspace_size",
     "mxq_attention_varlen", "mxq_attention_varlen_workspace_size",
+    "mxq_cache_pages_workspace_size", "mxq_cache_resize", "mxq_cache_fork", "mxq_cache_copy_pages",
+    "mxq_cache_compact",
 ]
+
+# what the compiled calls get besides the entry points that connect() takes one by one
+CONNECTED = ["mxq_cache_pages_workspace_size", "mxq_cache_resize", "mxq_cache_fork",
+             "mxq_cache_copy_pages", "mxq_cache_compact"]
 
 NOALLOC_SCRATCH_BYTES = 16 * 1024 * 1024
 
@@ -100,6 +106,13 @@ def _declare(lib):
                                       I32, I32, I32, F, I32, I32, P, P, I64, I64, P, P, SZ, P]),
         "mxq_attention_varlen_workspace_size": (st, [I64, I64, I32, I32, I32,
                                                      ctypes.POINTER(SZ)]),
+        "mxq_cache_pages_workspace_size": (st, [I64, I64, ctypes.POINTER(SZ)]),
+        "mxq_cache_resize": (st, [P, I64, I64, I64, P, P, P, I64, I32, I32, I32, P, SZ, P]),
+        "mxq_cache_fork": (st, [P, I64, I64, I64, P, P, I64, I32, P, I64, P, I64, P, P, P, SZ, P]),
+        "mxq_cache_copy_pages": (st, [P, P, I32, I64, I32, I32, I32, I64, I64, I64, I64, I64, I64,
+                                      P, I64, P]),
+        "mxq_cache_compact": (st, [P, P, I32, I64, I32, I32, I32, I64, I64, I64, I64, I64, I64, P,
+                                   I64, I64, I64, P, P, I64, I64, P, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -146,6 +159,8 @@ def load_calls(raw_stream):
                 lib.mxq_rope_append_kv, lib.mxq_paged_attention_decode,
                 lib.mxq_paged_attention_decode_workspace_size, lib.mxq_attention_varlen,
                 lib.mxq_attention_varlen_workspace_size, lib.mxq_current_device)], check, raw_stream)
+            mod.connect_more({name: ctypes.cast(getattr(lib, name), ctypes.c_void_p).value
+                              for name in CONNECTED})
             _calls = mod
         return _calls
 

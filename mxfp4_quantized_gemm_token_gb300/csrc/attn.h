@@ -71,6 +71,52 @@ struct PromptParams {
   int* status;
 };
 
+// Page tables and the counts of their pages (cache_resize, cache_fork).
+struct PagesParams {
+  int* table;              // [B, max_pages], row stride ld; fork only reads it
+  int64_t ld, B, max_pages;
+  const int32_t* lens;     // [B]
+  int* refs;               // [pages]
+  int64_t pages;
+  int page_size;
+  const int32_t* new_lens; // resize: [B]
+  int window, first;       // resize: 0, or what frees the pages in between
+  const int32_t* parents;  // fork: [n]
+  int64_t n;
+  int* new_table;          // [n, max_pages], row stride ld_new
+  int64_t ld_new;
+  int32_t* new_lens_out;   // [n]
+  int32_t* copies;         // [n, 3]
+  void* workspace;
+  int* status;
+  // in the workspace
+  int64_t* row_begin;
+  int *fresh, *children, *first_child;
+};
+
+// Rows moved inside a cache (cache_copy_pages, cache_compact).
+struct MoveParams {
+  void *k_cache, *v_cache;
+  int es, cols, per_head;  // bytes of an element; 16-byte pieces of a token and of a head
+  int64_t pages;
+  int page_size;
+  int64_t ck_p, ck_t, ck_h, cv_p, cv_t, cv_h;
+  const int32_t* copies;   // copy: [n, 3]
+  int64_t n;
+  const int32_t* table;    // compact: [B, max_pages], row stride ld
+  int64_t ld, B, max_pages;
+  const int32_t *starts, *kept, *counts;
+  int64_t ld_kept, most;   // kept is [B, most]
+  int width;               // columns of a block
+  int* status;
+};
+
+size_t pages_workspace_bytes(int64_t rows, int64_t pages);
+cudaError_t launch_resize_pages(const PagesParams& p, cudaStream_t stream);
+cudaError_t launch_fork_pages(const PagesParams& p, cudaStream_t stream);
+cudaError_t launch_copy_pages(const MoveParams& p, int num_sms, cudaStream_t stream);
+cudaError_t launch_compact(const MoveParams& p, int num_sms, cudaStream_t stream);
+
 cudaError_t launch_rope_append(const RopeAppendParams& p, int num_sms, cudaStream_t stream);
 size_t decode_workspace_bytes(int64_t B, int Hq, int Hkv, int D, int num_sms);
 cudaError_t launch_decode(const DecodeParams& p, int num_sms, cudaStream_t stream);

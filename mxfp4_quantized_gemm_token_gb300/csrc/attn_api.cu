@@ -282,3 +282,185 @@ extern "C" mxq_status mxq_attention_varlen(
   if (!err.empty()) return fail(MXQ_ERR_CUDA, err);
   return e == cudaSuccess ? MXQ_OK : cuda_fail(e, "prompt attention launch");
 }
+
+namespace {
+
+// A page table and the counts of its pages.
+mxq_status check_table(const char* name, const void* table, int64_t ld, int64_t rows,
+                       int64_t max_pages) {
+  if (rows > 0 && max_pages > 0 && !table)
+    return fail(MXQ_ERR_INVALID_ARG, std::string(name) + " must be non-NULL");
+  if (!aligned(table, 4))
+    return fail(MXQ_ERR_INVALID_ARG, std::string(name) + " must be 4-byte aligned");
+  if (ld < max_pages)
+    return fail(MXQ_ERR_INVALID_ARG, std::string(name) + ": row stride below max_pages");
+  return MXQ_OK;
+}
+
+mxq_status check_pages(int64_t B, int64_t max_pages, int64_t pages, int32_t page_size,
+                       const int32_t* refs) {
+  if (B < 0 || max_pages < 0) return fail(MXQ_ERR_INVALID_ARG, "need B >= 0 and max_pages >= 0");
+  if (pages <= 0 || page_size <= 0 || pages > 0x7fffffff)
+    return fail(MXQ_ERR_INVALID_ARG, "need 0 < pages < 2^31 and page_size > 0");
+  if (B > 0x3fffffff) return fail(MXQ_ERR_UNSUPPORTED, "more than 2^30 rows");
+  if (max_pages > 0x7fffffff / 2 / page_size)
+    return fail(MXQ_ERR_UNSUPPORTED, "sequences of more than 2^30 keys");
+  if (!refs) return fail(MXQ_ERR_INVALID_ARG, "page_refs must be non-NULL");
+  if (!aligned(refs, 16))
+    return fail(MXQ_ERR_UNSUPPORTED, "page_refs needs a 16-byte aligned base");
+  return MXQ_OK;
+}
+
+mxq_status fill_move(MoveParams* p, void* k_cache, void* v_cache, int32_t dtype, int64_t pages,
+                     int32_t page_size, int32_t Hkv, int32_t D, int64_t sck_p, int64_t sck_t,
+                     int64_t sck_h, int64_t scv_p, int64_t scv_t, int64_t scv_h) {
+  if (Hkv <= 0 || D <= 0) return fail(MXQ_ERR_INVALID_ARG, "need Hkv > 0 and D > 0");
+  if (D % 16 != 0 || D > 512)
+    return fail(MXQ_ERR_UNSUPPORTED, "the head dimension must be a multiple of 16 up to 512");
+  if (Hkv > 65535) return fail(MXQ_ERR_UNSUPPORTED, "more than 65535 heads");
+  if (pages <= 0 || page_size <= 0 || pages > 0x7fffffff)
+    return fail(MXQ_ERR_INVALID_ARG, "need 0 < pages < 2^31 and page_size > 0");
+  MXQ_TRY(check_cache("k_cache", k_cache, dtype, pages, page_size, Hkv, D, sck_p, sck_t, sck_h,
+                      false, 16));
+  MXQ_TRY(check_cache("v_cache", v_cache, dtype, pages, page_size, Hkv, D, scv_p, scv_t, scv_h,
+                      false, 16));
+  p->k_cache = k_cache, p->v_cache = v_cache;
+  p->es = dtype == MXQ_E4M3 ? 1 : 2;
+  p->per_head = D * p->es / 16, p->cols = Hkv * p->per_head;
+  p->pages = pages, p->page_size = page_size;
+  p->ck_p = sck_p, p->ck_t = sck_t, p->ck_h = sck_h;
+  p->cv_p = scv_p, p->cv_t = scv_t, p->cv_h = scv_h;
+  return MXQ_OK;
+}
+
+}  // namespace
+
+extern "C" mxq_status mxq_cache_pages_workspace_size(int64_t rows, int64_t pages, size_t* bytes) {
+  if (!bytes || rows < 0 || pages <= 0 || rows > 0x3fffffff || pages > 0x7fffffff)
+    return fail(MXQ_ERR_INVALID_ARG, "bad sizes or NULL result pointer");
+  *bytes = pages_workspace_bytes(rows, pages);
+  return MXQ_OK;
+}
+
+extern "C" mxq_status mxq_cache_resize(int32_t* page_table, int64_t ld_table, int64_t B,
+                                       int64_t max_pages, const int32_t* seq_lens,
+                                       const int32_t* new_lens, int32_t* page_refs, int64_t pages,
+                                       int32_t page_size, int32_t window, int32_t first,
+                                       void* workspace, size_t ws_bytes, mxq_stream_t stream) {
+  MXQ_TRY(check_pages(B, max_pages, pages, page_size, page_refs));
+  if (window < 0 || first < 0)
+    return fail(MXQ_ERR_INVALID_ARG, "window and first must be >= 0 (0: none)");
+  if (B == 0) return MXQ_OK;
+  MXQ_TRY(check_table("page_table", page_table, ld_table, B, max_pages));
+  if (!seq_lens || !new_lens)
+    return fail(MXQ_ERR_INVALID_ARG, "seq_lens and new_lens must be non-NULL");
+  if (!aligned(seq_lens, 4) || !aligned(new_lens, 4))
+    return fail(MXQ_ERR_INVALID_ARG, "4-byte arrays must be 4-byte aligned");
+  MXQ_TRY(check_workspace(workspace, ws_bytes, pages_workspace_bytes(B, pages),
+                          "mxq_cache_pages_workspace_size"));
+  DeviceInfo d;
+  std::string err;
+  if (!device_info(&d, &err)) return fail(MXQ_ERR_UNSUPPORTED, err);
+  PagesParams p = {};
+  p.table = page_table, p.ld = ld_table, p.B = B, p.max_pages = max_pages;
+  p.lens = seq_lens, p.new_lens = new_lens, p.refs = page_refs, p.pages = pages;
+  p.page_size = page_size, p.window = window, p.first = first;
+  p.workspace = workspace, p.status = d.status;
+  const cudaError_t e = launch_resize_pages(p, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? MXQ_OK : cuda_fail(e, "cache resize launch");
+}
+
+extern "C" mxq_status mxq_cache_fork(const int32_t* page_table, int64_t ld_table, int64_t B,
+                                     int64_t max_pages, const int32_t* seq_lens,
+                                     int32_t* page_refs, int64_t pages, int32_t page_size,
+                                     const int32_t* parents, int64_t n, int32_t* new_table,
+                                     int64_t ld_new, int32_t* new_lens, int32_t* copies,
+                                     void* workspace, size_t ws_bytes, mxq_stream_t stream) {
+  MXQ_TRY(check_pages(B, max_pages, pages, page_size, page_refs));
+  if (n < 0) return fail(MXQ_ERR_INVALID_ARG, "need n >= 0");
+  if (n > 0x3fffffff) return fail(MXQ_ERR_UNSUPPORTED, "more than 2^30 rows");
+  if (B == 0 && n == 0) return MXQ_OK;
+  MXQ_TRY(check_table("page_table", page_table, ld_table, B, max_pages));
+  MXQ_TRY(check_table("new_table", new_table, ld_new, n, max_pages));
+  if ((B > 0 && !seq_lens) || (n > 0 && (!parents || !new_lens || !copies)))
+    return fail(MXQ_ERR_INVALID_ARG, "seq_lens, parents, new_lens and copies must be non-NULL");
+  if (!aligned(seq_lens, 4) || !aligned(parents, 4) || !aligned(new_lens, 4) ||
+      !aligned(copies, 4))
+    return fail(MXQ_ERR_INVALID_ARG, "4-byte arrays must be 4-byte aligned");
+  if (page_table && new_table && max_pages > 0 && B > 0 && n > 0) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(page_table);
+    const uintptr_t b = reinterpret_cast<uintptr_t>(new_table);
+    if (a < b + 4 * ((n - 1) * ld_new + max_pages) && b < a + 4 * ((B - 1) * ld_table + max_pages))
+      return fail(MXQ_ERR_INVALID_ARG, "new_table must not overlap page_table");
+  }
+  MXQ_TRY(check_workspace(workspace, ws_bytes, pages_workspace_bytes(std::max(B, n), pages),
+                          "mxq_cache_pages_workspace_size"));
+  DeviceInfo d;
+  std::string err;
+  if (!device_info(&d, &err)) return fail(MXQ_ERR_UNSUPPORTED, err);
+  PagesParams p = {};
+  p.table = const_cast<int32_t*>(page_table), p.ld = ld_table, p.B = B, p.max_pages = max_pages;
+  p.lens = seq_lens, p.refs = page_refs, p.pages = pages, p.page_size = page_size;
+  p.parents = parents, p.n = n, p.new_table = new_table, p.ld_new = ld_new;
+  p.new_lens_out = new_lens, p.copies = copies;
+  p.workspace = workspace, p.status = d.status;
+  const cudaError_t e = launch_fork_pages(p, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? MXQ_OK : cuda_fail(e, "cache fork launch");
+}
+
+extern "C" mxq_status mxq_cache_copy_pages(void* k_cache, void* v_cache, int32_t cache_dtype,
+                                           int64_t pages, int32_t page_size, int32_t Hkv,
+                                           int32_t D, int64_t sck_p, int64_t sck_t, int64_t sck_h,
+                                           int64_t scv_p, int64_t scv_t, int64_t scv_h,
+                                           const int32_t* copies, int64_t n,
+                                           mxq_stream_t stream) {
+  if (n < 0) return fail(MXQ_ERR_INVALID_ARG, "need n >= 0");
+  MoveParams p = {};
+  MXQ_TRY(fill_move(&p, k_cache, v_cache, cache_dtype, pages, page_size, Hkv, D, sck_p, sck_t,
+                    sck_h, scv_p, scv_t, scv_h));
+  if (n == 0) return MXQ_OK;
+  if (n > 0x3fffffff) return fail(MXQ_ERR_UNSUPPORTED, "more than 2^30 copies");
+  if (!copies) return fail(MXQ_ERR_INVALID_ARG, "copies must be non-NULL");
+  if (!aligned(copies, 4))
+    return fail(MXQ_ERR_INVALID_ARG, "4-byte arrays must be 4-byte aligned");
+  DeviceInfo d;
+  std::string err;
+  if (!device_info(&d, &err)) return fail(MXQ_ERR_UNSUPPORTED, err);
+  p.copies = copies, p.n = n, p.status = d.status;
+  const cudaError_t e =
+      launch_copy_pages(p, d.num_sms, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? MXQ_OK : cuda_fail(e, "cache copy launch");
+}
+
+extern "C" mxq_status mxq_cache_compact(void* k_cache, void* v_cache, int32_t cache_dtype,
+                                        int64_t pages, int32_t page_size, int32_t Hkv, int32_t D,
+                                        int64_t sck_p, int64_t sck_t, int64_t sck_h, int64_t scv_p,
+                                        int64_t scv_t, int64_t scv_h, const int32_t* page_table,
+                                        int64_t ld_table, int64_t B, int64_t max_pages,
+                                        const int32_t* starts, const int32_t* kept,
+                                        int64_t ld_kept, int64_t most, const int32_t* counts,
+                                        mxq_stream_t stream) {
+  if (B < 0 || max_pages < 0 || most < 0)
+    return fail(MXQ_ERR_INVALID_ARG, "need B, max_pages and the kept rows >= 0");
+  MoveParams p = {};
+  MXQ_TRY(fill_move(&p, k_cache, v_cache, cache_dtype, pages, page_size, Hkv, D, sck_p, sck_t,
+                    sck_h, scv_p, scv_t, scv_h));
+  if (B == 0 || most == 0) return MXQ_OK;
+  if (B > 65535) return fail(MXQ_ERR_UNSUPPORTED, "more than 65535 sequences");
+  if (most > 0x3fffffff || max_pages > 0x7fffffff / 2 / page_size)
+    return fail(MXQ_ERR_UNSUPPORTED, "sequences of more than 2^30 keys");
+  MXQ_TRY(check_table("page_table", page_table, ld_table, B, max_pages));
+  if (!starts || !kept || !counts)
+    return fail(MXQ_ERR_INVALID_ARG, "starts, kept and counts must be non-NULL");
+  if (!aligned(starts, 4) || !aligned(kept, 4) || !aligned(counts, 4))
+    return fail(MXQ_ERR_INVALID_ARG, "4-byte arrays must be 4-byte aligned");
+  if (ld_kept < most) return fail(MXQ_ERR_INVALID_ARG, "kept: row stride below its width");
+  DeviceInfo d;
+  std::string err;
+  if (!device_info(&d, &err)) return fail(MXQ_ERR_UNSUPPORTED, err);
+  p.table = page_table, p.ld = ld_table, p.B = B, p.max_pages = max_pages;
+  p.starts = starts, p.kept = kept, p.counts = counts, p.ld_kept = ld_kept, p.most = most;
+  p.status = d.status;
+  const cudaError_t e = launch_compact(p, d.num_sms, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? MXQ_OK : cuda_fail(e, "cache compact launch");
+}

@@ -15,11 +15,13 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <exception>
 #include <initializer_list>
 #include <string>
+#include <type_traits>
 
 #include "mxq.h"
 
@@ -31,6 +33,11 @@ decltype(&mxq_paged_attention_decode_workspace_size) decode_size_fn;
 decltype(&mxq_attention_varlen) prompt_fn;
 decltype(&mxq_attention_varlen_workspace_size) prompt_size_fn;
 decltype(&mxq_current_device) device_fn;
+decltype(&mxq_cache_pages_workspace_size) pages_size_fn;
+decltype(&mxq_cache_resize) resize_fn;
+decltype(&mxq_cache_fork) fork_fn;
+decltype(&mxq_cache_copy_pages) copy_pages_fn;
+decltype(&mxq_cache_compact) compact_fn;
 PyObject* check_fn;        // raises for a status
 PyObject* stream_fn;       // device index -> the current stream's address
 
@@ -389,6 +396,156 @@ PyObject* prompt(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   });
 }
 
+// int32 [rows, width] with a unit inner stride
+struct Table {
+  int32_t* p;
+  int64_t rows, width, ld;
+  // rows < 0: any
+  Table(const char* name, const at::Tensor& t, int64_t n) {
+    if (t.dim() != 2 || t.scalar_type() != at::kInt || (n >= 0 && t.size(0) != n) ||
+        (t.size(1) > 1 && t.stride(1) != 1) || (t.size(0) > 1 && t.stride(0) < t.size(1)))
+      refuse(PyExc_ValueError, std::string(name) + " must be int32 [" +
+                                   (n < 0 ? std::string("rows") : std::to_string(n)) +
+                                   ", width] with a unit inner stride");
+    rows = t.size(0), width = t.size(1), ld = rows > 1 ? t.stride(0) : width;
+    p = static_cast<int32_t*>(t.data_ptr());
+  }
+};
+
+// (page_table, seq_lens, new_lens, page_refs, page_size, window, first, workspace)
+PyObject* resize(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
+  return guarded(nargs, 8, [&]() -> PyObject* {
+    const at::Tensor &table = needed("page_table", a[0]), &lens = needed("seq_lens", a[1]);
+    const at::Tensor &to = needed("new_lens", a[2]), &refs = needed("page_refs", a[3]);
+    const at::Tensor* ws = tensor("workspace", a[7]);
+    same_device({&table, &lens, &to, &refs, ws});
+    const Table t("page_table", table, -1);
+    const int32_t* l = vec<const int32_t>("seq_lens", &lens, at::kInt, t.rows);
+    const int32_t* n = vec<const int32_t>("new_lens", &to, at::kInt, t.rows);
+    int32_t* r = vec<int32_t>("page_refs", &refs, at::kInt, refs.numel());
+    const int32_t size = integer("page_size", a[4]), window = integer("window", a[5]);
+    const int32_t first = integer("first", a[6]);
+    at::Tensor space = workspace(ws);
+    const mxq_stream_t stream = stream_of(table);
+    check(unlocked([&] {
+      if (!space.defined()) {
+        size_t bytes = 0;
+        const mxq_status st = pages_size_fn(t.rows, refs.numel(), &bytes);
+        if (st != MXQ_OK) return st;
+        space = fresh({static_cast<int64_t>(bytes)}, at::kByte, table);
+      }
+      return resize_fn(t.p, t.ld, t.rows, t.width, l, n, r, refs.numel(), size, window, first,
+                       space.data_ptr(), space.nbytes(), stream);
+    }));
+    return Py_NewRef(a[0]);
+  });
+}
+
+// (page_table, seq_lens, page_refs, parents, page_size, out, workspace)
+PyObject* fork_rows(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
+  return guarded(nargs, 7, [&]() -> PyObject* {
+    const at::Tensor &table = needed("page_table", a[0]), &lens = needed("seq_lens", a[1]);
+    const at::Tensor &refs = needed("page_refs", a[2]), &parents = needed("parents", a[3]);
+    const at::Tensor *given = tensor("out", a[5]), *ws = tensor("workspace", a[6]);
+    same_device({&table, &lens, &refs, &parents, given, ws});
+    const Table t("page_table", table, -1);
+    const int64_t n = parents.numel();
+    const int32_t* l = vec<const int32_t>("seq_lens", &lens, at::kInt, t.rows);
+    int32_t* r = vec<int32_t>("page_refs", &refs, at::kInt, refs.numel());
+    const int32_t* from = vec<const int32_t>("parents", &parents, at::kInt, n);
+    const int32_t size = integer("page_size", a[4]);
+    at::Tensor out, space = workspace(ws), new_lens, copies;
+    if (given != nullptr) {
+      const Table o("out", *given, n);
+      if (o.width != t.width)
+        refuse(PyExc_ValueError, "out must be as wide as page_table, " + std::to_string(t.width));
+      out = *given;
+    }
+    const mxq_stream_t stream = stream_of(table);
+    check(unlocked([&] {
+      if (!space.defined()) {
+        size_t bytes = 0;
+        const mxq_status st = pages_size_fn(std::max(t.rows, n), refs.numel(), &bytes);
+        if (st != MXQ_OK) return st;
+        space = fresh({static_cast<int64_t>(bytes)}, at::kByte, table);
+      }
+      if (!out.defined()) out = fresh({n, t.width}, at::kInt, table);
+      new_lens = fresh({n}, at::kInt, table);
+      copies = fresh({n, 3}, at::kInt, table);
+      return fork_fn(t.p, t.ld, t.rows, t.width, l, r, refs.numel(), size, from, n,
+                     static_cast<int32_t*>(out.data_ptr()), n > 1 ? out.stride(0) : t.width,
+                     static_cast<int32_t*>(new_lens.data_ptr()),
+                     static_cast<int32_t*>(copies.data_ptr()), space.data_ptr(), space.nbytes(),
+                     stream);
+    }));
+    PyObject* parts[3] = {given != nullptr ? Py_NewRef(a[5]) : THPVariable_Wrap(out),
+                          THPVariable_Wrap(new_lens), THPVariable_Wrap(copies)};
+    PyObject* all = parts[0] && parts[1] && parts[2]
+                        ? PyTuple_Pack(3, parts[0], parts[1], parts[2]) : nullptr;
+    for (PyObject* o : parts) Py_XDECREF(o);
+    return all;
+  });
+}
+
+// (k_cache, v_cache, copies)
+PyObject* copy_pages(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
+  return guarded(nargs, 3, [&]() -> PyObject* {
+    const at::Tensor &kc = needed("k_cache", a[0]), &vc = needed("v_cache", a[1]);
+    const at::Tensor& copies = needed("copies", a[2]);
+    same_device({&kc, &vc, &copies});
+    const Caches c(kc, vc, -1, kc.dim() == 4 ? kc.size(3) : 0);
+    if (copies.dim() != 2 || copies.size(1) != 3)
+      refuse(PyExc_ValueError, "copies must be int32 [n, 3]: source page, destination, tokens");
+    const int64_t n = copies.size(0);
+    const int32_t* list = vec<const int32_t>("copies", &copies, at::kInt, 3 * n);
+    const int32_t Hkv = narrow("kv_heads", c.heads), D = narrow("head_dim", kc.size(3));
+    const mxq_stream_t stream = stream_of(kc);
+    check(unlocked([&] {
+      return copy_pages_fn(c.k, c.v, c.dtype, c.pages, c.page_size, Hkv, D, c.k0, c.k1, c.k2,
+                           c.v0, c.v1, c.v2, list, n, stream);
+    }));
+    Py_RETURN_NONE;
+  });
+}
+
+// (k_cache, v_cache, page_table, starts, kept, counts)
+PyObject* compact(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
+  return guarded(nargs, 6, [&]() -> PyObject* {
+    const at::Tensor &kc = needed("k_cache", a[0]), &vc = needed("v_cache", a[1]);
+    const at::Tensor &table = needed("page_table", a[2]), &starts = needed("starts", a[3]);
+    const at::Tensor &kept = needed("kept", a[4]), &counts = needed("counts", a[5]);
+    same_device({&kc, &vc, &table, &starts, &kept, &counts});
+    const Caches c(kc, vc, -1, kc.dim() == 4 ? kc.size(3) : 0);
+    const Table t("page_table", table, -1), list("kept", kept, t.rows);
+    const int32_t* s = vec<const int32_t>("starts", &starts, at::kInt, t.rows);
+    const int32_t* n = vec<const int32_t>("counts", &counts, at::kInt, t.rows);
+    const int32_t Hkv = narrow("kv_heads", c.heads), D = narrow("head_dim", kc.size(3));
+    const mxq_stream_t stream = stream_of(kc);
+    check(unlocked([&] {
+      return compact_fn(c.k, c.v, c.dtype, c.pages, c.page_size, Hkv, D, c.k0, c.k1, c.k2, c.v0,
+                        c.v1, c.v2, t.p, t.ld, t.rows, t.width, s, list.p, list.ld, list.width, n,
+                        stream);
+    }));
+    Py_RETURN_NONE;
+  });
+}
+
+// ({name: address}) of the further entry points: once, before their calls
+PyObject* connect_more(PyObject*, PyObject* by_name) {
+  auto set = [&](const char* name, auto* fn) {
+    PyObject* o = PyMapping_GetItemString(by_name, name);
+    if (o == nullptr) return false;
+    *fn = reinterpret_cast<std::remove_pointer_t<decltype(fn)>>(PyLong_AsVoidPtr(o));
+    Py_DECREF(o);
+    return !PyErr_Occurred();
+  };
+  if (!set("mxq_cache_pages_workspace_size", &pages_size_fn) ||
+      !set("mxq_cache_resize", &resize_fn) || !set("mxq_cache_fork", &fork_fn) ||
+      !set("mxq_cache_copy_pages", &copy_pages_fn) || !set("mxq_cache_compact", &compact_fn))
+    return nullptr;
+  Py_RETURN_NONE;
+}
+
 // (addresses of the six entry points, check, stream): once, before any call
 PyObject* connect(PyObject*, PyObject* args) {
   unsigned long long fn[6];
@@ -411,6 +568,11 @@ PyMethodDef methods[] = {
     {"append", reinterpret_cast<PyCFunction>(append), METH_FASTCALL, nullptr},
     {"decode", reinterpret_cast<PyCFunction>(decode), METH_FASTCALL, nullptr},
     {"prompt", reinterpret_cast<PyCFunction>(prompt), METH_FASTCALL, nullptr},
+    {"resize", reinterpret_cast<PyCFunction>(resize), METH_FASTCALL, nullptr},
+    {"fork", reinterpret_cast<PyCFunction>(fork_rows), METH_FASTCALL, nullptr},
+    {"copy_pages", reinterpret_cast<PyCFunction>(copy_pages), METH_FASTCALL, nullptr},
+    {"compact", reinterpret_cast<PyCFunction>(compact), METH_FASTCALL, nullptr},
+    {"connect_more", connect_more, METH_O, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_attn_calls", nullptr, -1, methods,
                       nullptr, nullptr, nullptr, nullptr};

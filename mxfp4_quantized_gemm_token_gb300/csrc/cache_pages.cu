@@ -1,0 +1,481 @@
+// cache_pages.cu — the pages of a key/value cache: taken and freed, forked, copied, and the
+// rows that stay of a sequence moved together.
+//
+// Pages are counted, not listed: refs[p] is the number of page-table entries that hold page
+// p, and a page is free where that is 0.  A call takes the lowest free pages, in the order
+// of its rows, so its result does not depend on timing; a page that a call frees is not taken
+// by the same call.  The atomics here add to counts, in any order.
+#include "attn.h"
+#include "internal.h"
+
+namespace mxq {
+
+namespace {
+
+// ------------------------------------------------------------- tables and counts
+// One cluster of eight blocks: the steps below depend on one another over all rows and pages,
+// a cluster's barrier takes a fraction of a launch, and a table and its counts are small (64K
+// pages: 256 KB).  Latency-bound.
+constexpr int kCluster = 8;
+constexpr int kTableThreads = 1024;
+constexpr int kAll = kCluster * kTableThreads;
+constexpr int kWarpsAll = kAll / 32;
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;"
+               ::: "memory");
+}
+
+// a 64-bit value of the same variable in block `rank` of the cluster
+__device__ __forceinline__ unsigned long long of_block(const unsigned long long* at, int rank) {
+  uint32_t there;
+  unsigned long long v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(smem_u32(at)), "r"(rank));
+  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(there) : "memory");
+  return v;
+}
+
+// Sums over the cluster's threads in their order: what comes before this thread, and all.
+// Every thread calls it; `sums` is reused, so a cluster_sync has to follow before the next call.
+__device__ __forceinline__ void scan_all(unsigned long long mine, unsigned long long* sums,
+                                         unsigned long long* before, unsigned long long* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rank = blockIdx.x;
+  unsigned long long incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned long long y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) sums[1 + warp] = incl;
+  __syncthreads();
+  unsigned long long w = lane < kTableThreads / 32 ? sums[1 + lane] : 0;
+  unsigned long long winc = w;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned long long y = __shfl_up_sync(0xffffffffu, winc, o);
+    if (lane >= o) winc += y;
+  }
+  const unsigned long long block = __shfl_sync(0xffffffffu, winc, 31);
+  const unsigned long long warps_before = __shfl_sync(0xffffffffu, winc - w, warp);
+  if (threadIdx.x == 0) sums[0] = block;
+  cluster_sync();
+  unsigned long long other = lane < kCluster ? of_block(sums, lane) : 0;
+  unsigned long long oinc = other;
+#pragma unroll
+  for (int o = 1; o < kCluster; o <<= 1) {
+    const unsigned long long y = __shfl_up_sync(0xffffffffu, oinc, o);
+    if (lane >= o) oinc += y;
+  }
+  *total = __shfl_sync(0xffffffffu, oinc, kCluster - 1);
+  *before = __shfl_sync(0xffffffffu, oinc - other, rank) + warps_before + incl - mine;
+}
+
+// Rows or pages of a thread, adjacent ones
+struct Span {
+  int64_t from, to;
+  __device__ __forceinline__ Span(int64_t n, int unit) {
+    const int64_t each = (n + static_cast<int64_t>(kAll) * unit - 1) /
+                         (static_cast<int64_t>(kAll) * unit) * unit;
+    const int64_t me = static_cast<int64_t>(blockIdx.x) * kTableThreads + threadIdx.x;
+    from = min(n, me * each);
+    to = min(n, from + each);
+  }
+};
+
+__device__ __forceinline__ int pages_of(int len, int page_size) {
+  return static_cast<int>((static_cast<int64_t>(len) + page_size - 1) / page_size);
+}
+
+// a length inside the table's width
+__device__ __forceinline__ int clamp_len(const PagesParams& p, int len, bool* bad) {
+  const int64_t most = p.max_pages * p.page_size;
+  if (len < 0 || len > most) *bad = true;
+  return static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(len), most)));
+}
+
+// The first `need` free pages, ascending, into fresh[]; their counts become 1.  `before`: free
+// pages of the threads before this one.
+__device__ __forceinline__ int64_t count_free(const PagesParams& p, const Span& s) {
+  int64_t n = 0;
+  int64_t i = s.from;
+  for (; i + 4 <= s.to; i += 4) {
+    // (a span begins at a multiple of four pages; the counts at 16 bytes)
+    const int4 r = *reinterpret_cast<const int4*>(p.refs + i);
+    n += (r.x == 0) + (r.y == 0) + (r.z == 0) + (r.w == 0);
+  }
+  for (; i < s.to; ++i) n += p.refs[i] == 0;
+  return n;
+}
+__device__ __forceinline__ void take_free(const PagesParams& p, const Span& s, int64_t before,
+                                          int64_t need, int* fresh) {
+  for (int64_t i = s.from; i < s.to && before < need; ++i)
+    if (p.refs[i] == 0) {
+      fresh[before++] = static_cast<int>(i);
+      p.refs[i] = 1;
+    }
+}
+
+// a count changed by n; one that falls below 0 was wrong before
+__device__ __forceinline__ void add_ref(const PagesParams& p, int page, int n, bool* bad) {
+  if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(p.pages)) {
+    if (page >= 0) *bad = true;
+    return;
+  }
+  if (n != 0 && atomicAdd(p.refs + page, n) + n < 0) *bad = true;
+}
+
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kTableThreads)
+    resize_kernel(const PagesParams p) {
+  __shared__ unsigned long long sums[2][1 + kTableThreads / 32];
+  pdl_wait();
+  pdl_launch_dependents();
+  bool bad = false;
+  // pages that each row takes
+  const Span rows(p.B, 1), pages(p.pages, 4);
+  int64_t need = 0;
+  for (int64_t b = rows.from; b < rows.to; ++b)
+    need += max(0, pages_of(clamp_len(p, p.new_lens[b], &bad), p.page_size) -
+                       pages_of(clamp_len(p, p.lens[b], &bad), p.page_size));
+  const int64_t free = count_free(p, pages);
+  unsigned long long need_before, need_all, free_before, free_all;
+  scan_all(need, sums[0], &need_before, &need_all);
+  scan_all(free, sums[1], &free_before, &free_all);
+  for (int64_t b = rows.from; b < rows.to; ++b) {
+    p.row_begin[b] = static_cast<int64_t>(need_before);
+    need_before += max(0, pages_of(clamp_len(p, p.new_lens[b], &bad), p.page_size) -
+                              pages_of(clamp_len(p, p.lens[b], &bad), p.page_size));
+  }
+  take_free(p, pages, static_cast<int64_t>(free_before), static_cast<int64_t>(need_all), p.fresh);
+  cluster_sync();
+  const int lane = threadIdx.x & 31;
+  const int64_t have = static_cast<int64_t>(free_all);
+  for (int64_t b = blockIdx.x * (kTableThreads / 32) + (threadIdx.x >> 5); b < p.B;
+       b += kWarpsAll) {
+    int* row = p.table + b * p.ld;
+    const int len = clamp_len(p, p.new_lens[b], &bad);
+    const int n0 = pages_of(clamp_len(p, p.lens[b], &bad), p.page_size);
+    const int n1 = pages_of(len, p.page_size);
+    const int64_t at = p.row_begin[b];
+    for (int i = n0 + lane; i < n1; i += 32) {
+      const int64_t k = at + i - n0;
+      row[i] = k < have ? p.fresh[k] : -1;
+      if (k >= have) bad = true;
+    }
+    auto drop = [&](int i) {
+      add_ref(p, row[i], -1, &bad);
+      row[i] = -1;
+    };
+    for (int i = n1 + lane; i < n0; i += 32) drop(i);
+    if (p.window > 0) {
+      // pages that end before the window and begin behind the first keys
+      const int from = pages_of(p.first, p.page_size);
+      const int to = min(min(n0, n1), max(0, len - p.window) / p.page_size);
+      for (int i = from + lane; i < to; i += 32)
+        if (row[i] != -1) drop(i);
+    }
+  }
+  if (bad) atomicOr(p.status, kStatusBadIndex);
+}
+
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kTableThreads)
+    fork_kernel(const PagesParams p) {
+  __shared__ unsigned long long sums[2][1 + kTableThreads / 32];
+  pdl_wait();
+  pdl_launch_dependents();
+  bool bad = false;
+  const Span old(p.B, 1), rows(p.n, 1), pages(p.pages, 4);
+  // children of every old row, and the first of them
+  for (int64_t r = old.from; r < old.to; ++r) p.children[r] = 0, p.first_child[r] = 0x7fffffff;
+  cluster_sync();
+  auto parent_of = [&](int64_t b) {
+    const int r = p.parents[b];
+    if (r < -1 || r >= p.B) bad = true;
+    return r >= 0 && r < p.B ? r : -1;
+  };
+  for (int64_t b = rows.from; b < rows.to; ++b) {
+    const int r = parent_of(b);
+    if (r < 0) continue;
+    atomicAdd(p.children + r, 1);
+    atomicMin(p.first_child + r, static_cast<int>(b));
+  }
+  cluster_sync();
+  // the open page of a row: the one that its next key goes to
+  struct Open {
+    int r, len, n, page;
+    bool wants;              // a page of its own
+  };
+  auto open_of = [&](int64_t b) {
+    Open o = {parent_of(b), 0, 0, -1, false};
+    if (o.r < 0) return o;
+    o.len = clamp_len(p, p.lens[o.r], &bad);
+    o.n = pages_of(o.len, p.page_size);
+    if (o.len % p.page_size == 0) return o;
+    o.page = p.table[o.r * p.ld + o.n - 1];
+    if (static_cast<uint32_t>(o.page) >= static_cast<uint32_t>(p.pages)) return o;
+    o.wants = p.refs[o.page] != 1 || p.first_child[o.r] != b;
+    return o;
+  };
+  int64_t need = 0;
+  for (int64_t b = rows.from; b < rows.to; ++b) need += open_of(b).wants;
+  const int64_t free = count_free(p, pages);
+  unsigned long long need_before, need_all, free_before, free_all;
+  scan_all(need, sums[0], &need_before, &need_all);
+  scan_all(free, sums[1], &free_before, &free_all);
+  for (int64_t b = rows.from; b < rows.to; ++b) {
+    const Open o = open_of(b);
+    // (-1: the row keeps its parent's pages as they are)
+    p.row_begin[b] = o.wants ? static_cast<int64_t>(need_before++) : -1;
+    p.new_lens_out[b] = o.len;
+  }
+  // no page is taken before every row has seen its open page's count
+  cluster_sync();
+  take_free(p, pages, static_cast<int64_t>(free_before), static_cast<int64_t>(need_all), p.fresh);
+  cluster_sync();
+  const int lane = threadIdx.x & 31;
+  const int warp = blockIdx.x * (kTableThreads / 32) + (threadIdx.x >> 5);
+  const int64_t have = static_cast<int64_t>(free_all);
+  for (int64_t b = warp; b < p.n; b += kWarpsAll) {
+    const int r = parent_of(b), len = p.new_lens_out[b];
+    const int n = pages_of(len, p.page_size);
+    const int64_t k = p.row_begin[b];
+    const int* from = p.table + static_cast<int64_t>(max(r, 0)) * p.ld;
+    int* to = p.new_table + b * p.ld_new;
+    for (int64_t i = lane; i < p.max_pages; i += 32) {
+      int page = i < n ? from[i] : -1;
+      if (i == n - 1 && k >= 0) {
+        const int src = page;
+        page = k < have ? p.fresh[k] : -1;
+        if (k >= have) bad = true;
+        p.copies[3 * b] = k < have ? src : -1;
+        p.copies[3 * b + 1] = page;
+        p.copies[3 * b + 2] = k < have ? len % p.page_size : 0;
+      }
+      to[i] = page;
+    }
+    if (k < 0 && lane < 3) p.copies[3 * b + lane] = lane < 2 ? -1 : 0;
+  }
+  // a row's pages are held by its children instead of by itself; its open page by the first
+  // child at most
+  for (int64_t r = warp; r < p.B; r += kWarpsAll) {
+    const int len = clamp_len(p, p.lens[r], &bad);
+    const int n = pages_of(len, p.page_size), full = len / p.page_size;
+    const int more = p.children[r] - 1;
+    const int* row = p.table + r * p.ld;
+    if (more != 0)
+      for (int i = lane; i < full; i += 32) add_ref(p, row[i], more, &bad);
+    if (full < n && lane == 0) {
+      const bool kept = more >= 0 && p.row_begin[p.first_child[r]] < 0;
+      if (!kept) add_ref(p, row[full], -1, &bad);
+    }
+  }
+  if (bad) atomicOr(p.status, kStatusBadIndex);
+}
+
+// ------------------------------------------------------------------- moving rows
+// A token's keys (or values) are `cols` pieces of 16 bytes: head h = col / per_head.
+constexpr int kMoveThreads = 256;
+constexpr int kDepth = 8;             // loads in flight a thread
+
+struct Column {
+  bool value;                         // of the values' cache
+  int64_t at;                         // bytes from a token's begin
+};
+__device__ __forceinline__ Column column_of(const MoveParams& p, int col) {
+  Column c;
+  c.value = col >= p.cols;
+  col -= c.value ? p.cols : 0;
+  const int h = static_cast<int>(static_cast<uint32_t>(col) / static_cast<uint32_t>(p.per_head));
+  c.at = h * (c.value ? p.cv_h : p.ck_h) * p.es + (col - h * p.per_head) * 16;
+  return c;
+}
+
+// Pages copied: block (part of the page, pair, keys or values).  HBM-bound; the pieces of a
+// token are adjacent threads', each with eight loads on their way.
+__global__ void __launch_bounds__(kMoveThreads) copy_pages_kernel(const MoveParams p) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int64_t pair = static_cast<int64_t>(blockIdx.y) + static_cast<int64_t>(blockIdx.z) * 65535;
+  if (pair >= p.n) return;
+  const int src = p.copies[3 * pair], dst = p.copies[3 * pair + 1];
+  const int tokens = p.copies[3 * pair + 2];
+  if (src < 0 || dst < 0 || tokens <= 0) return;
+  const int rows = min(tokens, p.page_size);
+  const bool bad = src >= p.pages || dst >= p.pages;
+  if ((bad || tokens > p.page_size) && blockIdx.x == 0 && threadIdx.x == 0)
+    atomicOr(p.status, kStatusBadIndex);
+  if (bad) return;
+  const int64_t all = 2 * static_cast<int64_t>(p.cols) * rows;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kMoveThreads;
+  for (int64_t i0 = static_cast<int64_t>(blockIdx.x) * kMoveThreads + threadIdx.x; i0 < all;
+       i0 += step * kDepth) {
+    uint4 v[kDepth];
+    char* to[kDepth];
+#pragma unroll
+    for (int u = 0; u < kDepth; ++u) {
+      const int64_t i = i0 + u * step;
+      to[u] = nullptr;
+      if (i >= all) continue;
+      // keys first, then values
+      const int64_t half = static_cast<int64_t>(p.cols) * rows;
+      const bool value = i >= half;
+      const int64_t j = value ? i - half : i;
+      int64_t t;
+      int col;
+      if (all <= 0xffffffffll) {
+        t = static_cast<uint32_t>(j) / static_cast<uint32_t>(p.cols);
+        col = static_cast<int>(static_cast<uint32_t>(j) -
+                               static_cast<uint32_t>(t) * static_cast<uint32_t>(p.cols));
+      } else {
+        t = j / p.cols;
+        col = static_cast<int>(j - t * p.cols);
+      }
+      const Column c = column_of(p, value ? col + p.cols : col);
+      char* base = static_cast<char*>(value ? p.v_cache : p.k_cache);
+      const int64_t sp = value ? p.cv_p : p.ck_p, st = value ? p.cv_t : p.ck_t;
+      const int64_t row = t * st * p.es + c.at;
+      v[u] = *reinterpret_cast<const uint4*>(base + src * sp * p.es + row);
+      to[u] = base + dst * sp * p.es + row;
+    }
+#pragma unroll
+    for (int u = 0; u < kDepth; ++u)
+      if (to[u] != nullptr) *reinterpret_cast<uint4*>(to[u]) = v[u];
+  }
+}
+
+// Rows moved together, in place: row start + kept[i] becomes row start + i.  A block owns
+// `width` columns of a sequence and takes its rows in turn, kDepth x 256 / width at a time:
+// all are read before any is written.  As kept[i] >= i, what is read later lies behind all
+// that is written, so no block waits for another, and a long list of few sequences
+// is shared out by columns (down to 32 bytes).  HBM-bound where it is long.
+__global__ void __launch_bounds__(kMoveThreads) compact_kernel(const MoveParams p) {
+  extern __shared__ int2 places[];    // of a step's rows: from, then to (page, row of it)
+  pdl_wait();
+  pdl_launch_dependents();
+  const int b = blockIdx.y;
+  const int rows = kMoveThreads / p.width;            // at once
+  const int step = rows * kDepth;
+  const int col = blockIdx.x * p.width + threadIdx.x % p.width, r0 = threadIdx.x / p.width;
+  const bool mine = col < 2 * p.cols;
+  const Column c = column_of(p, mine ? col : 0);
+  char* base = static_cast<char*>(c.value ? p.v_cache : p.k_cache) + c.at;
+  const int64_t sp = (c.value ? p.cv_p : p.ck_p) * p.es, st = (c.value ? p.cv_t : p.ck_t) * p.es;
+  const int start = p.starts[b], given = p.counts[b];
+  const int count = max(0, min(given, static_cast<int>(p.most)));
+  const int64_t slots = p.max_pages * p.page_size;
+  bool bad = given != count || start < 0;
+  const int* kept = p.kept + b * p.ld_kept;
+  const int* table = p.table + b * p.ld;
+  auto place = [&](int64_t key) {
+    int2 at = make_int2(-1, 0);
+    if (key >= slots) {
+      bad = true;
+      return at;
+    }
+    const uint32_t k = static_cast<uint32_t>(key), s = static_cast<uint32_t>(p.page_size);
+    const uint32_t n = k / s;
+    at = make_int2(table[n], static_cast<int>(k - n * s));
+    if (static_cast<uint32_t>(at.x) >= static_cast<uint32_t>(p.pages)) {
+      at.x = -1;
+      bad = true;
+    }
+    return at;
+  };
+  for (int i0 = 0; start >= 0 && i0 < count; i0 += step) {
+    const int n = min(step, count - i0);
+    for (int i = threadIdx.x; i < n; i += kMoveThreads) {
+      const int k = kept[i0 + i];
+      int2 from = make_int2(-1, 0), to = from;
+      if (k < i0 + i) {
+        bad = true;                   // would be overwritten before it is read
+      } else if (k != i0 + i) {
+        from = place(static_cast<int64_t>(start) + k);
+        to = place(static_cast<int64_t>(start) + i0 + i);
+      }
+      places[i] = from;
+      places[step + i] = to;
+    }
+    __syncthreads();
+    uint4 v[kDepth];
+#pragma unroll
+    for (int u = 0; u < kDepth; ++u) {
+      const int i = u * rows + r0;
+      if (!mine || i >= n) continue;
+      const int2 at = places[i];
+      if (at.x >= 0) v[u] = *reinterpret_cast<const uint4*>(base + at.x * sp + at.y * st);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < kDepth; ++u) {
+      const int i = u * rows + r0;
+      if (!mine || i >= n) continue;
+      const int2 from = places[i], to = places[step + i];
+      if (from.x >= 0 && to.x >= 0)
+        *reinterpret_cast<uint4*>(base + to.x * sp + to.y * st) = v[u];
+    }
+    __syncthreads();
+  }
+  if (bad) atomicOr(p.status, kStatusBadIndex);
+}
+
+size_t round256(size_t n) { return (n + 255) / 256 * 256; }
+
+}  // namespace
+
+// [rows] begins, [pages] fresh pages, [rows] children, [rows] first children
+size_t pages_workspace_bytes(int64_t rows, int64_t pages) {
+  return round256(rows * 8) + round256(pages * 4) + 2 * round256(rows * 4);
+}
+
+namespace {
+void spread(PagesParams* p, int64_t rows) {
+  char* ws = static_cast<char*>(p->workspace);
+  p->row_begin = reinterpret_cast<int64_t*>(ws);
+  ws += round256(rows * 8);
+  p->fresh = reinterpret_cast<int*>(ws);
+  ws += round256(p->pages * 4);
+  p->children = reinterpret_cast<int*>(ws);
+  p->first_child = reinterpret_cast<int*>(ws + round256(rows * 4));
+}
+}  // namespace
+
+cudaError_t launch_resize_pages(const PagesParams& given, cudaStream_t stream) {
+  PagesParams p = given;
+  spread(&p, p.B);
+  return launch_k(resize_kernel, dim3(kCluster), dim3(kTableThreads), 0, stream, p);
+}
+
+cudaError_t launch_fork_pages(const PagesParams& given, cudaStream_t stream) {
+  PagesParams p = given;
+  spread(&p, p.n > p.B ? p.n : p.B);
+  return launch_k(fork_kernel, dim3(kCluster), dim3(kTableThreads), 0, stream, p);
+}
+
+cudaError_t launch_copy_pages(const MoveParams& p, int num_sms, cudaStream_t stream) {
+  // parts of a page: enough blocks for the SMs, none with less than a pass
+  const int64_t pieces = 2 * static_cast<int64_t>(p.cols) * p.page_size;
+  const int64_t passes = (pieces + kMoveThreads * kDepth - 1) / (kMoveThreads * kDepth);
+  int64_t parts = (8 * static_cast<int64_t>(num_sms) + p.n - 1) / p.n;
+  if (parts > passes) parts = passes;
+  const int64_t y = p.n < 65535 ? p.n : 65535, z = (p.n + 65534) / 65535;
+  return launch_k(copy_pages_kernel,
+                  dim3(static_cast<unsigned>(parts), static_cast<unsigned>(y),
+                       static_cast<unsigned>(z)),
+                  dim3(kMoveThreads), 0, stream, p);
+}
+
+cudaError_t launch_compact(const MoveParams& given, int num_sms, cudaStream_t stream) {
+  MoveParams p = given;
+  // as wide as the longest list allows in one step, and narrower until there is a block an SM
+  int width = 128;
+  while (width > 2 && (static_cast<int64_t>(kMoveThreads / width) * kDepth < p.most)) width /= 2;
+  auto blocks = [&](int w) { return (2 * static_cast<int64_t>(p.cols) + w - 1) / w * p.B; };
+  if (width < 16) width = 16;
+  while (width > 2 && blocks(width) < num_sms) width /= 2;
+  p.width = width;
+  const size_t smem = static_cast<size_t>(kMoveThreads / width) * kDepth * 2 * sizeof(int2);
+  return launch_k(compact_kernel,
+                  dim3(static_cast<unsigned>(blocks(width) / p.B), static_cast<unsigned>(p.B)),
+                  dim3(kMoveThreads), smem, stream, p);
+}
+
+}  // namespace mxq
