@@ -489,6 +489,19 @@ mxq_status mxq_paged_attention_decode(const void* q, int64_t sq_b, int64_t sq_h,
                                       const float* v_scale, void* out, int64_t so_b, int64_t so_h,
                                       float* lse, void* workspace, size_t ws_bytes,
                                       mxq_stream_t stream);
+/* mxq_paged_attention_decode whose window leaves the first keys visible:
+ *   visible: with window > 0 the keys j < first and the last `window` of all;
+ *          with window 0 all j < seq_lens[b] (first has no effect)
+ * The same workspace; keys in between are not read, and their pages may be freed
+ * (mxq_cache_resize). */
+mxq_status mxq_paged_attention_decode_ex(
+    const void* q, int64_t sq_b, int64_t sq_h, int64_t B, int32_t Hq, int32_t Hkv, int32_t D,
+    const void* k_cache, const void* v_cache, int32_t cache_dtype, int64_t pages, int32_t page_size,
+    int64_t sck_p, int64_t sck_t, int64_t sck_h, int64_t scv_p, int64_t scv_t, int64_t scv_h,
+    const int32_t* page_table, int64_t ld_table, int64_t max_pages, const int32_t* seq_lens,
+    float scale, int32_t window, int32_t first, const float* sinks, const float* k_scale,
+    const float* v_scale, void* out, int64_t so_b, int64_t so_h, float* lse, void* workspace,
+    size_t ws_bytes, mxq_stream_t stream);
 mxq_status mxq_paged_attention_decode_workspace_size(int64_t B, int32_t Hq, int32_t Hkv, int32_t D,
                                                      size_t* bytes);
 
@@ -522,6 +535,18 @@ mxq_status mxq_attention_varlen(const void* q, int64_t sq_t, int64_t sq_h, const
                                 int32_t window, const float* sinks, void* out, int64_t so_t,
                                 int64_t so_h, float* lse, void* workspace, size_t ws_bytes,
                                 mxq_stream_t stream);
+/* mxq_attention_varlen whose window leaves the first keys of a sequence visible:
+ *   visible: with window > 0 the keys j <= position with j > position - window or
+ *          j < first; with window 0 as there (first has no effect)
+ * The same workspace. */
+mxq_status mxq_attention_varlen_ex(const void* q, int64_t sq_t, int64_t sq_h, const void* k,
+                                   int64_t sk_t, int64_t sk_h, const void* v, int64_t sv_t,
+                                   int64_t sv_h, const int32_t* cu_seqlens_q,
+                                   const int32_t* cu_seqlens_k, int64_t B, int64_t Tq, int64_t Tk,
+                                   int32_t Hq, int32_t Hkv, int32_t D, float scale, int32_t causal,
+                                   int32_t window, int32_t first, const float* sinks, void* out,
+                                   int64_t so_t, int64_t so_h, float* lse, void* workspace,
+                                   size_t ws_bytes, mxq_stream_t stream);
 mxq_status mxq_attention_varlen_workspace_size(int64_t Tq, int64_t B, int32_t Hq, int32_t Hkv,
                                                int32_t D, size_t* bytes);
 

@@ -520,7 +520,7 @@ def paged_attention_decode_workspace_size(batch: int, heads: int, kv_heads: int,
 
 def paged_attention_decode(q, k_cache, v_cache, page_table, seq_lens, scale=None, window: int = 0,
                            sinks=None, k_scale=None, v_scale=None, return_lse: bool = False,
-                           out=None, workspace=None):
+                           out=None, workspace=None, first: int = 0):
     """Attention of one new token per sequence over a paged cache.
 
     q: bf16 [B, Hq, D], D 64 or 128; k_cache, v_cache as in rope_append_kv,
@@ -530,9 +530,10 @@ def paged_attention_decode(q, k_cache, v_cache, page_table, seq_lens, scale=None
     value; k_scale, v_scale: fp32 [Hkv] of an e4m3 cache.  Returns out bf16
     [B, Hq, D], with return_lse also the fp32 [B, Hq] log-sum-exp.  workspace:
     a caller's buffer of paged_attention_decode_workspace_size bytes (None:
-    allocated here)."""
+    allocated here).  first: with a window, the first `first` keys are visible
+    too."""
     return _attn().decode(q, k_cache, v_cache, page_table, seq_lens, scale, window, sinks, k_scale,
-                          v_scale, return_lse, out, workspace)
+                          v_scale, return_lse, out, workspace, first)
 
 
 def attention_varlen_workspace_size(tokens: int, batch: int, heads: int, kv_heads: int,
@@ -545,7 +546,7 @@ def attention_varlen_workspace_size(tokens: int, batch: int, heads: int, kv_head
 
 def attention_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k=None, scale=None, causal: bool = True,
                      window: int = 0, sinks=None, return_lse: bool = False, out=None,
-                     workspace=None):
+                     workspace=None, first: int = 0):
     """Attention of whole prompts, sequences of different lengths packed.
 
     q: bf16 [Tq, Hq, D], k, v: bf16 [Tk, Hkv, D] (any token and head strides),
@@ -556,9 +557,10 @@ def attention_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k=None, scale=None, causa
     is 0; rows outside every sequence are not written.  Returns out bf16
     [Tq, Hq, D], with return_lse also the fp32 [Tq, Hq] log-sum-exp.
     workspace: a caller's buffer of attention_varlen_workspace_size bytes
-    (None: allocated here)."""
+    (None: allocated here).  first: with a window, the first `first` keys of a
+    sequence are visible too, up to the row's own."""
     return _attn().prompt(q, k, v, cu_seqlens_q, cu_seqlens_k, scale, causal, window, sinks,
-                          return_lse, out, workspace)
+                          return_lse, out, workspace, first)
 
 
 # --------------------------------------------------------- the pages of a cache

@@ -45,6 +45,7 @@ struct DecodeParams {
   const int32_t* seq_lens;
   float scale;
   int window;              // 0: none
+  int first;               // keys before the window that stay visible
   const float *sinks, *k_scale, *v_scale;
   void* out;
   int64_t o_b, o_h;
@@ -62,7 +63,7 @@ struct PromptParams {
   int Hq, Hkv, D;
   float scale;
   bool causal;
-  int window;
+  int window, first;
   const float* sinks;
   void* out;
   int64_t o_t, o_h;

@@ -69,12 +69,18 @@ mxq_status check_heads(int32_t Hq, int32_t Hkv, int32_t D) {
   return MXQ_OK;
 }
 
-mxq_status check_scale(float scale, int32_t window) {
+mxq_status check_scale(float scale, int32_t window, int32_t first) {
   // (the kernels multiply it by log2 e)
   if (!(scale > 0.f) || !std::isfinite(scale * 1.44269504088896340736f))
     return fail(MXQ_ERR_INVALID_ARG, "scale must be positive and finite, times log2 e as well");
-  if (window < 0) return fail(MXQ_ERR_INVALID_ARG, "window must be >= 0 (0: none)");
+  if (window < 0 || first < 0)
+    return fail(MXQ_ERR_INVALID_ARG, "window and first must be >= 0 (0: none)");
   return MXQ_OK;
+}
+
+// first keys that stay visible before a window: without one all do
+int first_keys(int32_t window, int32_t first) {
+  return window > 0 ? std::min(first, 1 << 30) : 0;
 }
 
 mxq_status check_workspace(const void* ws, size_t have, size_t need, const char* query) {
@@ -174,17 +180,17 @@ extern "C" mxq_status mxq_paged_attention_decode_workspace_size(int64_t B, int32
   return MXQ_OK;
 }
 
-extern "C" mxq_status mxq_paged_attention_decode(
+extern "C" mxq_status mxq_paged_attention_decode_ex(
     const void* q, int64_t sq_b, int64_t sq_h, int64_t B, int32_t Hq, int32_t Hkv, int32_t D,
     const void* k_cache, const void* v_cache, int32_t cache_dtype, int64_t pages, int32_t page_size,
     int64_t sck_p, int64_t sck_t, int64_t sck_h, int64_t scv_p, int64_t scv_t, int64_t scv_h,
     const int32_t* page_table, int64_t ld_table, int64_t max_pages, const int32_t* seq_lens,
-    float scale, int32_t window, const float* sinks, const float* k_scale, const float* v_scale,
-    void* out, int64_t so_b, int64_t so_h, float* lse, void* workspace, size_t ws_bytes,
-    mxq_stream_t stream) {
+    float scale, int32_t window, int32_t first, const float* sinks, const float* k_scale,
+    const float* v_scale, void* out, int64_t so_b, int64_t so_h, float* lse, void* workspace,
+    size_t ws_bytes, mxq_stream_t stream) {
   if (B < 0 || max_pages < 0) return fail(MXQ_ERR_INVALID_ARG, "need B >= 0 and max_pages >= 0");
   MXQ_TRY(check_heads(Hq, Hkv, D));
-  MXQ_TRY(check_scale(scale, window));
+  MXQ_TRY(check_scale(scale, window, first));
   if (pages <= 0 || page_size <= 0 || pages > 0x7fffffff)
     return fail(MXQ_ERR_INVALID_ARG, "need 0 < pages < 2^31 and page_size > 0");
   if (B == 0) return MXQ_OK;
@@ -216,12 +222,27 @@ extern "C" mxq_status mxq_paged_attention_decode(
   p.pages = pages, p.page_size = page_size;
   p.ck_p = sck_p, p.ck_t = sck_t, p.ck_h = sck_h, p.cv_p = scv_p, p.cv_t = scv_t, p.cv_h = scv_h;
   p.page_table = page_table, p.ld_table = ld_table, p.max_pages = max_pages, p.seq_lens = seq_lens;
-  p.scale = scale, p.window = std::min(window, 1 << 30);
+  p.scale = scale, p.window = std::min(window, 1 << 30), p.first = first_keys(window, first);
   p.sinks = sinks, p.k_scale = k_scale, p.v_scale = v_scale;
   p.out = out, p.o_b = so_b, p.o_h = so_h, p.lse = lse, p.workspace = workspace;
   p.status = d.status;
   const cudaError_t e = launch_decode(p, d.num_sms, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? MXQ_OK : cuda_fail(e, "decode attention launch");
+}
+
+extern "C" mxq_status mxq_paged_attention_decode(
+    const void* q, int64_t sq_b, int64_t sq_h, int64_t B, int32_t Hq, int32_t Hkv, int32_t D,
+    const void* k_cache, const void* v_cache, int32_t cache_dtype, int64_t pages, int32_t page_size,
+    int64_t sck_p, int64_t sck_t, int64_t sck_h, int64_t scv_p, int64_t scv_t, int64_t scv_h,
+    const int32_t* page_table, int64_t ld_table, int64_t max_pages, const int32_t* seq_lens,
+    float scale, int32_t window, const float* sinks, const float* k_scale, const float* v_scale,
+    void* out, int64_t so_b, int64_t so_h, float* lse, void* workspace, size_t ws_bytes,
+    mxq_stream_t stream) {
+  return mxq_paged_attention_decode_ex(q, sq_b, sq_h, B, Hq, Hkv, D, k_cache, v_cache, cache_dtype,
+                                       pages, page_size, sck_p, sck_t, sck_h, scv_p, scv_t, scv_h,
+                                       page_table, ld_table, max_pages, seq_lens, scale, window, 0,
+                                       sinks, k_scale, v_scale, out, so_b, so_h, lse, workspace,
+                                       ws_bytes, stream);
 }
 
 extern "C" mxq_status mxq_attention_varlen_workspace_size(int64_t Tq, int64_t B, int32_t Hq,
@@ -238,16 +259,16 @@ extern "C" mxq_status mxq_attention_varlen_workspace_size(int64_t Tq, int64_t B,
   return MXQ_OK;
 }
 
-extern "C" mxq_status mxq_attention_varlen(
+extern "C" mxq_status mxq_attention_varlen_ex(
     const void* q, int64_t sq_t, int64_t sq_h, const void* k, int64_t sk_t, int64_t sk_h,
     const void* v, int64_t sv_t, int64_t sv_h, const int32_t* cu_seqlens_q,
     const int32_t* cu_seqlens_k, int64_t B, int64_t Tq, int64_t Tk, int32_t Hq, int32_t Hkv,
-    int32_t D, float scale, int32_t causal, int32_t window, const float* sinks, void* out,
-    int64_t so_t, int64_t so_h, float* lse, void* workspace, size_t ws_bytes,
+    int32_t D, float scale, int32_t causal, int32_t window, int32_t first, const float* sinks,
+    void* out, int64_t so_t, int64_t so_h, float* lse, void* workspace, size_t ws_bytes,
     mxq_stream_t stream) {
   if (B < 0 || Tq < 0 || Tk < 0) return fail(MXQ_ERR_INVALID_ARG, "need B, Tq, Tk >= 0");
   MXQ_TRY(check_heads(Hq, Hkv, D));
-  MXQ_TRY(check_scale(scale, window));
+  MXQ_TRY(check_scale(scale, window, first));
   if (window > 0 && !causal)
     return fail(MXQ_ERR_INVALID_ARG, "a window needs a causal mask");
   if (B == 0 || Tq == 0) return MXQ_OK;
@@ -276,11 +297,24 @@ extern "C" mxq_status mxq_attention_varlen(
   p.cu_q = cu_seqlens_q, p.cu_k = cu_seqlens_k;
   p.B = static_cast<int>(B), p.Tq = Tq, p.Tk = Tk, p.Hq = Hq, p.Hkv = Hkv, p.D = D;
   p.scale = scale, p.causal = causal != 0, p.window = std::min(window, 1 << 30), p.sinks = sinks;
+  p.first = first_keys(window, first);
   p.out = out, p.o_t = so_t, p.o_h = so_h, p.lse = lse, p.workspace = workspace;
   p.status = d.status;
   const cudaError_t e = launch_prompt(p, d.num_sms, reinterpret_cast<cudaStream_t>(stream), &err);
   if (!err.empty()) return fail(MXQ_ERR_CUDA, err);
   return e == cudaSuccess ? MXQ_OK : cuda_fail(e, "prompt attention launch");
+}
+
+extern "C" mxq_status mxq_attention_varlen(
+    const void* q, int64_t sq_t, int64_t sq_h, const void* k, int64_t sk_t, int64_t sk_h,
+    const void* v, int64_t sv_t, int64_t sv_h, const int32_t* cu_seqlens_q,
+    const int32_t* cu_seqlens_k, int64_t B, int64_t Tq, int64_t Tk, int32_t Hq, int32_t Hkv,
+    int32_t D, float scale, int32_t causal, int32_t window, const float* sinks, void* out,
+    int64_t so_t, int64_t so_h, float* lse, void* workspace, size_t ws_bytes,
+    mxq_stream_t stream) {
+  return mxq_attention_varlen_ex(q, sq_t, sq_h, k, sk_t, sk_h, v, sv_t, sv_h, cu_seqlens_q,
+                                 cu_seqlens_k, B, Tq, Tk, Hq, Hkv, D, scale, causal, window, 0,
+                                 sinks, out, so_t, so_h, lse, workspace, ws_bytes, stream);
 }
 
 namespace {

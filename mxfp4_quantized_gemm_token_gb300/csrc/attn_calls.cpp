@@ -33,6 +33,8 @@ decltype(&mxq_paged_attention_decode_workspace_size) decode_size_fn;
 decltype(&mxq_attention_varlen) prompt_fn;
 decltype(&mxq_attention_varlen_workspace_size) prompt_size_fn;
 decltype(&mxq_current_device) device_fn;
+decltype(&mxq_paged_attention_decode_ex) decode_ex_fn;
+decltype(&mxq_attention_varlen_ex) prompt_ex_fn;
 decltype(&mxq_cache_pages_workspace_size) pages_size_fn;
 decltype(&mxq_cache_resize) resize_fn;
 decltype(&mxq_cache_fork) fork_fn;
@@ -302,9 +304,10 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
 }
 
 // (q, k_cache, v_cache, page_table, seq_lens, scale, window, sinks, k_scale, v_scale,
-// return_lse, out, workspace)
+// return_lse, out, workspace[, first])
 PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
-  return guarded(nargs, 13, [&]() -> PyObject* {
+  return guarded(nargs, nargs == 14 ? 14 : 13, [&]() -> PyObject* {
+    const int32_t first = nargs == 14 ? integer("first", a[13]) : 0;
     const at::Tensor &q = needed("q", a[0]), &kc = needed("k_cache", a[1]);
     const at::Tensor &vc = needed("v_cache", a[2]), &table = needed("page_table", a[3]);
     const at::Tensor& lens = needed("seq_lens", a[4]);
@@ -340,22 +343,29 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
       }
       if (!out.defined()) out = fresh(q.sizes(), at::kBFloat16, q);
       if (with_lse) lse = fresh({B, hq.heads}, at::kFloat, q);
+      const int32_t* pages = static_cast<const int32_t*>(table.data_ptr());
+      const int64_t ld = B > 1 ? table.stride(0) : width;
+      float* sums = with_lse ? static_cast<float*>(lse.data_ptr()) : nullptr;
+      if (first != 0)
+        return decode_ex_fn(hq.p, hq.s0, hq.s1, B, Hq, Hkv, d, c.k, c.v, c.dtype, c.pages,
+                            c.page_size, c.k0, c.k1, c.k2, c.v0, c.v1, c.v2, pages, ld, width,
+                            at_len, scale, window, first, sink, k_scale, v_scale, out.data_ptr(),
+                            out.stride(0), out.stride(1), sums, space.data_ptr(), space.nbytes(),
+                            stream);
       return decode_fn(hq.p, hq.s0, hq.s1, B, Hq, Hkv, d, c.k, c.v, c.dtype, c.pages, c.page_size,
-                       c.k0, c.k1, c.k2, c.v0, c.v1, c.v2,
-                       static_cast<const int32_t*>(table.data_ptr()),
-                       B > 1 ? table.stride(0) : width, width, at_len, scale, window, sink, k_scale,
-                       v_scale, out.data_ptr(), out.stride(0), out.stride(1),
-                       with_lse ? static_cast<float*>(lse.data_ptr()) : nullptr, space.data_ptr(),
-                       space.nbytes(), stream);
+                       c.k0, c.k1, c.k2, c.v0, c.v1, c.v2, pages, ld, width, at_len, scale, window,
+                       sink, k_scale, v_scale, out.data_ptr(), out.stride(0), out.stride(1), sums,
+                       space.data_ptr(), space.nbytes(), stream);
     }));
     return result(out, lse);
   });
 }
 
 // (q, k, v, cu_seqlens_q, cu_seqlens_k, scale, causal, window, sinks, return_lse, out,
-// workspace)
+// workspace[, first])
 PyObject* prompt(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
-  return guarded(nargs, 12, [&]() -> PyObject* {
+  return guarded(nargs, nargs == 13 ? 13 : 12, [&]() -> PyObject* {
+    const int32_t first = nargs == 13 ? integer("first", a[12]) : 0;
     const at::Tensor &q = needed("q", a[0]), &k = needed("k", a[1]), &v = needed("v", a[2]);
     const at::Tensor& cu_q = needed("cu_seqlens_q", a[3]);
     const at::Tensor *cu_k = tensor("cu_seqlens_k", a[4]), *sinks = tensor("sinks", a[8]);
@@ -386,11 +396,16 @@ PyObject* prompt(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
       }
       if (!out.defined()) out = fresh(q.sizes(), at::kBFloat16, q);
       if (with_lse) lse = fresh({hq.n, hq.heads}, at::kFloat, q);
+      float* sums = with_lse ? static_cast<float*>(lse.data_ptr()) : nullptr;
+      if (first != 0)
+        return prompt_ex_fn(hq.p, hq.s0, hq.s1, hk.p, hk.s0, hk.s1, hv.p, hv.s0, hv.s1, cq, ck, B,
+                            hq.n, hk.n, Hq, Hkv, D, scale, causal, window, first, sink,
+                            out.data_ptr(), out.stride(0), out.stride(1), sums, space.data_ptr(),
+                            space.nbytes(), stream);
       return prompt_fn(hq.p, hq.s0, hq.s1, hk.p, hk.s0, hk.s1, hv.p, hv.s0, hv.s1, cq, ck, B, hq.n,
                        hk.n, Hq, Hkv, D, scale, causal, window, sink, out.data_ptr(),
-                       out.stride(0), out.stride(1),
-                       with_lse ? static_cast<float*>(lse.data_ptr()) : nullptr, space.data_ptr(),
-                       space.nbytes(), stream);
+                       out.stride(0), out.stride(1), sums, space.data_ptr(), space.nbytes(),
+                       stream);
     }));
     return result(out, lse);
   });
@@ -541,6 +556,8 @@ PyObject* connect_more(PyObject*, PyObject* by_name) {
   };
   if (!set("mxq_cache_pages_workspace_size", &pages_size_fn) ||
       !set("mxq_cache_resize", &resize_fn) || !set("mxq_cache_fork", &fork_fn) ||
+      !set("mxq_paged_attention_decode_ex", &decode_ex_fn) ||
+      !set("mxq_attention_varlen_ex", &prompt_ex_fn) ||
       !set("mxq_cache_copy_pages", &copy_pages_fn) || !set("mxq_cache_compact", &compact_fn))
     return nullptr;
   Py_RETURN_NONE;

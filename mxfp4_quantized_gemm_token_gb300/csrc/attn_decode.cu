@@ -89,18 +89,23 @@ struct DecodeShape {
 };
 
 struct SeqRange {
-  int lo, len, first, steps;        // visible keys [lo, len); the first step's key; its steps
+  int lo, len;                      // visible keys [0, p.first) and [lo, len)
+  int head, skip, steps;            // step s begins at key s KS, + skip from step `head` on
 };
 
-// The visible keys of a sequence of `len` keys, in steps from a multiple of 16; at
-// least one step (without keys), so that every output is written.
+// The visible keys of a sequence of `len` keys, in steps: those of the first keys that a
+// window leaves visible, then from a multiple of 16; at least one step (without keys), so
+// that every output is written.
 template <int KS>
 __device__ __forceinline__ SeqRange seq_steps(const DecodeParams& p, int len) {
   SeqRange r;
   r.len = min(max(len, 0), static_cast<int>(p.max_pages * p.page_size));
   r.lo = p.window > 0 ? max(0, r.len - p.window) : 0;
-  r.first = r.lo & ~15;
-  r.steps = max(1, (r.len - r.first + KS - 1) / KS);
+  // (head steps that would reach the window's first one leave nothing out)
+  r.head = min((min(p.first, r.lo) + KS - 1) / KS, r.lo / KS);
+  r.skip = (r.lo & ~15) - r.head * KS;
+  if (min(p.first, r.lo) > r.head * KS) r.skip = 0;
+  r.steps = max(1, (r.len - r.skip + KS - 1) / KS);
   return r;
 }
 
@@ -353,8 +358,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1) decode_kernel(const DecodeArgs
     };
     auto look_up = [&]() {
       Spot r = {0, 0, false};
-      const int key = in.s.first + in.step * KS + lane;
-      r.seen = lane < KS && key >= in.s.lo && key < in.s.len;
+      const int key = in.step * KS + (in.step >= in.s.head ? in.s.skip : 0) + lane;
+      r.seen = lane < KS && (key >= in.s.lo || key < p.first) && key < in.s.len;
       if (r.seen) {
         const uint32_t n = static_cast<uint32_t>(key) / static_cast<uint32_t>(p.page_size);
         r.off = key - static_cast<int>(n) * p.page_size;
@@ -819,7 +824,10 @@ cudaError_t launch(const DecodeArgs& a, int grid, cudaStream_t stream) {
   // as long as eight steps (a window of 128 keys, D 128, 128 sequences: 32.0 us split and
   // joined, 23.1 whole; 4 sequences: 10.0 and 10.8).
   int64_t keys = a.p.max_pages * a.p.page_size;
-  if (a.p.window > 0) keys = std::min<int64_t>(keys, static_cast<int64_t>(a.p.window) + 15);
+  if (a.p.window > 0)
+    keys = std::min<int64_t>(keys, static_cast<int64_t>(a.p.window) + 15 +
+                                       (static_cast<int64_t>(a.p.first) + S::KS - 1) / S::KS *
+                                           S::KS);
   b.all_whole = keys <= kAllWhole * S::KS;
   e = launch_k(decode_kernel<D, FP8>, dim3(grid), dim3(32 * kWarps),
                static_cast<size_t>(S::kSmem), stream, b);

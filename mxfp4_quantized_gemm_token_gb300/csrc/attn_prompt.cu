@@ -130,6 +130,18 @@ __device__ __forceinline__ bool seq_range(const int32_t* cu, int b, int64_t tota
   return ok;
 }
 
+// With a window and first keys that stay visible, an item's blocks are those of the first
+// keys and then the window's, numbered one after the other: block v is the keys' block
+// v, or v + skip from block `head` on.
+struct PromptSkip {
+  int head, skip;
+};
+__device__ __forceinline__ PromptSkip skip_of(const PromptParams& p, int at0) {
+  const int kb0 = max(0, at0 - p.window + 1) / kBM;
+  const int head = min((p.first + kBM - 1) / kBM, kb0);
+  return {head, kb0 - head};
+}
+
 // Item i of a sequence.
 __device__ __forceinline__ PromptItem make_item(const PromptParams& p, int tokens_per_item, int q0,
                                                 int nq, int k0, int nk, int i) {
@@ -143,6 +155,10 @@ __device__ __forceinline__ PromptItem make_item(const PromptParams& p, int token
   const int hi = p.causal ? min(nk, it.at0 + it.ntok) : nk;
   it.kb1 = hi > 0 ? (hi + kBM - 1) / kBM : 0;
   it.kb0 = p.window > 0 ? max(0, it.at0 - p.window + 1) / kBM : 0;
+  if (p.first > 0) {
+    it.kb0 = 0;
+    it.kb1 = max(0, it.kb1 - skip_of(p, it.at0).skip);
+  }
   it.head = 0;
   return it;
 }
@@ -501,7 +517,8 @@ __device__ __forceinline__ void join_rows(const PromptArgs& a, const PromptPiece
   }
 }
 
-template <int D>
+// kFirst: first keys stay visible (a variant of its own: the softmax has no register to spare)
+template <int D, bool kFirst>
 __global__ void __launch_bounds__(kPromptThreads, 1)
     prompt_kernel(const __grid_constant__ PromptMaps maps, const PromptArgs a) {
   using L = PromptLayout<D>;
@@ -575,6 +592,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           const PromptItem& it = items.it;
           const int hk = it.head & ~kPiece;
           if (it.kb1 <= it.kb0) continue;
+          PromptSkip gap = {0, 0};
+          if constexpr (kFirst) gap = skip_of(p, it.at0);
           auto load_q = [&](int s) {
             if (!mbar_wait(&q_empty[s], (nq[s] & 1) ^ 1, wc)) return false;
             mbar_expect_tx(&q_full[s], q_bytes);
@@ -588,6 +607,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             const int st = fill % ST;
             if (!mbar_wait(&kv_empty[st], ((fill / ST) & 1) ^ 1, wc)) return false;
             mbar_expect_tx(&kv_full[st], L::kTileBytes);
+            if (kFirst && kb >= gap.head) kb += gap.skip;
             for (int c = 0; c < L::kChunks; ++c)
               tma_load_3d(ring + st * L::kTileBytes + c * L::kChunkBytes, map, &kv_full[st], c * 64,
                           hk, it.k_row + kb * kBM);
@@ -717,9 +737,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       const int lo = valid && p.window > 0 ? max(0, at - p.window + 1) : 0;
       const int all_lo = __reduce_max_sync(0xffffffffu, lo);
       const int all_hi = __reduce_min_sync(0xffffffffu, hi);
+      PromptSkip gap = {0, 0};
+      if constexpr (kFirst) gap = skip_of(p, it.at0);
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < n; ++j) {
-        const int k0 = (it.kb1 - 1 - j) * kBM;
+        int k0 = (it.kb1 - 1 - j) * kBM;
+        if (kFirst && it.kb1 - 1 - j >= gap.head) k0 += gap.skip * kBM;
         if (!mbar_wait_warp(&s_full[s], ns & 1, wc)) goto softmax_done;
         ++ns;
         tc_fence_after();
@@ -737,7 +760,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           for (int q = 0; q < 4; ++q) {
             const int kq = k0 + 32 * q;
             if (kq + 32 <= all_hi && kq >= all_lo) continue;
-            const uint32_t vis = low_bits(hi - kq) & ~low_bits(lo - kq);
+            uint32_t vis = ~low_bits(lo - kq);
+            if constexpr (kFirst) vis |= low_bits(p.first - kq);
+            vis &= low_bits(hi - kq);
 #pragma unroll
             for (int e = 0; e < 32; ++e)
               x[32 * q + e] = (vis >> e) & 1 ? x[32 * q + e] : -INFINITY;
@@ -958,7 +983,7 @@ PromptSpace prompt_space(int64_t Tq, int64_t B, int Hq, int Hkv, int D, int num_
   return s;
 }
 
-template <int D>
+template <int D, bool kFirst>
 cudaError_t launch(const PromptMaps& maps, const PromptArgs& a, cudaStream_t stream) {
   const int smem = PromptLayout<D>::kSmem + 1024;
   static bool configured[64] = {};
@@ -966,11 +991,11 @@ cudaError_t launch(const PromptMaps& maps, const PromptArgs& a, cudaStream_t str
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (!configured[dev]) {
-    e = cudaFuncSetAttribute(prompt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    e = cudaFuncSetAttribute(prompt_kernel<D, kFirst>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     configured[dev] = true;
   }
-  return launch_k(prompt_kernel<D>, dim3(a.grid), dim3(kPromptThreads), static_cast<size_t>(smem),
+  return launch_k(prompt_kernel<D, kFirst>, dim3(a.grid), dim3(kPromptThreads), static_cast<size_t>(smem),
                   stream, maps, a);
 }
 
@@ -1034,7 +1059,9 @@ cudaError_t launch_prompt(const PromptParams& p, int num_sms, cudaStream_t strea
                                    dim3(1), dim3(1024), 0, stream, a);
     if (e != cudaSuccess) return e;
   }
-  return p.D == 128 ? launch<128>(maps, a, stream) : launch<64>(maps, a, stream);
+  if (p.first > 0)
+    return p.D == 128 ? launch<128, true>(maps, a, stream) : launch<64, true>(maps, a, stream);
+  return p.D == 128 ? launch<128, false>(maps, a, stream) : launch<64, false>(maps, a, stream);
 }
 
 }  // namespace mxq
