@@ -551,6 +551,44 @@ mxq_status mxq_attention_varlen_workspace_size(int64_t Tq, int64_t B, int32_t Hq
                                                int32_t D, size_t* bytes);
 
 /*
+ * Attention of several new tokens per sequence over the paged cache: the drafted tokens of
+ * a tree, or a chunk of a prompt.  Sequence b holds the query rows [cu_seqlens_q[b],
+ * cu_seqlens_q[b+1]) of the packed T; their keys are the last nq of its seq_lens[b] keys and are
+ * already in the cache, in the rows' order.  P = seq_lens[b] - nq keys are its context.
+ *   parents  int32 [T], each row's parent among its sequence's rows: an earlier one, or
+ *          -1 (it continues the context); NULL: each row continues the one before it
+ *   visible to row i, which stands at position P + d, d the number of its
+ *          ancestors: the context's keys and the rows on its path (itself, its
+ *          parent, and so on up), a row's position being P + the number of its own
+ *          ancestors; with window > 0 of these only positions above P + d - window
+ *          and those below first
+ *   q, out bf16 [T, Hq, D] (strides s*_t, s*_h); heads, D, caches, page_table, scale,
+ *          sinks, k_scale, v_scale, lse (fp32 [T, Hq]) and precisions as in
+ *          mxq_paged_attention_decode
+ *   cu_seqlens_q int32 [B + 1], seq_lens int32 [B], on the device
+ *   workspace mxq_paged_attention_tree_workspace_size bytes (NULL if 0), 256-byte
+ *          aligned, not read before it is written
+ * Rows outside every sequence are not written.  Keys before the lowest window's
+ * that are not first ones are not read.  A *value* that is not finite may
+ * reach the rows of its sequence that do not see it, as 0 * inf is not 0; keys outside
+ * seq_lens[b] never do.  MXQ_ERR_DEVICE is set for mxq_sync_status by lengths outside [0, max_pages *
+ * page_size] (clamped), offsets that decrease or leave [0, T] and sequences of fewer
+ * keys than rows (left out, their rows not written), parents that are not
+ * earlier rows (taken as -1) and pages outside [0, pages) (their keys are not seen).
+ * B == 0 or T == 0 is a no-op.
+ */
+mxq_status mxq_paged_attention_tree(
+    const void* q, int64_t sq_t, int64_t sq_h, int64_t T, int32_t Hq, int32_t Hkv, int32_t D,
+    const void* k_cache, const void* v_cache, int32_t cache_dtype, int64_t pages, int32_t page_size,
+    int64_t sck_p, int64_t sck_t, int64_t sck_h, int64_t scv_p, int64_t scv_t, int64_t scv_h,
+    const int32_t* page_table, int64_t ld_table, int64_t max_pages, const int32_t* seq_lens,
+    const int32_t* cu_seqlens_q, const int32_t* parents, int64_t B, float scale, int32_t window,
+    int32_t first, const float* sinks, const float* k_scale, const float* v_scale, void* out,
+    int64_t so_t, int64_t so_h, float* lse, void* workspace, size_t ws_bytes, mxq_stream_t stream);
+mxq_status mxq_paged_attention_tree_workspace_size(int64_t T, int64_t B, int32_t Hq, int32_t Hkv,
+                                                   int32_t D, size_t* bytes);
+
+/*
  * Pages of a paged cache.  page_refs[p] (int32 [pages], 16-byte aligned) is the
  * number of page-table entries that hold page p; where it is 0 the page is free.
  * A table's row holds the pages of its sequence's keys in order, -1 where a page

@@ -15,6 +15,7 @@ arguments: shapes, strides, output/workspace allocation and the stream.
     rope_append_kv(k, v, k_cache, v_cache, slots, cos_sin, positions, q=None, ...)
     paged_attention_decode(q, k_cache, v_cache, page_table, seq_lens, ...)
     attention_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k=None, ...)
+    paged_attention_tree(q, k_cache, v_cache, page_table, seq_lens, cu_seqlens_q, ...)
     cache_resize(page_table, seq_lens, new_lens, page_refs, page_size, ...)
     cache_fork(page_table, seq_lens, page_refs, parents, page_size, ...)
     cache_copy_pages(k_cache, v_cache, copies)
@@ -35,6 +36,7 @@ __all__ = [
     "fp8_per_tensor_linear", "moe_align_block", "fused_experts", "align_capacity",
     "rope_append_kv", "paged_attention_decode", "paged_attention_decode_workspace_size",
     "attention_varlen", "attention_varlen_workspace_size",
+    "paged_attention_tree", "paged_attention_tree_workspace_size",
     "cache_resize", "cache_fork", "cache_copy_pages", "cache_compact",
     "cache_pages_workspace_size",
     "set_option", "get_option", "sync_status", "W_FP8_BLOCK128", "W_MXFP4",
@@ -561,6 +563,36 @@ def attention_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k=None, scale=None, causa
     sequence are visible too, up to the row's own."""
     return _attn().prompt(q, k, v, cu_seqlens_q, cu_seqlens_k, scale, causal, window, sinks,
                           return_lse, out, workspace, first)
+
+
+def paged_attention_tree_workspace_size(tokens: int, batch: int, heads: int, kv_heads: int,
+                                        head_dim: int) -> int:
+    n = ctypes.c_size_t(0)
+    check(_lib.load().mxq_paged_attention_tree_workspace_size(
+        tokens, batch, heads, kv_heads, head_dim, ctypes.byref(n)))
+    return n.value
+
+
+def paged_attention_tree(q, k_cache, v_cache, page_table, seq_lens, cu_seqlens_q, parents=None,
+                         scale=None, window: int = 0, first: int = 0, sinks=None, k_scale=None,
+                         v_scale=None, return_lse: bool = False, out=None, workspace=None):
+    """Attention of several new tokens per sequence over a paged cache: a
+    drafted tree, or a chunk of a prompt.
+
+    q: bf16 [T, Hq, D], the sequences' rows packed at cu_seqlens_q (int32
+    [B + 1]), D 64 or 128; k_cache, v_cache as in rope_append_kv, the rows' own
+    keys included, the last of seq_lens (int32 [B]); page_table: int32
+    [B, max_pages]; parents: int32 [T], the row of the same sequence that each row
+    continues (-1: the context), an earlier one; None: the row before it.  A
+    row sees the context and its path: itself, its parent and so on up.
+    window: of these only the last `window` positions (0: all), a row's position
+    being the context's length plus the number of its ancestors; first: and the
+    first `first`.  scale, sinks, k_scale, v_scale as in
+    paged_attention_decode.  Returns out bf16 [T, Hq, D], with return_lse also the
+    fp32 [T, Hq] log-sum-exp.  workspace: a caller's buffer of
+    paged_attention_tree_workspace_size bytes (None: allocated here)."""
+    return _attn().tree(q, k_cache, v_cache, page_table, seq_lens, cu_seqlens_q, parents, scale,
+                        window, first, sinks, k_scale, v_scale, return_lse, out, workspace)
 
 
 # --------------------------------------------------------- the pages of a cache

@@ -39,12 +39,14 @@ EXPORTED = [
     "mxq_attention_varlen", "mxq_attention_varlen_workspace_size",
     "mxq_cache_pages_workspace_size", "mxq_cache_resize", "mxq_cache_fork", "mxq_cache_copy_pages",
     "mxq_cache_compact", "mxq_paged_attention_decode_ex", "mxq_attention_varlen_ex",
+    "mxq_paged_attention_tree", "mxq_paged_attention_tree_workspace_size",
 ]
 
 # what the compiled calls get besides the entry points that connect() takes one by one
 CONNECTED = ["mxq_cache_pages_workspace_size", "mxq_cache_resize", "mxq_cache_fork",
              "mxq_cache_copy_pages", "mxq_cache_compact", "mxq_paged_attention_decode_ex",
-             "mxq_attention_varlen_ex"]
+             "mxq_attention_varlen_ex", "mxq_paged_attention_tree",
+             "mxq_paged_attention_tree_workspace_size"]
 
 NOALLOC_SCRATCH_BYTES = 16 * 1024 * 1024
 
@@ -113,6 +115,11 @@ def _declare(lib):
         "mxq_attention_varlen_ex": (st, [P, I64, I64, P, I64, I64, P, I64, I64, P, P, I64, I64,
                                          I64, I32, I32, I32, F, I32, I32, I32, P, P, I64, I64, P,
                                          P, SZ, P]),
+        "mxq_paged_attention_tree": (st, [P, I64, I64, I64, I32, I32, I32, P, P, I32, I64, I32,
+                                          I64, I64, I64, I64, I64, I64, P, I64, I64, P, P, P, I64,
+                                          F, I32, I32, P, P, P, P, I64, I64, P, P, SZ, P]),
+        "mxq_paged_attention_tree_workspace_size": (st, [I64, I64, I32, I32, I32,
+                                                         ctypes.POINTER(SZ)]),
         "mxq_cache_pages_workspace_size": (st, [I64, I64, ctypes.POINTER(SZ)]),
         "mxq_cache_resize": (st, [P, I64, I64, I64, P, P, P, I64, I32, I32, I32, P, SZ, P]),
         "mxq_cache_fork": (st, [P, I64, I64, I64, P, P, I64, I32, P, I64, P, I64, P, P, P, SZ, P]),

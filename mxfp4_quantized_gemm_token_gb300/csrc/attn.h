@@ -72,6 +72,30 @@ struct PromptParams {
   int* status;
 };
 
+struct TreeParams {
+  const void* q;
+  int64_t q_t, q_h, T;
+  int B, Hq, Hkv, D;
+  const void *k_cache, *v_cache;
+  bool fp8;
+  int64_t pages;
+  int page_size;
+  int64_t ck_p, ck_t, ck_h, cv_p, cv_t, cv_h;
+  const int32_t* page_table;
+  int64_t ld_table;
+  int64_t max_pages;       // columns of page_table
+  const int32_t *seq_lens, *cu_q;
+  const int32_t* parents;  // [T], or null: every row continues the one before
+  float scale;
+  int window, first;
+  const float *sinks, *k_scale, *v_scale;
+  void* out;
+  int64_t o_t, o_h;
+  float* lse;              // [T, Hq] or null
+  void* workspace;
+  int* status;
+};
+
 // Page tables and the counts of their pages (cache_resize, cache_fork).
 struct PagesParams {
   int* table;              // [B, max_pages], row stride ld; fork only reads it
@@ -112,6 +136,8 @@ struct MoveParams {
   int* status;
 };
 
+size_t tree_workspace_bytes(int64_t T, int64_t B, int Hq, int Hkv, int D, int num_sms);
+cudaError_t launch_tree(const TreeParams& p, int num_sms, cudaStream_t stream);
 size_t pages_workspace_bytes(int64_t rows, int64_t pages);
 cudaError_t launch_resize_pages(const PagesParams& p, cudaStream_t stream);
 cudaError_t launch_fork_pages(const PagesParams& p, cudaStream_t stream);

@@ -498,3 +498,73 @@ extern "C" mxq_status mxq_cache_compact(void* k_cache, void* v_cache, int32_t ca
   const cudaError_t e = launch_compact(p, d.num_sms, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? MXQ_OK : cuda_fail(e, "cache compact launch");
 }
+
+extern "C" mxq_status mxq_paged_attention_tree_workspace_size(int64_t T, int64_t B, int32_t Hq,
+                                                              int32_t Hkv, int32_t D,
+                                                              size_t* bytes) {
+  if (!bytes || B < 0 || T < 0)
+    return fail(MXQ_ERR_INVALID_ARG, "bad sizes or NULL result pointer");
+  MXQ_TRY(check_heads(Hq, Hkv, D));
+  *bytes = 0;
+  if (B == 0 || T == 0) return MXQ_OK;
+  DeviceInfo d;
+  std::string err;
+  if (!device_info(&d, &err)) return fail(MXQ_ERR_UNSUPPORTED, err);
+  *bytes = tree_workspace_bytes(T, B, Hq, Hkv, D, d.num_sms);
+  return MXQ_OK;
+}
+
+extern "C" mxq_status mxq_paged_attention_tree(
+    const void* q, int64_t sq_t, int64_t sq_h, int64_t T, int32_t Hq, int32_t Hkv, int32_t D,
+    const void* k_cache, const void* v_cache, int32_t cache_dtype, int64_t pages, int32_t page_size,
+    int64_t sck_p, int64_t sck_t, int64_t sck_h, int64_t scv_p, int64_t scv_t, int64_t scv_h,
+    const int32_t* page_table, int64_t ld_table, int64_t max_pages, const int32_t* seq_lens,
+    const int32_t* cu_seqlens_q, const int32_t* parents, int64_t B, float scale, int32_t window,
+    int32_t first, const float* sinks, const float* k_scale, const float* v_scale, void* out,
+    int64_t so_t, int64_t so_h, float* lse, void* workspace, size_t ws_bytes,
+    mxq_stream_t stream) {
+  if (B < 0 || T < 0 || max_pages < 0)
+    return fail(MXQ_ERR_INVALID_ARG, "need B, T and max_pages >= 0");
+  MXQ_TRY(check_heads(Hq, Hkv, D));
+  MXQ_TRY(check_scale(scale, window, first));
+  if (pages <= 0 || page_size <= 0 || pages > 0x7fffffff)
+    return fail(MXQ_ERR_INVALID_ARG, "need 0 < pages < 2^31 and page_size > 0");
+  if (B == 0 || T == 0) return MXQ_OK;
+  if (B > 65535 || T > (1 << 30))
+    return fail(MXQ_ERR_UNSUPPORTED, "more than 65535 sequences or 2^30 tokens");
+  if (max_pages > 0x7fffffff / 2 / page_size)
+    return fail(MXQ_ERR_UNSUPPORTED, "sequences of more than 2^30 keys");
+  if (!seq_lens || !cu_seqlens_q || (max_pages > 0 && !page_table))
+    return fail(MXQ_ERR_INVALID_ARG, "page_table, seq_lens and cu_seqlens_q must be non-NULL");
+  if (ld_table < max_pages) return fail(MXQ_ERR_INVALID_ARG, "ld_table must be >= max_pages");
+  if (!aligned(page_table, 4) || !aligned(seq_lens, 4) || !aligned(cu_seqlens_q, 4) ||
+      !aligned(parents, 4) || !aligned(sinks, 4) || !aligned(lse, 4) || !aligned(k_scale, 4) ||
+      !aligned(v_scale, 4))
+    return fail(MXQ_ERR_INVALID_ARG, "4-byte arrays must be 4-byte aligned");
+  MXQ_TRY(check_rows("q", q, T, Hq, sq_t, sq_h, D, 2, 16));
+  MXQ_TRY(check_rows("out", out, T, Hq, so_t, so_h, D, 2, 16));
+  const bool scaled = k_scale || v_scale;
+  MXQ_TRY(check_cache("k_cache", k_cache, cache_dtype, pages, page_size, Hkv, D, sck_p, sck_t,
+                      sck_h, scaled, 16));
+  MXQ_TRY(check_cache("v_cache", v_cache, cache_dtype, pages, page_size, Hkv, D, scv_p, scv_t,
+                      scv_h, scaled, 16));
+  DeviceInfo d;
+  std::string err;
+  if (!device_info(&d, &err)) return fail(MXQ_ERR_UNSUPPORTED, err);
+  MXQ_TRY(check_workspace(workspace, ws_bytes, tree_workspace_bytes(T, B, Hq, Hkv, D, d.num_sms),
+                          "mxq_paged_attention_tree_workspace_size"));
+  TreeParams p = {};
+  p.q = q, p.q_t = sq_t, p.q_h = sq_h, p.T = T;
+  p.B = static_cast<int>(B), p.Hq = Hq, p.Hkv = Hkv, p.D = D;
+  p.k_cache = k_cache, p.v_cache = v_cache, p.fp8 = cache_dtype == MXQ_E4M3;
+  p.pages = pages, p.page_size = page_size;
+  p.ck_p = sck_p, p.ck_t = sck_t, p.ck_h = sck_h, p.cv_p = scv_p, p.cv_t = scv_t, p.cv_h = scv_h;
+  p.page_table = page_table, p.ld_table = ld_table, p.max_pages = max_pages;
+  p.seq_lens = seq_lens, p.cu_q = cu_seqlens_q, p.parents = parents;
+  p.scale = scale, p.window = std::min(window, 1 << 30), p.first = first_keys(window, first);
+  p.sinks = sinks, p.k_scale = k_scale, p.v_scale = v_scale;
+  p.out = out, p.o_t = so_t, p.o_h = so_h, p.lse = lse, p.workspace = workspace;
+  p.status = d.status;
+  const cudaError_t e = launch_tree(p, d.num_sms, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? MXQ_OK : cuda_fail(e, "tree attention launch");
+}

@@ -35,6 +35,8 @@ decltype(&mxq_attention_varlen_workspace_size) prompt_size_fn;
 decltype(&mxq_current_device) device_fn;
 decltype(&mxq_paged_attention_decode_ex) decode_ex_fn;
 decltype(&mxq_attention_varlen_ex) prompt_ex_fn;
+decltype(&mxq_paged_attention_tree) tree_fn;
+decltype(&mxq_paged_attention_tree_workspace_size) tree_size_fn;
 decltype(&mxq_cache_pages_workspace_size) pages_size_fn;
 decltype(&mxq_cache_resize) resize_fn;
 decltype(&mxq_cache_fork) fork_fn;
@@ -427,6 +429,54 @@ struct Table {
   }
 };
 
+// (q, k_cache, v_cache, page_table, seq_lens, cu_seqlens_q, parents, scale, window, first, sinks,
+// k_scale, v_scale, return_lse, out, workspace)
+PyObject* tree(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
+  return guarded(nargs, 16, [&]() -> PyObject* {
+    const at::Tensor &q = needed("q", a[0]), &kc = needed("k_cache", a[1]);
+    const at::Tensor &vc = needed("v_cache", a[2]), &table = needed("page_table", a[3]);
+    const at::Tensor &lens = needed("seq_lens", a[4]), &cu = needed("cu_seqlens_q", a[5]);
+    const at::Tensor *par = tensor("parents", a[6]), *sinks = tensor("sinks", a[10]);
+    const at::Tensor *ks = tensor("k_scale", a[11]), *vs = tensor("v_scale", a[12]);
+    const at::Tensor *given = tensor("out", a[14]), *ws = tensor("workspace", a[15]);
+    same_device({&q, &kc, &vc, &table, &lens, &cu, par, sinks, ks, vs, given, ws});
+    const Heads hq("q", q);
+    const Caches c(kc, vc, -1, hq.D);
+    const int64_t B = lens.numel();
+    const Table t("page_table", table, B);
+    const int32_t Hq = narrow("heads", hq.heads), Hkv = narrow("kv_heads", c.heads);
+    const int32_t D = narrow("head_dim", hq.D);
+    const int32_t* at_len = vec<const int32_t>("seq_lens", &lens, at::kInt, B);
+    const int32_t* cq = vec<const int32_t>("cu_seqlens_q", &cu, at::kInt, B + 1);
+    const int32_t* parents = vec<const int32_t>("parents", par, at::kInt, hq.n);
+    const float scale = scale_of(a[7], hq.D);
+    const int32_t window = integer("window", a[8]), first = integer("first", a[9]);
+    const float* sink = vec<const float>("sinks", sinks, at::kFloat, Hq);
+    const float* k_scale = vec<const float>("k_scale", ks, at::kFloat, Hkv);
+    const float* v_scale = vec<const float>("v_scale", vs, at::kFloat, Hkv);
+    at::Tensor out = output("out", given, q.sizes()), space = workspace(ws), lse;
+    const bool with_lse = truth(a[13]) != 0;
+    const mxq_stream_t stream = stream_of(q);
+    check(unlocked([&] {
+      if (!space.defined()) {
+        size_t n = 0;
+        const mxq_status st = tree_size_fn(hq.n, B, Hq, Hkv, D, &n);
+        if (st != MXQ_OK) return st;
+        space = fresh({static_cast<int64_t>(n)}, at::kByte, q);
+      }
+      if (!out.defined()) out = fresh(q.sizes(), at::kBFloat16, q);
+      if (with_lse) lse = fresh({hq.n, hq.heads}, at::kFloat, q);
+      return tree_fn(hq.p, hq.s0, hq.s1, hq.n, Hq, Hkv, D, c.k, c.v, c.dtype, c.pages, c.page_size,
+                     c.k0, c.k1, c.k2, c.v0, c.v1, c.v2, t.p, t.ld, t.width, at_len, cq, parents,
+                     B, scale, window, first, sink, k_scale, v_scale, out.data_ptr(),
+                     out.stride(0), out.stride(1),
+                     with_lse ? static_cast<float*>(lse.data_ptr()) : nullptr, space.data_ptr(),
+                     space.nbytes(), stream);
+    }));
+    return result(out, lse);
+  });
+}
+
 // (page_table, seq_lens, new_lens, page_refs, page_size, window, first, workspace)
 PyObject* resize(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   return guarded(nargs, 8, [&]() -> PyObject* {
@@ -558,6 +608,8 @@ PyObject* connect_more(PyObject*, PyObject* by_name) {
       !set("mxq_cache_resize", &resize_fn) || !set("mxq_cache_fork", &fork_fn) ||
       !set("mxq_paged_attention_decode_ex", &decode_ex_fn) ||
       !set("mxq_attention_varlen_ex", &prompt_ex_fn) ||
+      !set("mxq_paged_attention_tree", &tree_fn) ||
+      !set("mxq_paged_attention_tree_workspace_size", &tree_size_fn) ||
       !set("mxq_cache_copy_pages", &copy_pages_fn) || !set("mxq_cache_compact", &compact_fn))
     return nullptr;
   Py_RETURN_NONE;
@@ -585,6 +637,7 @@ PyMethodDef methods[] = {
     {"append", reinterpret_cast<PyCFunction>(append), METH_FASTCALL, nullptr},
     {"decode", reinterpret_cast<PyCFunction>(decode), METH_FASTCALL, nullptr},
     {"prompt", reinterpret_cast<PyCFunction>(prompt), METH_FASTCALL, nullptr},
+    {"tree", reinterpret_cast<PyCFunction>(tree), METH_FASTCALL, nullptr},
     {"resize", reinterpret_cast<PyCFunction>(resize), METH_FASTCALL, nullptr},
     {"fork", reinterpret_cast<PyCFunction>(fork_rows), METH_FASTCALL, nullptr},
     {"copy_pages", reinterpret_cast<PyCFunction>(copy_pages), METH_FASTCALL, nullptr},
