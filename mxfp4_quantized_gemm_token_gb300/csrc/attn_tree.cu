@@ -18,9 +18,10 @@
 // maximum, sum and output, which meet at the end.  Either way the work of the tensor cores is one
 // list of turns: turn t belongs to warpgroup t & 1.
 //   warps 0-3, 4-7   softmax of the even and odd turns, one thread a row, and the output
-//   warps 8-11       load keys and values with 16-byte asynchronous copies, row by row, as pages
+//   warp 8           issues the MMAs
+//   warp 9           finds the pieces of items that the CTA works on
+//   warps 10-15      load keys and values with 16-byte asynchronous copies, row by row, as pages
 //                    are of any size; e4m3 is converted to f16 (exact) on its way
-//   warp 12          issues the MMAs
 // S0, S1, O0 and O1 are in tensor memory, P takes the place of S.  The reference a
 // row subtracts is raised only when its maximum grows by more than 2^8.
 //   bf16 cache: bf16 products.  e4m3 cache: f16 products, q scaled per row by a power of two to
@@ -49,10 +50,15 @@ namespace {
 
 constexpr int kBM = 128;             // rows of a tile, keys of a block
 constexpr int kRows = 2 * kBM;       // of an item
-constexpr int kTreeThreads = 416;
+constexpr int kTreeThreads = 512;
 constexpr int kTreeWarps = kTreeThreads / 32;
-constexpr int kLoadWarp = 8, kMmaWarp = 12;
-constexpr int kSeen = 16;            // blocks whose masks of loaded keys are kept: at most 8 are in use
+constexpr int kMmaWarp = 8, kWalkWarp = 9, kLoadWarp = 10;
+// registers a thread: the launch gives 128 to each; the softmax warpgroups keep most of a row of
+// 128 scores and take what the other two give up
+constexpr int kSoftmaxRegs = 184, kOtherRegs = 72;
+static_assert(2 * kSoftmaxRegs + 2 * kOtherRegs <= 4 * 128, "register split above the launch's");
+constexpr int kPieces = 8;           // pieces of items that may be under way
+constexpr int kSeen = 16;            // blocks whose masks of loaded keys are kept: some 10 are in use
 constexpr int kWhole = 2;            // items of at most this many blocks stay whole
 constexpr int kAllWhole = 3;         // calls whose items have at most this many: all do
 
@@ -69,7 +75,7 @@ struct TreeArgs {
   int G, TB;
   int parts, min_blocks;
   bool all_whole;                    // no item is cut
-  bool alike;                        // both caches have the same page and token strides
+  uint32_t page_mul, page_shift;     // key / page_size = (mulhi(key, mul) + key) >> shift
   TreeJoin* joins;                   // [part * Hkv + head]
   float2* part_ml;                   // [task][2][256]: reference (log2) and sum
   float* part_o;                     // [task][2][256][D]
@@ -85,16 +91,18 @@ struct TreeLayout {
   static constexpr int kRowBytes = FP8 ? D : 2 * D;      // of a cached key
   static constexpr int kLPR = kRowBytes / 16;            // lanes a row
   static constexpr int kRPI = 32 / kLPR;                 // rows a copy instruction
-  static constexpr int kCopies = 32 / kRPI;              // copies a thread and stage
-  // stages of 16-bit operands; copies ahead of what is handed over
+  static constexpr int kCopies = 32 / kRPI;              // copies a thread for 32 rows
   static constexpr int kStages = FP8 ? (D == 128 ? 3 : 6) : (D == 128 ? 5 : 10);
-  static constexpr int kLag = FP8 ? (D == 128 ? 3 : 6) : (D == 128 ? 3 : 6);
-  static constexpr int kRaw = FP8 ? (kLag + 1) * kBM * kRowBytes : 0;
-  static constexpr int kBars = 2 * 7 + 2 * kStages + 1;
-  static constexpr int kSmem = (2 + kStages) * kTileBytes + kRaw + 8 * kBars + 16 + 16 * kSeen;
-  static_assert(kSmem + 1024 <= 226 * 1024, "shared memory over budget");
-  // a stage is released once the copy after it has been handed over (see the loads)
-  static_assert(FP8 || kLag + 2 <= kStages, "the loads would wait for themselves");
+  static constexpr int kLoaders = FP8 && D == 128 ? 5 : 6;   // warps that load
+  // e4m3: units of 32 rows that a warp has on their way, and the one it converts
+  static constexpr int kAhead = FP8 ? (D == 128 ? 3 : 6) : 1;
+  static constexpr int kUnitBytes = 32 * kRowBytes;
+  static constexpr int kRaw = FP8 ? kAhead * kLoaders * kUnitBytes : 0;
+  static constexpr int kBars = 2 * 7 + 2 * kStages + 2 * kPieces + 1;
+  static constexpr int kSmem =
+      (2 + kStages) * kTileBytes + kRaw + 16 * kSeen + 64 * kPieces + 8 * kBars + 16;
+  static_assert(kSmem + 1024 + 512 <= 227 * 1024, "shared memory over budget");
+  static_assert(kLoadWarp + kLoaders <= kTreeWarps, "more warps than there are");
 };
 
 // A sequence: its rows [q0, q0 + nq) of the packed queries, behind len - nq keys.
@@ -135,79 +143,44 @@ __device__ __forceinline__ TreeItem tree_item(const TreeArgs& a, const TreeSeq& 
   return it;
 }
 
-// The pieces of items in a CTA's part of the line, in order.
-struct TreeWalk {
-  const TreeArgs& a;
-  int b, i, off;
-  int64_t pos, left;
-  TreeSeq s;
-  int next_to, next_len;             // of sequence b + 1
-  // the piece
-  TreeItem it;
-  int first;                         // its first token, of the sequence's
-  int v1, cnt;                       // its blocks v1 - 1, v1 - 2, ...
-  int64_t begin;                     // the item's place on the line
-  bool opened, closed;
-  __device__ __forceinline__ TreeWalk(const TreeArgs& args, int b0, int i0, int off0, int64_t s0,
-                                      int64_t s1)
-      : a(args), b(b0), i(i0), off(off0), pos(s0), left(s1 - s0) {
-    if (left <= 0) return;
-    s = tree_seq(a.p, a.p.cu_q[b], a.p.cu_q[b + 1], a.p.seq_lens[b]);
-    ahead();
-  }
-  __device__ __forceinline__ void ahead() {
-    const bool more = b + 1 < a.p.B;
-    next_to = more ? a.p.cu_q[b + 2] : 0;
-    next_len = more ? a.p.seq_lens[b + 1] : 0;
-  }
-  __device__ __forceinline__ bool next() {
-    if (left <= 0) return false;
-    while (true) {
-      if (i * 2 * a.TB >= s.nq) {
-        if (b + 1 >= a.p.B) return false;
-        const int from = a.p.cu_q[b + 1];
-        ++b;
-        s = tree_seq(a.p, from, next_to, next_len);
-        ahead();
-        i = 0;
-        continue;
-      }
-      it = tree_item(a, s, i);
-      if (off < it.n) break;
-      off = 0;
-      ++i;
-    }
-    first = i * 2 * a.TB;
-    begin = pos - off;
-    cnt = static_cast<int>(min(static_cast<int64_t>(it.n - off), left));
-    v1 = it.n - off;
-    opened = off == 0;
-    closed = off + cnt == it.n;
-    pos += cnt;
-    left -= cnt;
-    off += cnt;
-    return true;
-  }
+// A piece of an item: what a CTA's part of the line holds of it.  cnt 0: there are no more.
+struct __align__(16) TreePiece {
+  int q_row, ntok, P, first;         // the item's first row (of all, and of its sequence's)
+  int hi, lo, head, skip;            // as in TreeItem
+  int v1, cnt, flags, task;          // its blocks v1 - 1, v1 - 2, ...
+  int b, pad[3];
   // first key of the piece's block j
   __device__ __forceinline__ int key(int j) const {
     const int v = v1 - 1 - j;
-    return (v < it.head ? v : v + it.skip) * kBM;
+    return (v < head ? v : v + skip) * kBM;
   }
-  __device__ __forceinline__ bool single() const { return it.ntok <= a.TB; }
+};
+static_assert(sizeof(TreePiece) == 64, "four 16-byte words");
+constexpr int kOpened = 1, kClosed = 2, kSingle = 4, kSlot1 = 8;
+
+// The pieces that one warp hands to the others through a ring in shared memory.
+struct Pieces {
+  TreePiece* ring;
+  uint64_t *full, *empty;
+  uint32_t n = 0;
+  __device__ __forceinline__ Pieces(TreePiece* r, uint64_t* f, uint64_t* e)
+      : ring(r), full(f), empty(e) {}
+  // the next piece; false: there are none, or a wait gave up
+  __device__ __forceinline__ bool next(TreePiece* to, const WaitCtx& wc) {
+    const int at = n % kPieces;
+    if (!mbar_wait_warp(&full[at], (n / kPieces) & 1, wc)) return false;
+    *to = ring[at];
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&empty[at]);
+    ++n;
+    return to->cnt > 0;
+  }
 };
 
-template <int N>
-__device__ __forceinline__ void cp_wait_upto(int n) {
-  // all but the last n of at most N groups
-  if constexpr (N > 0) {
-    if (n >= N) {
-      cp_wait<N>();
-      return;
-    }
-    cp_wait_upto<N - 1>(n);
-  } else {
-    cp_wait<0>();
-  }
+// one arrival of this thread on `bar` when its copies so far have landed
+__device__ __forceinline__ void cp_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar))
+               : "memory");
 }
 
 template <int D, bool FP8>
@@ -221,14 +194,17 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeArgs a)
   uint8_t* ring = smem + 2 * L::kTileBytes;
   uint8_t* raw = ring + ST * L::kTileBytes;
   uint32_t* seen = reinterpret_cast<uint32_t*>(raw + L::kRaw);   // [kSeen][4]
-  uint64_t* q_full = reinterpret_cast<uint64_t*>(seen + 4 * kSeen);
+  TreePiece* piece_ring = reinterpret_cast<TreePiece*>(seen + 4 * kSeen);
+  uint64_t* q_full = reinterpret_cast<uint64_t*>(piece_ring + kPieces);
   uint64_t* s_full = q_full + 2;
   uint64_t* p_full = s_full + 2;      // [s][half]
   uint64_t* o_full = p_full + 4;
   uint64_t* merge = o_full + 2;       // both results there, both read
   uint64_t* kv_full = merge + 2;
   uint64_t* kv_empty = kv_full + ST;
-  uint64_t* drain = kv_empty + ST;
+  uint64_t* piece_full = kv_empty + ST;
+  uint64_t* piece_empty = piece_full + kPieces;
+  uint64_t* drain = piece_empty + kPieces;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
   __shared__ unsigned long long warp_sum[kTreeWarps];
@@ -249,8 +225,13 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeArgs a)
       mbar_init(&merge[i], 8);            // the warps of both
     }
     for (int i = 0; i < ST; ++i) {
-      mbar_init(&kv_full[i], 4);          // the loading warps
+      // four units of 32 rows: an arrival each, and one of every thread's copies
+      mbar_init(&kv_full[i], FP8 ? 4 : 4 + 128);
       mbar_init(&kv_empty[i], 1);
+    }
+    for (int i = 0; i < kPieces; ++i) {
+      mbar_init(&piece_full[i], 1);
+      mbar_init(&piece_empty[i], 8 + 1 + L::kLoaders);
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -335,123 +316,194 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeArgs a)
   const int64_t s0 = range[0], s1 = range[1];
   const int tasks = a.parts * p.Hkv;
 
-  if (warp >= kLoadWarp && warp < kMmaWarp) {
-    // ------------------------------------------------------------ loads
-    constexpr int es = FP8 ? 1 : 2;
-    const int lw = warp - kLoadWarp;                     // rows [32 lw, + 32) of a block
-    const int row_in = lane / L::kLPR, piece = lane % L::kLPR;
-    uint32_t issued = 0, given = 0, blocks = 0;          // copies begun and handed over
-    bool ok = true;
-    // Hands over the oldest copy.  It is released by the MMAs no later than after the copy
-    // that follows it has been handed over, so a stage's wait ends.
-    auto hand_over = [&]() {
-      cp_wait_upto<L::kLag>(static_cast<int>(issued - given) - 1);
-      const int st = given % ST;
-      if constexpr (FP8) {
-        if (!mbar_wait_warp(&kv_empty[st], ((given / ST) & 1) ^ 1, wc)) return false;
-        const uint8_t* src = raw + (given % (L::kLag + 1)) * (kBM * L::kRowBytes) +
-                             (lw * L::kCopies * 32 + lane) * 16;
-        uint8_t* dst = ring + st * L::kTileBytes + (piece >> 2) * L::kChunkBytes;
-#pragma unroll
-        for (int i = 0; i < L::kCopies; ++i) {
-          const uint4 x = *reinterpret_cast<const uint4*>(src + i * 512);
-          const int r = lw * 32 + i * L::kRPI + row_in;
-          uint4 lo, hi;
-          e4m3x4_f16(x.x, &lo.x, &lo.y);
-          e4m3x4_f16(x.y, &lo.z, &lo.w);
-          e4m3x4_f16(x.z, &hi.x, &hi.y);
-          e4m3x4_f16(x.w, &hi.z, &hi.w);
-          // (the second chunk's lanes write their pieces the other way round: the first's
-          // are in the same banks)
-          const int c0 = (2 * piece) & 7, swap = piece >> 2;
-          uint8_t* to = dst + r * 128;
-          *reinterpret_cast<uint4*>(to + (((c0 + swap) ^ (r & 7)) << 4)) = swap ? hi : lo;
-          *reinterpret_cast<uint4*>(to + (((c0 + 1 - swap) ^ (r & 7)) << 4)) = swap ? lo : hi;
+  Pieces pieces(piece_ring, piece_full, piece_empty);
+  if (warp >= kMmaWarp) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+  if (warp == kWalkWarp) {
+    // ----------------------------------------------------- the part's pieces
+    if (lane == 0) {
+      uint32_t n = 0;
+      auto put = [&](const TreePiece& it) {
+        const int at = n % kPieces;
+        if (!mbar_wait(&piece_empty[at], ((n / kPieces) & 1) ^ 1, wc)) return false;
+        piece_ring[at] = it;
+        mbar_arrive(&piece_full[at]);
+        ++n;
+        return true;
+      };
+      bool ok = true;
+      for (int task = blockIdx.x; ok && task < tasks; task += gridDim.x) {
+        a.joins[task].ntok = 0;
+        if (s0 >= s1) continue;
+        int b = start[0], i = start[1], off = start[2];
+        int64_t pos = s0, left = s1 - s0;
+        TreeSeq sq = seq(b);
+        while (ok && left > 0) {
+          if (i * 2 * a.TB >= sq.nq) {
+            if (++b >= p.B) break;
+            sq = seq(b);
+            i = 0;
+            continue;
+          }
+          const TreeItem it = tree_item(a, sq, i);
+          if (off < it.n) {
+            TreePiece t = {};
+            t.first = i * 2 * a.TB;
+            t.q_row = sq.q0 + t.first;
+            t.ntok = it.ntok;
+            t.P = sq.len - sq.nq;
+            t.hi = it.hi, t.lo = it.lo, t.head = it.head, t.skip = it.skip;
+            t.v1 = it.n - off;
+            t.cnt = static_cast<int>(min(static_cast<int64_t>(it.n - off), left));
+            t.task = task, t.b = b;
+            const int64_t begin = pos - off;
+            const bool opened = off == 0, closed = off + t.cnt == it.n;
+            t.flags = (opened ? kOpened : 0) | (closed ? kClosed : 0) |
+                      (it.ntok <= a.TB ? kSingle : 0) | (opened && raw0 < begin ? kSlot1 : 0);
+            ok = put(t);
+            if (opened && !closed) {
+              TreeJoin& to = a.joins[task];
+              to.q_row = t.q_row;
+              to.ntok = t.ntok;
+              to.w0 = part;
+              to.w1 = static_cast<int>((begin + it.n - 1) / per);
+              to.first = raw0 < begin ? 1 : 0;
+            }
+            pos += t.cnt;
+            left -= t.cnt;
+          }
+          off = 0;
+          ++i;
         }
+      }
+      if (ok) put(TreePiece{});
+    }
+  } else if (warp >= kLoadWarp && warp < kLoadWarp + L::kLoaders) {
+    // ------------------------------------------------------------ loads
+    // A copy of a block's keys or values is four units of 32 rows; the units of all copies, in
+    // the order K_0, K_1, V_0, K_2, V_1, ..., go round the loading warps.
+    constexpr int es = FP8 ? 1 : 2, NW = L::kLoaders;
+    const int lw = warp - kLoadWarp;
+    const int row_in = lane / L::kLPR, piece = lane % L::kLPR;
+    uint32_t unit = lw;                                  // the next one of this warp, of all
+    uint32_t base = 0, blocks = 0;                       // copies and blocks before the piece
+    [[maybe_unused]] uint32_t raw_unit = lw, pending = 0;
+    const uint32_t raw_at = smem_u32(raw) + lw * (L::kAhead * L::kUnitBytes) + lane * 16;
+    // e4m3: the oldest unit on its way becomes f16 rows of its stage
+    [[maybe_unused]] auto convert = [&]() {
+      const uint32_t fill = raw_unit >> 2;
+      const int st = fill % ST, rows = (raw_unit & 3) * 32 + row_in;
+      if (!mbar_wait_warp(&kv_empty[st], ((fill / ST) & 1) ^ 1, wc)) return false;
+      const uint8_t* src = raw + lw * (L::kAhead * L::kUnitBytes) +
+                           (raw_unit / NW) % L::kAhead * L::kUnitBytes + lane * 16;
+      uint4 x[L::kCopies];
+#pragma unroll
+      for (int i = 0; i < L::kCopies; ++i) x[i] = *reinterpret_cast<const uint4*>(src + i * 512);
+      uint8_t* dst = ring + st * L::kTileBytes + (piece >> 2) * L::kChunkBytes + rows * 128;
+      // (the second chunk's lanes write their 16-byte pieces the other way round: the first's are
+      // in the same banks)
+      const int c0 = (2 * piece) & 7, swap = piece >> 2;
+#pragma unroll
+      for (int i = 0; i < L::kCopies; ++i) {
+        uint4 lo, hi;
+        e4m3x4_f16(x[i].x, &lo.x, &lo.y);
+        e4m3x4_f16(x[i].y, &lo.z, &lo.w);
+        e4m3x4_f16(x[i].z, &hi.x, &hi.y);
+        e4m3x4_f16(x[i].w, &hi.z, &hi.w);
+        const int r7 = (rows + i * L::kRPI) & 7;
+        uint8_t* to = dst + i * L::kRPI * 128;
+        *reinterpret_cast<uint4*>(to + (((c0 + swap) ^ r7) << 4)) = swap ? hi : lo;
+        *reinterpret_cast<uint4*>(to + (((c0 + 1 - swap) ^ r7) << 4)) = swap ? lo : hi;
       }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&kv_full[st]);
-      ++given;
+      raw_unit += NW;
+      --pending;
       return true;
     };
-    if (a.inject_stall) goto loads_done;
-    for (int task = blockIdx.x; ok && task < tasks; task += gridDim.x) {
-      const int hk = task % p.Hkv;
+    TreePiece it;
+    while (!a.inject_stall && pieces.next(&it, wc)) {
+      const int hk = it.task % p.Hkv;
       const char* k_base = static_cast<const char*>(p.k_cache) + hk * p.ck_h * es + piece * 16;
       const char* v_base = static_cast<const char*>(p.v_cache) + hk * p.cv_h * es + piece * 16;
-      TreeWalk walk(a, start[0], start[1], start[2], s0, s1);
-      while (ok && walk.next()) {
-        // this lane's key of a block: its page, looked up a block ahead
-        struct Spot {
-          int page, off;
-          bool wanted;
-        };
-        const int32_t* table = p.page_table + walk.b * p.ld_table;
-        auto look_up = [&](int j) {
-          Spot r = {0, 0, false};
-          if (j >= walk.cnt) return r;
-          const int key = walk.key(j) + lw * 32 + lane;
-          r.wanted = key < walk.it.hi && (key >= walk.it.lo || key < p.first);
-          if (r.wanted) {
-            const uint32_t n = static_cast<uint32_t>(key) / static_cast<uint32_t>(p.page_size);
-            r.off = key - static_cast<int>(n) * p.page_size;
-            r.page = __ldg(table + n);
-          }
-          return r;
-        };
-        // a copy of 32 rows; mask: those that exist
-        auto copy = [&](const char* base, int64_t at, uint32_t mask) {
-          uint32_t dst;
-          if constexpr (FP8) {
-            dst = smem_u32(raw) + (issued % (L::kLag + 1)) * (kBM * L::kRowBytes) +
-                  (lw * L::kCopies * 32 + lane) * 16;
+      const int32_t* table = p.page_table + it.b * p.ld_table;
+      // a unit's copy: of keys or values, of block j
+      auto of_unit = [&](uint32_t u, bool* value) {
+        const int f = static_cast<int>((u >> 2) - base);
+        *value = (f > 0 && (f & 1) == 0) || f == 2 * it.cnt - 1;
+        return f == 0 ? 0 : *value ? (f - 1) / 2 : (f + 1) / 2;
+      };
+      // this lane's key of a unit: its page, looked up a unit ahead
+      struct Spot {
+        int page, off;
+        bool wanted;
+      };
+      auto look_up = [&](uint32_t u) {
+        Spot r = {0, 0, false};
+        bool value;
+        const int j = of_unit(u, &value);
+        if ((u >> 2) - base >= 2u * it.cnt) return r;
+        const int key = it.key(j) + (u & 3) * 32 + lane;
+        r.wanted = key < it.hi && (key >= it.lo || key < p.first);
+        if (r.wanted) {
+          const uint32_t k = static_cast<uint32_t>(key);
+          const uint32_t n = (__umulhi(k, a.page_mul) + k) >> a.page_shift;
+          r.off = key - static_cast<int>(n) * p.page_size;
+          r.page = __ldg(table + n);
+        }
+        return r;
+      };
+      Spot next = look_up(unit);
+      for (; (unit >> 2) - base < 2u * it.cnt; unit += NW) {
+        bool value;
+        const int j = of_unit(unit, &value);
+        const Spot now = next;
+        next = look_up(unit + NW);
+        const bool there =
+            now.wanted && static_cast<uint32_t>(now.page) < static_cast<uint32_t>(p.pages);
+        if (now.wanted && !there) atomicOr(p.status, kStatusBadIndex);
+        const int64_t page = there ? now.page : 0, off = there ? now.off : 0;
+        const int64_t at = (value ? page * p.cv_p + off * p.cv_t : page * p.ck_p + off * p.ck_t) * es;
+        uint32_t mask = __ballot_sync(0xffffffffu, there);
+        if (lane == 0 && !value) seen[((blocks + j) % kSeen) * 4 + (unit & 3)] = mask;
+        mask >>= row_in;
+        const char* src = value ? v_base : k_base;
+        // (the rows' places first: a shuffle before each copy held the copies back)
+        int64_t from[L::kCopies];
 #pragma unroll
-            for (int i = 0; i < L::kCopies; ++i) {
-              const int r = i * L::kRPI + row_in;
-              cp16(dst + i * 512, base + __shfl_sync(0xffffffffu, at, r), (mask >> r) & 1);
-            }
-          } else {
-            const int st = issued % ST;
-            if (!mbar_wait_warp(&kv_empty[st], ((issued / ST) & 1) ^ 1, wc)) return false;
-            dst = smem_u32(ring) + st * L::kTileBytes + (piece >> 3) * L::kChunkBytes;
+        for (int i = 0; i < L::kCopies; ++i)
+          from[i] = __shfl_sync(0xffffffffu, at, i * L::kRPI + row_in);
+        if constexpr (FP8) {
+          if (pending == L::kAhead && !convert()) goto loads_done;
+          const uint32_t dst = raw_at + (unit / NW) % L::kAhead * L::kUnitBytes;
 #pragma unroll
-            for (int i = 0; i < L::kCopies; ++i) {
-              const int r = i * L::kRPI + row_in, rt = lw * 32 + r;
-              cp16(dst + rt * 128 + (((piece & 7) ^ (rt & 7)) << 4),
-                   base + __shfl_sync(0xffffffffu, at, r), (mask >> r) & 1);
-            }
-          }
+          for (int i = 0; i < L::kCopies; ++i)
+            cp16(dst + i * 512, src + from[i], (mask >> (i * L::kRPI)) & 1);
           cp_commit();
-          ++issued;
-          return issued - given <= L::kLag || hand_over();
-        };
-        Spot next = look_up(0);
-        int64_t v_at = 0;
-        uint32_t v_mask = 0;
-        // K_0, K_1, V_0, K_2, V_1, ...
-        for (int j = 0; ok && j <= walk.cnt; ++j) {
-          const int64_t vo = v_at;
-          const uint32_t vm = v_mask;
-          if (j < walk.cnt) {
-            const Spot now = next;
-            next = look_up(j + 1);
-            const bool there =
-                now.wanted && static_cast<uint32_t>(now.page) < static_cast<uint32_t>(p.pages);
-            if (now.wanted && !there) atomicOr(p.status, kStatusBadIndex);
-            const int64_t page = there ? now.page : 0, off = there ? now.off : 0;
-            const int64_t ko = (page * p.ck_p + off * p.ck_t) * es;
-            v_at = a.alike ? ko : (page * p.cv_p + off * p.cv_t) * es;
-            v_mask = __ballot_sync(0xffffffffu, there);
-            if (lane == 0) seen[(blocks % kSeen) * 4 + lw] = v_mask;
-            ++blocks;
-            ok = copy(k_base, ko, v_mask);
-          }
-          if (ok && j > 0) ok = copy(v_base, vo, vm);
+          ++pending;
+          if (pending == L::kAhead) cp_wait<L::kAhead - 1>();
+        } else {
+          const uint32_t fill = unit >> 2;
+          const int st = fill % ST, rows = (unit & 3) * 32 + row_in;
+          if (!mbar_wait_warp(&kv_empty[st], ((fill / ST) & 1) ^ 1, wc)) goto loads_done;
+          const uint32_t dst = smem_u32(ring) + st * L::kTileBytes +
+                               (piece >> 3) * L::kChunkBytes + rows * 128;
+#pragma unroll
+          for (int i = 0; i < L::kCopies; ++i)
+            cp16(dst + i * L::kRPI * 128 + (((piece & 7) ^ ((rows + i * L::kRPI) & 7)) << 4),
+                 src + from[i], (mask >> (i * L::kRPI)) & 1);
+          cp_arrive(&kv_full[st]);
+          if (lane == 0) mbar_arrive(&kv_full[st]);
         }
       }
+      base += 2 * it.cnt;
+      blocks += it.cnt;
     }
-    while (ok && given < issued) ok = hand_over();
+    if constexpr (FP8) {
+      cp_wait<0>();
+      while (pending > 0 && convert()) {
+      }
+    }
   loads_done:
     cp_wait<0>();
   } else if (warp == kMmaWarp) {
@@ -462,6 +514,13 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeArgs a)
     const uint64_t q_desc = sw128_desc(smem_u32(sQ)), k_desc = sw128_desc(smem_u32(ring));
     const uint64_t v_desc = sw128_desc_mn(smem_u32(ring), L::kChunkBytes);
     uint32_t base = 0, nq[2] = {0, 0}, np[2] = {0, 0};   // ring position, items, turns so far
+    // What the operands' rows were written by: the copies of other threads, which have arrived
+    // on the barrier, become visible to the tensor core's reads here; converted rows, and
+    // q, have been made so by their writers.
+    auto see = [&]() {
+      tc_fence_after();
+      if constexpr (!FP8) fence_proxy_async_smem();
+    };
     auto issue_s = [&](int s, uint32_t fill) {
       const uint64_t qd = q_desc + s * (L::kTileBytes / 16);
       const uint64_t kd = k_desc + (fill % ST) * (L::kTileBytes / 16);
@@ -483,58 +542,56 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeArgs a)
     auto wait_kv = [&](uint32_t fill) {
       return mbar_wait_warp(&kv_full[fill % ST], (fill / ST) & 1, wc);
     };
-    for (int task = blockIdx.x; task < tasks; task += gridDim.x) {
-      TreeWalk walk(a, start[0], start[1], start[2], s0, s1);
-      while (walk.next()) {
-        const bool single = walk.single();
-        const int cnt = walk.cnt, turns = single ? cnt : 2 * cnt;
-        auto block_of = [&](int t) { return single ? t : t >> 1; };
-        auto k_fill = [&](int j) { return base + (j == 0 ? 0 : 2 * j - 1); };
-        auto v_fill = [&](int j) { return base + (j + 1 < cnt ? 2 * j + 2 : 2 * j + 1); };
-        for (int t = 0; t < 2 && t < turns; ++t) {
-          const uint32_t f = k_fill(block_of(t));
-          if (!wait_kv(f)) goto mma_done;
-          if (!mbar_wait_warp(&q_full[t], nq[t] & 1, wc)) goto mma_done;
-          ++nq[t];
-          if (leader) {
-            tc_fence_after();
-            issue_s(t, f);
-            mma_commit(&s_full[t]);
-            if (single || t == 1) mma_commit(&kv_empty[f % ST]);
-          }
-          __syncwarp();
+    TreePiece it;
+    while (pieces.next(&it, wc)) {
+      const bool single = it.flags & kSingle;
+      const int cnt = it.cnt, turns = single ? cnt : 2 * cnt;
+      auto block_of = [&](int t) { return single ? t : t >> 1; };
+      auto k_fill = [&](int j) { return base + (j == 0 ? 0 : 2 * j - 1); };
+      auto v_fill = [&](int j) { return base + (j + 1 < cnt ? 2 * j + 2 : 2 * j + 1); };
+      for (int t = 0; t < 2 && t < turns; ++t) {
+        const uint32_t f = k_fill(block_of(t));
+        if (!wait_kv(f)) goto mma_done;
+        if (!mbar_wait_warp(&q_full[t], nq[t] & 1, wc)) goto mma_done;
+        ++nq[t];
+        if (leader) {
+          see();
+          issue_s(t, f);
+          mma_commit(&s_full[t]);
+          if (single || t == 1) mma_commit(&kv_empty[f % ST]);
         }
-        for (int t = 0; t < turns; ++t) {
-          const int s = t & 1;
-          const uint32_t vf = v_fill(block_of(t));
-          if (!wait_kv(vf)) goto mma_done;
-#pragma unroll
-          for (int part = 1; part >= 0; --part) {
-            if (!mbar_wait_warp(&p_full[2 * s + part], np[s] & 1, wc)) goto mma_done;
-            if (leader) {
-              tc_fence_after();
-              issue_o(s, vf, part, t > 1 || part == 0);
-            }
-            __syncwarp();
-          }
-          ++np[s];
-          if (leader && (single || s == 1)) mma_commit(&kv_empty[vf % ST]);
-          if (t + 2 < turns) {
-            const uint32_t kf = k_fill(block_of(t + 2));
-            if (!wait_kv(kf)) goto mma_done;
-            if (leader) {
-              tc_fence_after();
-              issue_s(s, kf);
-              mma_commit(&s_full[s]);
-              if (single || s == 1) mma_commit(&kv_empty[kf % ST]);
-            }
-          } else if (leader) {
-            mma_commit(&o_full[s]);          // the piece's O is complete
-          }
-          __syncwarp();
-        }
-        base += 2 * cnt;
+        __syncwarp();
       }
+      for (int t = 0; t < turns; ++t) {
+        const int s = t & 1;
+        const uint32_t vf = v_fill(block_of(t));
+        if (!wait_kv(vf)) goto mma_done;
+#pragma unroll
+        for (int part = 1; part >= 0; --part) {
+          if (!mbar_wait_warp(&p_full[2 * s + part], np[s] & 1, wc)) goto mma_done;
+          if (leader) {
+            see();
+            issue_o(s, vf, part, t > 1 || part == 0);
+          }
+          __syncwarp();
+        }
+        ++np[s];
+        if (leader && (single || s == 1)) mma_commit(&kv_empty[vf % ST]);
+        if (t + 2 < turns) {
+          const uint32_t kf = k_fill(block_of(t + 2));
+          if (!wait_kv(kf)) goto mma_done;
+          if (leader) {
+            see();
+            issue_s(s, kf);
+            mma_commit(&s_full[s]);
+            if (single || s == 1) mma_commit(&kv_empty[kf % ST]);
+          }
+        } else if (leader) {
+          mma_commit(&o_full[s]);          // the piece's O is complete
+        }
+        __syncwarp();
+      }
+      base += 2 * cnt;
     }
   mma_done:
     // the products in flight end before the tensor memory is freed
@@ -542,8 +599,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeArgs a)
     volatile int zero = 0;
     WaitCtx dw{p.status, &zero, 1000000000ull};
     mbar_wait(drain, 0, dw);
-  } else {
+  } else if (warp < kMmaWarp) {
     // ----------------------------------------------------------- softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     const int s = warp >> 2;                            // warpgroup
     const int row = threadIdx.x & 127;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
@@ -551,20 +609,19 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeArgs a)
     const int tok = row / a.G, g = row - tok * a.G;
     uint8_t* q_tile = sQ + s * L::kTileBytes;
     uint32_t ns = 0, no = 0, nm = 0, blocks = 0;
-    for (int task = blockIdx.x; task < tasks; task += gridDim.x) {
-      const int hk = task % p.Hkv, h = hk * a.G + g;
-      const float ks = FP8 && p.k_scale != nullptr ? __ldg(p.k_scale + hk) : 1.f;
-      const float vs = FP8 && p.v_scale != nullptr ? __ldg(p.v_scale + hk) : 1.f;
-      if (threadIdx.x == 0) a.joins[task].ntok = 0;
-      TreeWalk walk(a, start[0], start[1], start[2], s0, s1);
-      while (walk.next()) {
-        const bool single = walk.single();
-        const int cnt = walk.cnt;
+    TreePiece it;
+    while (pieces.next(&it, wc)) {
+      {
+        const int hk = it.task % p.Hkv, h = hk * a.G + g;
+        const float ks = FP8 && p.k_scale != nullptr ? __ldg(p.k_scale + hk) : 1.f;
+        const float vs = FP8 && p.v_scale != nullptr ? __ldg(p.v_scale + hk) : 1.f;
+        const bool single = it.flags & kSingle;
+        const int cnt = it.cnt;
         const int turns = single ? (cnt - s + 1) / 2 : cnt;      // of this warpgroup
         const int i = (single ? 0 : s * a.TB) + tok;             // of the item's tokens
-        const bool valid = tok < a.TB && i < walk.it.ntok;
-        const int64_t tokr = static_cast<int64_t>(walk.s.q0) + walk.first + i;
-        const int me = walk.first + i, P = walk.s.len - walk.s.nq;
+        const bool valid = tok < a.TB && i < it.ntok;
+        const int64_t tokr = static_cast<int64_t>(it.q_row) + i;
+        const int me = it.first + i, P = it.P;
         float c = p.scale * kLog2e;
         if (turns > 0) {
           // q, in the layout of the K operand's rows (16-byte pieces swizzled by the row)
@@ -611,7 +668,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeArgs a)
         // the row's place: visible keys [0, first) and [lo, hi), and the path `cur`, its
         // parent, ... of which `up` steps are behind (a row that is not stored may see anything)
         const bool tree = p.parents != nullptr;
-        const int32_t* parents = p.parents + walk.s.q0;
+        const int32_t* parents = p.parents + (it.q_row - it.first);
         auto parent = [&](int k) {
           const int r = __ldg(parents + k);
           if (r >= -1 && r < k) return r;
@@ -630,7 +687,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeArgs a)
         float m = -INFINITY, l = 0.f;
         for (int t = 0; t < turns; ++t) {
           const int j = single ? 2 * t + s : t;
-          const int k0 = walk.key(j);
+          const int k0 = it.key(j);
           if (!mbar_wait_warp(&s_full[s], ns & 1, wc)) goto softmax_done;
           ++ns;
           tc_fence_after();
@@ -658,32 +715,34 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeArgs a)
             for (int q = 0; q < 4; ++q) vis[q] &= own[q];
             __syncwarp();
           }
-          // 64 scores, those that the mask hides as -inf, and their maximum
-          auto scores = [&](float* x, int half) {
-            tmem_ld32_async(tS + 64 * half, x);
-            tmem_ld32_async(tS + 64 * half + 32, x + 32);
-            tmem_wait32(x);
-            tmem_wait32(x + 32);
+          // 32 scores, those that the mask hides as -inf
+          auto hide = [&](float* x, int q) {
             if (masked) {
 #pragma unroll
-              for (int e = 0; e < 64; ++e)
-                x[e] = (vis[2 * half + (e >> 5)] >> (e & 31)) & 1 ? x[e] : -INFINITY;
+              for (int e = 0; e < 32; ++e) x[e] = (vis[q] >> e) & 1 ? x[e] : -INFINITY;
             }
           };
           auto top = [&](const float* x) {
             float mq[2] = {fmaxf(x[0], x[1]), fmaxf(x[2], x[3])};
 #pragma unroll
-            for (int e = 4; e < 64; e += 4) {
+            for (int e = 4; e < 32; e += 4) {
               mq[0] = fmaxf(mq[0], fmaxf(x[e], x[e + 1]));
               mq[1] = fmaxf(mq[1], fmaxf(x[e + 2], x[e + 3]));
             }
             return fmaxf(mq[0], mq[1]);
           };
-          float x[64];
-          scores(x, 0);
-          float mx = top(x);
-          scores(x, 1);
-          mx = fmaxf(mx, top(x));
+          // the row's scores and their maximum
+          float x[128];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) tmem_ld32_async(tS + 32 * q, x + 32 * q);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) tmem_wait32(x + 32 * q);
+          float mx = -INFINITY;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            hide(x + 32 * q, q);
+            mx = fmaxf(mx, top(x + 32 * q));
+          }
           // raise the reference if it grows by more than 2^8 (at first: from -inf)
           const bool raise = (mx - m) * c > 8.f;
           if (__any_sync(0xffffffffu, raise)) {
@@ -706,28 +765,34 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeArgs a)
           }
           const float mc = m == -INFINITY ? 0.f : m * c;
           const uint64_t c2 = pack2(c, c), n2 = pack2(-mc, -mc);
-          // weights, the second half first: it is in registers, the first one's scores are
-          // read again (a row of 128 would not fit)
+          // weights, the second half of the keys first
           uint64_t sum[2] = {0, 0};
-          auto weights = [&](const float* v, int half) {
-            uint32_t w[32];
+          auto weights = [&](uint32_t* w, const float* v) {
 #pragma unroll
-            for (int e = 0; e < 64; e += 2) {
+            for (int e = 0; e < 32; e += 2) {
               float y, z;
               unpack2(fma2(pack2(v[e], v[e + 1]), c2, n2), &y, &z);
               y = ex2(y), z = ex2(z);
               w[e / 2] = FP8 ? f16x2(y, z) : bf16x2(y, z);
               sum[(e / 2) & 1] = add2(sum[(e / 2) & 1], pack2(y, z));
             }
-            tmem_st32(tS + 64 * half, w);
+          };
+          auto hand_over = [&](int half) {
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&p_full[2 * s + half]);
           };
-          weights(x, 1);
-          scores(x, 0);
-          weights(x, 0);
+          uint32_t w[32];
+          weights(w, x + 64);
+          weights(w + 16, x + 96);
+          tmem_st32(tS + 64, w);
+          uint32_t w1[32];
+          weights(w1, x);
+          hand_over(1);
+          weights(w1 + 16, x + 32);
+          tmem_st32(tS, w1);
+          hand_over(0);
           float y, z;
           unpack2(add2(sum[0], sum[1]), &y, &z);
           l += y + z;
@@ -762,7 +827,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeArgs a)
           d0 = s * (D / 2), d1 = d0 + D / 2;
         }
         const uint32_t from = tO + (single ? 0 : s * 128);
-        const bool direct = walk.opened && walk.closed;
+        const bool direct = (it.flags & (kOpened | kClosed)) == (kOpened | kClosed);
         RowEnd end = {1.f, 0.f, false};
         float f = 1.f;
         if (direct) {
@@ -770,7 +835,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeArgs a)
           f = end.factor * vs;
         }
         const int64_t slot =
-            (static_cast<int64_t>(task) * 2 + (walk.opened && raw0 < walk.begin ? 1 : 0)) * kRows +
+            (static_cast<int64_t>(it.task) * 2 + (it.flags & kSlot1 ? 1 : 0)) * kRows +
             (single ? 0 : s * kBM) + row;
         __nv_bfloat16* dst =
             static_cast<__nv_bfloat16*>(p.out) + tokr * p.o_t + static_cast<int64_t>(h) * p.o_h;
@@ -806,14 +871,6 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeArgs a)
           } else {
             a.part_ml[slot] = make_float2(ref, l);
           }
-        }
-        if (threadIdx.x == 0 && walk.opened && !walk.closed) {
-          TreeJoin& to = a.joins[task];
-          to.q_row = walk.s.q0 + walk.first;
-          to.ntok = walk.it.ntok;
-          to.w0 = part;
-          to.w1 = static_cast<int>((walk.begin + walk.it.n - 1) / per);
-          to.first = raw0 < walk.begin ? 1 : 0;
         }
         tc_fence_before();
         if (single) {
@@ -936,7 +993,9 @@ cudaError_t launch_tree(const TreeParams& p, int num_sms, cudaStream_t stream) {
   a.TB = kBM / a.G;
   a.parts = parts_of(p.Hkv, num_sms);
   a.min_blocks = 2;
-  a.alike = p.ck_p == p.cv_p && p.ck_t == p.cv_t;
+  while ((1u << a.page_shift) < static_cast<uint32_t>(p.page_size)) ++a.page_shift;
+  a.page_mul = static_cast<uint32_t>(
+      ((1ull << 32) * ((1ull << a.page_shift) - p.page_size)) / p.page_size + 1);
   // Blocks of the longest item that there can be
   int64_t blocks = (p.max_pages * p.page_size + kBM - 1) / kBM;
   if (p.window > 0)
