@@ -55,7 +55,7 @@ constexpr int kTreeWarps = kTreeThreads / 32;
 constexpr int kMmaWarp = 8, kWalkWarp = 9, kLoadWarp = 10;
 // registers a thread: the launch gives 128 to each; the softmax warpgroups keep most of a row of
 // 128 scores and take what the other two give up
-constexpr int kSoftmaxRegs = 184, kOtherRegs = 72;
+constexpr int kSoftmaxRegs = 168, kOtherRegs = 88;
 static_assert(2 * kSoftmaxRegs + 2 * kOtherRegs <= 4 * 128, "register split above the launch's");
 constexpr int kPieces = 8;           // pieces of items that may be under way
 constexpr int kSeen = 16;            // blocks whose masks of loaded keys are kept: some 10 are in use
@@ -158,22 +158,24 @@ struct __align__(16) TreePiece {
 static_assert(sizeof(TreePiece) == 64, "four 16-byte words");
 constexpr int kOpened = 1, kClosed = 2, kSingle = 4, kSlot1 = 8;
 
-// The pieces that one warp hands to the others through a ring in shared memory.
+// The pieces that one warp hands to the others through a ring in shared memory; their fields are
+// read there as they are needed (registers are short).
 struct Pieces {
-  TreePiece* ring;
+  const TreePiece* ring;
   uint64_t *full, *empty;
   uint32_t n = 0;
-  __device__ __forceinline__ Pieces(TreePiece* r, uint64_t* f, uint64_t* e)
+  __device__ __forceinline__ Pieces(const TreePiece* r, uint64_t* f, uint64_t* e)
       : ring(r), full(f), empty(e) {}
-  // the next piece; false: there are none, or a wait gave up
-  __device__ __forceinline__ bool next(TreePiece* to, const WaitCtx& wc) {
+  // the next piece; null: there are none, or a wait gave up
+  __device__ __forceinline__ const TreePiece* next(const WaitCtx& wc) {
     const int at = n % kPieces;
-    if (!mbar_wait_warp(&full[at], (n / kPieces) & 1, wc)) return false;
-    *to = ring[at];
+    if (!mbar_wait_warp(&full[at], (n / kPieces) & 1, wc)) return nullptr;
+    return ring[at].cnt > 0 ? ring + at : nullptr;
+  }
+  __device__ __forceinline__ void done() {
     __syncwarp();
-    if ((threadIdx.x & 31) == 0) mbar_arrive(&empty[at]);
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&empty[n % kPieces]);
     ++n;
-    return to->cnt > 0;
   }
 };
 
@@ -395,24 +397,27 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeArgs a)
       if (!mbar_wait_warp(&kv_empty[st], ((fill / ST) & 1) ^ 1, wc)) return false;
       const uint8_t* src = raw + lw * (L::kAhead * L::kUnitBytes) +
                            (raw_unit / NW) % L::kAhead * L::kUnitBytes + lane * 16;
-      uint4 x[L::kCopies];
-#pragma unroll
-      for (int i = 0; i < L::kCopies; ++i) x[i] = *reinterpret_cast<const uint4*>(src + i * 512);
       uint8_t* dst = ring + st * L::kTileBytes + (piece >> 2) * L::kChunkBytes + rows * 128;
       // (the second chunk's lanes write their 16-byte pieces the other way round: the first's are
       // in the same banks)
       const int c0 = (2 * piece) & 7, swap = piece >> 2;
 #pragma unroll
-      for (int i = 0; i < L::kCopies; ++i) {
-        uint4 lo, hi;
-        e4m3x4_f16(x[i].x, &lo.x, &lo.y);
-        e4m3x4_f16(x[i].y, &lo.z, &lo.w);
-        e4m3x4_f16(x[i].z, &hi.x, &hi.y);
-        e4m3x4_f16(x[i].w, &hi.z, &hi.w);
-        const int r7 = (rows + i * L::kRPI) & 7;
-        uint8_t* to = dst + i * L::kRPI * 128;
-        *reinterpret_cast<uint4*>(to + (((c0 + swap) ^ r7) << 4)) = swap ? hi : lo;
-        *reinterpret_cast<uint4*>(to + (((c0 + 1 - swap) ^ r7) << 4)) = swap ? lo : hi;
+      for (int i0 = 0; i0 < L::kCopies; i0 += 4) {
+        uint4 x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const uint4*>(src + (i0 + i) * 512);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint4 lo, hi;
+          e4m3x4_f16(x[i].x, &lo.x, &lo.y);
+          e4m3x4_f16(x[i].y, &lo.z, &lo.w);
+          e4m3x4_f16(x[i].z, &hi.x, &hi.y);
+          e4m3x4_f16(x[i].w, &hi.z, &hi.w);
+          const int r = (i0 + i) * L::kRPI, r7 = (rows + r) & 7;
+          uint8_t* to = dst + r * 128;
+          *reinterpret_cast<uint4*>(to + (((c0 + swap) ^ r7) << 4)) = swap ? hi : lo;
+          *reinterpret_cast<uint4*>(to + (((c0 + 1 - swap) ^ r7) << 4)) = swap ? lo : hi;
+        }
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -421,83 +426,87 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeArgs a)
       --pending;
       return true;
     };
-    TreePiece it;
-    while (!a.inject_stall && pieces.next(&it, wc)) {
+    while (!a.inject_stall) {
+      const TreePiece* at_piece = pieces.next(wc);
+      if (at_piece == nullptr) break;
+      const TreePiece& it = *at_piece;
       const int hk = it.task % p.Hkv;
       const char* k_base = static_cast<const char*>(p.k_cache) + hk * p.ck_h * es + piece * 16;
       const char* v_base = static_cast<const char*>(p.v_cache) + hk * p.cv_h * es + piece * 16;
       const int32_t* table = p.page_table + it.b * p.ld_table;
-      // a unit's copy: of keys or values, of block j
-      auto of_unit = [&](uint32_t u, bool* value) {
-        const int f = static_cast<int>((u >> 2) - base);
-        *value = (f > 0 && (f & 1) == 0) || f == 2 * it.cnt - 1;
-        return f == 0 ? 0 : *value ? (f - 1) / 2 : (f + 1) / 2;
-      };
-      // this lane's key of a unit: its page, looked up a unit ahead
-      struct Spot {
-        int page, off;
-        bool wanted;
+      // A unit: its copy's kind and block, and this lane's key's place, looked up a unit ahead.
+      struct Unit {
+        int j, page, off;              // page -1: no key of its row is loaded
+        bool value;
       };
       auto look_up = [&](uint32_t u) {
-        Spot r = {0, 0, false};
-        bool value;
-        const int j = of_unit(u, &value);
-        if ((u >> 2) - base >= 2u * it.cnt) return r;
-        const int key = it.key(j) + (u & 3) * 32 + lane;
-        r.wanted = key < it.hi && (key >= it.lo || key < p.first);
-        if (r.wanted) {
-          const uint32_t k = static_cast<uint32_t>(key);
-          const uint32_t n = (__umulhi(k, a.page_mul) + k) >> a.page_shift;
+        const int f = static_cast<int>((u >> 2) - base);
+        Unit r;
+        r.value = (f > 0 && (f & 1) == 0) || f == 2 * it.cnt - 1;
+        r.j = f == 0 ? 0 : r.value ? (f - 1) / 2 : (f + 1) / 2;
+        r.page = -1, r.off = 0;
+        const int key = it.key(r.j) + (u & 3) * 32 + lane;
+        if (f < 2 * it.cnt && key < it.hi && (key >= it.lo || key < p.first)) {
+          const uint32_t n = (__umulhi(key, a.page_mul) + key) >> a.page_shift;
           r.off = key - static_cast<int>(n) * p.page_size;
-          r.page = __ldg(table + n);
+          // (a page below 0 is as wrong as one past the cache, and no reason to stop here)
+          r.page = __ldg(table + n) & 0x7fffffff;
         }
         return r;
       };
-      Spot next = look_up(unit);
+      Unit next = look_up(unit);
       for (; (unit >> 2) - base < 2u * it.cnt; unit += NW) {
-        bool value;
-        const int j = of_unit(unit, &value);
-        const Spot now = next;
+        const Unit now = next;
         next = look_up(unit + NW);
-        const bool there =
-            now.wanted && static_cast<uint32_t>(now.page) < static_cast<uint32_t>(p.pages);
-        if (now.wanted && !there) atomicOr(p.status, kStatusBadIndex);
-        const int64_t page = there ? now.page : 0, off = there ? now.off : 0;
-        const int64_t at = (value ? page * p.cv_p + off * p.cv_t : page * p.ck_p + off * p.ck_t) * es;
+        const bool there = static_cast<uint32_t>(now.page) < static_cast<uint32_t>(p.pages);
+        if (now.page >= 0 && !there) atomicOr(p.status, kStatusBadIndex);
+        int64_t at = 0;
+        if (there)
+          at = now.value ? now.page * p.cv_p + now.off * p.cv_t
+                         : now.page * p.ck_p + now.off * p.ck_t;
+        at *= es;
         uint32_t mask = __ballot_sync(0xffffffffu, there);
-        if (lane == 0 && !value) seen[((blocks + j) % kSeen) * 4 + (unit & 3)] = mask;
+        if (lane == 0 && !now.value) seen[((blocks + now.j) % kSeen) * 4 + (unit & 3)] = mask;
         mask >>= row_in;
-        const char* src = value ? v_base : k_base;
-        // (the rows' places first: a shuffle before each copy held the copies back)
-        int64_t from[L::kCopies];
-#pragma unroll
-        for (int i = 0; i < L::kCopies; ++i)
-          from[i] = __shfl_sync(0xffffffffu, at, i * L::kRPI + row_in);
+        const char* src = now.value ? v_base : k_base;
+        const uint32_t fill = unit >> 2;
+        const int st = fill % ST, rows = (unit & 3) * 32 + row_in;
+        uint32_t dst;
         if constexpr (FP8) {
           if (pending == L::kAhead && !convert()) goto loads_done;
-          const uint32_t dst = raw_at + (unit / NW) % L::kAhead * L::kUnitBytes;
+          dst = raw_at + (unit / NW) % L::kAhead * L::kUnitBytes;
+        } else {
+          if (!mbar_wait_warp(&kv_empty[st], ((fill / ST) & 1) ^ 1, wc)) goto loads_done;
+          dst = smem_u32(ring) + st * L::kTileBytes + (piece >> 3) * L::kChunkBytes + rows * 128;
+        }
+        // (the places of several rows first: a shuffle before each copy held the copies back)
+        constexpr int kBatch = 4;
 #pragma unroll
-          for (int i = 0; i < L::kCopies; ++i)
-            cp16(dst + i * 512, src + from[i], (mask >> (i * L::kRPI)) & 1);
+        for (int i0 = 0; i0 < L::kCopies; i0 += kBatch) {
+          int64_t from[kBatch];
+#pragma unroll
+          for (int i = 0; i < kBatch && i0 + i < L::kCopies; ++i)
+            from[i] = __shfl_sync(0xffffffffu, at, (i0 + i) * L::kRPI + row_in);
+#pragma unroll
+          for (int i = 0; i < kBatch && i0 + i < L::kCopies; ++i) {
+            const int r = (i0 + i) * L::kRPI;
+            cp16(FP8 ? dst + (i0 + i) * 512
+                     : dst + r * 128 + (((piece & 7) ^ ((rows + r) & 7)) << 4),
+                 src + from[i], (mask >> r) & 1);
+          }
+        }
+        if constexpr (FP8) {
           cp_commit();
           ++pending;
           if (pending == L::kAhead) cp_wait<L::kAhead - 1>();
         } else {
-          const uint32_t fill = unit >> 2;
-          const int st = fill % ST, rows = (unit & 3) * 32 + row_in;
-          if (!mbar_wait_warp(&kv_empty[st], ((fill / ST) & 1) ^ 1, wc)) goto loads_done;
-          const uint32_t dst = smem_u32(ring) + st * L::kTileBytes +
-                               (piece >> 3) * L::kChunkBytes + rows * 128;
-#pragma unroll
-          for (int i = 0; i < L::kCopies; ++i)
-            cp16(dst + i * L::kRPI * 128 + (((piece & 7) ^ ((rows + i * L::kRPI) & 7)) << 4),
-                 src + from[i], (mask >> (i * L::kRPI)) & 1);
           cp_arrive(&kv_full[st]);
           if (lane == 0) mbar_arrive(&kv_full[st]);
         }
       }
       base += 2 * it.cnt;
       blocks += it.cnt;
+      pieces.done();
     }
     if constexpr (FP8) {
       cp_wait<0>();
@@ -542,10 +551,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeArgs a)
     auto wait_kv = [&](uint32_t fill) {
       return mbar_wait_warp(&kv_full[fill % ST], (fill / ST) & 1, wc);
     };
-    TreePiece it;
-    while (pieces.next(&it, wc)) {
-      const bool single = it.flags & kSingle;
-      const int cnt = it.cnt, turns = single ? cnt : 2 * cnt;
+    while (const TreePiece* it = pieces.next(wc)) {
+      const bool single = it->flags & kSingle;
+      const int cnt = it->cnt, turns = single ? cnt : 2 * cnt;
       auto block_of = [&](int t) { return single ? t : t >> 1; };
       auto k_fill = [&](int j) { return base + (j == 0 ? 0 : 2 * j - 1); };
       auto v_fill = [&](int j) { return base + (j + 1 < cnt ? 2 * j + 2 : 2 * j + 1); };
@@ -592,6 +600,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeArgs a)
         __syncwarp();
       }
       base += 2 * cnt;
+      pieces.done();
     }
   mma_done:
     // the products in flight end before the tensor memory is freed
@@ -609,8 +618,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeArgs a)
     const int tok = row / a.G, g = row - tok * a.G;
     uint8_t* q_tile = sQ + s * L::kTileBytes;
     uint32_t ns = 0, no = 0, nm = 0, blocks = 0;
-    TreePiece it;
-    while (pieces.next(&it, wc)) {
+    while (const TreePiece* at_piece = pieces.next(wc)) {
+      const TreePiece& it = *at_piece;
       {
         const int hk = it.task % p.Hkv, h = hk * a.G + g;
         const float ks = FP8 && p.k_scale != nullptr ? __ldg(p.k_scale + hk) : 1.f;
@@ -715,34 +724,34 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeArgs a)
             for (int q = 0; q < 4; ++q) vis[q] &= own[q];
             __syncwarp();
           }
-          // 32 scores, those that the mask hides as -inf
-          auto hide = [&](float* x, int q) {
+          // 64 scores, those that the mask hides as -inf, and their maximum
+          auto scores = [&](float* x, int half) {
+            tmem_ld32_async(tS + 64 * half, x);
+            tmem_ld32_async(tS + 64 * half + 32, x + 32);
+            tmem_wait32(x);
+            tmem_wait32(x + 32);
             if (masked) {
 #pragma unroll
-              for (int e = 0; e < 32; ++e) x[e] = (vis[q] >> e) & 1 ? x[e] : -INFINITY;
+              for (int e = 0; e < 64; ++e)
+                x[e] = (vis[2 * half + (e >> 5)] >> (e & 31)) & 1 ? x[e] : -INFINITY;
             }
           };
           auto top = [&](const float* x) {
             float mq[2] = {fmaxf(x[0], x[1]), fmaxf(x[2], x[3])};
 #pragma unroll
-            for (int e = 4; e < 32; e += 4) {
+            for (int e = 4; e < 64; e += 4) {
               mq[0] = fmaxf(mq[0], fmaxf(x[e], x[e + 1]));
               mq[1] = fmaxf(mq[1], fmaxf(x[e + 2], x[e + 3]));
             }
             return fmaxf(mq[0], mq[1]);
           };
-          // the row's scores and their maximum
-          float x[128];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) tmem_ld32_async(tS + 32 * q, x + 32 * q);
-#pragma unroll
-          for (int q = 0; q < 4; ++q) tmem_wait32(x + 32 * q);
-          float mx = -INFINITY;
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            hide(x + 32 * q, q);
-            mx = fmaxf(mx, top(x + 32 * q));
-          }
+          // the row's scores; those of the first half are read again below (a row of 128
+          // does not fit)
+          float x[64];
+          scores(x, 0);
+          float mx = top(x);
+          scores(x, 1);
+          mx = fmaxf(mx, top(x));
           // raise the reference if it grows by more than 2^8 (at first: from -inf)
           const bool raise = (mx - m) * c > 8.f;
           if (__any_sync(0xffffffffu, raise)) {
@@ -784,14 +793,14 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeArgs a)
             if (lane == 0) mbar_arrive(&p_full[2 * s + half]);
           };
           uint32_t w[32];
-          weights(w, x + 64);
-          weights(w + 16, x + 96);
+          weights(w, x);
+          weights(w + 16, x + 32);
           tmem_st32(tS + 64, w);
-          uint32_t w1[32];
-          weights(w1, x);
+          scores(x, 0);
           hand_over(1);
-          weights(w1 + 16, x + 32);
-          tmem_st32(tS, w1);
+          weights(w, x);
+          weights(w + 16, x + 32);
+          tmem_st32(tS, w);
           hand_over(0);
           float y, z;
           unpack2(add2(sum[0], sum[1]), &y, &z);
@@ -881,6 +890,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeArgs a)
           ++nm;
         }
       }
+      pieces.done();
     }
   softmax_done:;
   }
