@@ -179,6 +179,16 @@ struct Pieces {
   }
 };
 
+// a / b for a >= 0, b > 0: 64-bit division only where it is needed
+__device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
+
+__device__ __forceinline__ void prefetch(const void* at) {
+  asm volatile("prefetch.global.L1 [%0];" ::"l"(at));
+}
+
 // one arrival of this thread on `bar` when its copies so far have landed
 __device__ __forceinline__ void cp_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar))
@@ -213,6 +223,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeArgs a)
   __shared__ int warp_longest[kTreeWarps];
   __shared__ long long range[2];      // the part's blocks on the line
   __shared__ int start[3];            // its first sequence, item and block of that
+  __shared__ TreeSeq start_seq;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const TreeParams& p = a.p;
   WaitCtx wc{p.status, abort_flag, a.budget_ns};
@@ -252,8 +263,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeArgs a)
   auto seq = [&](int b) { return tree_seq(p, p.cu_q[b], p.cu_q[b + 1], p.seq_lens[b]); };
   unsigned long long mine = 0;
   int longest = 0;
+  TreeSeq kept = {0, 0, 0, false};    // where a thread has one sequence, it is read once
   for (int b = b0; b < b1; ++b) {
     const TreeSeq s = seq(b);
+    kept = s;
     if (s.bad && blockIdx.x == 0) atomicOr(p.status, kStatusBadIndex);
     for (int i = 0; i * 2 * a.TB < s.nq; ++i) {
       const int n = tree_item(a, s, i).n;
@@ -279,7 +292,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeArgs a)
     total += static_cast<int64_t>(warp_sum[w]);
     longest = max(longest, warp_longest[w]);
   }
-  int64_t per = max((total + a.parts - 1) / a.parts, static_cast<int64_t>(a.min_blocks));
+  int64_t per = max(divide(total + a.parts - 1, a.parts), static_cast<int64_t>(a.min_blocks));
   // where all stay whole, a part has room for the longest, or some would get two
   if (a.all_whole && per < longest) per = longest;
   const int whole =
@@ -298,7 +311,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeArgs a)
       at = before;
       bool found = false;
       for (int b = b0; b < b1 && !found; ++b) {
-        const TreeSeq s = seq(b);
+        const TreeSeq s = per_thread == 1 ? kept : seq(b);
         for (int i = 0; i * 2 * a.TB < s.nq && !found; ++i) {
           const int n = tree_item(a, s, i).n;
           if (at + n <= pos) {
@@ -309,7 +322,13 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeArgs a)
           int off = static_cast<int>(pos - at);
           if (n <= whole) off = 2 * off >= n && off > 0 ? n : 0;
           range[end] = at + off;
-          if (end == 0) start[0] = b, start[1] = i, start[2] = off;
+          if (end == 0) {
+            start[0] = b, start[1] = i, start[2] = off;
+            start_seq = s;
+            // on its way: the pages of its last keys
+            if (s.len > 0)
+              prefetch(p.page_table + b * p.ld_table + (s.len - 1) / p.page_size);
+          }
         }
       }
     }
@@ -338,7 +357,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeArgs a)
         if (s0 >= s1) continue;
         int b = start[0], i = start[1], off = start[2];
         int64_t pos = s0, left = s1 - s0;
-        TreeSeq sq = seq(b);
+        TreeSeq sq = start_seq;
         while (ok && left > 0) {
           if (i * 2 * a.TB >= sq.nq) {
             if (++b >= p.B) break;
@@ -367,7 +386,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeArgs a)
               to.q_row = t.q_row;
               to.ntok = t.ntok;
               to.w0 = part;
-              to.w1 = static_cast<int>((begin + it.n - 1) / per);
+              to.w1 = static_cast<int>(divide(begin + it.n - 1, per));
               to.first = raw0 < begin ? 1 : 0;
             }
             pos += t.cnt;
@@ -843,11 +862,31 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeArgs a)
           end = finish_row(ref * kLn2, l, p.sinks != nullptr && valid ? p.sinks + h : nullptr);
           f = end.factor * vs;
         }
-        const int64_t slot =
+        const int64_t slot0 =
             (static_cast<int64_t>(it.task) * 2 + (it.flags & kSlot1 ? 1 : 0)) * kRows +
-            (single ? 0 : s * kBM) + row;
-        __nv_bfloat16* dst =
-            static_cast<__nv_bfloat16*>(p.out) + tokr * p.o_t + static_cast<int64_t>(h) * p.o_h;
+            (single ? 0 : s * kBM);
+        const int64_t slot = slot0 + row;
+        // Through shared memory (the tile of q is done with), so that four lanes write 64
+        // adjacent bytes of a row: 32 columns of the output, or 16 of a partial result.
+        uint8_t* stage = q_tile + 1024 + (warp & 3) * 2048;
+        const uint32_t stored = __ballot_sync(0xffffffffu, valid);
+        const int sub = lane >> 2, ch = lane & 3;
+        const int64_t out_at = tokr * p.o_t + static_cast<int64_t>(h) * p.o_h;
+        auto write_rows = [&](const uint4* v, char* base, auto at_of) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            *reinterpret_cast<uint4*>(stage + lane * 64 + ((e ^ ((lane >> 1) & 3)) << 4)) = v[e];
+          __syncwarp();
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int r = 8 * e + sub;
+            const uint4 w = *reinterpret_cast<const uint4*>(stage + r * 64 +
+                                                            ((ch ^ ((r >> 1) & 3)) << 4));
+            const int64_t to = at_of(r);
+            if ((stored >> r) & 1) *reinterpret_cast<uint4*>(base + to + ch * 16) = w;
+          }
+          __syncwarp();
+        };
         for (int d = d0; d < d1; d += 32) {
           float o[32];
           tmem_ld32(from + d, o);
@@ -857,22 +896,32 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeArgs a)
 #pragma unroll
             for (int e = 0; e < 32; ++e) o[e] = o[e] * f0 + o1[e] * f1;
           }
-          if (valid && direct) {
+          uint4 v[4];
+          if (direct) {
 #pragma unroll
-            for (int e = 0; e < 32; e += 8)
-              *reinterpret_cast<uint4*>(dst + d + e) =
-                  end.none ? make_uint4(0u, 0u, 0u, 0u)
-                           : make_uint4(bf16x2(o[e] * f, o[e + 1] * f),
-                                        bf16x2(o[e + 2] * f, o[e + 3] * f),
-                                        bf16x2(o[e + 4] * f, o[e + 5] * f),
-                                        bf16x2(o[e + 6] * f, o[e + 7] * f));
-          } else if (valid) {
+            for (int e = 0; e < 4; ++e)
+              v[e] = end.none ? make_uint4(0u, 0u, 0u, 0u)
+                              : make_uint4(bf16x2(o[8 * e] * f, o[8 * e + 1] * f),
+                                           bf16x2(o[8 * e + 2] * f, o[8 * e + 3] * f),
+                                           bf16x2(o[8 * e + 4] * f, o[8 * e + 5] * f),
+                                           bf16x2(o[8 * e + 6] * f, o[8 * e + 7] * f));
+            write_rows(v, static_cast<char*>(p.out), [&](int r) {
+              return 2 * (__shfl_sync(0xffffffffu, out_at, r) + d);
+            });
+          } else {
+            const int64_t first = (slot0 + (warp & 3) * 32) * D + d;
 #pragma unroll
-            for (int e = 0; e < 32; e += 4)
-              *reinterpret_cast<float4*>(a.part_o + slot * D + d + e) =
-                  make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+            for (int half = 0; half < 2; ++half) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float* x = o + 16 * half + 4 * e;
+                v[e] = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]),
+                                  __float_as_uint(x[2]), __float_as_uint(x[3]));
+              }
+              write_rows(v, reinterpret_cast<char*>(a.part_o),
+                         [&](int r) { return 4 * (first + r * D + 16 * half); });
+            }
           }
-          __syncwarp();
         }
         if (valid && d0 == 0) {
           if (direct) {
@@ -903,56 +952,81 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeArgs a)
 }
 
 // Joins the partial results of an item that several parts share, in the parts' order:
-// out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i, a warp a row.
+// out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i.  D / 4 lanes take two rows, four columns
+// each, reading four parts of both at a time: what counts is one chain of loads.  (A warp a row:
+// 16 us for two chunks of 300 rows.)
+constexpr int kJoinWarps = 4;
 template <int D>
-__global__ void __launch_bounds__(256) tree_join_kernel(const TreeArgs a) {
-  constexpr int N = D / 32, U = 8;
+struct JoinShape {
+  static constexpr int kLPR = D / 4, kRPW = 2 * (32 / kLPR);      // rows of a warp
+};
+template <int D>
+__global__ void __launch_bounds__(32 * kJoinWarps) tree_join_kernel(const TreeArgs a) {
+  using S = JoinShape<D>;
+  constexpr int U = 4;
   const TreeParams& p = a.p;
   pdl_wait();
   pdl_launch_dependents();
   const TreeJoin j = a.joins[blockIdx.x];
   if (j.ntok == 0) return;
   const int lane = threadIdx.x & 31, hk = blockIdx.x % p.Hkv;
-  const int row = blockIdx.y * 8 + (threadIdx.x >> 5);
-  const int s = row / kBM, in = row - s * kBM;
-  const int tok = in / a.G, g = in - tok * a.G, i = s * a.TB + tok;
-  if (tok >= a.TB || i >= j.ntok) return;
-  float m = -INFINITY, l = 0.f, o[N] = {};
-  for (int w = j.w0; w <= j.w1; w += U) {
-    float2 ml[U];
-    float v[U][N];
+  const int col = 4 * (lane % S::kLPR);
+  const int row0 = (blockIdx.y * kJoinWarps + (threadIdx.x >> 5)) * S::kRPW + 2 * (lane / S::kLPR);
+  bool valid[2];
+  int token[2], head[2];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      ml[u] = make_float2(-INFINITY, 0.f);
-      if (w + u > j.w1) continue;
-      const int64_t task = static_cast<int64_t>(w + u) * p.Hkv + hk;
-      const int64_t slot = (task * 2 + (w + u == j.w0 ? j.first : 0)) * kRows + row;
-      ml[u] = a.part_ml[slot];
-#pragma unroll
-      for (int e = 0; e < N; ++e) v[u][e] = a.part_o[slot * D + lane + 32 * e];
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (w + u > j.w1) continue;
-      // a part whose scores are all NaN has no reference, but a sum: it counts
-      const float n = fmaxf(m, ml[u].x), at = n == -INFINITY ? 0.f : n;
-      const float f = ex2(m - at), k = ex2(ml[u].x - at);
-      l = l * f + ml[u].y * k;
-#pragma unroll
-      for (int e = 0; e < N; ++e) o[e] = o[e] * f + v[u][e] * k;
-      m = n;
-    }
+  for (int r = 0; r < 2; ++r) {
+    const int row = row0 + r, s = row / kBM, in = row - s * kBM, tok = in / a.G;
+    token[r] = s * a.TB + tok;
+    head[r] = hk * a.G + in - tok * a.G;
+    valid[r] = tok < a.TB && token[r] < j.ntok;
   }
-  const int h = hk * a.G + g;
-  const int64_t tokr = static_cast<int64_t>(j.q_row) + i;
-  const RowEnd end = finish_row(m * kLn2, l, p.sinks ? p.sinks + h : nullptr);
-  const float f = end.factor * (p.v_scale != nullptr ? __ldg(p.v_scale + hk) : 1.f);
-  __nv_bfloat16* dst =
-      static_cast<__nv_bfloat16*>(p.out) + tokr * p.o_t + static_cast<int64_t>(h) * p.o_h;
+  if (!valid[0] && !valid[1]) return;
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+  float4 o[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+  for (int w = j.w0; w <= j.w1; w += U) {
+    float2 ml[U][2];
+    float4 v[U][2];
 #pragma unroll
-  for (int e = 0; e < N; ++e)
-    dst[lane + 32 * e] = end.none ? __float2bfloat16_rn(0.f) : __float2bfloat16_rn(o[e] * f);
-  if (p.lse != nullptr && lane == 0) p.lse[tokr * p.Hq + h] = end.lse;
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        if (w + u > j.w1 || !valid[r]) continue;
+        const int64_t task = static_cast<int64_t>(w + u) * p.Hkv + hk;
+        const int64_t slot = (task * 2 + (w + u == j.w0 ? j.first : 0)) * kRows + row0 + r;
+        ml[u][r] = a.part_ml[slot];
+        v[u][r] = *reinterpret_cast<const float4*>(a.part_o + slot * D + col);
+      }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        if (w + u > j.w1 || !valid[r]) continue;
+        // a part whose scores are all NaN has no reference, but a sum: it counts
+        const float n = fmaxf(m[r], ml[u][r].x), at = n == -INFINITY ? 0.f : n;
+        const float f = ex2(m[r] - at), k = ex2(ml[u][r].x - at);
+        l[r] = l[r] * f + ml[u][r].y * k;
+        o[r].x = o[r].x * f + v[u][r].x * k;
+        o[r].y = o[r].y * f + v[u][r].y * k;
+        o[r].z = o[r].z * f + v[u][r].z * k;
+        o[r].w = o[r].w * f + v[u][r].w * k;
+        m[r] = n;
+      }
+  }
+  const float vs = p.v_scale != nullptr ? __ldg(p.v_scale + hk) : 1.f;
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    if (!valid[r]) continue;
+    const int64_t tokr = static_cast<int64_t>(j.q_row) + token[r];
+    const RowEnd end = finish_row(m[r] * kLn2, l[r], p.sinks ? p.sinks + head[r] : nullptr);
+    const float f = end.factor * vs;
+    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + tokr * p.o_t +
+                         static_cast<int64_t>(head[r]) * p.o_h + col;
+    *reinterpret_cast<uint2*>(dst) =
+        end.none ? make_uint2(0u, 0u)
+                 : make_uint2(bf16x2(o[r].x * f, o[r].y * f), bf16x2(o[r].z * f, o[r].w * f));
+    if (p.lse != nullptr && col == 0) p.lse[tokr * p.Hq + head[r]] = end.lse;
+  }
 }
 
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
@@ -986,7 +1060,12 @@ cudaError_t launch(const TreeArgs& a, int num_sms, cudaStream_t stream) {
   e = launch_k(tree_kernel<D, FP8>, dim3(std::min(tasks, num_sms)), dim3(kTreeThreads),
                static_cast<size_t>(smem), stream, a);
   if (e != cudaSuccess || a.all_whole) return e;
-  return launch_k(tree_join_kernel<D>, dim3(tasks, kRows / 8), dim3(256), 0, stream, a);
+  // rows that an item can have
+  const int64_t T = a.p.T;
+  const int rows = T > a.TB ? kRows : static_cast<int>(T) * a.G;
+  constexpr int kPerBlock = kJoinWarps * JoinShape<D>::kRPW;
+  return launch_k(tree_join_kernel<D>, dim3(tasks, (rows + kPerBlock - 1) / kPerBlock),
+                  dim3(32 * kJoinWarps), 0, stream, a);
 }
 
 }  // namespace
