@@ -73,7 +73,7 @@ struct __align__(16) TreeJoin {
 struct TreeArgs {
   TreeParams p;
   int G, TB;
-  int parts, min_blocks;
+  int parts;
   bool all_whole;                    // no item is cut
   uint32_t page_mul, page_shift;     // key / page_size = (mulhi(key, mul) + key) >> shift
   TreeJoin* joins;                   // [part * Hkv + head]
@@ -93,14 +93,16 @@ struct TreeLayout {
   static constexpr int kRPI = 32 / kLPR;                 // rows a copy instruction
   static constexpr int kCopies = 32 / kRPI;              // copies a thread for 32 rows
   static constexpr int kStages = FP8 ? (D == 128 ? 3 : 6) : (D == 128 ? 5 : 10);
-  static constexpr int kLoaders = FP8 && D == 128 ? 5 : 6;   // warps that load
-  // e4m3: units of 32 rows that a warp has on their way, and the one it converts
-  static constexpr int kAhead = FP8 ? (D == 128 ? 3 : 6) : 1;
-  static constexpr int kUnitBytes = 32 * kRowBytes;
-  static constexpr int kRaw = FP8 ? kAhead * kLoaders * kUnitBytes : 0;
-  static constexpr int kBars = 2 * 7 + 2 * kStages + 2 * kPieces + 1;
-  static constexpr int kSmem =
-      (2 + kStages) * kTileBytes + kRaw + 16 * kSeen + 64 * kPieces + 8 * kBars + 16;
+  static constexpr int kLoaders = 6;                     // warps that load
+  // e4m3: two of them copy rows as they are cached into stages of their own, the other four
+  // convert a quarter of each to f16 (all six doing both took 253 us for 16 long sequences of 16
+  // drafts)
+  static constexpr int kFetchers = 2;
+  static constexpr int kRawStages = FP8 ? (D == 128 ? 4 : 8) : 0;
+  static constexpr int kUnitBytes = 32 * kRowBytes, kRawBytes = 4 * kUnitBytes;
+  static constexpr int kBars = 2 * 7 + 2 * kStages + 2 * kPieces + 2 * kRawStages + 1;
+  static constexpr int kSmem = (2 + kStages) * kTileBytes + kRawStages * kRawBytes + 16 * kSeen +
+                               64 * kPieces + 8 * kBars + 16;
   static_assert(kSmem + 1024 + 512 <= 227 * 1024, "shared memory over budget");
   static_assert(kLoadWarp + kLoaders <= kTreeWarps, "more warps than there are");
 };
@@ -143,7 +145,21 @@ __device__ __forceinline__ TreeItem tree_item(const TreeArgs& a, const TreeSeq& 
   return it;
 }
 
+// What an item counts on the line: a block of one tile 3 (bf16 at D 128: ~3000 cycles, its bytes'
+// share of the memory), of two 4 (~3900, the softmax), at D 64 3 and 5; its begin and end as
+// much as two blocks (64 ragged sequences: 182 us, with one 184, without 188).
+constexpr int kItemCost = 6, kMinCost = 6;
+template <int D>
+__device__ __forceinline__ int block_cost(const TreeArgs& a, const TreeItem& it) {
+  return it.ntok <= a.TB ? 3 : D == 128 ? 4 : 5;
+}
+template <int D>
+__device__ __forceinline__ int item_cost(const TreeArgs& a, const TreeItem& it) {
+  return kItemCost + it.n * block_cost<D>(a, it);
+}
+
 // A piece of an item: what a CTA's part of the line holds of it.  cnt 0: there are no more.
+// Its keys and values are copied in the order K_0, K_1, V_0, K_2, V_1, ..., V_(cnt-1).
 struct __align__(16) TreePiece {
   int q_row, ntok, P, first;         // the item's first row (of all, and of its sequence's)
   int hi, lo, head, skip;            // as in TreeItem
@@ -153,6 +169,13 @@ struct __align__(16) TreePiece {
   __device__ __forceinline__ int key(int j) const {
     const int v = v1 - 1 - j;
     return (v < head ? v : v + skip) * kBM;
+  }
+  // copy f: whether it is of values, and its block
+  __device__ __forceinline__ bool is_value(int f) const {
+    return (f > 0 && (f & 1) == 0) || f == 2 * cnt - 1;
+  }
+  __device__ __forceinline__ int block(int f) const {
+    return f == 0 ? 0 : is_value(f) ? (f - 1) / 2 : (f + 1) / 2;
   }
 };
 static_assert(sizeof(TreePiece) == 64, "four 16-byte words");
@@ -205,7 +228,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeArgs a)
   uint8_t* sQ = smem;
   uint8_t* ring = smem + 2 * L::kTileBytes;
   uint8_t* raw = ring + ST * L::kTileBytes;
-  uint32_t* seen = reinterpret_cast<uint32_t*>(raw + L::kRaw);   // [kSeen][4]
+  uint32_t* seen = reinterpret_cast<uint32_t*>(raw + L::kRawStages * L::kRawBytes);   // [kSeen][4]
   TreePiece* piece_ring = reinterpret_cast<TreePiece*>(seen + 4 * kSeen);
   uint64_t* q_full = reinterpret_cast<uint64_t*>(piece_ring + kPieces);
   uint64_t* s_full = q_full + 2;
@@ -216,13 +239,15 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeArgs a)
   uint64_t* kv_empty = kv_full + ST;
   uint64_t* piece_full = kv_empty + ST;
   uint64_t* piece_empty = piece_full + kPieces;
-  uint64_t* drain = piece_empty + kPieces;
+  [[maybe_unused]] uint64_t* raw_full = piece_empty + kPieces;
+  [[maybe_unused]] uint64_t* raw_empty = raw_full + L::kRawStages;
+  uint64_t* drain = raw_full + 2 * L::kRawStages;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
   __shared__ unsigned long long warp_sum[kTreeWarps];
   __shared__ int warp_longest[kTreeWarps];
-  __shared__ long long range[2];      // the part's blocks on the line
-  __shared__ int start[3];            // its first sequence, item and block of that
+  __shared__ int ends[2][3];          // the part's begin and end: sequence, item and block of that
+  __shared__ long long start_at;      // the line up to the first item
   __shared__ TreeSeq start_seq;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const TreeParams& p = a.p;
@@ -245,6 +270,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeArgs a)
     for (int i = 0; i < kPieces; ++i) {
       mbar_init(&piece_full[i], 1);
       mbar_init(&piece_empty[i], 8 + 1 + L::kLoaders);
+    }
+    for (int i = 0; i < L::kRawStages; ++i) {
+      mbar_init(&raw_full[i], 33 * L::kFetchers);
+      mbar_init(&raw_empty[i], 4);
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -269,9 +298,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeArgs a)
     kept = s;
     if (s.bad && blockIdx.x == 0) atomicOr(p.status, kStatusBadIndex);
     for (int i = 0; i * 2 * a.TB < s.nq; ++i) {
-      const int n = tree_item(a, s, i).n;
-      mine += n;
-      longest = max(longest, n);
+      const int cost = item_cost<D>(a, tree_item(a, s, i));
+      mine += cost;
+      longest = max(longest, cost);
     }
   }
   longest = __reduce_max_sync(0xffffffffu, longest);
@@ -292,49 +321,44 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeArgs a)
     total += static_cast<int64_t>(warp_sum[w]);
     longest = max(longest, warp_longest[w]);
   }
-  int64_t per = max(divide(total + a.parts - 1, a.parts), static_cast<int64_t>(a.min_blocks));
+  int64_t per = max(divide(total + a.parts - 1, a.parts), static_cast<int64_t>(kMinCost));
   // where all stay whole, a part has room for the longest, or some would get two
   if (a.all_whole && per < longest) per = longest;
-  const int whole =
-      a.all_whole ? longest : static_cast<int>(min(static_cast<int64_t>(kWhole), per));
   const int part = static_cast<int>(blockIdx.x) / p.Hkv;
   const int64_t raw0 = part * per;
-  if (threadIdx.x < 2) range[threadIdx.x] = total;
+  if (threadIdx.x < 2) ends[threadIdx.x][0] = p.B, ends[threadIdx.x][1] = ends[threadIdx.x][2] = 0;
   __syncthreads();
-  {
-    // the thread that holds an end of the part finds its item; inside a short one it moves to
-    // the nearer end
+  // The thread that holds an end of the part finds its item and the block there; inside an item
+  // that stays whole it is the nearer end of it.
+  for (int end = 0; end < 2; ++end) {
+    const int64_t pos = raw0 + end * per;
+    if (pos < before || pos >= before + static_cast<int64_t>(mine)) continue;
     int64_t at = before;
-    for (int end = 0; end < 2; ++end) {
-      const int64_t pos = raw0 + end * per;
-      if (pos < before || pos >= before + static_cast<int64_t>(mine)) continue;
-      at = before;
-      bool found = false;
-      for (int b = b0; b < b1 && !found; ++b) {
-        const TreeSeq s = per_thread == 1 ? kept : seq(b);
-        for (int i = 0; i * 2 * a.TB < s.nq && !found; ++i) {
-          const int n = tree_item(a, s, i).n;
-          if (at + n <= pos) {
-            at += n;
-            continue;
-          }
-          found = true;
-          int off = static_cast<int>(pos - at);
-          if (n <= whole) off = 2 * off >= n && off > 0 ? n : 0;
-          range[end] = at + off;
-          if (end == 0) {
-            start[0] = b, start[1] = i, start[2] = off;
-            start_seq = s;
-            // on its way: the pages of its last keys
-            if (s.len > 0)
-              prefetch(p.page_table + b * p.ld_table + (s.len - 1) / p.page_size);
-          }
+    bool found = false;
+    for (int b = b0; b < b1 && !found; ++b) {
+      const TreeSeq s = per_thread == 1 ? kept : seq(b);
+      for (int i = 0; i * 2 * a.TB < s.nq && !found; ++i) {
+        const TreeItem it = tree_item(a, s, i);
+        const int cost = item_cost<D>(a, it);
+        if (at + cost <= pos) {
+          at += cost;
+          continue;
+        }
+        found = true;
+        const int in = max(0, static_cast<int>(pos - at) - kItemCost);
+        int off = in / block_cost<D>(a, it);
+        if (a.all_whole || it.n <= kWhole) off = 2 * off >= it.n && off > 0 ? it.n : 0;
+        ends[end][0] = b, ends[end][1] = i, ends[end][2] = off;
+        if (end == 0) {
+          start_at = at;
+          start_seq = s;
+          // on its way: the page of its last keys
+          if (s.len > 0) prefetch(p.page_table + b * p.ld_table + (s.len - 1) / p.page_size);
         }
       }
     }
   }
   __syncthreads();
-  const int64_t s0 = range[0], s1 = range[1];
   const int tasks = a.parts * p.Hkv;
 
   Pieces pieces(piece_ring, piece_full, piece_empty);
@@ -354,11 +378,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeArgs a)
       bool ok = true;
       for (int task = blockIdx.x; ok && task < tasks; task += gridDim.x) {
         a.joins[task].ntok = 0;
-        if (s0 >= s1) continue;
-        int b = start[0], i = start[1], off = start[2];
-        int64_t pos = s0, left = s1 - s0;
+        int b = ends[0][0], i = ends[0][1], off = ends[0][2];
+        const int last_b = ends[1][0], last_i = ends[1][1], last_off = ends[1][2];
+        if (b >= p.B) continue;
+        int64_t begin = start_at;
         TreeSeq sq = start_seq;
-        while (ok && left > 0) {
+        while (ok) {
           if (i * 2 * a.TB >= sq.nq) {
             if (++b >= p.B) break;
             sq = seq(b);
@@ -366,7 +391,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeArgs a)
             continue;
           }
           const TreeItem it = tree_item(a, sq, i);
-          if (off < it.n) {
+          const bool at_end = b > last_b || (b == last_b && i >= last_i);
+          const int to_block = !at_end ? it.n : b == last_b && i == last_i ? last_off : 0;
+          if (off < to_block) {
             TreePiece t = {};
             t.first = i * 2 * a.TB;
             t.q_row = sq.q0 + t.first;
@@ -374,10 +401,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeArgs a)
             t.P = sq.len - sq.nq;
             t.hi = it.hi, t.lo = it.lo, t.head = it.head, t.skip = it.skip;
             t.v1 = it.n - off;
-            t.cnt = static_cast<int>(min(static_cast<int64_t>(it.n - off), left));
+            t.cnt = to_block - off;
             t.task = task, t.b = b;
-            const int64_t begin = pos - off;
-            const bool opened = off == 0, closed = off + t.cnt == it.n;
+            const bool opened = off == 0, closed = to_block == it.n;
             t.flags = (opened ? kOpened : 0) | (closed ? kClosed : 0) |
                       (it.ntok <= a.TB ? kSingle : 0) | (opened && raw0 < begin ? kSlot1 : 0);
             ok = put(t);
@@ -386,154 +412,238 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeArgs a)
               to.q_row = t.q_row;
               to.ntok = t.ntok;
               to.w0 = part;
-              to.w1 = static_cast<int>(divide(begin + it.n - 1, per));
+              to.w1 = static_cast<int>(divide(begin + item_cost<D>(a, it) - 1, per));
               to.first = raw0 < begin ? 1 : 0;
             }
-            pos += t.cnt;
-            left -= t.cnt;
           }
+          if (at_end) break;
+          begin += item_cost<D>(a, it);
           off = 0;
           ++i;
         }
       }
       if (ok) put(TreePiece{});
     }
-  } else if (warp >= kLoadWarp && warp < kLoadWarp + L::kLoaders) {
-    // ------------------------------------------------------------ loads
-    // A copy of a block's keys or values is four units of 32 rows; the units of all copies, in
-    // the order K_0, K_1, V_0, K_2, V_1, ..., go round the loading warps.
-    constexpr int es = FP8 ? 1 : 2, NW = L::kLoaders;
-    const int lw = warp - kLoadWarp;
-    const int row_in = lane / L::kLPR, piece = lane % L::kLPR;
-    uint32_t unit = lw;                                  // the next one of this warp, of all
-    uint32_t base = 0, blocks = 0;                       // copies and blocks before the piece
-    [[maybe_unused]] uint32_t raw_unit = lw, pending = 0;
-    const uint32_t raw_at = smem_u32(raw) + lw * (L::kAhead * L::kUnitBytes) + lane * 16;
-    // e4m3: the oldest unit on its way becomes f16 rows of its stage
-    [[maybe_unused]] auto convert = [&]() {
-      const uint32_t fill = raw_unit >> 2;
-      const int st = fill % ST, rows = (raw_unit & 3) * 32 + row_in;
-      if (!mbar_wait_warp(&kv_empty[st], ((fill / ST) & 1) ^ 1, wc)) return false;
-      const uint8_t* src = raw + lw * (L::kAhead * L::kUnitBytes) +
-                           (raw_unit / NW) % L::kAhead * L::kUnitBytes + lane * 16;
-      uint8_t* dst = ring + st * L::kTileBytes + (piece >> 2) * L::kChunkBytes + rows * 128;
+  } else if (FP8 && warp >= kLoadWarp + L::kFetchers) {
+    // ------------------------------------------------- e4m3 rows to f16
+    if constexpr (FP8) {
+      const int quarter = warp - kLoadWarp - L::kFetchers;
+      const int rows = quarter * 32 + lane / L::kLPR, piece = lane % L::kLPR;
+      const uint8_t* src = raw + quarter * L::kUnitBytes + lane * 16;
+      uint8_t* dst = ring + (piece >> 2) * L::kChunkBytes + rows * 128;
       // (the second chunk's lanes write their 16-byte pieces the other way round: the first's are
       // in the same banks)
       const int c0 = (2 * piece) & 7, swap = piece >> 2;
+      uint32_t fill = 0;
+      while (!a.inject_stall) {
+        const TreePiece* it = pieces.next(wc);
+        if (it == nullptr) break;
+        for (const uint32_t end = fill + 2 * it->cnt; fill != end; ++fill) {
+          const int from = fill % L::kRawStages, to = fill % ST;
+          if (!mbar_wait_warp(&raw_full[from], (fill / L::kRawStages) & 1, wc)) goto convert_done;
+          uint4 x[L::kCopies];
 #pragma unroll
-      for (int i0 = 0; i0 < L::kCopies; i0 += 4) {
-        uint4 x[4];
+          for (int i = 0; i < L::kCopies; ++i)
+            x[i] = *reinterpret_cast<const uint4*>(src + from * L::kRawBytes + i * 512);
+          if (!mbar_wait_warp(&kv_empty[to], ((fill / ST) & 1) ^ 1, wc)) goto convert_done;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const uint4*>(src + (i0 + i) * 512);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint4 lo, hi;
-          e4m3x4_f16(x[i].x, &lo.x, &lo.y);
-          e4m3x4_f16(x[i].y, &lo.z, &lo.w);
-          e4m3x4_f16(x[i].z, &hi.x, &hi.y);
-          e4m3x4_f16(x[i].w, &hi.z, &hi.w);
-          const int r = (i0 + i) * L::kRPI, r7 = (rows + r) & 7;
-          uint8_t* to = dst + r * 128;
-          *reinterpret_cast<uint4*>(to + (((c0 + swap) ^ r7) << 4)) = swap ? hi : lo;
-          *reinterpret_cast<uint4*>(to + (((c0 + 1 - swap) ^ r7) << 4)) = swap ? lo : hi;
-        }
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&kv_full[st]);
-      raw_unit += NW;
-      --pending;
-      return true;
-    };
-    while (!a.inject_stall) {
-      const TreePiece* at_piece = pieces.next(wc);
-      if (at_piece == nullptr) break;
-      const TreePiece& it = *at_piece;
-      const int hk = it.task % p.Hkv;
-      const char* k_base = static_cast<const char*>(p.k_cache) + hk * p.ck_h * es + piece * 16;
-      const char* v_base = static_cast<const char*>(p.v_cache) + hk * p.cv_h * es + piece * 16;
-      const int32_t* table = p.page_table + it.b * p.ld_table;
-      // A unit: its copy's kind and block, and this lane's key's place, looked up a unit ahead.
-      struct Unit {
-        int j, page, off;              // page -1: no key of its row is loaded
-        bool value;
-      };
-      auto look_up = [&](uint32_t u) {
-        const int f = static_cast<int>((u >> 2) - base);
-        Unit r;
-        r.value = (f > 0 && (f & 1) == 0) || f == 2 * it.cnt - 1;
-        r.j = f == 0 ? 0 : r.value ? (f - 1) / 2 : (f + 1) / 2;
-        r.page = -1, r.off = 0;
-        const int key = it.key(r.j) + (u & 3) * 32 + lane;
-        if (f < 2 * it.cnt && key < it.hi && (key >= it.lo || key < p.first)) {
-          const uint32_t n = (__umulhi(key, a.page_mul) + key) >> a.page_shift;
-          r.off = key - static_cast<int>(n) * p.page_size;
-          // (a page below 0 is as wrong as one past the cache, and no reason to stop here)
-          r.page = __ldg(table + n) & 0x7fffffff;
-        }
-        return r;
-      };
-      Unit next = look_up(unit);
-      for (; (unit >> 2) - base < 2u * it.cnt; unit += NW) {
-        const Unit now = next;
-        next = look_up(unit + NW);
-        const bool there = static_cast<uint32_t>(now.page) < static_cast<uint32_t>(p.pages);
-        if (now.page >= 0 && !there) atomicOr(p.status, kStatusBadIndex);
-        int64_t at = 0;
-        if (there)
-          at = now.value ? now.page * p.cv_p + now.off * p.cv_t
-                         : now.page * p.ck_p + now.off * p.ck_t;
-        at *= es;
-        uint32_t mask = __ballot_sync(0xffffffffu, there);
-        if (lane == 0 && !now.value) seen[((blocks + now.j) % kSeen) * 4 + (unit & 3)] = mask;
-        mask >>= row_in;
-        const char* src = now.value ? v_base : k_base;
-        const uint32_t fill = unit >> 2;
-        const int st = fill % ST, rows = (unit & 3) * 32 + row_in;
-        uint32_t dst;
-        if constexpr (FP8) {
-          if (pending == L::kAhead && !convert()) goto loads_done;
-          dst = raw_at + (unit / NW) % L::kAhead * L::kUnitBytes;
-        } else {
-          if (!mbar_wait_warp(&kv_empty[st], ((fill / ST) & 1) ^ 1, wc)) goto loads_done;
-          dst = smem_u32(ring) + st * L::kTileBytes + (piece >> 3) * L::kChunkBytes + rows * 128;
-        }
-        // (the places of several rows first: a shuffle before each copy held the copies back)
-        constexpr int kBatch = 4;
-#pragma unroll
-        for (int i0 = 0; i0 < L::kCopies; i0 += kBatch) {
-          int64_t from[kBatch];
-#pragma unroll
-          for (int i = 0; i < kBatch && i0 + i < L::kCopies; ++i)
-            from[i] = __shfl_sync(0xffffffffu, at, (i0 + i) * L::kRPI + row_in);
-#pragma unroll
-          for (int i = 0; i < kBatch && i0 + i < L::kCopies; ++i) {
-            const int r = (i0 + i) * L::kRPI;
-            cp16(FP8 ? dst + (i0 + i) * 512
-                     : dst + r * 128 + (((piece & 7) ^ ((rows + r) & 7)) << 4),
-                 src + from[i], (mask >> r) & 1);
+          for (int i = 0; i < L::kCopies; ++i) {
+            uint4 lo, hi;
+            e4m3x4_f16(x[i].x, &lo.x, &lo.y);
+            e4m3x4_f16(x[i].y, &lo.z, &lo.w);
+            e4m3x4_f16(x[i].z, &hi.x, &hi.y);
+            e4m3x4_f16(x[i].w, &hi.z, &hi.w);
+            const int r7 = (rows + i * L::kRPI) & 7;
+            uint8_t* at = dst + to * L::kTileBytes + i * L::kRPI * 128;
+            *reinterpret_cast<uint4*>(at + (((c0 + swap) ^ r7) << 4)) = swap ? hi : lo;
+            *reinterpret_cast<uint4*>(at + (((c0 + 1 - swap) ^ r7) << 4)) = swap ? lo : hi;
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&kv_full[to]);
+            mbar_arrive(&raw_empty[from]);
           }
         }
-        if constexpr (FP8) {
-          cp_commit();
-          ++pending;
-          if (pending == L::kAhead) cp_wait<L::kAhead - 1>();
-        } else {
+        pieces.done();
+      }
+    convert_done:;
+    }
+  } else if (FP8 && warp >= kLoadWarp) {
+    // ------------------------------------------------------- e4m3 rows
+    // A warp takes two quarters of a block (32 rows each), keys and, from the same places,
+    // values.
+    if constexpr (FP8) {
+      constexpr int NF = L::kFetchers, NQ = 4 / NF;
+      const int first = warp - kLoadWarp;
+      const int row_in = lane / L::kLPR, piece = lane % L::kLPR;
+      const uint32_t raw_at = smem_u32(raw) + first * L::kUnitBytes + lane * 16;
+      uint32_t fill = 0, blocks = 0;
+      while (!a.inject_stall) {
+        const TreePiece* at_piece = pieces.next(wc);
+        if (at_piece == nullptr) break;
+        const TreePiece& it = *at_piece;
+        const int hk = it.task % p.Hkv;
+        const char* k_base = static_cast<const char*>(p.k_cache) + hk * p.ck_h + piece * 16;
+        const char* v_base = static_cast<const char*>(p.v_cache) + hk * p.cv_h + piece * 16;
+        const int32_t* table = p.page_table + it.b * p.ld_table;
+        // this lane's keys of a block, looked up a block ahead; page -1: not loaded
+        struct Spot {
+          int page[NQ], off[NQ];
+        };
+        auto look_up = [&](int j) {
+          Spot r;
+          const int key0 = j < it.cnt ? it.key(j) + lane : 1 << 30;
+#pragma unroll
+          for (int i = 0; i < NQ; ++i) {
+            const int key = key0 + (first + i * NF) * 32;
+            r.page[i] = -1, r.off[i] = 0;
+            if (key < it.hi && (key >= it.lo || key < p.first)) {
+              const uint32_t n = (__umulhi(key, a.page_mul) + key) >> a.page_shift;
+              r.off[i] = key - static_cast<int>(n) * p.page_size;
+              // (a page below 0 is as wrong as one past the cache, and no reason to stop here)
+              r.page[i] = __ldg(table + n) & 0x7fffffff;
+            }
+          }
+          return r;
+        };
+        auto copy = [&](const char* base, const int64_t* at, const uint32_t* mask) {
+          const int st = fill % L::kRawStages;
+          if (!mbar_wait_warp(&raw_empty[st], ((fill / L::kRawStages) & 1) ^ 1, wc)) return false;
+          const uint32_t dst = raw_at + st * L::kRawBytes;
+#pragma unroll
+          for (int q = 0; q < NQ; ++q)
+#pragma unroll
+            for (int i0 = 0; i0 < L::kCopies; i0 += 4) {
+              // (the places of several rows first: a shuffle before each copy held the copies back)
+              int64_t from[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                from[i] = __shfl_sync(0xffffffffu, at[q], (i0 + i) * L::kRPI + row_in);
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                cp16(dst + q * NF * L::kUnitBytes + (i0 + i) * 512, base + from[i],
+                     (mask[q] >> ((i0 + i) * L::kRPI + row_in)) & 1);
+            }
+          cp_arrive(&raw_full[st]);
+          if (lane == 0) mbar_arrive(&raw_full[st]);
+          ++fill;
+          return true;
+        };
+        Spot next = look_up(0);
+        int64_t at[NQ] = {};
+        uint32_t mask[NQ] = {};
+        bool ok = true;
+        for (int j = 0; ok && j <= it.cnt; ++j) {
+          int64_t v_at[NQ];
+          uint32_t v_mask[NQ];
+#pragma unroll
+          for (int i = 0; i < NQ; ++i) v_at[i] = at[i], v_mask[i] = mask[i];
+          if (j < it.cnt) {
+            const Spot now = next;
+            next = look_up(j + 1);
+            int64_t k_at[NQ];
+#pragma unroll
+            for (int i = 0; i < NQ; ++i) {
+              const bool there =
+                  static_cast<uint32_t>(now.page[i]) < static_cast<uint32_t>(p.pages);
+              if (now.page[i] >= 0 && !there) atomicOr(p.status, kStatusBadIndex);
+              k_at[i] = there ? now.page[i] * p.ck_p + now.off[i] * p.ck_t : 0;
+              at[i] = there ? now.page[i] * p.cv_p + now.off[i] * p.cv_t : 0;
+              mask[i] = __ballot_sync(0xffffffffu, there);
+              if (lane == 0) seen[((blocks + j) % kSeen) * 4 + first + i * NF] = mask[i];
+            }
+            ok = copy(k_base, k_at, mask);
+          }
+          if (ok && j > 0) ok = copy(v_base, v_at, v_mask);
+        }
+        if (!ok) break;
+        blocks += it.cnt;
+        pieces.done();
+      }
+      cp_wait<0>();
+    }
+  } else if (warp >= kLoadWarp) {
+    // ------------------------------------------------------- bf16 rows
+    // A copy of a block's keys or values is four units of 32 rows; the units of all copies go
+    // round the loading warps.
+    if constexpr (!FP8) {
+      constexpr int NW = L::kLoaders;
+      const int row_in = lane / L::kLPR, piece = lane % L::kLPR;
+      uint32_t unit = warp - kLoadWarp;                  // the next one of this warp, of all
+      uint32_t base = 0, blocks = 0;                     // copies and blocks before the piece
+      while (!a.inject_stall) {
+        const TreePiece* at_piece = pieces.next(wc);
+        if (at_piece == nullptr) break;
+        const TreePiece& it = *at_piece;
+        const int hk = it.task % p.Hkv;
+        const char* k_base = static_cast<const char*>(p.k_cache) + hk * p.ck_h * 2 + piece * 16;
+        const char* v_base = static_cast<const char*>(p.v_cache) + hk * p.cv_h * 2 + piece * 16;
+        const int32_t* table = p.page_table + it.b * p.ld_table;
+        // A unit: its copy's kind and block, and this lane's key's place, looked up a unit ahead.
+        struct Unit {
+          int j, page, off;              // page -1: not loaded
+          bool value;
+        };
+        auto look_up = [&](uint32_t u) {
+          const int f = static_cast<int>((u >> 2) - base);
+          Unit r;
+          r.value = it.is_value(f);
+          r.j = it.block(f);
+          r.page = -1, r.off = 0;
+          const int key = it.key(r.j) + (u & 3) * 32 + lane;
+          if (f < 2 * it.cnt && key < it.hi && (key >= it.lo || key < p.first)) {
+            const uint32_t n = (__umulhi(key, a.page_mul) + key) >> a.page_shift;
+            r.off = key - static_cast<int>(n) * p.page_size;
+            // (a page below 0 is as wrong as one past the cache, and no reason to stop here)
+            r.page = __ldg(table + n) & 0x7fffffff;
+          }
+          return r;
+        };
+        Unit next = look_up(unit);
+        for (; (unit >> 2) - base < 2u * it.cnt; unit += NW) {
+          const Unit now = next;
+          next = look_up(unit + NW);
+          const bool there = static_cast<uint32_t>(now.page) < static_cast<uint32_t>(p.pages);
+          if (now.page >= 0 && !there) atomicOr(p.status, kStatusBadIndex);
+          int64_t at = 0;
+          if (there)
+            at = 2 * (now.value ? now.page * p.cv_p + now.off * p.cv_t
+                                : now.page * p.ck_p + now.off * p.ck_t);
+          uint32_t mask = __ballot_sync(0xffffffffu, there);
+          if (lane == 0 && !now.value)
+            seen[((blocks + now.j) % kSeen) * 4 + (unit & 3)] = mask;
+          mask >>= row_in;
+          const char* src = now.value ? v_base : k_base;
+          const uint32_t fill = unit >> 2;
+          const int st = fill % ST, rows = (unit & 3) * 32 + row_in;
+          if (!mbar_wait_warp(&kv_empty[st], ((fill / ST) & 1) ^ 1, wc)) goto loads_done;
+          const uint32_t dst = smem_u32(ring) + st * L::kTileBytes +
+                               (piece >> 3) * L::kChunkBytes + rows * 128;
+          // (the places of several rows first: a shuffle before each copy held the copies back)
+#pragma unroll
+          for (int i0 = 0; i0 < L::kCopies; i0 += 4) {
+            int64_t from[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              from[i] = __shfl_sync(0xffffffffu, at, (i0 + i) * L::kRPI + row_in);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int r = (i0 + i) * L::kRPI;
+              cp16(dst + r * 128 + (((piece & 7) ^ ((rows + r) & 7)) << 4), src + from[i],
+                   (mask >> r) & 1);
+            }
+          }
           cp_arrive(&kv_full[st]);
           if (lane == 0) mbar_arrive(&kv_full[st]);
         }
+        base += 2 * it.cnt;
+        blocks += it.cnt;
+        pieces.done();
       }
-      base += 2 * it.cnt;
-      blocks += it.cnt;
-      pieces.done();
-    }
-    if constexpr (FP8) {
+    loads_done:
       cp_wait<0>();
-      while (pending > 0 && convert()) {
-      }
     }
-  loads_done:
-    cp_wait<0>();
   } else if (warp == kMmaWarp) {
     // -------------------------------------------------------------- MMAs
     constexpr uint32_t kDescS = FP8 ? idesc_f16(kBM, kBM) : idesc_bf16(kBM, kBM);
@@ -1081,7 +1191,6 @@ cudaError_t launch_tree(const TreeParams& p, int num_sms, cudaStream_t stream) {
   a.G = p.Hq / p.Hkv;
   a.TB = kBM / a.G;
   a.parts = parts_of(p.Hkv, num_sms);
-  a.min_blocks = 2;
   while ((1u << a.page_shift) < static_cast<uint32_t>(p.page_size)) ++a.page_shift;
   a.page_mul = static_cast<uint32_t>(
       ((1ull << 32) * ((1ull << a.page_shift) - p.page_size)) / p.page_size + 1);
