@@ -487,7 +487,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeArgs a)
         const char* k_base = static_cast<const char*>(p.k_cache) + hk * p.ck_h + piece * 16;
         const char* v_base = static_cast<const char*>(p.v_cache) + hk * p.cv_h + piece * 16;
         const int32_t* table = p.page_table + it.b * p.ld_table;
-        // this lane's keys of a block, looked up a block ahead; page -1: not loaded
+        // this lane's keys of a block, looked up a block ahead; off -1: not loaded (nothing is
+        // done to a page here: it would be waited for)
         struct Spot {
           int page[NQ], off[NQ];
         };
@@ -497,12 +498,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeArgs a)
 #pragma unroll
           for (int i = 0; i < NQ; ++i) {
             const int key = key0 + (first + i * NF) * 32;
-            r.page[i] = -1, r.off[i] = 0;
+            r.page[i] = 0, r.off[i] = -1;
             if (key < it.hi && (key >= it.lo || key < p.first)) {
               const uint32_t n = (__umulhi(key, a.page_mul) + key) >> a.page_shift;
               r.off[i] = key - static_cast<int>(n) * p.page_size;
-              // (a page below 0 is as wrong as one past the cache, and no reason to stop here)
-              r.page[i] = __ldg(table + n) & 0x7fffffff;
+              r.page[i] = __ldg(table + n);
             }
           }
           return r;
@@ -546,8 +546,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeArgs a)
 #pragma unroll
             for (int i = 0; i < NQ; ++i) {
               const bool there =
+                  now.off[i] >= 0 &&
                   static_cast<uint32_t>(now.page[i]) < static_cast<uint32_t>(p.pages);
-              if (now.page[i] >= 0 && !there) atomicOr(p.status, kStatusBadIndex);
+              if (now.off[i] >= 0 && !there) atomicOr(p.status, kStatusBadIndex);
               k_at[i] = there ? now.page[i] * p.ck_p + now.off[i] * p.ck_t : 0;
               at[i] = there ? now.page[i] * p.cv_p + now.off[i] * p.cv_t : 0;
               mask[i] = __ballot_sync(0xffffffffu, there);
@@ -580,9 +581,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeArgs a)
         const char* k_base = static_cast<const char*>(p.k_cache) + hk * p.ck_h * 2 + piece * 16;
         const char* v_base = static_cast<const char*>(p.v_cache) + hk * p.cv_h * 2 + piece * 16;
         const int32_t* table = p.page_table + it.b * p.ld_table;
-        // A unit: its copy's kind and block, and this lane's key's place, looked up a unit ahead.
+        // A unit: its copy's kind and block, and this lane's key's place, looked up a unit ahead
+        // (nothing is done to the page here: it would be waited for).
         struct Unit {
-          int j, page, off;              // page -1: not loaded
+          int j, page, off;              // off -1: not loaded
           bool value;
         };
         auto look_up = [&](uint32_t u) {
@@ -590,13 +592,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeArgs a)
           Unit r;
           r.value = it.is_value(f);
           r.j = it.block(f);
-          r.page = -1, r.off = 0;
+          r.page = 0, r.off = -1;
           const int key = it.key(r.j) + (u & 3) * 32 + lane;
           if (f < 2 * it.cnt && key < it.hi && (key >= it.lo || key < p.first)) {
             const uint32_t n = (__umulhi(key, a.page_mul) + key) >> a.page_shift;
             r.off = key - static_cast<int>(n) * p.page_size;
-            // (a page below 0 is as wrong as one past the cache, and no reason to stop here)
-            r.page = __ldg(table + n) & 0x7fffffff;
+            r.page = __ldg(table + n);
           }
           return r;
         };
@@ -604,8 +605,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeArgs a)
         for (; (unit >> 2) - base < 2u * it.cnt; unit += NW) {
           const Unit now = next;
           next = look_up(unit + NW);
-          const bool there = static_cast<uint32_t>(now.page) < static_cast<uint32_t>(p.pages);
-          if (now.page >= 0 && !there) atomicOr(p.status, kStatusBadIndex);
+          const bool there =
+              now.off >= 0 && static_cast<uint32_t>(now.page) < static_cast<uint32_t>(p.pages);
+          if (now.off >= 0 && !there) atomicOr(p.status, kStatusBadIndex);
           int64_t at = 0;
           if (there)
             at = 2 * (now.value ? now.page * p.cv_p + now.off * p.cv_t
