@@ -548,6 +548,11 @@ extern "C" mxq_status mxq_paged_attention_tree(
                       sck_h, scaled, 16));
   MXQ_TRY(check_cache("v_cache", v_cache, cache_dtype, pages, page_size, Hkv, D, scv_p, scv_t,
                       scv_h, scaled, 16));
+  // (the kernel counts them in 16 bytes, in 32 bits)
+  const int64_t far = int64_t(1) << 35;
+  if ((pages > 1 && (sck_p >= far || scv_p >= far)) ||
+      (page_size > 1 && (sck_t >= far || scv_t >= far)))
+    return fail(MXQ_ERR_UNSUPPORTED, "a page or token stride of 2^35 elements or more");
   DeviceInfo d;
   std::string err;
   if (!device_info(&d, &err)) return fail(MXQ_ERR_UNSUPPORTED, err);

@@ -75,6 +75,7 @@ struct TreeArgs {
   int G, TB;
   int parts;
   bool all_whole;                    // no item is cut
+  uint32_t k_page, k_key, v_page, v_key;   // strides of the caches, in 16 bytes
   uint32_t page_mul, page_shift;     // key / page_size = (mulhi(key, mul) + key) >> shift
   TreeJoin* joins;                   // [part * Hkv + head]
   float2* part_ml;                   // [task][2][256]: reference (log2) and sum
@@ -210,6 +211,12 @@ __device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
 
 __device__ __forceinline__ void prefetch(const void* at) {
   asm volatile("prefetch.global.L1 [%0];" ::"l"(at));
+}
+
+// where a key's row begins in a cache, in 16 bytes
+__device__ __forceinline__ uint64_t row_at(uint32_t page, uint32_t off, uint32_t page_stride,
+                                           uint32_t key_stride) {
+  return static_cast<uint64_t>(page) * page_stride + static_cast<uint64_t>(off) * key_stride;
 }
 
 // one arrival of this thread on `bar` when its copies so far have landed
@@ -487,6 +494,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeArgs a)
         const char* k_base = static_cast<const char*>(p.k_cache) + hk * p.ck_h + piece * 16;
         const char* v_base = static_cast<const char*>(p.v_cache) + hk * p.cv_h + piece * 16;
         const int32_t* table = p.page_table + it.b * p.ld_table;
+        const int hi = it.hi, lo = it.lo, head = it.head, skip = it.skip, v1 = it.v1, cnt = it.cnt;
         // this lane's keys of a block, looked up a block ahead; off -1: not loaded (nothing is
         // done to a page here: it would be waited for)
         struct Spot {
@@ -494,12 +502,13 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeArgs a)
         };
         auto look_up = [&](int j) {
           Spot r;
-          const int key0 = j < it.cnt ? it.key(j) + lane : 1 << 30;
+          const int v = v1 - 1 - j;
+          const int key0 = j < cnt ? (v < head ? v : v + skip) * kBM + first * 32 + lane : 1 << 30;
 #pragma unroll
           for (int i = 0; i < NQ; ++i) {
-            const int key = key0 + (first + i * NF) * 32;
+            const int key = key0 + i * NF * 32;
             r.page[i] = 0, r.off[i] = -1;
-            if (key < it.hi && (key >= it.lo || key < p.first)) {
+            if (key < hi && (key >= lo || key < p.first)) {
               const uint32_t n = (__umulhi(key, a.page_mul) + key) >> a.page_shift;
               r.off[i] = key - static_cast<int>(n) * p.page_size;
               r.page[i] = __ldg(table + n);
@@ -507,7 +516,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeArgs a)
           }
           return r;
         };
-        auto copy = [&](const char* base, const int64_t* at, const uint32_t* mask) {
+        auto copy = [&](const char* base, const uint64_t* at, const uint32_t* mask) {
           const int st = fill % L::kRawStages;
           if (!mbar_wait_warp(&raw_empty[st], ((fill / L::kRawStages) & 1) ^ 1, wc)) return false;
           const uint32_t dst = raw_at + st * L::kRawBytes;
@@ -516,14 +525,14 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeArgs a)
 #pragma unroll
             for (int i0 = 0; i0 < L::kCopies; i0 += 4) {
               // (the places of several rows first: a shuffle before each copy held the copies back)
-              int64_t from[4];
+              uint64_t from[4];
 #pragma unroll
               for (int i = 0; i < 4; ++i)
                 from[i] = __shfl_sync(0xffffffffu, at[q], (i0 + i) * L::kRPI + row_in);
 #pragma unroll
               for (int i = 0; i < 4; ++i)
-                cp16(dst + q * NF * L::kUnitBytes + (i0 + i) * 512, base + from[i],
-                     (mask[q] >> ((i0 + i) * L::kRPI + row_in)) & 1);
+                cp16(dst + q * NF * L::kUnitBytes + (i0 + i) * 512, base + from[i] * 16,
+                     (mask[q] >> ((i0 + i) * L::kRPI)) & 1);
             }
           cp_arrive(&raw_full[st]);
           if (lane == 0) mbar_arrive(&raw_full[st]);
@@ -531,35 +540,37 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeArgs a)
           return true;
         };
         Spot next = look_up(0);
-        int64_t at[NQ] = {};
+        uint64_t at[NQ] = {};
         uint32_t mask[NQ] = {};
         bool ok = true;
-        for (int j = 0; ok && j <= it.cnt; ++j) {
-          int64_t v_at[NQ];
+        for (int j = 0; ok && j <= cnt; ++j) {
+          uint64_t v_at[NQ];
           uint32_t v_mask[NQ];
 #pragma unroll
           for (int i = 0; i < NQ; ++i) v_at[i] = at[i], v_mask[i] = mask[i];
-          if (j < it.cnt) {
+          if (j < cnt) {
             const Spot now = next;
             next = look_up(j + 1);
-            int64_t k_at[NQ];
+            uint64_t k_at[NQ];
 #pragma unroll
             for (int i = 0; i < NQ; ++i) {
               const bool there =
                   now.off[i] >= 0 &&
                   static_cast<uint32_t>(now.page[i]) < static_cast<uint32_t>(p.pages);
               if (now.off[i] >= 0 && !there) atomicOr(p.status, kStatusBadIndex);
-              k_at[i] = there ? now.page[i] * p.ck_p + now.off[i] * p.ck_t : 0;
-              at[i] = there ? now.page[i] * p.cv_p + now.off[i] * p.cv_t : 0;
+              // (the source of a row that is not there is not read)
+              k_at[i] = there ? row_at(now.page[i], now.off[i], a.k_page, a.k_key) : 0;
+              at[i] = there ? row_at(now.page[i], now.off[i], a.v_page, a.v_key) : 0;
               mask[i] = __ballot_sync(0xffffffffu, there);
               if (lane == 0) seen[((blocks + j) % kSeen) * 4 + first + i * NF] = mask[i];
+              mask[i] >>= row_in;
             }
             ok = copy(k_base, k_at, mask);
           }
           if (ok && j > 0) ok = copy(v_base, v_at, v_mask);
         }
         if (!ok) break;
-        blocks += it.cnt;
+        blocks += cnt;
         pieces.done();
       }
       cp_wait<0>();
@@ -608,10 +619,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeArgs a)
           const bool there =
               now.off >= 0 && static_cast<uint32_t>(now.page) < static_cast<uint32_t>(p.pages);
           if (now.off >= 0 && !there) atomicOr(p.status, kStatusBadIndex);
-          int64_t at = 0;
-          if (there)
-            at = 2 * (now.value ? now.page * p.cv_p + now.off * p.cv_t
-                                : now.page * p.ck_p + now.off * p.ck_t);
+          const uint64_t at = !there ? 0
+                              : now.value ? row_at(now.page, now.off, a.v_page, a.v_key)
+                                          : row_at(now.page, now.off, a.k_page, a.k_key);
           uint32_t mask = __ballot_sync(0xffffffffu, there);
           if (lane == 0 && !now.value)
             seen[((blocks + now.j) % kSeen) * 4 + (unit & 3)] = mask;
@@ -625,14 +635,14 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeArgs a)
           // (the places of several rows first: a shuffle before each copy held the copies back)
 #pragma unroll
           for (int i0 = 0; i0 < L::kCopies; i0 += 4) {
-            int64_t from[4];
+            uint64_t from[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i)
               from[i] = __shfl_sync(0xffffffffu, at, (i0 + i) * L::kRPI + row_in);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const int r = (i0 + i) * L::kRPI;
-              cp16(dst + r * 128 + (((piece & 7) ^ ((rows + r) & 7)) << 4), src + from[i],
+              cp16(dst + r * 128 + (((piece & 7) ^ ((rows + r) & 7)) << 4), src + from[i] * 16,
                    (mask >> r) & 1);
             }
           }
@@ -1193,6 +1203,9 @@ cudaError_t launch_tree(const TreeParams& p, int num_sms, cudaStream_t stream) {
   a.G = p.Hq / p.Hkv;
   a.TB = kBM / a.G;
   a.parts = parts_of(p.Hkv, num_sms);
+  const int64_t unit = p.fp8 ? 16 : 8;                   // elements in 16 bytes
+  a.k_page = static_cast<uint32_t>(p.ck_p / unit), a.k_key = static_cast<uint32_t>(p.ck_t / unit);
+  a.v_page = static_cast<uint32_t>(p.cv_p / unit), a.v_key = static_cast<uint32_t>(p.cv_t / unit);
   while ((1u << a.page_shift) < static_cast<uint32_t>(p.page_size)) ++a.page_shift;
   a.page_mul = static_cast<uint32_t>(
       ((1ull << 32) * ((1ull << a.page_shift) - p.page_size)) / p.page_size + 1);
