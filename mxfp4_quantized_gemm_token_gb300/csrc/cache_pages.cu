@@ -13,17 +13,24 @@ namespace mxq {
 namespace {
 
 // ------------------------------------------------------------- tables and counts
-// One cluster of eight blocks: the steps below depend on one another over all rows and pages,
-// a cluster's barrier takes a fraction of a launch, and a table and its counts are small (64K
-// pages: 256 KB).  Latency-bound.
+// One cluster of blocks: the steps below depend on one another over all rows and pages, a
+// cluster's barrier takes a fraction of a launch, and a table and its counts are small (64K
+// pages: 256 KB).  Latency-bound: chains of loads and barriers, so a step's two sums are made
+// together, and what a thread finds out about its rows it leaves for itself in the workspace.
+// A single block where rows, entries and pages are few.
 constexpr int kCluster = 8;
 constexpr int kTableThreads = 1024;
-constexpr int kAll = kCluster * kTableThreads;
-constexpr int kWarpsAll = kAll / 32;
+constexpr int kWarps = kTableThreads / 32;
+constexpr int kChildren = 4096;       // old rows whose children are counted in shared memory
 
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;"
-               ::: "memory");
+template <int C>
+__device__ __forceinline__ void all_sync() {
+  if constexpr (C == 1)
+    __syncthreads();
+  else
+    asm volatile(
+        "barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::
+            : "memory");
 }
 
 // a 64-bit value of the same variable in block `rank` of the cluster
@@ -35,47 +42,64 @@ __device__ __forceinline__ unsigned long long of_block(const unsigned long long*
   return v;
 }
 
-// Sums over the cluster's threads in their order: what comes before this thread, and all.
-// Every thread calls it; `sums` is reused, so a cluster_sync has to follow before the next call.
-__device__ __forceinline__ void scan_all(unsigned long long mine, unsigned long long* sums,
-                                         unsigned long long* before, unsigned long long* total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rank = blockIdx.x;
-  unsigned long long incl = mine;
+// Two sums over all threads in their order: what comes before this thread, and all.  Every
+// thread calls it, once a kernel; a barrier has to follow before its block ends.
+struct Sums {
+  unsigned long long before[2], total[2];
+};
+template <int C>
+__device__ __forceinline__ Sums scan_all(unsigned long long first, unsigned long long second) {
+  __shared__ unsigned long long warp_sums[2][kWarps], block_sums[2];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  unsigned long long incl[2] = {first, second};
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const unsigned long long y = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += y;
-  }
-  if (lane == 31) sums[1 + warp] = incl;
+  for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const unsigned long long y = __shfl_up_sync(0xffffffffu, incl[k], o);
+      if (lane >= o) incl[k] += y;
+    }
+  if (lane == 31) warp_sums[0][warp] = incl[0], warp_sums[1][warp] = incl[1];
   __syncthreads();
-  unsigned long long w = lane < kTableThreads / 32 ? sums[1 + lane] : 0;
-  unsigned long long winc = w;
+  Sums r;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const unsigned long long y = __shfl_up_sync(0xffffffffu, winc, o);
-    if (lane >= o) winc += y;
-  }
-  const unsigned long long block = __shfl_sync(0xffffffffu, winc, 31);
-  const unsigned long long warps_before = __shfl_sync(0xffffffffu, winc - w, warp);
-  if (threadIdx.x == 0) sums[0] = block;
-  cluster_sync();
-  unsigned long long other = lane < kCluster ? of_block(sums, lane) : 0;
-  unsigned long long oinc = other;
+  for (int k = 0; k < 2; ++k) {
+    const unsigned long long w = warp_sums[k][lane];
+    unsigned long long winc = w;
 #pragma unroll
-  for (int o = 1; o < kCluster; o <<= 1) {
-    const unsigned long long y = __shfl_up_sync(0xffffffffu, oinc, o);
-    if (lane >= o) oinc += y;
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned long long y = __shfl_up_sync(0xffffffffu, winc, o);
+      if (lane >= o) winc += y;
+    }
+    r.total[k] = __shfl_sync(0xffffffffu, winc, 31);
+    r.before[k] = __shfl_sync(0xffffffffu, winc - w, warp) + incl[k] - (k == 0 ? first : second);
   }
-  *total = __shfl_sync(0xffffffffu, oinc, kCluster - 1);
-  *before = __shfl_sync(0xffffffffu, oinc - other, rank) + warps_before + incl - mine;
+  if constexpr (C > 1) {
+    if (threadIdx.x == 0) block_sums[0] = r.total[0], block_sums[1] = r.total[1];
+    all_sync<C>();
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const unsigned long long other = lane < C ? of_block(&block_sums[k], lane) : 0;
+      unsigned long long oinc = other;
+#pragma unroll
+      for (int o = 1; o < C; o <<= 1) {
+        const unsigned long long y = __shfl_up_sync(0xffffffffu, oinc, o);
+        if (lane >= o) oinc += y;
+      }
+      r.total[k] = __shfl_sync(0xffffffffu, oinc, C - 1);
+      r.before[k] += __shfl_sync(0xffffffffu, oinc - other, static_cast<int>(blockIdx.x));
+    }
+  }
+  return r;
 }
 
 // Rows or pages of a thread, adjacent ones
+template <int C>
 struct Span {
   int64_t from, to;
   __device__ __forceinline__ Span(int64_t n, int unit) {
-    const int64_t each = (n + static_cast<int64_t>(kAll) * unit - 1) /
-                         (static_cast<int64_t>(kAll) * unit) * unit;
+    constexpr int64_t all = static_cast<int64_t>(C) * kTableThreads;
+    const int64_t each = n <= all * unit ? unit : (n + all * unit - 1) / (all * unit) * unit;
     const int64_t me = static_cast<int64_t>(blockIdx.x) * kTableThreads + threadIdx.x;
     from = min(n, me * each);
     to = min(n, from + each);
@@ -83,34 +107,36 @@ struct Span {
 };
 
 __device__ __forceinline__ int pages_of(int len, int page_size) {
-  return static_cast<int>((static_cast<int64_t>(len) + page_size - 1) / page_size);
+  return static_cast<int>((static_cast<uint32_t>(len) + static_cast<uint32_t>(page_size) - 1) /
+                          static_cast<uint32_t>(page_size));
 }
 
-// a length inside the table's width
+// a length inside the table's width (at most 2^30 keys)
 __device__ __forceinline__ int clamp_len(const PagesParams& p, int len, bool* bad) {
-  const int64_t most = p.max_pages * p.page_size;
+  const int most = static_cast<int>(p.max_pages) * p.page_size;
   if (len < 0 || len > most) *bad = true;
-  return static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(len), most)));
+  return max(0, min(len, most));
 }
 
-// The first `need` free pages, ascending, into fresh[]; their counts become 1.  `before`: free
-// pages of the threads before this one.
-__device__ __forceinline__ int64_t count_free(const PagesParams& p, const Span& s) {
-  int64_t n = 0;
-  int64_t i = s.from;
-  for (; i + 4 <= s.to; i += 4) {
+__device__ __forceinline__ int count_free(const PagesParams& p, int64_t from, int64_t to) {
+  int n = 0;
+  int64_t i = from;
+#pragma unroll 4
+  for (; i + 4 <= to; i += 4) {
     // (a span begins at a multiple of four pages; the counts at 16 bytes)
     const int4 r = *reinterpret_cast<const int4*>(p.refs + i);
     n += (r.x == 0) + (r.y == 0) + (r.z == 0) + (r.w == 0);
   }
-  for (; i < s.to; ++i) n += p.refs[i] == 0;
+  for (; i < to; ++i) n += p.refs[i] == 0;
   return n;
 }
-__device__ __forceinline__ void take_free(const PagesParams& p, const Span& s, int64_t before,
-                                          int64_t need, int* fresh) {
-  for (int64_t i = s.from; i < s.to && before < need; ++i)
+// The first `need` free pages, ascending, into fresh[]; their counts become 1.  `before`: free
+// pages of the threads before this one.
+__device__ __forceinline__ void take_free(const PagesParams& p, int64_t from, int64_t to,
+                                          unsigned long long before, unsigned long long need) {
+  for (int64_t i = from; i < to && before < need; ++i)
     if (p.refs[i] == 0) {
-      fresh[before++] = static_cast<int>(i);
+      p.fresh[before++] = static_cast<int>(i);
       p.refs[i] = 1;
     }
 }
@@ -124,40 +150,39 @@ __device__ __forceinline__ void add_ref(const PagesParams& p, int page, int n, b
   if (n != 0 && atomicAdd(p.refs + page, n) + n < 0) *bad = true;
 }
 
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kTableThreads)
-    resize_kernel(const PagesParams p) {
-  __shared__ unsigned long long sums[2][1 + kTableThreads / 32];
+template <int C>
+__device__ __forceinline__ void resize(const PagesParams& p) {
   pdl_wait();
   pdl_launch_dependents();
   bool bad = false;
   // pages that each row takes
-  const Span rows(p.B, 1), pages(p.pages, 4);
-  int64_t need = 0;
-  for (int64_t b = rows.from; b < rows.to; ++b)
-    need += max(0, pages_of(clamp_len(p, p.new_lens[b], &bad), p.page_size) -
-                       pages_of(clamp_len(p, p.lens[b], &bad), p.page_size));
-  const int64_t free = count_free(p, pages);
-  unsigned long long need_before, need_all, free_before, free_all;
-  scan_all(need, sums[0], &need_before, &need_all);
-  scan_all(free, sums[1], &free_before, &free_all);
+  const Span<C> rows(p.B, 1), pages(p.pages, 4);
+  unsigned long long need = 0;
   for (int64_t b = rows.from; b < rows.to; ++b) {
-    p.row_begin[b] = static_cast<int64_t>(need_before);
-    need_before += max(0, pages_of(clamp_len(p, p.new_lens[b], &bad), p.page_size) -
-                              pages_of(clamp_len(p, p.lens[b], &bad), p.page_size));
+    const int more = max(0, pages_of(clamp_len(p, p.new_lens[b], &bad), p.page_size) -
+                                pages_of(clamp_len(p, p.lens[b], &bad), p.page_size));
+    p.row_begin[b] = more;
+    need += more;
   }
-  take_free(p, pages, static_cast<int64_t>(free_before), static_cast<int64_t>(need_all), p.fresh);
-  cluster_sync();
+  const Sums sums = scan_all<C>(need, count_free(p, pages.from, pages.to));
+  unsigned long long at = sums.before[0];
+  for (int64_t b = rows.from; b < rows.to; ++b) {
+    const int64_t more = p.row_begin[b];
+    p.row_begin[b] = static_cast<int64_t>(at);
+    at += more;
+  }
+  take_free(p, pages.from, pages.to, sums.before[1], sums.total[0]);
+  all_sync<C>();
   const int lane = threadIdx.x & 31;
-  const int64_t have = static_cast<int64_t>(free_all);
-  for (int64_t b = blockIdx.x * (kTableThreads / 32) + (threadIdx.x >> 5); b < p.B;
-       b += kWarpsAll) {
+  const int64_t have = static_cast<int64_t>(sums.total[1]);
+  for (int64_t b = blockIdx.x * kWarps + (threadIdx.x >> 5); b < p.B; b += C * kWarps) {
     int* row = p.table + b * p.ld;
     const int len = clamp_len(p, p.new_lens[b], &bad);
     const int n0 = pages_of(clamp_len(p, p.lens[b], &bad), p.page_size);
     const int n1 = pages_of(len, p.page_size);
-    const int64_t at = p.row_begin[b];
+    const int64_t first = p.row_begin[b];
     for (int i = n0 + lane; i < n1; i += 32) {
-      const int64_t k = at + i - n0;
+      const int64_t k = first + i - n0;
       row[i] = k < have ? p.fresh[k] : -1;
       if (k >= have) bad = true;
     }
@@ -177,64 +202,66 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kTableThreads
   if (bad) atomicOr(p.status, kStatusBadIndex);
 }
 
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kTableThreads)
-    fork_kernel(const PagesParams p) {
-  __shared__ unsigned long long sums[2][1 + kTableThreads / 32];
+template <int C>
+__device__ __forceinline__ void fork(const PagesParams& p) {
+  __shared__ int near_children[kChildren], near_first[kChildren];
+  const bool near = p.B <= kChildren;      // each block counts all children for itself
+  int* children = near ? near_children : p.children;
+  int* first_child = near ? near_first : p.first_child;
+  const int lane = threadIdx.x & 31;
+  const int warp = blockIdx.x * kWarps + (threadIdx.x >> 5);
   pdl_wait();
   pdl_launch_dependents();
   bool bad = false;
-  const Span old(p.B, 1), rows(p.n, 1), pages(p.pages, 4);
+  const Span<C> rows(p.n, 1), pages(p.pages, 4);
   // children of every old row, and the first of them
-  for (int64_t r = old.from; r < old.to; ++r) p.children[r] = 0, p.first_child[r] = 0x7fffffff;
-  cluster_sync();
+  const int64_t me = near ? threadIdx.x : static_cast<int64_t>(blockIdx.x) * kTableThreads + threadIdx.x;
+  const int64_t step = near ? kTableThreads : C * kTableThreads;
+  for (int64_t r = me; r < p.B; r += step) children[r] = 0, first_child[r] = 0x7fffffff;
   auto parent_of = [&](int64_t b) {
     const int r = p.parents[b];
     if (r < -1 || r >= p.B) bad = true;
     return r >= 0 && r < p.B ? r : -1;
   };
-  for (int64_t b = rows.from; b < rows.to; ++b) {
+  if (near)
+    __syncthreads();
+  else
+    all_sync<C>();
+  for (int64_t b = me; b < p.n; b += step) {
     const int r = parent_of(b);
     if (r < 0) continue;
-    atomicAdd(p.children + r, 1);
-    atomicMin(p.first_child + r, static_cast<int>(b));
+    atomicAdd(children + r, 1);
+    atomicMin(first_child + r, static_cast<int>(b));
   }
-  cluster_sync();
-  // the open page of a row: the one that its next key goes to
-  struct Open {
-    int r, len, n, page;
-    bool wants;              // a page of its own
-  };
-  auto open_of = [&](int64_t b) {
-    Open o = {parent_of(b), 0, 0, -1, false};
-    if (o.r < 0) return o;
-    o.len = clamp_len(p, p.lens[o.r], &bad);
-    o.n = pages_of(o.len, p.page_size);
-    if (o.len % p.page_size == 0) return o;
-    o.page = p.table[o.r * p.ld + o.n - 1];
-    if (static_cast<uint32_t>(o.page) >= static_cast<uint32_t>(p.pages)) return o;
-    o.wants = p.refs[o.page] != 1 || p.first_child[o.r] != b;
-    return o;
-  };
-  int64_t need = 0;
-  for (int64_t b = rows.from; b < rows.to; ++b) need += open_of(b).wants;
-  const int64_t free = count_free(p, pages);
-  unsigned long long need_before, need_all, free_before, free_all;
-  scan_all(need, sums[0], &need_before, &need_all);
-  scan_all(free, sums[1], &free_before, &free_all);
+  if (near)
+    __syncthreads();
+  else
+    all_sync<C>();
+  // Rows whose open page (the one that the next key goes to) has to be a page of their own
+  unsigned long long need = 0;
   for (int64_t b = rows.from; b < rows.to; ++b) {
-    const Open o = open_of(b);
-    // (-1: the row keeps its parent's pages as they are)
-    p.row_begin[b] = o.wants ? static_cast<int64_t>(need_before++) : -1;
-    p.new_lens_out[b] = o.len;
+    const int r = parent_of(b), len = r < 0 ? 0 : clamp_len(p, p.lens[r], &bad);
+    bool wants = false;
+    if (len % p.page_size != 0) {
+      const int page = p.table[r * p.ld + len / p.page_size];
+      wants = static_cast<uint32_t>(page) < static_cast<uint32_t>(p.pages) &&
+              (p.refs[page] != 1 || first_child[r] != b);
+    }
+    need += wants;
+    p.row_begin[b] = wants ? 0 : -1;
+    p.new_lens_out[b] = len;
   }
-  // no page is taken before every row has seen its open page's count
-  cluster_sync();
-  take_free(p, pages, static_cast<int64_t>(free_before), static_cast<int64_t>(need_all), p.fresh);
-  cluster_sync();
-  const int lane = threadIdx.x & 31;
-  const int warp = blockIdx.x * (kTableThreads / 32) + (threadIdx.x >> 5);
-  const int64_t have = static_cast<int64_t>(free_all);
-  for (int64_t b = warp; b < p.n; b += kWarpsAll) {
+  const Sums sums = scan_all<C>(need, count_free(p, pages.from, pages.to));
+  unsigned long long at = sums.before[0];
+  // (-1: the row keeps its parent's pages as they are)
+  for (int64_t b = rows.from; b < rows.to; ++b)
+    if (p.row_begin[b] == 0) p.row_begin[b] = static_cast<int64_t>(at++);
+  // every row has seen its open page's count: the sums were made after it
+  if constexpr (C == 1) __syncthreads();
+  take_free(p, pages.from, pages.to, sums.before[1], sums.total[0]);
+  all_sync<C>();
+  const int64_t have = static_cast<int64_t>(sums.total[1]);
+  for (int64_t b = warp; b < p.n; b += C * kWarps) {
     const int r = parent_of(b), len = p.new_lens_out[b];
     const int n = pages_of(len, p.page_size);
     const int64_t k = p.row_begin[b];
@@ -256,19 +283,34 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kTableThreads
   }
   // a row's pages are held by its children instead of by itself; its open page by the first
   // child at most
-  for (int64_t r = warp; r < p.B; r += kWarpsAll) {
+  for (int64_t r = warp; r < p.B; r += C * kWarps) {
     const int len = clamp_len(p, p.lens[r], &bad);
     const int n = pages_of(len, p.page_size), full = len / p.page_size;
-    const int more = p.children[r] - 1;
+    const int more = children[r] - 1;
     const int* row = p.table + r * p.ld;
     if (more != 0)
       for (int i = lane; i < full; i += 32) add_ref(p, row[i], more, &bad);
     if (full < n && lane == 0) {
-      const bool kept = more >= 0 && p.row_begin[p.first_child[r]] < 0;
+      const bool kept = more >= 0 && p.row_begin[first_child[r]] < 0;
       if (!kept) add_ref(p, row[full], -1, &bad);
     }
   }
   if (bad) atomicOr(p.status, kStatusBadIndex);
+}
+
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kTableThreads)
+    resize_kernel(const PagesParams p) {
+  resize<kCluster>(p);
+}
+__global__ void __launch_bounds__(kTableThreads) resize_small_kernel(const PagesParams p) {
+  resize<1>(p);
+}
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kTableThreads)
+    fork_kernel(const PagesParams p) {
+  fork<kCluster>(p);
+}
+__global__ void __launch_bounds__(kTableThreads) fork_small_kernel(const PagesParams p) {
+  fork<1>(p);
 }
 
 // ------------------------------------------------------------------- moving rows
@@ -438,16 +480,25 @@ void spread(PagesParams* p, int64_t rows) {
 }
 }  // namespace
 
+// One block: rows of a warp each and pages of a few loads
+static bool small(const PagesParams& p, int64_t rows) {
+  return rows <= 64 && p.max_pages <= 1024 && p.pages <= 16384;
+}
+
 cudaError_t launch_resize_pages(const PagesParams& given, cudaStream_t stream) {
   PagesParams p = given;
   spread(&p, p.B);
-  return launch_k(resize_kernel, dim3(kCluster), dim3(kTableThreads), 0, stream, p);
+  return small(p, p.B)
+             ? launch_k(resize_small_kernel, dim3(1), dim3(kTableThreads), 0, stream, p)
+             : launch_k(resize_kernel, dim3(kCluster), dim3(kTableThreads), 0, stream, p);
 }
 
 cudaError_t launch_fork_pages(const PagesParams& given, cudaStream_t stream) {
   PagesParams p = given;
-  spread(&p, p.n > p.B ? p.n : p.B);
-  return launch_k(fork_kernel, dim3(kCluster), dim3(kTableThreads), 0, stream, p);
+  const int64_t rows = p.n > p.B ? p.n : p.B;
+  spread(&p, rows);
+  return small(p, rows) ? launch_k(fork_small_kernel, dim3(1), dim3(kTableThreads), 0, stream, p)
+                        : launch_k(fork_kernel, dim3(kCluster), dim3(kTableThreads), 0, stream, p);
 }
 
 cudaError_t launch_copy_pages(const MoveParams& p, int num_sms, cudaStream_t stream) {
