@@ -317,6 +317,7 @@ __global__ void __launch_bounds__(kTableThreads) fork_small_kernel(const PagesPa
 // A token's keys (or values) are `cols` pieces of 16 bytes: head h = col / per_head.
 constexpr int kMoveThreads = 256;
 constexpr int kDepth = 8;             // loads in flight a thread
+constexpr int kMinWidth = 2;          // columns of a block, at least: a sector
 
 struct Column {
   bool value;                         // of the values' cache
@@ -389,8 +390,12 @@ __global__ void __launch_bounds__(kMoveThreads) copy_pages_kernel(const MovePara
 // all are read before any is written.  As kept[i] >= i, what is read later lies behind all
 // that is written, so no block waits for another, and a long list of few sequences
 // is shared out by columns (down to 32 bytes).  HBM-bound where it is long.
-__global__ void __launch_bounds__(kMoveThreads) compact_kernel(const MoveParams p) {
-  extern __shared__ int2 places[];    // of a step's rows: from, then to (page, row of it)
+// kFind: rows of a step a thread, at most (1 where a block is 8 columns wide or more: registers
+// for three blocks an SM).
+template <int kFind>
+__global__ void __launch_bounds__(kMoveThreads, kFind == 1 ? 3 : 2)
+    compact_kernel(const MoveParams p) {
+  extern __shared__ int2 places[];    // [3] of a step's rows: from, then to (page, row of it)
   pdl_wait();
   pdl_launch_dependents();
   const int b = blockIdx.y;
@@ -407,54 +412,84 @@ __global__ void __launch_bounds__(kMoveThreads) compact_kernel(const MoveParams 
   bool bad = given != count || start < 0;
   const int* kept = p.kept + b * p.ld_kept;
   const int* table = p.table + b * p.ld;
+  // a key's page (not looked at here: it would be waited for) and its row of it; row -1: none
   auto place = [&](int64_t key) {
-    int2 at = make_int2(-1, 0);
     if (key >= slots) {
       bad = true;
-      return at;
+      return make_int2(0, -1);
     }
     const uint32_t k = static_cast<uint32_t>(key), s = static_cast<uint32_t>(p.page_size);
     const uint32_t n = k / s;
-    at = make_int2(table[n], static_cast<int>(k - n * s));
-    if (static_cast<uint32_t>(at.x) >= static_cast<uint32_t>(p.pages)) {
-      at.x = -1;
-      bad = true;
-    }
-    return at;
+    return make_int2(table[n], static_cast<int>(k - n * s));
   };
-  for (int i0 = 0; start >= 0 && i0 < count; i0 += step) {
-    const int n = min(step, count - i0);
-    for (int i = threadIdx.x; i < n; i += kMoveThreads) {
-      const int k = kept[i0 + i];
-      int2 from = make_int2(-1, 0), to = from;
+  auto there = [&](int2 at) {
+    if (at.y < 0) return false;
+    const bool ok = static_cast<uint32_t>(at.x) < static_cast<uint32_t>(p.pages);
+    if (!ok) bad = true;
+    return ok;
+  };
+  // Where the rows of a step come from and go to is found a step ahead, in one of three tables
+  // (one is being read by the stores of the step before), and the list is read two ahead.
+  int listed[kFind];
+  auto read_list = [&](int i0) {
+#pragma unroll
+    for (int f = 0; f < kFind; ++f) {
+      const int i = threadIdx.x + f * kMoveThreads;
+      if (i < min(step, count - i0)) listed[f] = kept[i0 + i];
+    }
+  };
+  auto find = [&](int i0, int which) {
+    int2* from = places + which * 2 * step;
+    int2 a[kFind], b[kFind];
+#pragma unroll
+    for (int f = 0; f < kFind; ++f) {
+      const int i = threadIdx.x + f * kMoveThreads;
+      a[f] = b[f] = make_int2(0, -1);
+      if (i >= min(step, count - i0)) continue;
+      const int k = listed[f];
       if (k < i0 + i) {
         bad = true;                   // would be overwritten before it is read
       } else if (k != i0 + i) {
-        from = place(static_cast<int64_t>(start) + k);
-        to = place(static_cast<int64_t>(start) + i0 + i);
+        a[f] = place(static_cast<int64_t>(start) + k);
+        b[f] = place(static_cast<int64_t>(start) + i0 + i);
       }
-      places[i] = from;
-      places[step + i] = to;
     }
+    read_list(i0 + step);
+#pragma unroll
+    for (int f = 0; f < kFind; ++f) {
+      const int i = threadIdx.x + f * kMoveThreads;
+      if (i < step) from[i] = a[f], from[step + i] = b[f];
+    }
+  };
+  if (start >= 0 && count > 0) {
+    read_list(0);
+    find(0, 0);
     __syncthreads();
+  }
+  int which = 0;
+  for (int i0 = 0; start >= 0 && i0 < count; i0 += step) {
+    const int2* from = places + which * 2 * step;
+    const int n = min(step, count - i0);
     uint4 v[kDepth];
 #pragma unroll
     for (int u = 0; u < kDepth; ++u) {
       const int i = u * rows + r0;
       if (!mine || i >= n) continue;
-      const int2 at = places[i];
-      if (at.x >= 0) v[u] = *reinterpret_cast<const uint4*>(base + at.x * sp + at.y * st);
+      const int2 at = from[i];
+      if (there(at)) v[u] = *reinterpret_cast<const uint4*>(base + at.x * sp + at.y * st);
     }
+    which = which == 2 ? 0 : which + 1;
+    find(i0 + step, which);
+    // all of the step is read, and what the next one reads lies behind what this one writes
     __syncthreads();
 #pragma unroll
     for (int u = 0; u < kDepth; ++u) {
       const int i = u * rows + r0;
       if (!mine || i >= n) continue;
-      const int2 from = places[i], to = places[step + i];
-      if (from.x >= 0 && to.x >= 0)
-        *reinterpret_cast<uint4*>(base + to.x * sp + to.y * st) = v[u];
+      const int2 a = from[i], b = from[step + i];
+      if (there(a) && there(b))
+        *reinterpret_cast<uint4*>(base + b.x * sp + b.y * st) = v[u];
     }
-    __syncthreads();
   }
   if (bad) atomicOr(p.status, kStatusBadIndex);
 }
@@ -521,10 +556,10 @@ cudaError_t launch_compact(const MoveParams& given, int num_sms, cudaStream_t st
   while (width > 2 && (static_cast<int64_t>(kMoveThreads / width) * kDepth < p.most)) width /= 2;
   auto blocks = [&](int w) { return (2 * static_cast<int64_t>(p.cols) + w - 1) / w * p.B; };
   if (width < 16) width = 16;
-  while (width > 2 && blocks(width) < num_sms) width /= 2;
+  while (width > kMinWidth && blocks(width) < num_sms) width /= 2;
   p.width = width;
-  const size_t smem = static_cast<size_t>(kMoveThreads / width) * kDepth * 2 * sizeof(int2);
-  return launch_k(compact_kernel,
+  const size_t smem = static_cast<size_t>(kMoveThreads / width) * kDepth * 6 * sizeof(int2);
+  return launch_k(width >= kDepth ? compact_kernel<1> : compact_kernel<kDepth / kMinWidth>,
                   dim3(static_cast<unsigned>(blocks(width) / p.B), static_cast<unsigned>(p.B)),
                   dim3(kMoveThreads), smem, stream, p);
 }
