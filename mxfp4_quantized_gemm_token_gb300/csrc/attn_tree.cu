@@ -431,6 +431,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeArgs a)
       }
       if (ok) put(TreePiece{});
     }
+    __syncwarp();
   } else if (FP8 && warp >= kLoadWarp + L::kFetchers) {
     // ------------------------------------------------- e4m3 rows to f16
     if constexpr (FP8) {

@@ -30,7 +30,8 @@ TREE = dict(q=P, sq_t=512, sq_h=64, T=7, Hq=8, Hkv=2, D=64, k_cache=P, v_cache=P
     (dict(q=P + 8), UNSUPPORTED), (dict(out=None), INVALID), (dict(so_h=60), INVALID),
     (dict(dtype=7), UNSUPPORTED), (dict(k_scale=P), INVALID), (dict(ckh=68), UNSUPPORTED),
     (dict(dtype=_lib.E4M3, ckh=72), UNSUPPORTED), (dict(v_cache=None), INVALID),
-    (dict(k_cache=P + 8), UNSUPPORTED)])
+    (dict(k_cache=P + 8), UNSUPPORTED), (dict(ckp=1 << 35), UNSUPPORTED),
+    (dict(cvt=1 << 36), UNSUPPORTED)])
 def test_tree(changed, status):
     lib = _lib.load()
     args = dict(TREE)

@@ -463,3 +463,24 @@ def test_a_verified_tree_end_to_end():
             r = attend(q[9 * b + 8:9 * b + 9, h], kk[:, h // 4], vv[:, h // 4], seen, D ** -0.5)
             assert_within(got[b:b + 1, h], r[0], r[2], "decode")
             assert_within(out[9 * b + 8:9 * b + 9, h], r[0], r[2], "tree")
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("nq,lens", [([16], [3000]), ([64, 3], [500, 40])])
+def test_stalled_loads_time_out_and_recover(nq, lens, fp8):
+    """With the test-only switch nothing is loaded: every wait runs out, the status
+    says so, and the next call is right."""
+    c = Case(nq, lens, 8, 2, 128, fp8=fp8, seed=23)
+    mxq.sync_status()
+    old = mxq.get_option(_lib.OPT_WAIT_BUDGET_NS)
+    try:
+        mxq.set_option(_lib.OPT_WAIT_BUDGET_NS, 20_000_000)
+        mxq.set_option(_lib.OPT_INJECT_STALL, 1)
+        c.call()
+        with pytest.raises(mxq.MxqError) as e:
+            mxq.sync_status()
+        assert e.value.status == _lib.ERR_TIMEOUT
+    finally:
+        mxq.set_option(_lib.OPT_INJECT_STALL, 0)
+        mxq.set_option(_lib.OPT_WAIT_BUDGET_NS, old)
+    c.check()
