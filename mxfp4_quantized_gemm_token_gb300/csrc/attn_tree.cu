@@ -1077,24 +1077,59 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeArgs a)
 // Joins the partial results of an item that several parts share, in the parts' order:
 // out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i.  D / 4 lanes take two rows, four columns
 // each, reading four parts of both at a time: what counts is one chain of loads.  (A warp a row:
-// 16 us for two chunks of 300 rows.)
+// 16 us for two chunks of 300 rows.)  A block's y is its rows, its x the head and the part that
+// begins the item.  kSplit: few rows, whose parts the block's warps share, and few items, so that x
+// counts those that are shared (one tree over 20000 keys in 19 parts: 25.7 us, without 35.6; finding
+// them costs 64 ragged sequences 4 us).
 constexpr int kJoinWarps = 4;
 template <int D>
 struct JoinShape {
   static constexpr int kLPR = D / 4, kRPW = 2 * (32 / kLPR);      // rows of a warp
 };
-template <int D>
+struct JoinSum {
+  float m = -INFINITY, l = 0.f;
+  float4 o = {0.f, 0.f, 0.f, 0.f};
+  __device__ __forceinline__ void add(float2 ml, float4 v) {
+    // a part whose scores are all NaN has no reference, but a sum: it counts
+    const float n = fmaxf(m, ml.x), at = n == -INFINITY ? 0.f : n;
+    const float f = ex2(m - at), k = ex2(ml.x - at);
+    l = l * f + ml.y * k;
+    o.x = o.x * f + v.x * k;
+    o.y = o.y * f + v.y * k;
+    o.z = o.z * f + v.z * k;
+    o.w = o.w * f + v.w * k;
+    m = n;
+  }
+};
+template <int D, bool kSplit>
 __global__ void __launch_bounds__(32 * kJoinWarps) tree_join_kernel(const TreeArgs a) {
   using S = JoinShape<D>;
   constexpr int U = 4;
   const TreeParams& p = a.p;
+  __shared__ float4 so[kSplit ? kJoinWarps : 1][2][32];
+  __shared__ float2 sml[kSplit ? kJoinWarps : 1][2][32];
   pdl_wait();
   pdl_launch_dependents();
-  const TreeJoin j = a.joins[blockIdx.x];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int hk = blockIdx.x % p.Hkv;
+  // the part that begins the item
+  int which = blockIdx.x / p.Hkv, begins = kSplit ? -1 : which;
+  for (int w = 0; w < a.parts && begins < 0; w += 32) {
+    const bool one = w + lane < a.parts && a.joins[(w + lane) * p.Hkv + hk].ntok > 0;
+    uint32_t mask = __ballot_sync(0xffffffffu, one);
+    const int n = __popc(mask);
+    if (which < n) {
+      for (; which > 0; --which) mask &= mask - 1;
+      begins = w + __ffs(mask) - 1;
+    }
+    which -= n;
+  }
+  if (begins < 0) return;
+  const TreeJoin j = a.joins[begins * p.Hkv + hk];
   if (j.ntok == 0) return;
-  const int lane = threadIdx.x & 31, hk = blockIdx.x % p.Hkv;
   const int col = 4 * (lane % S::kLPR);
-  const int row0 = (blockIdx.y * kJoinWarps + (threadIdx.x >> 5)) * S::kRPW + 2 * (lane / S::kLPR);
+  const int row0 = (kSplit ? blockIdx.y : blockIdx.y * kJoinWarps + warp) * S::kRPW +
+                   2 * (lane / S::kLPR);
   bool valid[2];
   int token[2], head[2];
 #pragma unroll
@@ -1102,52 +1137,58 @@ __global__ void __launch_bounds__(32 * kJoinWarps) tree_join_kernel(const TreeAr
     const int row = row0 + r, s = row / kBM, in = row - s * kBM, tok = in / a.G;
     token[r] = s * a.TB + tok;
     head[r] = hk * a.G + in - tok * a.G;
-    valid[r] = tok < a.TB && token[r] < j.ntok;
+    valid[r] = row < kRows && tok < a.TB && token[r] < j.ntok;
   }
-  if (!valid[0] && !valid[1]) return;
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-  float4 o[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
-  for (int w = j.w0; w <= j.w1; w += U) {
+  JoinSum sum[2];
+  const int step = kSplit ? kJoinWarps : 1;
+  for (int w = j.w0 + (kSplit ? warp : 0); w <= j.w1; w += U * step) {
     float2 ml[U][2];
     float4 v[U][2];
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        if (w + u > j.w1 || !valid[r]) continue;
-        const int64_t task = static_cast<int64_t>(w + u) * p.Hkv + hk;
-        const int64_t slot = (task * 2 + (w + u == j.w0 ? j.first : 0)) * kRows + row0 + r;
+        const int k = w + u * step;
+        if (k > j.w1 || !valid[r]) continue;
+        const int64_t task = static_cast<int64_t>(k) * p.Hkv + hk;
+        const int64_t slot = (task * 2 + (k == j.w0 ? j.first : 0)) * kRows + row0 + r;
         ml[u][r] = a.part_ml[slot];
         v[u][r] = *reinterpret_cast<const float4*>(a.part_o + slot * D + col);
       }
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        if (w + u > j.w1 || !valid[r]) continue;
-        // a part whose scores are all NaN has no reference, but a sum: it counts
-        const float n = fmaxf(m[r], ml[u][r].x), at = n == -INFINITY ? 0.f : n;
-        const float f = ex2(m[r] - at), k = ex2(ml[u][r].x - at);
-        l[r] = l[r] * f + ml[u][r].y * k;
-        o[r].x = o[r].x * f + v[u][r].x * k;
-        o[r].y = o[r].y * f + v[u][r].y * k;
-        o[r].z = o[r].z * f + v[u][r].z * k;
-        o[r].w = o[r].w * f + v[u][r].w * k;
-        m[r] = n;
-      }
+      for (int r = 0; r < 2; ++r)
+        if (w + u * step <= j.w1 && valid[r]) sum[r].add(ml[u][r], v[u][r]);
+  }
+  if constexpr (kSplit) {
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      sml[warp][r][lane] = make_float2(sum[r].m, sum[r].l);
+      so[warp][r][lane] = sum[r].o;
+    }
+    __syncthreads();
+    if (warp > 0) return;
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+#pragma unroll
+      for (int w = 1; w < kJoinWarps; ++w) sum[r].add(sml[w][r][lane], so[w][r][lane]);
   }
   const float vs = p.v_scale != nullptr ? __ldg(p.v_scale + hk) : 1.f;
 #pragma unroll
   for (int r = 0; r < 2; ++r) {
     if (!valid[r]) continue;
     const int64_t tokr = static_cast<int64_t>(j.q_row) + token[r];
-    const RowEnd end = finish_row(m[r] * kLn2, l[r], p.sinks ? p.sinks + head[r] : nullptr);
+    const float4 o = sum[r].o;
+    const RowEnd end =
+        finish_row(sum[r].m * kLn2, sum[r].l, p.sinks ? p.sinks + head[r] : nullptr);
     const float f = end.factor * vs;
     __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + tokr * p.o_t +
                          static_cast<int64_t>(head[r]) * p.o_h + col;
-    *reinterpret_cast<uint2*>(dst) =
-        end.none ? make_uint2(0u, 0u)
-                 : make_uint2(bf16x2(o[r].x * f, o[r].y * f), bf16x2(o[r].z * f, o[r].w * f));
+    *reinterpret_cast<uint2*>(dst) = end.none
+                                         ? make_uint2(0u, 0u)
+                                         : make_uint2(bf16x2(o.x * f, o.y * f),
+                                                      bf16x2(o.z * f, o.w * f));
     if (p.lse != nullptr && col == 0) p.lse[tokr * p.Hq + head[r]] = end.lse;
   }
 }
@@ -1183,11 +1224,18 @@ cudaError_t launch(const TreeArgs& a, int num_sms, cudaStream_t stream) {
   e = launch_k(tree_kernel<D, FP8>, dim3(std::min(tasks, num_sms)), dim3(kTreeThreads),
                static_cast<size_t>(smem), stream, a);
   if (e != cudaSuccess || a.all_whole) return e;
-  // rows that an item can have
+  // rows that an item can have, and items that parts may share
   const int64_t T = a.p.T;
   const int rows = T > a.TB ? kRows : static_cast<int>(T) * a.G;
-  constexpr int kPerBlock = kJoinWarps * JoinShape<D>::kRPW;
-  return launch_k(tree_join_kernel<D>, dim3(tasks, (rows + kPerBlock - 1) / kPerBlock),
+  const int64_t items = std::min<int64_t>(a.parts, T / (2 * a.TB) + a.p.B);
+  constexpr int kRPW = JoinShape<D>::kRPW, kPerBlock = kJoinWarps * kRPW;
+  const unsigned fine = static_cast<unsigned>((rows + kRPW - 1) / kRPW);
+  if (items * a.p.Hkv * fine <= 8 * num_sms)
+    return launch_k(tree_join_kernel<D, true>,
+                    dim3(static_cast<unsigned>(items * a.p.Hkv), fine), dim3(32 * kJoinWarps), 0,
+                    stream, a);
+  return launch_k(tree_join_kernel<D, false>,
+                  dim3(static_cast<unsigned>(tasks), static_cast<unsigned>((rows + kPerBlock - 1) / kPerBlock)),
                   dim3(32 * kJoinWarps), 0, stream, a);
 }
 
