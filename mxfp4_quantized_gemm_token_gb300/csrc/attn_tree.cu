@@ -60,6 +60,7 @@ static_assert(2 * kSoftmaxRegs + 2 * kOtherRegs <= 4 * 128, "register split abov
 constexpr int kPieces = 8;           // pieces of items that may be under way
 constexpr int kSeen = 16;            // blocks whose masks of loaded keys are kept: some 10 are in use
 constexpr int kWhole = 2;            // items of at most this many blocks stay whole
+constexpr int kAloneSequences = 32;    // calls of at most this many: one warp cuts the line
 constexpr int kAllWhole = 3;         // calls whose items have at most this many: all do
 
 // What joins an item that several parts share: written by the CTA that begins it.
@@ -293,79 +294,98 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeArgs a)
   pdl_wait();
   pdl_launch_dependents();
 
-  // ---- the line, and this CTA's part of it
-  const int per_thread = (p.B + kTreeThreads - 1) / kTreeThreads;
-  const int b0 = threadIdx.x * per_thread, b1 = min(p.B, b0 + per_thread);
-  auto seq = [&](int b) { return tree_seq(p, p.cu_q[b], p.cu_q[b + 1], p.seq_lens[b]); };
-  unsigned long long mine = 0;
-  int longest = 0;
-  TreeSeq kept = {0, 0, 0, false};    // where a thread has one sequence, it is read once
-  for (int b = b0; b < b1; ++b) {
-    const TreeSeq s = seq(b);
-    kept = s;
-    if (s.bad && blockIdx.x == 0) atomicOr(p.status, kStatusBadIndex);
-    for (int i = 0; i * 2 * a.TB < s.nq; ++i) {
-      const int cost = item_cost<D>(a, tree_item(a, s, i));
-      mine += cost;
-      longest = max(longest, cost);
-    }
-  }
-  longest = __reduce_max_sync(0xffffffffu, longest);
-  unsigned long long incl = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const unsigned long long y = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += y;
-  }
-  if (lane == 31) warp_sum[warp] = incl, warp_longest[warp] = longest;
+  // The barriers and the tensor memory are there.
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  int64_t before = static_cast<int64_t>(incl - mine), total = 0;
-  for (int w = 0; w < kTreeWarps; ++w) {
-    if (w < warp) before += static_cast<int64_t>(warp_sum[w]);
-    total += static_cast<int64_t>(warp_sum[w]);
-    longest = max(longest, warp_longest[w]);
-  }
-  int64_t per = max(divide(total + a.parts - 1, a.parts), static_cast<int64_t>(kMinCost));
-  // where all stay whole, a part has room for the longest, or some would get two
-  if (a.all_whole && per < longest) per = longest;
+
+  // ---- the line, and this CTA's part of it: found by the warp that needs it, where a lane has
+  // few sequences (no word to the other warps: a tree over 1500 keys 13.6 us, by the whole
+  // block 14.2), or by all
+  const bool alone = p.B <= kAloneSequences;
   const int part = static_cast<int>(blockIdx.x) / p.Hkv;
-  const int64_t raw0 = part * per;
-  if (threadIdx.x < 2) ends[threadIdx.x][0] = p.B, ends[threadIdx.x][1] = ends[threadIdx.x][2] = 0;
-  __syncthreads();
-  // The thread that holds an end of the part finds its item and the block there; inside an item
-  // that stays whole it is the nearer end of it.
-  for (int end = 0; end < 2; ++end) {
-    const int64_t pos = raw0 + end * per;
-    if (pos < before || pos >= before + static_cast<int64_t>(mine)) continue;
-    int64_t at = before;
-    bool found = false;
-    for (int b = b0; b < b1 && !found; ++b) {
-      const TreeSeq s = per_thread == 1 ? kept : seq(b);
-      for (int i = 0; i * 2 * a.TB < s.nq && !found; ++i) {
-        const TreeItem it = tree_item(a, s, i);
-        const int cost = item_cost<D>(a, it);
-        if (at + cost <= pos) {
-          at += cost;
-          continue;
-        }
-        found = true;
-        const int in = max(0, static_cast<int>(pos - at) - kItemCost);
-        int off = in / block_cost<D>(a, it);
-        if (a.all_whole || it.n <= kWhole) off = 2 * off >= it.n && off > 0 ? it.n : 0;
-        ends[end][0] = b, ends[end][1] = i, ends[end][2] = off;
-        if (end == 0) {
-          start_at = at;
-          start_seq = s;
-          // on its way: the page of its last keys
-          if (s.len > 0) prefetch(p.page_table + b * p.ld_table + (s.len - 1) / p.page_size);
+  int64_t per = 0, raw0 = 0;
+  auto seq = [&](int b) { return tree_seq(p, p.cu_q[b], p.cu_q[b + 1], p.seq_lens[b]); };
+  auto sync = [&]() {
+    if (alone)
+      __syncwarp();
+    else
+      __syncthreads();
+  };
+  if (!alone || warp == kWalkWarp) {
+    const int team = alone ? 32 : kTreeThreads, me = alone ? lane : threadIdx.x;
+    const int per_thread = (p.B + team - 1) / team;
+    const int b0 = me * per_thread, b1 = min(p.B, b0 + per_thread);
+    unsigned long long mine = 0;
+    int longest = 0;
+    TreeSeq kept = {0, 0, 0, false};  // where a thread has one sequence, it is read once
+    for (int b = b0; b < b1; ++b) {
+      const TreeSeq s = seq(b);
+      kept = s;
+      if (s.bad && blockIdx.x == 0) atomicOr(p.status, kStatusBadIndex);
+      for (int i = 0; i * 2 * a.TB < s.nq; ++i) {
+        const int cost = item_cost<D>(a, tree_item(a, s, i));
+        mine += cost;
+        longest = max(longest, cost);
+      }
+    }
+    longest = __reduce_max_sync(0xffffffffu, longest);
+    unsigned long long incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned long long y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    if (me < 2) ends[me][0] = p.B, ends[me][1] = ends[me][2] = 0;
+    if (!alone && lane == 31) warp_sum[warp] = incl, warp_longest[warp] = longest;
+    sync();
+    int64_t before = static_cast<int64_t>(incl - mine), total = 0;
+    if (alone) {
+      total = static_cast<int64_t>(__shfl_sync(0xffffffffu, incl, 31));
+    } else {
+      for (int w = 0; w < kTreeWarps; ++w) {
+        if (w < warp) before += static_cast<int64_t>(warp_sum[w]);
+        total += static_cast<int64_t>(warp_sum[w]);
+        longest = max(longest, warp_longest[w]);
+      }
+    }
+    per = max(divide(total + a.parts - 1, a.parts), static_cast<int64_t>(kMinCost));
+    // where all stay whole, a part has room for the longest, or some would get two
+    if (a.all_whole && per < longest) per = longest;
+    raw0 = part * per;
+    // The thread that holds an end of the part finds its item and the block there; inside an item
+    // that stays whole it is the nearer end of it.
+    for (int end = 0; end < 2; ++end) {
+      const int64_t pos = raw0 + end * per;
+      if (pos < before || pos >= before + static_cast<int64_t>(mine)) continue;
+      int64_t at = before;
+      bool found = false;
+      for (int b = b0; b < b1 && !found; ++b) {
+        const TreeSeq s = per_thread == 1 ? kept : seq(b);
+        for (int i = 0; i * 2 * a.TB < s.nq && !found; ++i) {
+          const TreeItem it = tree_item(a, s, i);
+          const int cost = item_cost<D>(a, it);
+          if (at + cost <= pos) {
+            at += cost;
+            continue;
+          }
+          found = true;
+          const int in = max(0, static_cast<int>(pos - at) - kItemCost);
+          int off = in / block_cost<D>(a, it);
+          if (a.all_whole || it.n <= kWhole) off = 2 * off >= it.n && off > 0 ? it.n : 0;
+          ends[end][0] = b, ends[end][1] = i, ends[end][2] = off;
+          if (end == 0) {
+            start_at = at;
+            start_seq = s;
+            // on its way: the page of its last keys
+            if (s.len > 0) prefetch(p.page_table + b * p.ld_table + (s.len - 1) / p.page_size);
+          }
         }
       }
     }
+    sync();
   }
-  __syncthreads();
   const int tasks = a.parts * p.Hkv;
 
   Pieces pieces(piece_ring, piece_full, piece_empty);
