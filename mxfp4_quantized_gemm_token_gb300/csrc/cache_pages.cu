@@ -391,9 +391,9 @@ __global__ void __launch_bounds__(kMoveThreads) copy_pages_kernel(const MovePara
 // that is written, so no block waits for another, and a long list of few sequences
 // is shared out by columns (down to 32 bytes).  HBM-bound where it is long.
 // kFind: rows of a step a thread, at most (1 where a block is 8 columns wide or more: registers
-// for three blocks an SM).
+// for two blocks an SM).
 template <int kFind>
-__global__ void __launch_bounds__(kMoveThreads, kFind == 1 ? 3 : 2)
+__global__ void __launch_bounds__(kMoveThreads, kFind == 1 ? 2 : 1)
     compact_kernel(const MoveParams p) {
   extern __shared__ int2 places[];    // [3] of a step's rows: from, then to (page, row of it)
   pdl_wait();
@@ -461,34 +461,48 @@ __global__ void __launch_bounds__(kMoveThreads, kFind == 1 ? 3 : 2)
       if (i < step) from[i] = a[f], from[step + i] = b[f];
     }
   };
-  if (start >= 0 && count > 0) {
-    read_list(0);
-    find(0, 0);
-    __syncthreads();
-  }
-  int which = 0;
-  for (int i0 = 0; start >= 0 && i0 < count; i0 += step) {
+  auto load = [&](uint4* v, int i0, int which) {
     const int2* from = places + which * 2 * step;
-    const int n = min(step, count - i0);
-    uint4 v[kDepth];
 #pragma unroll
     for (int u = 0; u < kDepth; ++u) {
       const int i = u * rows + r0;
-      if (!mine || i >= n) continue;
+      if (!mine || i >= min(step, count - i0)) continue;
       const int2 at = from[i];
       if (there(at)) v[u] = *reinterpret_cast<const uint4*>(base + at.x * sp + at.y * st);
     }
-    which = which == 2 ? 0 : which + 1;
-    find(i0 + step, which);
-    // all of the step is read, and what the next one reads lies behind what this one writes
-    __syncthreads();
+  };
+  auto store = [&](const uint4* v, int i0, int which) {
+    const int2* from = places + which * 2 * step;
 #pragma unroll
     for (int u = 0; u < kDepth; ++u) {
       const int i = u * rows + r0;
-      if (!mine || i >= n) continue;
+      if (!mine || i >= min(step, count - i0)) continue;
       const int2 a = from[i], b = from[step + i];
-      if (there(a) && there(b))
-        *reinterpret_cast<uint4*>(base + b.x * sp + b.y * st) = v[u];
+      if (there(a) && there(b)) *reinterpret_cast<uint4*>(base + b.x * sp + b.y * st) = v[u];
+    }
+  };
+  if (start >= 0 && count > 0) {
+    uint4 v[kDepth], w[kDepth];
+    read_list(0);
+    find(0, 0);
+    __syncthreads();
+    load(v, 0, 0);
+    find(step, 1);
+    __syncthreads();
+    // Of the step, all is read before the barrier and written behind it; the next one's rows,
+    // which lie behind all that is written here, are on their way meanwhile.
+    int which = 0;
+    auto turn = [&](const uint4* now, uint4* next, int i0) {
+      const int ahead = which == 2 ? 0 : which + 1, far = ahead == 2 ? 0 : ahead + 1;
+      load(next, i0 + step, ahead);
+      store(now, i0, which);
+      find(i0 + 2 * step, far);
+      __syncthreads();
+      which = ahead;
+    };
+    for (int i0 = 0; i0 < count; i0 += 2 * step) {
+      turn(v, w, i0);
+      if (i0 + step < count) turn(w, v, i0 + step);
     }
   }
   if (bad) atomicOr(p.status, kStatusBadIndex);
