@@ -42,7 +42,8 @@
 // are half as long: the 64 sequences 91 us, 5.7 TB/s, in e4m3 66 us, 4.0 TB/s; the 16 in
 // e4m3 78 us, 4.2 TB/s.  One sequence of 1500 keys: 10.4 us; 128 sequences with a window
 // of 128 keys, D 64: 13.9 us: there the chain length -> page -> key, a load each, and the
-// launches count.
+// launches count.  A window of 2048 keys with 100 first keys, 96 sequences of 1-16384: 122 us, 6.2
+// TB/s; of 1024 with 4, one sequence: 10.0 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math.h>

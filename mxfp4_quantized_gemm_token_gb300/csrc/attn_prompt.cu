@@ -46,7 +46,9 @@
 // at D 64 ~2500 against 1280, and the same prompt takes 276 us (141 at the burst rate).
 // 11 packed prompts of 8192 tokens: 80 us (42 at the burst rate), 65 at D 64 (21); here an
 // item's beginning and end count, ~2 us.  Two chunks of 300 rows over 7892 keys, in pieces:
-// 71 us (40).  One prompt of 2048 tokens is cut into pieces too: 65 us (18).
+// 71 us (40).  One prompt of 2048 tokens is cut into pieces too: 65 us (18).  Blocks between first
+// keys that stay visible and the window are left out: 5 prompts of 8192 tokens, a window of 1024 and
+// 16 first keys, 101 us (54).
 #include <cuda_bf16.h>
 #include <math.h>
 

@@ -21,7 +21,7 @@
 //   warp 8           issues the MMAs
 //   warp 9           finds the pieces of items that the CTA works on
 //   warps 10-15      load keys and values with 16-byte asynchronous copies, row by row, as pages
-//                    are of any size; e4m3 is converted to f16 (exact) on its way
+//                    are of any size; for an e4m3 cache two of them, and four convert to f16 (exact)
 // S0, S1, O0 and O1 are in tensor memory, P takes the place of S.  The reference a
 // row subtracts is raised only when its maximum grows by more than 2^8.
 //   bf16 cache: bf16 products.  e4m3 cache: f16 products, q scaled per row by a power of two to
@@ -30,10 +30,18 @@
 // A row's path is followed while its blocks are taken, from the last key down: the thread holds
 // the next ancestor, and a block's part of the path becomes a bit mask.
 //
-// Work.  The key blocks of all items form one line, cut into equal parts; a (part, key/value
-// head) pair is one CTA's, the heads of a part at work at the same time.  Items that parts share
-// leave at most two partial results per CTA in the workspace, which a second kernel joins in
+// Work.  The key blocks of all items form one line, cut into parts of equal cost; a (part,
+// key/value head) pair is one CTA's, the heads of a part at work at the same time.  Items that parts
+// share leave at most two partial results per CTA in the workspace, which a second kernel joins in
 // a fixed order.  A part's end inside a short item moves to the nearer end of it.
+//
+// Measured.  64 sequences of 5-8192 keys with trees of up to 32, 32 / 8 heads of 128, bf16: 185 us
+// (179 before the join: 6.0 TB/s of keys and values, 90 % of a plain copy's rate); 16 sequences of
+// 9000-32768 keys with 16 rows, 64 / 8 heads: 202 us, 6.4 TB/s, at D 64 126 us.  What bounds the
+// rest: of two tiles (32 rows of those) the chain scores -> maximum -> weights -> product, ~3900
+// cycles a block against 2048 of products: 268 us; with e4m3 the conversion's warps and that chain
+// (16 rows 192 us, 32 rows 300, up to 48 rows 409).  One tree over 1500 keys: 13.6 us, half of it
+// launches, the chain length -> page -> key, and a call's first use of each instruction.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math.h>

@@ -17,7 +17,8 @@ namespace {
 // cluster's barrier takes a fraction of a launch, and a table and its counts are small (64K
 // pages: 256 KB).  Latency-bound: chains of loads and barriers, so a step's two sums are made
 // together, and what a thread finds out about its rows it leaves for itself in the workspace.
-// A single block where rows, entries and pages are few.
+// A single block where rows, entries and pages are few.  Fork of 64 x 4 beams of ~2000 tokens: 9 us,
+// of 2 x 4 beams 5.7 (a cluster 11.6, a single block for the former 20); resize 6.5 and 3.4.
 constexpr int kCluster = 8;
 constexpr int kTableThreads = 1024;
 constexpr int kWarps = kTableThreads / 32;
@@ -377,7 +378,9 @@ __global__ void __launch_bounds__(kMoveThreads) copy_pages_kernel(const MovePara
 // `width` columns of a sequence and takes its rows in turn, kDepth x 256 / width at a time:
 // all are read before any is written.  As kept[i] >= i, what is read later lies behind all
 // that is written, so no block waits for another, and a long list of few sequences
-// is shared out by columns (down to 32 bytes).  HBM-bound where it is long.
+// is shared out by columns (down to 32 bytes).  HBM-bound where it is long: 4096 of
+// 9000-16384 keys of 8 sequences, 8 heads of 128, 52 us (78 % of a copy's rate), half of the keys of
+// one sequence of 16384 29 us (34 %: 32 bytes of each row a block).
 // kFind: rows of a step a thread, at most (1 where a block is 8 columns wide or more: registers
 // for two blocks an SM).
 template <int kFind>
