@@ -575,6 +575,7 @@ mxq_status mxq_attention_varlen_workspace_size(int64_t Tq, int64_t B, int32_t Hq
  * page_size] (clamped), offsets that decrease or leave [0, T] and sequences of fewer
  * keys than rows (left out, their rows not written), parents that are not
  * earlier rows (taken as -1) and pages outside [0, pages) (their keys are not seen).
+ * Where the other sequences then overlap, it is not defined whose rows are written.
  * Page and token strides of 2^35 elements or more give MXQ_ERR_UNSUPPORTED.
  * B == 0 or T == 0 is a no-op.
  */

@@ -171,7 +171,8 @@ def test_windows(window, first, kind, fp8):
     ([2] * 70, [150 + 40 * i for i in range(70)], 4, 4, 128),
     ([64] * 5, [3000, 100, 64, 2000, 700], 64, 8, 128),
     ([1] * 400, [1 + i % 97 for i in range(400)], 2, 1, 64),
-    ([700], [2500], 16, 2, 64)])
+    ([700], [2500], 16, 2, 64), ([5, 9], [300, 140], 200, 200, 64),
+    ([4100, 30], [4500, 3000], 2, 1, 64)])
 @pytest.mark.parametrize("fp8", [False, True])
 def test_long_and_many(nq, lens, H, KV, D, fp8):
     Case(nq, lens, H, KV, D, 16, fp8=fp8, seed=7).check()
@@ -368,6 +369,16 @@ def test_rows_outside_every_sequence_stay():
     mxq.sync_status()
     assert torch.equal(out[2:9], want)
     assert bool((out[:2] == 5).all()) and bool((out[9:] == 5).all())
+
+
+def test_sequences_without_keys_or_a_table():
+    q = torch.zeros(3, 4, 64, dtype=torch.bfloat16, device="cuda")
+    kc = torch.zeros(2, 16, 2, 64, dtype=torch.bfloat16, device="cuda")
+    out = torch.full_like(q, 5.0)
+    table = torch.zeros(2, 0, dtype=torch.int32, device="cuda")
+    mxq.paged_attention_tree(q, kc, kc, table, ints([0, 0]), ints([0, 0, 0]), out=out)
+    mxq.sync_status()
+    assert bool((out == 5).all())
 
 
 def test_empty_calls():
