@@ -37,10 +37,10 @@
 //
 // Measured.  64 sequences of 5-8192 keys with trees of up to 32, 32 / 8 heads of 128, bf16: 185 us
 // (179 before the join: 6.0 TB/s of keys and values, 90 % of a plain copy's rate); 16 sequences of
-// 9000-32768 keys with 16 rows, 64 / 8 heads: 202 us, 6.4 TB/s, at D 64 126 us.  What bounds the
+// 9000-32768 keys with 16 rows, 64 / 8 heads: 202 us, 6.4 TB/s, at D 64 125 us.  What bounds the
 // rest: of two tiles (32 rows of those) the chain scores -> maximum -> weights -> product, ~3900
-// cycles a block against 2048 of products: 268 us; with e4m3 the conversion's warps and that chain
-// (16 rows 192 us, 32 rows 300, up to 48 rows 409).  One tree over 1500 keys: 13.6 us, half of it
+// cycles a block against 2048 of products: 266 us; with e4m3 the conversion's warps and that chain
+// (16 rows 202 us, 32 rows 287, up to 48 rows 386).  One tree over 1500 keys: 13.6 us, half of it
 // launches, the chain length -> page -> key, and a call's first use of each instruction.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -104,6 +104,11 @@ struct TreeLayout {
   static constexpr int kRPI = 32 / kLPR;                 // rows a copy instruction
   static constexpr int kCopies = 32 / kRPI;              // copies a thread for 32 rows
   static constexpr int kStages = FP8 ? (D == 128 ? 3 : 6) : (D == 128 ? 5 : 10);
+  // Beside the warps that convert e4m3 rows of 128 the instructions' supply is short: there a mask
+  // is written to the scores in a pass of its own, and the weights' code stands once for both
+  // halves (16 long e4m3 sequences 400 -> 386 us; bf16 is up to 3 % slower so, e4m3 at D 64 146 us
+  // instead of 139).
+  static constexpr bool kRolled = FP8 && D == 128;
   static constexpr int kLoaders = 6;                     // warps that load
   // e4m3: two of them copy rows as they are cached into stages of their own, the other four
   // convert a quarter of each to f16 (all six doing both took 253 us for 16 long sequences of 16
@@ -907,6 +912,21 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeArgs a)
 #pragma unroll
             for (int q = 0; q < 4; ++q) vis[q] &= own[q];
             __syncwarp();
+            if constexpr (L::kRolled) {
+#pragma unroll 1
+              for (int q = 0; q < 4; ++q) {
+                const uint32_t word = q < 2 ? vis[q == 0 ? 0 : 1] : vis[q == 2 ? 2 : 3];
+                if (__all_sync(0xffffffffu, word == 0xffffffffu)) continue;
+                float y[32];
+                tmem_ld32(tS + 32 * q, y);
+                uint32_t z[32];
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                  z[e] = __float_as_uint((word >> e) & 1 ? y[e] : -INFINITY);
+                tmem_st32(tS + 32 * q, z);
+              }
+              tmem_st_wait();
+            }
           }
           // 64 scores, those that the mask hides as -inf, and their maximum
           auto scores = [&](float* x, int half) {
@@ -914,7 +934,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeArgs a)
             tmem_ld32_async(tS + 64 * half + 32, x + 32);
             tmem_wait32(x);
             tmem_wait32(x + 32);
-            if (masked) {
+            if (!L::kRolled && masked) {
 #pragma unroll
               for (int e = 0; e < 64; ++e)
                 x[e] = (vis[2 * half + (e >> 5)] >> (e & 31)) & 1 ? x[e] : -INFINITY;
@@ -976,16 +996,28 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeArgs a)
             __syncwarp();
             if (lane == 0) mbar_arrive(&p_full[2 * s + half]);
           };
-          uint32_t w[32];
-          weights(w, x);
-          weights(w + 16, x + 32);
-          tmem_st32(tS + 64, w);
-          scores(x, 0);
-          hand_over(1);
-          weights(w, x);
-          weights(w + 16, x + 32);
-          tmem_st32(tS, w);
-          hand_over(0);
+          if constexpr (L::kRolled) {
+#pragma unroll 1
+            for (int half = 1; half >= 0; --half) {
+              uint32_t w[32];
+              scores(x, half);
+              weights(w, x);
+              weights(w + 16, x + 32);
+              tmem_st32(tS + 64 * half, w);
+              hand_over(half);
+            }
+          } else {
+            uint32_t w[32];
+            weights(w, x);
+            weights(w + 16, x + 32);
+            tmem_st32(tS + 64, w);
+            scores(x, 0);
+            hand_over(1);
+            weights(w, x);
+            weights(w + 16, x + 32);
+            tmem_st32(tS, w);
+            hand_over(0);
+          }
           float y, z;
           unpack2(add2(sum[0], sum[1]), &y, &z);
           l += y + z;

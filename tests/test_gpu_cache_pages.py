@@ -327,3 +327,20 @@ def test_a_captured_step_replays():
         table, refs = ref.resize(new, new_lens, lens, refs, size)
         assert t.tolist() == table and n.tolist() == lens and r.tolist() == refs
     assert torch.equal(bits(k), bits(wk)) and torch.equal(bits(v), bits(wv))
+
+
+def test_rows_past_32_bits():
+    """Copies and compaction in a cache of more than 2^32 elements."""
+    pages, size, heads, dim = 70, 16, 2, 64
+    flat = torch.empty(pages << 26, dtype=torch.bfloat16, device="cuda")      # 4.7e9 elements
+    k, v = (flat.as_strided((pages, size, heads, dim), (1 << 26, heads * dim, dim, 1),
+                            half << 25) for half in range(2))
+    sk, sv = caches(pages, size, heads, dim, torch.bfloat16, "token")
+    k.copy_(sk), v.copy_(sv)
+    table, copies = ints([[69, 3, 66, 68]]), ints([[69, 65, 16], [1, 67, 5], [68, 0, 9]])
+    kept = ints([[1, 2, 17, 30, 31, 33, 50, 63]])
+    for a, b in ((k, v), (sk, sv)):
+        mxq.cache_compact(a, b, table, ints([0]), kept, ints([8]))
+        mxq.cache_copy_pages(a, b, copies)
+    mxq.sync_status()
+    assert torch.equal(bits(k), bits(sk)) and torch.equal(bits(v), bits(sv))

@@ -495,3 +495,28 @@ def test_stalled_loads_time_out_and_recover(nq, lens, fp8):
         mxq.set_option(_lib.OPT_INJECT_STALL, 0)
         mxq.set_option(_lib.OPT_WAIT_BUDGET_NS, old)
     c.check()
+
+
+def test_pages_further_apart_than_64_gib():
+    """Pages of keys and of values by turns, 2^30 bytes from one of the keys to the next."""
+    page, KV, pages = 24, 2, 67
+    buffer = torch.empty(pages << 30, dtype=torch.uint8, device="cuda")
+    for dtype in (torch.bfloat16, FP8):
+        flat = buffer.view(dtype)
+        size = flat.element_size()
+        for D, nq, lens in ((128, 16, 60), (128, 40, 300), (64, 5, 301)):
+            c = Case([nq], [lens], 8, KV, D, page, seed=71, fp8=dtype == FP8)
+            kc, vc = (flat.as_strided((pages, page, KV, D), ((1 << 30) // size, KV * D, D, 1),
+                                      half * (1 << 29) // size) for half in range(2))
+            used = [66, 0, 65, 64, 1, 63, 59, 8, 33, 2, 3, 4, 62][:-(-lens // page)]
+            for mine, theirs in zip(used, c.rows[0]):
+                kc[mine], vc[mine] = c.kc[theirs], c.vc[theirs]
+            want, wl = c.call()
+            c.table = ints([used])
+            out, lse = mxq.paged_attention_tree(
+                c.q, kc, vc, c.table, ints([lens]), cumulated([nq]), c.parents, scale=c.scale,
+                k_scale=c.ks, v_scale=c.vs, return_lse=True)
+            mxq.sync_status()
+            assert torch.equal(out, want) and torch.equal(lse, wl)
+    del buffer, flat, kc, vc
+    torch.cuda.empty_cache()
