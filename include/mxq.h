@@ -619,9 +619,10 @@ mxq_status mxq_cache_resize(int32_t* page_table, int64_t ld_table, int64_t B, in
                             void* workspace, size_t ws_bytes, mxq_stream_t stream);
 
 /*
- * Sequences fork: row b < n of new_table (int32 [n, max_pages], row stride ld_new, apart
- * from page_table) continues row parents[b] of page_table (int32 [B, max_pages]);
- * -1: an empty row.  new_lens[b] is its length.  Full pages are shared.  An open last
+ * Sequences fork: row b < n of new_table (int32 [n, max_pages], row stride ld_new)
+ * continues row parents[b] of page_table (int32 [B, max_pages]); -1: an empty row.
+ * new_lens[b] is its length.  The memory from the first to the last element of new_table,
+ * new_lens and copies overlaps that of no input (MXQ_ERR_INVALID_ARG).  Full pages are shared.  An open last
  * page (a length that is no multiple of page_size) is kept by its row's first child
  * if the page's count is 1 before the call; every other child gets a fresh page, and
  * copies[b] (int32 [n, 3]) = source page, fresh page, tokens to copy

@@ -629,8 +629,9 @@ def cache_fork(page_table, seq_lens, page_refs, parents, page_size: int, out=Non
     each new row continues (-1: none).  Full pages are shared; an open last
     page that nothing else holds stays with the row's first child, other
     children get a fresh page.  Rows without children are freed.  Returns the new
-    table [n, max_pages] (out, if given), its lengths int32 [n] and copies
-    int32 [n, 3]: what cache_copy_pages has to copy in every layer."""
+    table [n, max_pages] (out, if given: memory apart from all arguments'),
+    its lengths int32 [n] and copies int32 [n, 3]: what cache_copy_pages has to
+    copy in every layer."""
     return _attn().fork(page_table, seq_lens, page_refs, parents, page_size, out, workspace)
 
 

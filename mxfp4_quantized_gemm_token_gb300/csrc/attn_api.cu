@@ -319,6 +319,17 @@ extern "C" mxq_status mxq_attention_varlen(
 
 namespace {
 
+// `n` int32 places from p on; none where there are no rows
+struct Extent {
+  const int32_t* p;
+  int64_t n, rows;
+  bool overlaps(const Extent& o) const {
+    if (!p || !o.p || rows <= 0 || o.rows <= 0) return false;
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(o.p);
+    return a < b + 4 * o.n && b < a + 4 * n;
+  }
+};
+
 // A page table and the counts of its pages.
 mxq_status check_table(const char* name, const void* table, int64_t ld, int64_t rows,
                        int64_t max_pages) {
@@ -421,12 +432,18 @@ extern "C" mxq_status mxq_cache_fork(const int32_t* page_table, int64_t ld_table
   if (!aligned(seq_lens, 4) || !aligned(parents, 4) || !aligned(new_lens, 4) ||
       !aligned(copies, 4))
     return fail(MXQ_ERR_INVALID_ARG, "4-byte arrays must be 4-byte aligned");
-  if (page_table && new_table && max_pages > 0 && B > 0 && n > 0) {
-    const uintptr_t a = reinterpret_cast<uintptr_t>(page_table);
-    const uintptr_t b = reinterpret_cast<uintptr_t>(new_table);
-    if (a < b + 4 * ((n - 1) * ld_new + max_pages) && b < a + 4 * ((B - 1) * ld_table + max_pages))
-      return fail(MXQ_ERR_INVALID_ARG, "new_table must not overlap page_table");
-  }
+  // (what the call reads again after it has begun to write)
+  const Extent in[] = {{page_table, (B - 1) * ld_table + max_pages, B},
+                       {seq_lens, B, B},
+                       {parents, n, n},
+                       {page_refs, pages, pages}};
+  const Extent results[] = {{new_table, (n - 1) * ld_new + max_pages, n}, {new_lens, n, n},
+                            {copies, 3 * n, n}};
+  for (const Extent& x : in)
+    for (const Extent& y : results)
+      if (x.overlaps(y))
+        return fail(MXQ_ERR_INVALID_ARG, "new_table, new_lens and copies must not overlap what "
+                                         "the call reads");
   MXQ_TRY(check_workspace(workspace, ws_bytes, pages_workspace_bytes(std::max(B, n), pages),
                           "mxq_cache_pages_workspace_size"));
   DeviceInfo d;

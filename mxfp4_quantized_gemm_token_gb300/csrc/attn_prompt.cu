@@ -970,12 +970,13 @@ cudaError_t launch(const PromptMaps& maps, const PromptArgs& a, cudaStream_t str
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (!configured[dev]) {
-    e = cudaFuncSetAttribute(prompt_kernel<D, kFirst>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    e = cudaFuncSetAttribute(prompt_kernel<D, kFirst>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     configured[dev] = true;
   }
-  return launch_k(prompt_kernel<D, kFirst>, dim3(a.grid), dim3(kPromptThreads), static_cast<size_t>(smem),
-                  stream, maps, a);
+  return launch_k(prompt_kernel<D, kFirst>, dim3(a.grid), dim3(kPromptThreads),
+                  static_cast<size_t>(smem), stream, maps, a);
 }
 
 }  // namespace

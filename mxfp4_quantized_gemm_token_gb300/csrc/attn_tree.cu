@@ -1309,7 +1309,8 @@ cudaError_t launch(const TreeArgs& a, int num_sms, cudaStream_t stream) {
                     dim3(static_cast<unsigned>(items * a.p.Hkv), fine), dim3(32 * kJoinWarps), 0,
                     stream, a);
   return launch_k(tree_join_kernel<D, false>,
-                  dim3(static_cast<unsigned>(tasks), static_cast<unsigned>((rows + kPerBlock - 1) / kPerBlock)),
+                  dim3(static_cast<unsigned>(tasks),
+                       static_cast<unsigned>((rows + kPerBlock - 1) / kPerBlock)),
                   dim3(32 * kJoinWarps), 0, stream, a);
 }
 

@@ -61,6 +61,21 @@ def test_fork(lib, changed, status):
     assert status == OK or lib.mxq_last_error()
 
 
+@pytest.mark.parametrize("output", ["new", "new_lens", "copies"])
+@pytest.mark.parametrize("read", ["table", "lens", "parents", "refs"])
+def test_fork_results_lie_apart_from_what_it_reads(lib, output, read):
+    """Side by side with it on either side it is the workspace that is refused."""
+    apart = dict(table=1 << 24, lens=2 << 24, parents=3 << 24, refs=4 << 24, new=5 << 24,
+                 new_lens=6 << 24, copies=7 << 24, ws=None)
+    size = dict(table=(3 - 1) * 8 + 8, lens=3, parents=4, refs=20, new=(4 - 1) * 8 + 8, new_lens=4,
+                copies=12)
+    for at, meet in ((4 * size[read] - 16, True), (4 * size[read], False),
+                     (-4 * size[output] + 16, True), (-4 * size[output], False)):
+        args = dict(apart, **{output: apart[read] + at})
+        assert call(lib, "mxq_cache_fork", FORK, args) == INVALID
+        assert (b"must not overlap" in lib.mxq_last_error()) == meet
+
+
 BAD_CACHE = [
     (dict(k=None), INVALID), (dict(v=None), INVALID), (dict(k=P + 8), UNSUPPORTED),
     (dict(dtype=_lib.F32), UNSUPPORTED), (dict(D=72), UNSUPPORTED), (dict(D=0), INVALID),
