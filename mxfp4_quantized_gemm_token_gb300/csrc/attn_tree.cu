@@ -19,8 +19,9 @@
 // list of turns: turn t belongs to warpgroup t & 1.
 //   warps 0-3, 4-7   softmax of the even and odd turns, one thread a row, and the output
 //   warp 8           issues the MMAs
-//   warp 9           finds the pieces of items that the CTA works on
-//   warps 10-15      load keys and values with 16-byte asynchronous copies, row by row, as pages
+//   warp 12          finds the pieces of items that the CTA works on (next to warp 8, which needs its
+//                    scheduler's turns: two tiles 2 % faster than with a loading warp there)
+//   the other six    load keys and values with 16-byte asynchronous copies, row by row, as pages
 //                    are of any size; for an e4m3 cache two of them, and four convert to f16 (exact)
 // S0, S1, O0 and O1 are in tensor memory, P takes the place of S.  The reference a
 // row subtracts is raised only when its maximum grows by more than 2^8.
@@ -60,7 +61,7 @@ constexpr int kBM = 128;             // rows of a tile, keys of a block
 constexpr int kRows = 2 * kBM;       // of an item
 constexpr int kTreeThreads = 512;
 constexpr int kTreeWarps = kTreeThreads / 32;
-constexpr int kMmaWarp = 8, kWalkWarp = 9, kLoadWarp = 10;
+constexpr int kMmaWarp = 8, kWalkWarp = 12;
 // registers a thread: the launch gives 128 to each; the softmax warpgroups keep most of a row of
 // 128 scores and take what the other two give up
 constexpr int kSoftmaxRegs = 168, kOtherRegs = 88;
@@ -120,7 +121,7 @@ struct TreeLayout {
   static constexpr int kSmem = (2 + kStages) * kTileBytes + kRawStages * kRawBytes + 16 * kSeen +
                                64 * kPieces + 8 * kBars + 16;
   static_assert(kSmem + 1024 + 512 <= 227 * 1024, "shared memory over budget");
-  static_assert(kLoadWarp + kLoaders <= kTreeWarps, "more warps than there are");
+  static_assert(kMmaWarp + 2 + kLoaders <= kTreeWarps, "more warps than there are");
 };
 
 // A sequence: its rows [q0, q0 + nq) of the packed queries, behind len - nq keys.
@@ -197,6 +198,19 @@ struct __align__(16) TreePiece {
 static_assert(sizeof(TreePiece) == 64, "four 16-byte words");
 constexpr int kOpened = 1, kClosed = 2, kSingle = 4, kSlot1 = 8;
 
+// mbar_wait_warp that calls what follows a first try without success: the roles of the kernel
+// share the instructions' supply, and where the barrier is complete, as for the MMAs' warp nearly
+// always, no more than the try is fetched (with it, counted places and low words of descriptors
+// there: two tiles of e4m3 286 -> 261 us, of bf16 268 -> 253; the softmax has no
+// registers for a call).
+__device__ __noinline__ bool wait_longer(uint64_t* bar, uint32_t parity, const WaitCtx& w) {
+  return mbar_wait(bar, parity, w);
+}
+__device__ __forceinline__ bool wait_lean(uint64_t* bar, uint32_t parity, const WaitCtx& w) {
+  const bool ok = mbar_try_wait(bar, parity);
+  return __all_sync(0xffffffffu, ok) || __all_sync(0xffffffffu, wait_longer(bar, parity, w));
+}
+
 // The pieces that one warp hands to the others through a ring in shared memory; their fields are
 // read there as they are needed (registers are short).
 struct Pieces {
@@ -206,9 +220,12 @@ struct Pieces {
   __device__ __forceinline__ Pieces(const TreePiece* r, uint64_t* f, uint64_t* e)
       : ring(r), full(f), empty(e) {}
   // the next piece; null: there are none, or a wait gave up
+  template <bool kLean = true>
   __device__ __forceinline__ const TreePiece* next(const WaitCtx& wc) {
     const int at = n % kPieces;
-    if (!mbar_wait_warp(&full[at], (n / kPieces) & 1, wc)) return nullptr;
+    const uint32_t phase = (n / kPieces) & 1;
+    if (!(kLean ? wait_lean(&full[at], phase, wc) : mbar_wait_warp(&full[at], phase, wc)))
+      return nullptr;
     return ring[at].cnt > 0 ? ring + at : nullptr;
   }
   __device__ __forceinline__ void done() {
@@ -304,6 +321,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeArgs a)
   __shared__ long long start_at;      // the line up to the first item
   __shared__ TreeSeq start_seq;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int loader = warp - kMmaWarp - 1 - (warp > kWalkWarp);
   const TreeParams& p = a.p;
   WaitCtx wc{p.status, abort_flag, a.budget_ns};
 
@@ -498,10 +516,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeArgs a)
       if (ok) put(TreePiece{});
     }
     __syncwarp();
-  } else if (FP8 && warp >= kLoadWarp + L::kFetchers) {
+  } else if (FP8 && loader >= L::kFetchers) {
     // ------------------------------------------------- e4m3 rows to f16
     if constexpr (FP8) {
-      const int quarter = warp - kLoadWarp - L::kFetchers;
+      const int quarter = loader - L::kFetchers;
       const int rows = quarter * 32 + lane / L::kLPR, piece = lane % L::kLPR;
       const uint8_t* src = raw + quarter * L::kUnitBytes + lane * 16;
       uint8_t* dst = ring + (piece >> 2) * L::kChunkBytes + rows * 128;
@@ -514,12 +532,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeArgs a)
         if (it == nullptr) break;
         for (const uint32_t end = fill + 2 * it->cnt; fill != end; ++fill) {
           const int from = fill % L::kRawStages, to = fill % ST;
-          if (!mbar_wait_warp(&raw_full[from], (fill / L::kRawStages) & 1, wc)) goto convert_done;
+          if (!wait_lean(&raw_full[from], (fill / L::kRawStages) & 1, wc)) goto convert_done;
           uint4 x[L::kCopies];
 #pragma unroll
           for (int i = 0; i < L::kCopies; ++i)
             x[i] = *reinterpret_cast<const uint4*>(src + from * L::kRawBytes + i * 512);
-          if (!mbar_wait_warp(&kv_empty[to], ((fill / ST) & 1) ^ 1, wc)) goto convert_done;
+          if (!wait_lean(&kv_empty[to], ((fill / ST) & 1) ^ 1, wc)) goto convert_done;
 #pragma unroll
           for (int i = 0; i < L::kCopies; ++i) {
             uint4 lo, hi;
@@ -543,13 +561,13 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeArgs a)
       }
     convert_done:;
     }
-  } else if (FP8 && warp >= kLoadWarp) {
+  } else if (FP8 && loader >= 0) {
     // ------------------------------------------------------- e4m3 rows
     // A warp takes two quarters of a block (32 rows each), keys and, from the same places,
     // values.
     if constexpr (FP8) {
       constexpr int NF = L::kFetchers, NQ = 4 / NF;
-      const int first = warp - kLoadWarp;
+      const int first = loader;
       const int row_in = lane / L::kLPR, piece = lane % L::kLPR;
       const uint32_t raw_at = smem_u32(raw) + first * L::kUnitBytes + lane * 16;
       uint32_t fill = 0, blocks = 0;
@@ -613,7 +631,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeArgs a)
           for (int kind = 0; kind < 2; ++kind) {
             if (kind == 0 ? j >= cnt : j == 0) continue;
             const int st = fill % L::kRawStages;
-            ok = mbar_wait_warp(&raw_empty[st], ((fill / L::kRawStages) & 1) ^ 1, wc);
+            ok = wait_lean(&raw_empty[st], ((fill / L::kRawStages) & 1) ^ 1, wc);
             if (!ok) break;
             const uint32_t dst = raw_at + st * L::kRawBytes;
 #pragma unroll
@@ -633,7 +651,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeArgs a)
       }
       cp_wait<0>();
     }
-  } else if (warp >= kLoadWarp) {
+  } else if (loader >= 0) {
     // ------------------------------------------------------- bf16 rows
     // A copy of a block's keys or values is four units of 32 rows; the units of all copies go
     // round the loading warps.
@@ -641,7 +659,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeArgs a)
       constexpr int NW = L::kLoaders;
       const int row_in = lane / L::kLPR, piece = lane % L::kLPR;
       const uint32_t sw = ((piece & 7) ^ row_in) << 4;
-      uint32_t unit = warp - kLoadWarp;                  // the next one of this warp, of all
+      uint32_t unit = loader;                  // the next one of this warp, of all
       uint32_t base = 0, blocks = 0;                     // copies and blocks before the piece
       while (!a.inject_stall) {
         const TreePiece* at_piece = pieces.next(wc);
@@ -687,7 +705,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeArgs a)
           const char* src = now.value ? v_base : k_base;
           const uint32_t fill = unit >> 2;
           const int st = fill % ST, rows = (unit & 3) * 32 + row_in;
-          if (!mbar_wait_warp(&kv_empty[st], ((fill / ST) & 1) ^ 1, wc)) goto loads_done;
+          if (!wait_lean(&kv_empty[st], ((fill / ST) & 1) ^ 1, wc)) goto loads_done;
           const uint32_t dst = smem_u32(ring) + st * L::kTileBytes +
                                (piece >> 3) * L::kChunkBytes + rows * 128;
           copy_rows<L::kCopies, L::kRPI>(src, at, mask, row_in, a.far, [&](int i) {
@@ -711,84 +729,107 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeArgs a)
     const bool leader = elect_one();
     const uint64_t q_desc = sw128_desc(smem_u32(sQ)), k_desc = sw128_desc(smem_u32(ring));
     const uint64_t v_desc = sw128_desc_mn(smem_u32(ring), L::kChunkBytes);
-    uint32_t base = 0, nq[2] = {0, 0}, np[2] = {0, 0};   // ring position, items, turns so far
-    // What the operands' rows were written by: the copies of other threads, which have arrived
-    // on the barrier, become visible to the tensor core's reads here; converted rows, and
-    // q, have been made so by their writers.
-    auto see = [&]() {
-      tc_fence_after();
-      if constexpr (!FP8) fence_proxy_async_smem();
+    // All that this warp waits for is usually there: what a turn costs it in instructions bounds
+    // the kernel where the memory does not.  So places and phases are counted on, not divided
+    // out of positions, and known to be the same in all lanes; offsets go into the
+    // descriptors' low words.
+    uint32_t nq[2] = {0, 0}, np[2] = {0, 0};             // items, turns so far
+    int slot0 = 0;                                       // of the piece's first copy
+    uint32_t phase0 = 0;
+    struct Place {
+      int slot;
+      uint32_t phase;
+      __device__ __forceinline__ void move(int by) {
+        slot += by;
+        if (slot >= ST) slot -= ST, phase ^= 1;
+      }
     };
-    auto issue_s = [&](int s, uint32_t fill) {
-      const uint64_t qd = q_desc + s * (L::kTileBytes / 16);
-      const uint64_t kd = k_desc + (fill % ST) * (L::kTileBytes / 16);
+    auto with_low = [](uint64_t d, uint32_t low) { return (d & 0xFFFFFFFF00000000ull) | low; };
+    auto issue_s = [&](int s, int slot) {
+      const uint32_t qd = static_cast<uint32_t>(q_desc) + s * (L::kTileBytes / 16);
+      const uint32_t kd = static_cast<uint32_t>(k_desc) + slot * (L::kTileBytes / 16);
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
         const int off = (k / 4) * (L::kChunkBytes / 16) + (k % 4) * 2;
-        mma_f16(tmem + s * 128, qd + off, kd + off, kDescS, k > 0);
+        mma_f16(tmem + s * 128, with_low(q_desc, qd + off), with_low(k_desc, kd + off), kDescS,
+                k > 0);
       }
     };
     // the keys of half `part` of a block; P of keys 64-127 lies where their scores began
-    auto issue_o = [&](int s, uint32_t fill, int part, bool accumulate) {
-      const uint64_t vd = v_desc + (fill % ST) * (L::kTileBytes / 16) + part * (4 * 2048 / 16);
+    auto issue_o = [&](int s, int slot, int part, bool accumulate) {
+      const uint32_t vd = static_cast<uint32_t>(v_desc) + slot * (L::kTileBytes / 16) +
+                          part * (4 * 2048 / 16);
       const uint32_t pa = tmem + s * 128 + part * 64;
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-        mma_f16_ts(tmem + 256 + s * 128, pa + k * 8, vd + k * (2048 / 16), kDescO,
+        mma_f16_ts(tmem + 256 + s * 128, pa + k * 8, with_low(v_desc, vd + k * (2048 / 16)), kDescO,
                    accumulate || k > 0);
     };
-    auto wait_kv = [&](uint32_t fill) {
-      return mbar_wait_warp(&kv_full[fill % ST], (fill / ST) & 1, wc);
+    // A copy has arrived.  What rows were written by, the copies of other threads, becomes visible
+    // to the tensor core's reads here; converted rows, and q, have been made so by their writers.
+    auto wait_kv = [&](const Place& at) {
+      if (!wait_lean(&kv_full[at.slot], at.phase, wc)) return false;
+      if constexpr (!FP8) fence_proxy_async_smem();
+      return true;
     };
     while (const TreePiece* it = pieces.next(wc)) {
-      const bool single = it->flags & kSingle;
-      const int cnt = it->cnt, turns = single ? cnt : 2 * cnt;
-      auto block_of = [&](int t) { return single ? t : t >> 1; };
-      auto k_fill = [&](int j) { return base + (j == 0 ? 0 : 2 * j - 1); };
-      auto v_fill = [&](int j) { return base + (j + 1 < cnt ? 2 * j + 2 : 2 * j + 1); };
+      const bool single = __shfl_sync(0xffffffffu, it->flags, 0) & kSingle;
+      const int cnt = __shfl_sync(0xffffffffu, it->cnt, 0), turns = single ? cnt : 2 * cnt;
+      Place k = {slot0, phase0}, v = k;
+      v.move(cnt > 1 ? 2 : 1);
+      int left = cnt - 1;                                // blocks whose values follow v's
       for (int t = 0; t < 2 && t < turns; ++t) {
-        const uint32_t f = k_fill(block_of(t));
-        if (!wait_kv(f)) goto mma_done;
-        if (!mbar_wait_warp(&q_full[t], nq[t] & 1, wc)) goto mma_done;
+        if (t == 1 && single) k.move(1);
+        if (t == 0 || single)
+          if (!wait_kv(k)) goto mma_done;
+        if (!wait_lean(&q_full[t], nq[t] & 1, wc)) goto mma_done;
         ++nq[t];
         if (leader) {
-          see();
-          issue_s(t, f);
+          tc_fence_after();
+          issue_s(t, k.slot);
           mma_commit(&s_full[t]);
-          if (single || t == 1) mma_commit(&kv_empty[f % ST]);
+          if (single || t == 1) mma_commit(&kv_empty[k.slot]);
         }
-        __syncwarp();
       }
+      bool first_k = !single;                            // the next K is one copy on, then two
       for (int t = 0; t < turns; ++t) {
         const int s = t & 1;
-        const uint32_t vf = v_fill(block_of(t));
-        if (!wait_kv(vf)) goto mma_done;
+        const bool fresh = single || s == 0, last = single || s == 1;
+        if (fresh)
+          if (!wait_kv(v)) goto mma_done;
 #pragma unroll
         for (int part = 1; part >= 0; --part) {
-          if (!mbar_wait_warp(&p_full[2 * s + part], np[s] & 1, wc)) goto mma_done;
+          if (!wait_lean(&p_full[2 * s + part], np[s] & 1, wc)) goto mma_done;
           if (leader) {
-            see();
-            issue_o(s, vf, part, t > 1 || part == 0);
+            tc_fence_after();
+            issue_o(s, v.slot, part, t > 1 || part == 0);
           }
-          __syncwarp();
         }
         ++np[s];
-        if (leader && (single || s == 1)) mma_commit(&kv_empty[vf % ST]);
+        if (leader && last) mma_commit(&kv_empty[v.slot]);
+        if (last) {
+          --left;
+          v.move(left > 0 ? 2 : 1);
+        }
         if (t + 2 < turns) {
-          const uint32_t kf = k_fill(block_of(t + 2));
-          if (!wait_kv(kf)) goto mma_done;
+          if (fresh) {
+            k.move(first_k ? 1 : 2);
+            first_k = false;
+            if (!wait_kv(k)) goto mma_done;
+          }
           if (leader) {
-            see();
-            issue_s(s, kf);
+            tc_fence_after();
+            issue_s(s, k.slot);
             mma_commit(&s_full[s]);
-            if (single || s == 1) mma_commit(&kv_empty[kf % ST]);
+            if (last) mma_commit(&kv_empty[k.slot]);
           }
         } else if (leader) {
           mma_commit(&o_full[s]);          // the piece's O is complete
         }
-        __syncwarp();
       }
-      base += 2 * cnt;
+      slot0 += 2 * cnt;
+      phase0 ^= slot0 / ST & 1;
+      slot0 %= ST;
       pieces.done();
     }
   mma_done:
@@ -807,7 +848,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeArgs a)
     const int tok = row / a.G, g = row - tok * a.G;
     uint8_t* q_tile = sQ + s * L::kTileBytes;
     uint32_t ns = 0, no = 0, nm = 0, blocks = 0;
-    while (const TreePiece* at_piece = pieces.next(wc)) {
+    while (const TreePiece* at_piece = pieces.next<false>(wc)) {
       const TreePiece& it = *at_piece;
       {
         const int hk = it.task % p.Hkv, h = hk * a.G + g;
