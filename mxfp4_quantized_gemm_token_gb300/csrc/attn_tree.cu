@@ -625,9 +625,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeArgs a)
               if (lane == 0) seen[((blocks + j) % kSeen) * 4 + first + i * NF] = mask[i];
             }
           }
-          // K_j, then V_(j-1): one place in the code (the roles share the instructions' supply; at D 64
-          // two are faster, 139 us against 151 for 16 long sequences of 16 drafts)
-#pragma unroll (D == 64 ? 2 : 1)
+          // K_j, then V_(j-1) (in one place of the code 16 long sequences of 16 drafts 196 us, in two 179)
+#pragma unroll
           for (int kind = 0; kind < 2; ++kind) {
             if (kind == 0 ? j >= cnt : j == 0) continue;
             const int st = fill % L::kRawStages;
