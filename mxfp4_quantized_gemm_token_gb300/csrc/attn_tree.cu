@@ -198,19 +198,6 @@ struct __align__(16) TreePiece {
 static_assert(sizeof(TreePiece) == 64, "four 16-byte words");
 constexpr int kOpened = 1, kClosed = 2, kSingle = 4, kSlot1 = 8;
 
-// mbar_wait_warp that calls what follows a first try without success: the roles of the kernel
-// share the instructions' supply, and where the barrier is complete, as for the MMAs' warp nearly
-// always, no more than the try is fetched (with it, counted places and low words of descriptors
-// there: two tiles of e4m3 286 -> 261 us, of bf16 268 -> 253; the softmax has no
-// registers for a call).
-__device__ __noinline__ bool wait_longer(uint64_t* bar, uint32_t parity, const WaitCtx& w) {
-  return mbar_wait(bar, parity, w);
-}
-__device__ __forceinline__ bool wait_lean(uint64_t* bar, uint32_t parity, const WaitCtx& w) {
-  const bool ok = mbar_try_wait(bar, parity);
-  return __all_sync(0xffffffffu, ok) || __all_sync(0xffffffffu, wait_longer(bar, parity, w));
-}
-
 // The pieces that one warp hands to the others through a ring in shared memory; their fields are
 // read there as they are needed (registers are short).
 struct Pieces {
@@ -729,21 +716,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeArgs a)
     const uint64_t q_desc = sw128_desc(smem_u32(sQ)), k_desc = sw128_desc(smem_u32(ring));
     const uint64_t v_desc = sw128_desc_mn(smem_u32(ring), L::kChunkBytes);
     // All that this warp waits for is usually there: what a turn costs it in instructions bounds
-    // the kernel where the memory does not.  So places and phases are counted on, not divided
-    // out of positions, and known to be the same in all lanes; offsets go into the
-    // descriptors' low words.
+    // the kernel where the memory does not.  So places and phases are counted, and known to be
+    // the same in all lanes.
     uint32_t nq[2] = {0, 0}, np[2] = {0, 0};             // items, turns so far
     int slot0 = 0;                                       // of the piece's first copy
     uint32_t phase0 = 0;
-    struct Place {
-      int slot;
-      uint32_t phase;
-      __device__ __forceinline__ void move(int by) {
-        slot += by;
-        if (slot >= ST) slot -= ST, phase ^= 1;
-      }
-    };
-    auto with_low = [](uint64_t d, uint32_t low) { return (d & 0xFFFFFFFF00000000ull) | low; };
     auto issue_s = [&](int s, int slot) {
       const uint32_t qd = static_cast<uint32_t>(q_desc) + s * (L::kTileBytes / 16);
       const uint32_t kd = static_cast<uint32_t>(k_desc) + slot * (L::kTileBytes / 16);
@@ -766,7 +743,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeArgs a)
     };
     // A copy has arrived.  What rows were written by, the copies of other threads, becomes visible
     // to the tensor core's reads here; converted rows, and q, have been made so by their writers.
-    auto wait_kv = [&](const Place& at) {
+    auto wait_kv = [&](const RingPlace<ST>& at) {
       if (!wait_lean(&kv_full[at.slot], at.phase, wc)) return false;
       if constexpr (!FP8) fence_proxy_async_smem();
       return true;
@@ -774,7 +751,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeArgs a)
     while (const TreePiece* it = pieces.next(wc)) {
       const bool single = __shfl_sync(0xffffffffu, it->flags, 0) & kSingle;
       const int cnt = __shfl_sync(0xffffffffu, it->cnt, 0), turns = single ? cnt : 2 * cnt;
-      Place k = {slot0, phase0}, v = k;
+      RingPlace<ST> k = {slot0, phase0}, v = k;
       v.move(cnt > 1 ? 2 : 1);
       int left = cnt - 1;                                // blocks whose values follow v's
       for (int t = 0; t < 2 && t < turns; ++t) {
