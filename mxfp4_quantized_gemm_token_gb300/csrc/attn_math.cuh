@@ -102,8 +102,8 @@ __device__ __forceinline__ RowEnd finish_row(float ms, float l, const float* sin
 // mbar_wait_warp that calls what follows a first try without success.  The roles of a kernel
 // share the instructions' supply, and the warp that issues the MMAs, which find their operands
 // ready nearly always, is the one whose turns the others wait for: it fetches no more than
-// the try (a prompt of 8192 tokens 324 -> 304 us, a tree's two tiles of e4m3 286 -> 261;
-// the softmax has no registers for a call).
+// the try (a prompt of 8192 tokens 324 -> 306 us, a tree's two tiles of e4m3 286 -> 258; the
+// softmax has no registers for a call).
 struct LeanWait {
   static __device__ __noinline__ bool longer(uint64_t* bar, uint32_t parity, const WaitCtx& w) {
     return mbar_wait(bar, parity, w);
@@ -113,21 +113,6 @@ __device__ __forceinline__ bool wait_lean(uint64_t* bar, uint32_t parity, const 
   const bool ok = mbar_try_wait(bar, parity);
   return __all_sync(0xffffffffu, ok) ||
          __all_sync(0xffffffffu, LeanWait::longer(bar, parity, w));
-}
-
-// For the same warp: a place in a ring of N and its phase, counted instead of divided out of a
-// position; and a matrix descriptor whose offset goes into the low word alone.
-template <int N>
-struct RingPlace {
-  int slot;
-  uint32_t phase;
-  __device__ __forceinline__ void move(int by) {
-    slot += by;
-    if (slot >= N) slot -= N, phase ^= 1;
-  }
-};
-__device__ __forceinline__ uint64_t with_low(uint64_t desc, uint32_t low) {
-  return (desc & 0xFFFFFFFF00000000ull) | low;
 }
 
 }  // namespace mxq

@@ -615,75 +615,74 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       // descriptors of the first tiles; offsets are added in 16-byte units
       const uint64_t q_desc = sw128_desc(smem_u32(sQ)), k_desc = sw128_desc(smem_u32(ring));
       const uint64_t v_desc = sw128_desc_mn(smem_u32(ring), L::kChunkBytes);
-      uint32_t nq = 0, np = 0;               // items, blocks so far
-      RingPlace<ST> k = {0, 0};              // the next K, and, one behind, the next V
-      auto issue_s = [&](int s) {
-        const uint32_t qd = static_cast<uint32_t>(q_desc) + s * (L::kTileBytes / 16);
-        const uint32_t kd = static_cast<uint32_t>(k_desc) + k.slot * (L::kTileBytes / 16);
+      uint32_t base = 0, nq = 0, np = 0;     // ring position of K_0, items, blocks so far
+      auto issue_s = [&](int s, uint32_t fill) {
+        const uint64_t qd = q_desc + s * (L::kTileBytes / 16);
+        const uint64_t kd = k_desc + (fill % ST) * (L::kTileBytes / 16);
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          const int off = (i / 4) * (L::kChunkBytes / 16) + (i % 4) * 2;
-          mma_f16(tmem + s * 128, with_low(q_desc, qd + off), with_low(k_desc, kd + off), kDescS,
-                  i > 0);
+        for (int k = 0; k < D / 16; ++k) {
+          const int off = (k / 4) * (L::kChunkBytes / 16) + (k % 4) * 2;
+          mma_f16(tmem + s * 128, qd + off, kd + off, kDescS, k > 0);
         }
       };
       // the keys of half `part` of a block
-      auto issue_o = [&](int s, int slot, int part, bool accumulate) {
-        const uint32_t vd = static_cast<uint32_t>(v_desc) + slot * (L::kTileBytes / 16) +
-                            part * (4 * 2048 / 16);
+      auto issue_o = [&](int s, uint32_t fill, int part, bool accumulate) {
+        const uint64_t vd = v_desc + (fill % ST) * (L::kTileBytes / 16) + part * (4 * 2048 / 16);
         const uint32_t pa = tmem + s * 128 + part * 32;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          mma_f16_ts(tmem + 256 + s * 128, pa + i * 8, with_low(v_desc, vd + i * (2048 / 16)),
-                     kDescO, accumulate || i > 0);
+        for (int k = 0; k < 4; ++k)
+          mma_f16_ts(tmem + 256 + s * 128, pa + k * 8, vd + k * (2048 / 16), kDescO,
+                     accumulate || k > 0);
       };
-      auto wait_kv = [&](const RingPlace<ST>& at) {
-        return wait_lean(&kv_full[at.slot], at.phase, wc);
+      auto wait_kv = [&](uint32_t fill) {
+        return wait_lean(&kv_full[fill % ST], (fill / ST) & 1, wc);
       };
       Items items(a);
       while (items.next()) {
-        const int n = __shfl_sync(0xffffffffu, items.it.kb1 - items.it.kb0, 0);
+        const int n = items.it.kb1 - items.it.kb0;
         if (n <= 0) continue;
-        if (!wait_kv(k)) goto mma_done;
+        if (!wait_kv(base)) goto mma_done;
         for (int s = 0; s < 2; ++s) {
           if (!wait_lean(&q_full[s], nq & 1, wc)) goto mma_done;
           if (leader) {
             tc_fence_after();
-            issue_s(s);
+            issue_s(s, base);
             mma_commit(&s_full[s]);
             if (n == 1) mma_commit(&q_empty[s]);
-            if (s == 1) mma_commit(&kv_empty[k.slot]);
+            if (s == 1) mma_commit(&kv_empty[base % ST]);
           }
+          __syncwarp();
         }
         for (int j = 0; j < n; ++j, ++np) {
-          RingPlace<ST> v = k;
-          v.move(1);
-          k.move(2);
-          if (!wait_kv(v)) goto mma_done;
+          const uint32_t vf = base + 2 * j + 1, kf = vf + 1;
+          if (!wait_kv(vf)) goto mma_done;
           for (int s = 0; s < 2; ++s) {
 #pragma unroll
             for (int part = 0; part < 2; ++part) {
               if (!wait_lean(&p_full[2 * s + part], np & 1, wc)) goto mma_done;
               if (leader) {
                 tc_fence_after();
-                issue_o(s, v.slot, part, j > 0 || part > 0);
+                issue_o(s, vf, part, j > 0 || part > 0);
               }
+              __syncwarp();
             }
-            if (leader && s == 1) mma_commit(&kv_empty[v.slot]);
+            if (leader && s == 1) mma_commit(&kv_empty[vf % ST]);
             if (j + 1 < n) {
-              if (s == 0 && !wait_kv(k)) goto mma_done;
+              if (s == 0 && !wait_kv(kf)) goto mma_done;
               if (leader) {
                 tc_fence_after();
-                issue_s(s);
+                issue_s(s, kf);
                 mma_commit(&s_full[s]);
                 if (j + 2 == n) mma_commit(&q_empty[s]);
-                if (s == 1) mma_commit(&kv_empty[k.slot]);
+                if (s == 1) mma_commit(&kv_empty[kf % ST]);
               }
             } else if (leader) {
               mma_commit(&o_full[s]);        // the item's O is complete
             }
+            __syncwarp();
           }
         }
+        base += 2 * n;
         ++nq;
       }
     mma_done:

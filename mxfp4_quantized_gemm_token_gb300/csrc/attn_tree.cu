@@ -715,97 +715,83 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeArgs a)
     const bool leader = elect_one();
     const uint64_t q_desc = sw128_desc(smem_u32(sQ)), k_desc = sw128_desc(smem_u32(ring));
     const uint64_t v_desc = sw128_desc_mn(smem_u32(ring), L::kChunkBytes);
-    // All that this warp waits for is usually there: what a turn costs it in instructions bounds
-    // the kernel where the memory does not.  So places and phases are counted, and known to be
-    // the same in all lanes.
-    uint32_t nq[2] = {0, 0}, np[2] = {0, 0};             // items, turns so far
-    int slot0 = 0;                                       // of the piece's first copy
-    uint32_t phase0 = 0;
-    auto issue_s = [&](int s, int slot) {
-      const uint32_t qd = static_cast<uint32_t>(q_desc) + s * (L::kTileBytes / 16);
-      const uint32_t kd = static_cast<uint32_t>(k_desc) + slot * (L::kTileBytes / 16);
+    // (All that this warp waits for is usually there: what a turn costs it in instructions bounds
+    // the kernel where the memory does not.)
+    uint32_t base = 0, nq[2] = {0, 0}, np[2] = {0, 0};   // ring position, items, turns so far
+    // What the operands' rows were written by: the copies of other threads, which have arrived
+    // on the barrier, become visible to the tensor core's reads here; converted rows, and
+    // q, have been made so by their writers.
+    auto see = [&]() {
+      tc_fence_after();
+      if constexpr (!FP8) fence_proxy_async_smem();
+    };
+    auto issue_s = [&](int s, uint32_t fill) {
+      const uint64_t qd = q_desc + s * (L::kTileBytes / 16);
+      const uint64_t kd = k_desc + (fill % ST) * (L::kTileBytes / 16);
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
         const int off = (k / 4) * (L::kChunkBytes / 16) + (k % 4) * 2;
-        mma_f16(tmem + s * 128, with_low(q_desc, qd + off), with_low(k_desc, kd + off), kDescS,
-                k > 0);
+        mma_f16(tmem + s * 128, qd + off, kd + off, kDescS, k > 0);
       }
     };
     // the keys of half `part` of a block; P of keys 64-127 lies where their scores began
-    auto issue_o = [&](int s, int slot, int part, bool accumulate) {
-      const uint32_t vd = static_cast<uint32_t>(v_desc) + slot * (L::kTileBytes / 16) +
-                          part * (4 * 2048 / 16);
+    auto issue_o = [&](int s, uint32_t fill, int part, bool accumulate) {
+      const uint64_t vd = v_desc + (fill % ST) * (L::kTileBytes / 16) + part * (4 * 2048 / 16);
       const uint32_t pa = tmem + s * 128 + part * 64;
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-        mma_f16_ts(tmem + 256 + s * 128, pa + k * 8, with_low(v_desc, vd + k * (2048 / 16)), kDescO,
+        mma_f16_ts(tmem + 256 + s * 128, pa + k * 8, vd + k * (2048 / 16), kDescO,
                    accumulate || k > 0);
     };
-    // A copy has arrived.  What rows were written by, the copies of other threads, becomes visible
-    // to the tensor core's reads here; converted rows, and q, have been made so by their writers.
-    auto wait_kv = [&](const RingPlace<ST>& at) {
-      if (!wait_lean(&kv_full[at.slot], at.phase, wc)) return false;
-      if constexpr (!FP8) fence_proxy_async_smem();
-      return true;
+    auto wait_kv = [&](uint32_t fill) {
+      return wait_lean(&kv_full[fill % ST], (fill / ST) & 1, wc);
     };
     while (const TreePiece* it = pieces.next(wc)) {
-      const bool single = __shfl_sync(0xffffffffu, it->flags, 0) & kSingle;
-      const int cnt = __shfl_sync(0xffffffffu, it->cnt, 0), turns = single ? cnt : 2 * cnt;
-      RingPlace<ST> k = {slot0, phase0}, v = k;
-      v.move(cnt > 1 ? 2 : 1);
-      int left = cnt - 1;                                // blocks whose values follow v's
+      const bool single = it->flags & kSingle;
+      const int cnt = it->cnt, turns = single ? cnt : 2 * cnt;
+      auto block_of = [&](int t) { return single ? t : t >> 1; };
+      auto k_fill = [&](int j) { return base + (j == 0 ? 0 : 2 * j - 1); };
+      auto v_fill = [&](int j) { return base + (j + 1 < cnt ? 2 * j + 2 : 2 * j + 1); };
       for (int t = 0; t < 2 && t < turns; ++t) {
-        if (t == 1 && single) k.move(1);
-        if (t == 0 || single)
-          if (!wait_kv(k)) goto mma_done;
+        const uint32_t f = k_fill(block_of(t));
+        if (!wait_kv(f)) goto mma_done;
         if (!wait_lean(&q_full[t], nq[t] & 1, wc)) goto mma_done;
         ++nq[t];
         if (leader) {
-          tc_fence_after();
-          issue_s(t, k.slot);
+          see();
+          issue_s(t, f);
           mma_commit(&s_full[t]);
-          if (single || t == 1) mma_commit(&kv_empty[k.slot]);
+          if (single || t == 1) mma_commit(&kv_empty[f % ST]);
         }
       }
-      bool first_k = !single;                            // the next K is one copy on, then two
       for (int t = 0; t < turns; ++t) {
         const int s = t & 1;
-        const bool fresh = single || s == 0, last = single || s == 1;
-        if (fresh)
-          if (!wait_kv(v)) goto mma_done;
+        const uint32_t vf = v_fill(block_of(t));
+        if (!wait_kv(vf)) goto mma_done;
 #pragma unroll
         for (int part = 1; part >= 0; --part) {
           if (!wait_lean(&p_full[2 * s + part], np[s] & 1, wc)) goto mma_done;
           if (leader) {
-            tc_fence_after();
-            issue_o(s, v.slot, part, t > 1 || part == 0);
+            see();
+            issue_o(s, vf, part, t > 1 || part == 0);
           }
         }
         ++np[s];
-        if (leader && last) mma_commit(&kv_empty[v.slot]);
-        if (last) {
-          --left;
-          v.move(left > 0 ? 2 : 1);
-        }
+        if (leader && (single || s == 1)) mma_commit(&kv_empty[vf % ST]);
         if (t + 2 < turns) {
-          if (fresh) {
-            k.move(first_k ? 1 : 2);
-            first_k = false;
-            if (!wait_kv(k)) goto mma_done;
-          }
+          const uint32_t kf = k_fill(block_of(t + 2));
+          if (!wait_kv(kf)) goto mma_done;
           if (leader) {
-            tc_fence_after();
-            issue_s(s, k.slot);
+            see();
+            issue_s(s, kf);
             mma_commit(&s_full[s]);
-            if (last) mma_commit(&kv_empty[k.slot]);
+            if (single || s == 1) mma_commit(&kv_empty[kf % ST]);
           }
         } else if (leader) {
           mma_commit(&o_full[s]);          // the piece's O is complete
         }
       }
-      slot0 += 2 * cnt;
-      phase0 ^= slot0 / ST & 1;
-      slot0 %= ST;
+      base += 2 * cnt;
       pieces.done();
     }
   mma_done:

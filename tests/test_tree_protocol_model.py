@@ -165,17 +165,14 @@ class Model:
                 if single or s == 1:
                     commit(self.kv_empty[fill % self.stages])
 
-            # (a block that both tiles take is waited for once)
             for t in range(min(2, turns)):
-                if single or t == 0:
-                    yield kv(k_fill(of(t)))
+                yield kv(k_fill(of(t)))
                 yield self.q_full[t], at["nq"][t] & 1
                 at["nq"][t] += 1
                 scores(t, of(t), k_fill(of(t)))
             for t in range(turns):
                 s, vf = t & 1, v_fill(of(t))
-                if single or s == 0:
-                    yield kv(vf)
+                yield kv(vf)
                 for part in (1, 0):
                     yield self.p_full[s][part], at["np"][s] & 1
                     self.tensor.append(("o", s, i, of(t), vf % self.stages, part, t < 2))
@@ -183,8 +180,7 @@ class Model:
                 if single or s == 1:
                     commit(self.kv_empty[vf % self.stages])
                 if t + 2 < turns:
-                    if single or s == 0:
-                        yield kv(k_fill(of(t + 2)))
+                    yield kv(k_fill(of(t + 2)))
                     scores(s, of(t + 2), k_fill(of(t + 2)))
                 else:
                     commit(self.o_full[s])
