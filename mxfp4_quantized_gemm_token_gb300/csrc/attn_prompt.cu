@@ -39,16 +39,18 @@
 //
 // Bound.  Arithmetic: 4 D operations a visible (query head, key) pair, on the
 // tensor cores at best.  One causal prompt of 8192 tokens, 32 query and 8 key/value
-// heads of 128: 323 us, 1.70 PFLOP/s, 87 % of a plain bf16 product's burst rate (342-364 us
-// when run for seconds, by the device: 87-93 % of its sustained rate under the power limit);
-// the tensor pipe is busy 72 % of the time, the rest is the chain scores -> maximum ->
-// weights -> product of each tile, ~3000 cycles for a block of both against 2048 of products;
-// at D 64 ~2500 against 1280, and the same prompt takes 276 us (141 at the burst rate).
-// 11 packed prompts of 8192 tokens: 80 us (42 at the burst rate), 65 at D 64 (21); here an
+// heads of 128: 307 us, 1.78 PFLOP/s, 92 % of a plain bf16 product's burst rate (341-350 us
+// when run for seconds, by the device, under the power limit);
+// the tensor pipe is busy 77 % of the time, the rest is the chain scores -> maximum ->
+// weights -> product of each tile, ~2850 cycles for a block of both against 2048 of products;
+// at D 64 ~2450 against 1280, and the same prompt takes 269 us (141 at the burst rate).  The warp
+// that issues the products finds its operands ready nearly always: what it fetches of
+// instructions counts (waits by calls: 324 -> 307 us).
+// 11 packed prompts of 8192 tokens: 78 us (42 at the burst rate), 64 at D 64 (21); here an
 // item's beginning and end count, ~2 us.  Two chunks of 300 rows over 7892 keys, in pieces:
-// 71 us (40).  One prompt of 2048 tokens is cut into pieces too: 65 us (18).  Blocks between first
+// 70 us (40).  One prompt of 2048 tokens is cut into pieces too: 65 us (18).  Blocks between first
 // keys that stay visible and the window are left out: 5 prompts of 8192 tokens, a window of 1024 and
-// 16 first keys, 101 us (54).
+// 16 first keys, 96 us (54).
 #include <cuda_bf16.h>
 #include <math.h>
 

@@ -36,13 +36,15 @@
 // share leave at most two partial results per CTA in the workspace, which a second kernel joins in
 // a fixed order.  A part's end inside a short item moves to the nearer end of it.
 //
-// Measured.  64 sequences of 5-8192 keys with trees of up to 32, 32 / 8 heads of 128, bf16: 185 us
-// (179 before the join: 6.0 TB/s of keys and values, 90 % of a plain copy's rate); 16 sequences of
-// 9000-32768 keys with 16 rows, 64 / 8 heads: 202 us, 6.4 TB/s, at D 64 125 us.  What bounds the
-// rest: of two tiles (32 rows of those) the chain scores -> maximum -> weights -> product, ~3900
-// cycles a block against 2048 of products: 266 us; with e4m3 the conversion's warps and that chain
-// (16 rows 202 us, 32 rows 287, up to 48 rows 386).  One tree over 1500 keys: 13.6 us, half of it
-// launches, the chain length -> page -> key, and a call's first use of each instruction.
+// Measured.  64 sequences of 5-8192 keys with trees of up to 32, 32 / 8 heads of 128, bf16: 184 us
+// (178 before the join: 6.0 TB/s of keys and values, 90 % of a plain copy's rate); 16 sequences of
+// 9000-32768 keys with 16 rows, 64 / 8 heads: 202 us, 6.4 TB/s, at D 64 124 us.  What bounds the
+// rest: of two tiles (32 rows of those) the warp that issues the products, 251 us.  It finds its
+// operands ready nearly always, but the roles share the supply of instructions, and a turn costs it
+// ~1800 cycles against 1024 of products (at D 64 ~1450 against 640).  With e4m3 that and the
+// conversion, 1800 cycles of shared memory a block (16 rows 179 us, 32 rows 258, up to 48 rows 348).
+// One tree over 1500 keys: 13.5 us, half of it launches, the chain length -> page -> key, and a
+// call's first use of each instruction.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math.h>
@@ -107,8 +109,7 @@ struct TreeLayout {
   static constexpr int kStages = FP8 ? (D == 128 ? 3 : 6) : (D == 128 ? 5 : 10);
   // Beside the warps that convert e4m3 rows of 128 the instructions' supply is short: there a mask
   // is written to the scores in a pass of its own, and the weights' code stands once for both
-  // halves (16 long e4m3 sequences 400 -> 386 us; bf16 is up to 3 % slower so, e4m3 at D 64 146 us
-  // instead of 139).
+  // halves (16 long e4m3 sequences 368 -> 360 us; bf16 is 1 % slower so, D 64 up to 4 %).
   static constexpr bool kRolled = FP8 && D == 128;
   static constexpr int kLoaders = 6;                     // warps that load
   // e4m3: two of them copy rows as they are cached into stages of their own, the other four
@@ -163,7 +164,7 @@ __device__ __forceinline__ TreeItem tree_item(const TreeArgs& a, const TreeSeq& 
 }
 
 // What an item counts on the line: a block of one tile 3 (bf16 at D 128: ~3000 cycles, its bytes'
-// share of the memory), of two 4 (~3900, the softmax), at D 64 3 and 5; its begin and end as
+// share of the memory), of two 4 (~3600), at D 64 3 and 5; its begin and end as
 // much as two blocks (64 ragged sequences: 182 us, with one 184, without 188).
 constexpr int kItemCost = 6, kMinCost = 6;
 template <int D>
