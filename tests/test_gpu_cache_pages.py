@@ -344,3 +344,41 @@ def test_rows_past_32_bits():
         mxq.cache_copy_pages(a, b, copies)
     mxq.sync_status()
     assert torch.equal(bits(k), bits(sk)) and torch.equal(bits(v), bits(sv))
+
+
+def test_compact_takes_a_row_twice_and_replays():
+    """A row that is kept twice, and a captured call that works on what the lists hold then."""
+    rng = random.Random(5)
+    size, heads, dim, n, most = 24, 3, 64, 700, 300
+    k, v = caches(64, size, heads, dim, torch.bfloat16, "token")
+    pages = list(range(64))
+    rng.shuffle(pages)
+    rows = [pages[:30], pages[30:60]]
+    table, starts = ints(rows), ints([3, 0])
+    kept, counts = torch.zeros(2, most, dtype=torch.int32, device="cuda"), ints([0, 0])
+    stream = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(stream):
+        mxq.cache_compact(k, v, table, starts, kept, counts)            # nothing is kept
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph, stream=stream):
+            mxq.cache_compact(k, v, table, starts, kept, counts)
+    for m in (1, 9, 300):
+        lists = [[max(i, rng.randrange(n)) for i in range(m)] for _ in range(2)]
+        lists[0] = [x for x in lists[0][::2] for _ in range(2)][:m] if m > 1 else lists[0]
+        lists = [[max(i, x) for i, x in enumerate(row)] for row in lists]
+        wk, wv = bits(k).clone(), bits(v).clone()
+        for row, s, list_ in zip(rows, (3, 0), lists):
+            src = torch.tensor([s + x for x in list_], device="cuda")
+            dst = torch.arange(s, s + len(list_), device="cuda")
+            at = torch.tensor(row, device="cuda")
+            for w, c in ((wk, k), (wv, v)):
+                w[at[dst // size], dst % size] = bits(c)[at[src // size], src % size]
+        for b, list_ in enumerate(lists):
+            kept[b, :len(list_)] = ints(list_)
+        counts.copy_(ints([len(x) for x in lists]))
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        mxq.sync_status()
+        assert torch.equal(bits(k), wk) and torch.equal(bits(v), wv)
