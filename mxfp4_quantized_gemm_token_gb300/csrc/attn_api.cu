@@ -409,7 +409,9 @@ extern "C" mxq_status mxq_cache_resize(int32_t* page_table, int64_t ld_table, in
   PagesParams p = {};
   p.table = page_table, p.ld = ld_table, p.B = B, p.max_pages = max_pages;
   p.lens = seq_lens, p.new_lens = new_lens, p.refs = page_refs, p.pages = pages;
-  p.page_size = page_size, p.window = window, p.first = first;
+  // (the kernel counts pages from the first keys' end on in 32 bits; no row has more than 2^30 keys)
+  p.page_size = page_size, p.window = std::min(window, 1 << 30);
+  p.first = first_keys(window, first);
   p.workspace = workspace, p.status = d.status;
   const cudaError_t e = launch_resize_pages(p, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? MXQ_OK : cuda_fail(e, "cache resize launch");
