@@ -1068,8 +1068,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeArgs a)
             (single ? 0 : s * kBM);
         const int64_t slot = slot0 + row;
         // Through shared memory (the tile of q is done with), so that four lanes write 64
-        // adjacent bytes of a row: 32 columns of the output, or 16 of a partial result.
-        uint8_t* stage = q_tile + 1024 + (warp & 3) * 2048;
+        // adjacent bytes of a row: 32 columns of the output, or 16 of a partial result.  In the
+        // warp's own rows of q, behind the references: after an item of two tiles no barrier keeps
+        // the next one's q, which another warp may write at once, from other rows.
+        uint8_t* stage = q_tile + 1024 + (warp & 3) * 4096;
         const uint32_t stored = __ballot_sync(0xffffffffu, valid);
         const int sub = lane >> 2, ch = lane & 3;
         const int64_t out_at = tokr * p.o_t + static_cast<int64_t>(h) * p.o_h;
