@@ -611,7 +611,11 @@ mxq_status mxq_cache_pages_workspace_size(int64_t rows, int64_t pages, size_t* b
  * new ones; new_lens[b] = 0 frees the row.  With window > 0, entries that the
  * row at position new_lens[b] - 1 and later ones do not see are freed too: pages
  * that had keys before the call, end at or before new_lens[b] - window and begin at or
- * behind key `first`.  seq_lens, new_lens int32 [B].  B == 0 is a no-op.
+ * behind key `first`.  Earlier rows see further back: a call that makes room for n drafted
+ * tokens, or a chunk, of an attention with a window is given window 0 or that window + n
+ * (mxq_paged_attention_tree's first row sees keys from seq_lens[b] - window + 1 on, and the
+ * sequence sees them again where drafts are rejected), and the call that cuts off what was
+ * rejected the window itself.  seq_lens, new_lens int32 [B].  B == 0 is a no-op.
  */
 mxq_status mxq_cache_resize(int32_t* page_table, int64_t ld_table, int64_t B, int64_t max_pages,
                             const int32_t* seq_lens, const int32_t* new_lens, int32_t* page_refs,

@@ -615,6 +615,9 @@ def cache_resize(page_table, seq_lens, new_lens, page_refs, page_size: int, wind
     (sync_status raises).  window: entries of pages that end before the last
     `window` keys of new_lens and begin behind the first `first` are freed as
     well: what paged_attention_decode with these arguments no longer reads.
+    Drafts and chunks see further back: grow the table for n of their rows with
+    window 0 or window + n, and free with the window itself once it is
+    known which rows stay.
     workspace: a caller's buffer of cache_pages_workspace_size bytes (None:
     allocated here).  Returns page_table."""
     return _attn().resize(page_table, seq_lens, new_lens, page_refs, page_size, window, first,
