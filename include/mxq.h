@@ -615,7 +615,12 @@ mxq_status mxq_cache_pages_workspace_size(int64_t rows, int64_t pages, size_t* b
  * tokens, or a chunk, of an attention with a window is given window 0 or that window + n
  * (mxq_paged_attention_tree's first row sees keys from seq_lens[b] - window + 1 on, and the
  * sequence sees them again where drafts are rejected), and the call that cuts off what was
- * rejected the window itself.  seq_lens, new_lens int32 [B].  B == 0 is a no-op.
+ * rejected the window itself.
+ * A row may be cut inside a full page that other rows hold too (mxq_cache_fork shares
+ * them): the page stays shared, open for this row, and keys that are appended or moved there
+ * replace the others'.  mxq_cache_fork with parents[b] = b for every row gives such
+ * rows a page of their own, with its copy, and leaves the others as they are.
+ * seq_lens, new_lens int32 [B].  B == 0 is a no-op.
  */
 mxq_status mxq_cache_resize(int32_t* page_table, int64_t ld_table, int64_t B, int64_t max_pages,
                             const int32_t* seq_lens, const int32_t* new_lens, int32_t* page_refs,

@@ -618,6 +618,9 @@ def cache_resize(page_table, seq_lens, new_lens, page_refs, page_size: int, wind
     Drafts and chunks see further back: grow the table for n of their rows with
     window 0 or window + n, and free with the window itself once it is
     known which rows stay.
+    A row cut inside a page that cache_fork shared leaves it shared: before
+    anything is appended there, cache_fork with parents 0, 1, ... gives the row
+    a page of its own.
     workspace: a caller's buffer of cache_pages_workspace_size bytes (None:
     allocated here).  Returns page_table."""
     return _attn().resize(page_table, seq_lens, new_lens, page_refs, page_size, window, first,
