@@ -69,7 +69,7 @@ constexpr int kMmaWarp = 8, kWalkWarp = 12;
 constexpr int kSoftmaxRegs = 168, kOtherRegs = 88;
 static_assert(2 * kSoftmaxRegs + 2 * kOtherRegs <= 4 * 128, "register split above the launch's");
 constexpr int kPieces = 8;           // pieces of items that may be under way
-constexpr int kSeen = 16;            // blocks whose masks of loaded keys are kept: some 10 are in use
+constexpr int kSeen = 16;            // blocks whose masks of loaded keys are kept
 constexpr int kWhole = 2;            // items of at most this many blocks stay whole
 constexpr int kAloneSequences = 32;    // calls of at most this many: one warp cuts the line
 constexpr int kAllWhole = 3;         // calls whose items have at most this many: all do
@@ -123,6 +123,11 @@ struct TreeLayout {
                                64 * kPieces + 8 * kBars + 16;
   static_assert(kSmem + 1024 + 512 <= 227 * 1024, "shared memory over budget");
   static_assert(kMmaWarp + 2 + kLoaders <= kTreeWarps, "more warps than there are");
+  // Block b's masks are read until its weights are handed over, and so while its values, copy 2 b + 2
+  // at most, keep their place: a warp has begun at most kStages + kRawStages + 1 copies behind those
+  // (+ 1: the units of six warps reach into a second copy), and the keys of block x are copy 2 x - 1
+  // at least.
+  static_assert(kSeen > (kStages + kRawStages) / 2 + 2, "masks overwritten by copies ahead");
 };
 
 // A sequence: its rows [q0, q0 + nq) of the packed queries, behind len - nq keys.
