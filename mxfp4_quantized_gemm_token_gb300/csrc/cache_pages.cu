@@ -257,8 +257,7 @@ __device__ __forceinline__ void fork(const PagesParams& p) {
   // (-1: the row keeps its parent's pages as they are)
   for (int64_t b = rows.from; b < rows.to; ++b)
     if (p.row_begin[b] == 0) p.row_begin[b] = static_cast<int64_t>(at++);
-  // every row has seen its open page's count: the sums were made after it
-  if constexpr (C == 1) __syncthreads();
+  // (every row has seen its open page's count: the sums' barrier lies behind that)
   take_free(p, pages.from, pages.to, sums.before[1], sums.total[0]);
   all_sync<C>();
   const int64_t have = static_cast<int64_t>(sums.total[1]);
