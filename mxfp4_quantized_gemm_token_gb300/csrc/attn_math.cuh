@@ -102,8 +102,8 @@ __device__ __forceinline__ RowEnd finish_row(float ms, float l, const float* sin
 // mbar_wait_warp that calls what follows a first try without success.  The roles of a kernel
 // share the instructions' supply, and the warp that issues the MMAs, which find their operands
 // ready nearly always, is the one whose turns the others wait for: it fetches no more than
-// the try (a prompt of 8192 tokens 324 -> 307 us, a tree's two tiles of e4m3 286 -> 259; the
-// softmax has no registers for a call).
+// the try (a prompt of 8192 tokens 324 -> 307 us, a tree's two tiles of e4m3 286 -> 259; one prompt of
+// 2048 tokens 65.5 -> 67.5, whichever of the waits are calls; the softmax has no registers for one).
 struct LeanWait {
   static __device__ __noinline__ bool longer(uint64_t* bar, uint32_t parity, const WaitCtx& w) {
     return mbar_wait(bar, parity, w);

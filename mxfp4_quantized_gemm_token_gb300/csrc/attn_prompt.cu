@@ -48,7 +48,8 @@
 // instructions counts (waits by calls: 324 -> 307 us).
 // 11 packed prompts of 8192 tokens: 78 us (42 at the burst rate), 64 at D 64 (21); here an
 // item's beginning and end count, ~2 us.  Two chunks of 300 rows over 7892 keys, in pieces:
-// 70 us (40).  One prompt of 2048 tokens is cut into pieces too: 65 us (18).  Blocks between first
+// 70 us (40).  One prompt of 2048 tokens is cut into pieces too: 67.5 us (18), where the waits by calls
+// cost 3 % (one of 3000 tokens 60 -> 57.5 by them).  Blocks between first
 // keys that stay visible and the window are left out: 5 prompts of 8192 tokens, a window of 1024 and
 // 16 first keys, 96 us (54).
 #include <cuda_bf16.h>

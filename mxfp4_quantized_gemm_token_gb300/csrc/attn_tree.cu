@@ -70,9 +70,17 @@ constexpr int kSoftmaxRegs = 168, kOtherRegs = 88;
 static_assert(2 * kSoftmaxRegs + 2 * kOtherRegs <= 4 * 128, "register split above the launch's");
 constexpr int kPieces = 8;           // pieces of items that may be under way
 constexpr int kSeen = 16;            // blocks whose masks of loaded keys are kept
-constexpr int kWhole = 2;            // items of at most this many blocks stay whole
-constexpr int kAloneSequences = 32;    // calls of at most this many: one warp cuts the line
-constexpr int kAllWhole = 3;         // calls whose items have at most this many: all do
+// Items of at most this many blocks stay whole, so that no piece of theirs is joined; in calls that are
+// cut anyway it makes no difference in time (64 ragged sequences 184 us, 16 of 200-600 keys 21.5,
+// with 0, 1 and 2 alike).
+constexpr int kWhole = 2;
+// Calls of at most this many sequences: one warp cuts the line, a lane has one at most (one tree over 1500
+// keys 13.5 us, by the whole block 14.0; 100 sequences of 300-700 keys, four a lane, 67.5, by the block
+// 66.3).
+constexpr int kAloneSequences = 32;
+// Calls whose items have at most this many blocks: none is cut, and there is nothing to join (one
+// sequence of 300 keys 10.3 us, cut 12.6; 64 of 50-300 32.4 and 38.4; 48 of 200-250 26.1 and 32.1).
+constexpr int kAllWhole = 3;
 
 // What joins an item that several parts share: written by the CTA that begins it.
 struct __align__(16) TreeJoin {
@@ -1164,8 +1172,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const TreeArgs a)
 // each, reading four parts of both at a time: what counts is one chain of loads.  (A warp a row:
 // 16 us for two chunks of 300 rows.)  A block's y is its rows, its x the head and the part that
 // begins the item.  kSplit: few rows, whose parts the block's warps share, and few items, so that x
-// counts those that are shared (one tree over 20000 keys in 19 parts: 25.7 us, without 35.6; finding
-// them costs 64 ragged sequences 4 us).
+// counts those that are shared (one tree over 20000 keys in 19 parts: 25.7 us, without 35.2; over 4000
+// keys 14.0 and 21.5; finding them costs 64 ragged sequences 4 us).  "Few" is 8 blocks an SM: with 2 or
+// 32 none of 17 shapes of 1 to 200 sequences is faster or slower.
 constexpr int kJoinWarps = 4;
 template <int D>
 struct JoinShape {
